@@ -62,6 +62,7 @@ enum { NVFP4_1D16 = 0, NVFP4_2D16x16 = 1 };           /* block scaling     */
 enum { NVFP4_ROWWISE = 1, NVFP4_COLWISE = 2 };        /* output bitmask    */
 enum { NVFP4_SF_ROWMAJOR = 0, NVFP4_SF_MMA = 1 };     /* scale-byte layout */
 enum { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 };       /* GEMM / dequant output */
+enum { NVFP4_SOFTMAX = 0, NVFP4_SIGMOID = 1 };        /* routing scores    */
 
 /*
  * Scale-byte layouts.
@@ -403,6 +404,161 @@ nvfp4_status mxfp8_combine(const uint8_t* q, const uint8_t* e8, int64_t rows, in
                            const int32_t* slot_row, const float* weight, int64_t tokens, int k,
                            void* out_bf16, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * nvfp4_rmsnorm -- root-mean-square norm with the residual's addition, in bf16
+ * or as the MXFP8 operand of mxfp8_gemm, in one pass over the data.  (The pages
+ * name no norm; it is the step before the layers they quantise.)
+ *   h = bf16(x + residual)    (h = x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight   (FP32)
+ * x, residual [rows, ld] bf16; weight [cols] of weight_dtype (NVFP4_OUT_F32 or
+ * NVFP4_OUT_BF16).  Outputs, each only where its pointer is given:
+ *   h [rows, ldh] bf16 (with a residual only, and then required; may be x or
+ *     residual itself, at the same stride);
+ *   y [rows, ldy] bf16;  rstd [rows] FP32 (nvfp4_rmsnorm_backward reads it);
+ *   amax_out [1] FP32: max |y| as stored, for nvfp4_quant_params.amax_in;
+ *   mx_q [rows, cols] E4M3 codes and mx_sf E8M0 bytes of y, unrounded before, by
+ *     mxfp8_quantize's rule; mx_sf in mx_sf_layout.  In the NVFP4_SF_MMA layout
+ *     (mxfp8_sf_mma_bytes) the bytes of the padding rows are zeroed.
+ * At least one of y and mx_q.  rows >= 0; cols a multiple of 8 (with mx_q: of
+ * 32, tiled: of 128), at most 32768; pointers 16-byte aligned, strides
+ * multiples of 8.  eps >= 0; with eps = 0 a row of zeros gives NaN.
+ */
+nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr,
+                           const void* weight, int weight_dtype, float eps, int64_t rows,
+                           int64_t cols, void* h_bf16, int64_t ldh, void* y_bf16, int64_t ldy,
+                           float* rstd, float* amax_out, uint8_t* mx_q, uint8_t* mx_sf,
+                           int mx_sf_layout, void* stream);
+
+/* Workspace bytes nvfp4_rmsnorm_backward needs for dweight. */
+size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * nvfp4_rmsnorm_backward -- gradients of nvfp4_rmsnorm from those of y (dy) and
+ * of h (dh, NULL = none): with n = h * rstd,
+ *   dx = dh + rstd * (weight * dy - n * mean(weight * dy * n)),
+ *   dweight = sum over rows of dy * n        (NULL = not wanted).
+ * dx is the gradient of x and of residual.  It may be dy or dh itself.  dweight
+ * has weight_dtype; its sum is FP32 in a fixed order.  Shapes and alignment as
+ * for nvfp4_rmsnorm.  The workspace is read only for dweight.
+ */
+nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy, const void* h_bf16,
+                                    int64_t ldh, const void* dh_bf16, int64_t lddh,
+                                    const void* weight, int weight_dtype, const float* rstd,
+                                    int64_t rows, int64_t cols, void* dx_bf16, int64_t lddx,
+                                    void* dweight, void* workspace, size_t ws_bytes, void* stream);
+
+typedef struct {
+    int top_k;        /* experts per token, 1..32                                   */
+    int score;        /* NVFP4_SOFTMAX | NVFP4_SIGMOID                              */
+    int groups;       /* expert groups of equal size, 1..32 (1 = no limit)          */
+    int topk_groups;  /* groups a token may choose from                             */
+    int group_top;    /* 1 | 2: a group's rank is the sum of that many best scores  */
+    int renormalize;  /* 1: weights divided by the chosen scores' sum               */
+    float scale;      /* factor on the weights                                      */
+} nvfp4_route_params;
+
+/* Workspace bytes nvfp4_route needs (none for up to 128 tokens). */
+size_t nvfp4_route_workspace_size(int64_t tokens, int experts);
+
+/*
+ * nvfp4_route -- MoE routing (iitak, "Details": tokens travel to their experts):
+ * the experts of each token, the combine's weights, and the order of the routed
+ * rows that nvfp4_gather_rows, the grouped products and the combines read.
+ *   logits [tokens, ld] of logits_dtype; s = softmax or sigmoid of a token's
+ *   logits.  The top_k experts are chosen by s + bias (bias [experts] FP32 or
+ *   NULL, it steers the choice only) among the topk_groups groups whose
+ *   group_top best s + bias sum highest; ties go to the lower index, and the
+ *   comparison is that of the exact scores.  weight = scale * s, divided by the
+ *   sum of the chosen s with renormalize.
+ * A logit at or below bf16's lowest finite value (-3.3895e38; FP32's lowest and
+ * -inf among them) masks its expert.  Where fewer than top_k experts are left,
+ * the remaining slots have expert -1, weight 0 and row -1.  A NaN logit ranks
+ * last.
+ * Outputs: expert, weight [tokens, top_k], by falling rank; group_offsets
+ * [experts + 1]; row_index [tokens * top_k]: the token of each routed row, rows
+ * in expert order and by (token, slot) within an expert, -1 behind the last row
+ * (group_offsets[experts]); slot_row [tokens, top_k]: each slot's row.
+ * tokens >= 0; 1 <= top_k <= experts / groups * topk_groups; experts <= 512.
+ */
+nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,
+                         int64_t tokens, int experts, const nvfp4_route_params* p, int32_t* expert,
+                         float* weight, int32_t* group_offsets, int32_t* row_index,
+                         int32_t* slot_row, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * nvfp4_route_backward -- the logits' gradient from that of nvfp4_route's
+ * weights (dweight [tokens, top_k] FP32), for the experts it chose: dlogits
+ * [tokens, ldd] of logits_dtype, every entry written (the choice itself has no
+ * gradient, bias neither).  Slots with expert -1 give nothing.  Of p, top_k,
+ * score, renormalize and scale count.
+ */
+nvfp4_status nvfp4_route_backward(const float* dweight, const void* logits, int logits_dtype,
+                                  int64_t ld, const int32_t* expert, int64_t tokens, int experts,
+                                  const nvfp4_route_params* p, void* dlogits, int64_t ldd,
+                                  void* stream);
+
+/*
+ * nvfp4_combine -- weighted sum of each token's expert rows, where they are on
+ * this GPU in bf16 or FP32 (mxfp8_combine is the form for rows that travelled):
+ *   out[t] = base[t] + sum_j weight[t][j] * rows[slot_row[t][j]]
+ * in FP32 in slot order, rounded once to bf16.  rows [n_rows, cols] of
+ * rows_dtype; slot_row, weight [tokens, k]; base, out [tokens, cols] bf16 (base
+ * NULL = 0; out may be base).  Slots with a negative row are left out; a row
+ * index >= n_rows is left out and reported in the optional workspace's status
+ * word.  cols a multiple of 8, 1 <= k <= 64, row pointers 16-byte aligned.
+ */
+nvfp4_status nvfp4_combine(const void* rows, int rows_dtype, int64_t n_rows, int64_t cols,
+                           const int32_t* slot_row, const float* weight, int64_t tokens, int k,
+                           const void* base_bf16, void* out_bf16, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Workspace bytes nvfp4_combine_backward needs (the status word, a bit a row). */
+size_t nvfp4_combine_backward_workspace_size(int64_t n_rows);
+
+/*
+ * nvfp4_combine_backward -- gradients of nvfp4_combine:
+ *   drows[slot_row[t][j]] = weight[t][j] * dout[t]      (rows_dtype)
+ *   dweight[t][j] = <dout[t], rows[slot_row[t][j]]>     (FP32; 0 for left-out slots)
+ * Each row belongs to one slot at most, as nvfp4_route's do: a row that a second
+ * slot names is reported (NVFP4_ERR_INDEX) and that slot left out.  used_rows
+ * (device int32, group_offsets + experts of nvfp4_route): the rows from
+ * *used_rows on are zeroed; NULL: rows that no slot names are left as they were.
+ */
+nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void* rows, int rows_dtype,
+                                    int64_t n_rows, int64_t cols, const int32_t* slot_row,
+                                    const float* weight, int64_t tokens, int k,
+                                    const int32_t* used_rows, void* drows, float* dweight,
+                                    void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * nvfp4_gemv -- a few bf16 rows times an NVFP4 matrix (asector, "NVFP4 and
+ * Blackwell"), the form of nvfp4_gemm for single tokens:
+ *   D[i][j] = g * sum_k x[i][k] * (e2m1(q_jk) * e4m3(sf(j, k/16)))
+ * x [rows, ldx] bf16, not quantised; q [N, K/2], sf and g as nvfp4_gemm's B
+ * (NVFP4_SF_MMA layout).  Sums are FP32, in a fixed order.  D [rows, ldd] FP32 or
+ * bf16 (RNE).  Any number of rows; meant for up to about 32, since the matrix is
+ * read again for every 16.  N a multiple of 16, K of 64, ldx >= K of 8;
+ * x, q, sf 16-byte aligned.
+ */
+nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t ldx, int64_t rows, const uint8_t* q,
+                        const uint8_t* sf, const float* g, int64_t N, int64_t K, int out_dtype,
+                        void* D, int64_t ldd, void* stream);
+
+/*
+ * nvfp4_grouped_gemv -- nvfp4_gemv with one matrix per group, the form of
+ * nvfp4_grouped_gemm for a few tokens: row i of D, in group e by group_offsets
+ * (device int32 [G + 1], 1 <= G <= 256), is row row_index[i] of x [src_rows, ldx]
+ * (NULL: row i) times matrix e.  q [G, N, K/2], sf [G] consecutive NVFP4_SF_MMA
+ * blocks, g [G].  Rows behind group_offsets[G] are left as they were; an index
+ * outside x gives a row of zeros and is reported in the optional workspace's
+ * status word.  N a multiple of 128; otherwise as nvfp4_gemv.
+ */
+nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, int64_t total_rows,
+                                const void* x_bf16, int64_t ldx, int64_t src_rows,
+                                const int32_t* row_index, const uint8_t* q, const uint8_t* sf,
+                                const float* g, int64_t N, int64_t K, int out_dtype, void* D,
+                                int64_t ldd, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream` and return the device status word of a workspace
  * (NVFP4_OK, NVFP4_ERR_TIMEOUT or NVFP4_ERR_INDEX); clears it. */
 nvfp4_status nvfp4_workspace_status(void* workspace, void* stream);
@@ -412,7 +568,8 @@ const char* nvfp4_status_string(nvfp4_status s);
 
 /* Library version: major * 10000 + minor * 100 + patch (200: adds mx_sf_layout
  * to nvfp4_quant_params, the sf_layout argument of mxfp4_quantize, mxfp8_gemm,
- * mxfp4_gemm and mxfp8_sf_mma_bytes). */
+ * mxfp4_gemm and mxfp8_sf_mma_bytes; 300: adds the norm, routing, combine and
+ * gemv calls). */
 int nvfp4_version(void);
 
 #ifdef __cplusplus

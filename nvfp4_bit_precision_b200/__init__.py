@@ -2,15 +2,17 @@
 block-scaled GEMM.
 
 The C functions keep their names (``nvfp4_quantize``, ``nvfp4_dequantize``,
-``mxfp8_quantize``, ``mxfp4_quantize``, ``nvfp4_gemm``, ``nvfp4_grouped_gemm``); this module only
-marshals arguments: torch tensors become device pointers and the current torch
+``mxfp8_quantize``, ``mxfp4_quantize``, ``nvfp4_gemm``, ``nvfp4_grouped_gemm``, ``nvfp4_rmsnorm``,
+``nvfp4_route``, ``nvfp4_combine``, ``nvfp4_gemv``, ``nvfp4_grouped_gemv`` and the backward calls); this
+module only marshals arguments: torch tensors become device pointers and the current torch
 stream becomes the ``cudaStream_t``.  Every arithmetic step runs in the CUDA
 kernels of ``libnvfp4.so``.  There is no fallback: importing this package
 raises if the library is missing, and every call raises ``NVFP4Error`` on a
 non-zero status.
 
 The convenience wrappers (``quantize``, ``dequantize``, ``mxfp8``, ``mxfp4``, ``gemm``,
-``grouped_gemm``) allocate their outputs with torch and call the C functions.
+``grouped_gemm``, ``rmsnorm``, ``route``, ``combine``, ``gemv``, ``grouped_gemv``) allocate their outputs
+with torch and call the C functions.
 """
 from __future__ import annotations
 
@@ -40,6 +42,7 @@ NVFP4_1D16, NVFP4_2D16x16 = 0, 1
 NVFP4_ROWWISE, NVFP4_COLWISE = 1, 2
 NVFP4_SF_ROWMAJOR, NVFP4_SF_MMA = 0, 1
 NVFP4_OUT_F32, NVFP4_OUT_BF16 = 0, 1
+NVFP4_SOFTMAX, NVFP4_SIGMOID = 0, 1
 
 EXPORTED = [
     "nvfp4_quantize", "nvfp4_dequantize", "mxfp8_quantize", "nvfp4_gemm", "nvfp4_grouped_gemm",
@@ -47,7 +50,10 @@ EXPORTED = [
     "nvfp4_sf_mma_grouped_bytes", "nvfp4_workspace_status", "nvfp4_status_string",
     "nvfp4_version", "nvfp4_quantize_noalloc", "nvfp4_quantize_noalloc_status",
     "nvfp4_gather_rows", "mxfp4_quantize", "mxfp8_gemm", "mxfp8_sf_mma_bytes", "mxfp4_gemm",
-    "mxfp8_combine", "nvfp4_gemm_cycles",
+    "mxfp8_combine", "nvfp4_gemm_cycles", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward",
+    "nvfp4_rmsnorm_backward_workspace_size", "nvfp4_route", "nvfp4_route_backward",
+    "nvfp4_route_workspace_size", "nvfp4_combine", "nvfp4_combine_backward",
+    "nvfp4_combine_backward_workspace_size", "nvfp4_gemv", "nvfp4_grouped_gemv",
 ]
 
 
@@ -64,6 +70,15 @@ class QuantParams(ctypes.Structure):
         ("mx_q_row", ctypes.c_void_p), ("mx_sf_row", ctypes.c_void_p),
         ("mx_q_col", ctypes.c_void_p), ("mx_sf_col", ctypes.c_void_p),
         ("mx_sf_layout", ctypes.c_int),
+    ]
+
+
+class RouteParams(ctypes.Structure):
+    """Mirror of ``nvfp4_route_params`` (include/nvfp4.h)."""
+    _fields_ = [
+        ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int),
+        ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -104,10 +119,33 @@ _lib.nvfp4_quantize_noalloc_status.argtypes = [_P]
 _lib.nvfp4_status_string.argtypes = [ctypes.c_int]
 _lib.nvfp4_status_string.restype = ctypes.c_char_p
 _lib.nvfp4_version.restype = ctypes.c_int
+_INT, _F32 = ctypes.c_int, ctypes.c_float
+_lib.nvfp4_rmsnorm.argtypes = [_P, _I64, _P, _I64, _P, _INT, _F32, _I64, _I64, _P, _I64, _P, _I64, _P, _P,
+                               _P, _P, _INT, _P]
+_lib.nvfp4_rmsnorm_backward.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _INT, _P, _I64, _I64, _P, _I64,
+                                        _P, _P, _SZ, _P]
+_lib.nvfp4_rmsnorm_backward_workspace_size.argtypes = [_I64, _I64]
+_lib.nvfp4_rmsnorm_backward_workspace_size.restype = _SZ
+_lib.nvfp4_route.argtypes = [_P, _INT, _I64, _P, _I64, _INT, ctypes.POINTER(RouteParams), _P, _P, _P, _P,
+                             _P, _P, _SZ, _P]
+_lib.nvfp4_route_backward.argtypes = [_P, _P, _INT, _I64, _P, _I64, _INT, ctypes.POINTER(RouteParams), _P,
+                                      _I64, _P]
+_lib.nvfp4_route_workspace_size.argtypes = [_I64, _INT]
+_lib.nvfp4_route_workspace_size.restype = _SZ
+_lib.nvfp4_combine.argtypes = [_P, _INT, _I64, _I64, _P, _P, _I64, _INT, _P, _P, _P, _SZ, _P]
+_lib.nvfp4_combine_backward.argtypes = [_P, _P, _INT, _I64, _I64, _P, _P, _I64, _INT, _P, _P, _P, _P, _SZ,
+                                        _P]
+_lib.nvfp4_combine_backward_workspace_size.argtypes = [_I64]
+_lib.nvfp4_combine_backward_workspace_size.restype = _SZ
+_lib.nvfp4_gemv.argtypes = [_P, _I64, _I64, _P, _P, _P, _I64, _I64, _INT, _P, _I64, _P]
+_lib.nvfp4_grouped_gemv.argtypes = [_INT, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _INT, _P,
+                                    _I64, _P, _SZ, _P]
 for _n in ("nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_quantize", "mxfp4_quantize",
            "nvfp4_dequantize", "nvfp4_gemm", "mxfp8_gemm", "mxfp4_gemm", "mxfp8_combine",
            "nvfp4_grouped_gemm", "nvfp4_gather_rows", "nvfp4_workspace_status",
-           "nvfp4_quantize_noalloc_status", "nvfp4_gemm_cycles"):
+           "nvfp4_quantize_noalloc_status", "nvfp4_gemm_cycles", "nvfp4_rmsnorm",
+           "nvfp4_rmsnorm_backward", "nvfp4_route", "nvfp4_route_backward", "nvfp4_combine",
+           "nvfp4_combine_backward", "nvfp4_gemv", "nvfp4_grouped_gemv"):
     getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -137,7 +175,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -223,6 +261,76 @@ def nvfp4_gather_rows(q_src, sf_src, src_rows, k, row_index, rows, group_offsets
                                   _ptr(group_offsets), num_groups, _ptr(q_dst), _ptr(sf_dst),
                                   _ptr(workspace), ws_bytes, _stream(stream)),
            "nvfp4_gather_rows")
+
+
+def nvfp4_rmsnorm(x, ldx, residual, ldr, weight, weight_dtype, eps, rows, cols, h, ldh, y, ldy, rstd,
+                  amax_out, mx_q, mx_sf, mx_sf_layout, stream=None) -> None:
+    _check(_lib.nvfp4_rmsnorm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), weight_dtype, eps, rows, cols,
+                              _ptr(h), ldh, _ptr(y), ldy, _ptr(rstd), _ptr(amax_out), _ptr(mx_q),
+                              _ptr(mx_sf), mx_sf_layout, _stream(stream)), "nvfp4_rmsnorm")
+
+
+def nvfp4_rmsnorm_backward(dy, lddy, h, ldh, dh, lddh, weight, weight_dtype, rstd, rows, cols, dx, lddx,
+                           dweight, workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_rmsnorm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(dh), lddh, _ptr(weight),
+                                       weight_dtype, _ptr(rstd), rows, cols, _ptr(dx), lddx, _ptr(dweight),
+                                       _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_rmsnorm_backward")
+
+
+def nvfp4_route(logits, logits_dtype, ld, bias, tokens, experts, params: RouteParams, expert, weight,
+                group_offsets, row_index, slot_row, workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_route(_ptr(logits), logits_dtype, ld, _ptr(bias), tokens, experts,
+                            ctypes.byref(params), _ptr(expert), _ptr(weight), _ptr(group_offsets),
+                            _ptr(row_index), _ptr(slot_row), _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_route")
+
+
+def nvfp4_route_backward(dweight, logits, logits_dtype, ld, expert, tokens, experts, params: RouteParams,
+                         dlogits, ldd, stream=None) -> None:
+    _check(_lib.nvfp4_route_backward(_ptr(dweight), _ptr(logits), logits_dtype, ld, _ptr(expert), tokens,
+                                     experts, ctypes.byref(params), _ptr(dlogits), ldd, _stream(stream)),
+           "nvfp4_route_backward")
+
+
+def nvfp4_combine(rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k, base, out, workspace=None,
+                  ws_bytes=0, stream=None) -> None:
+    _check(_lib.nvfp4_combine(_ptr(rows), rows_dtype, n_rows, cols, _ptr(slot_row), _ptr(weight), tokens, k,
+                              _ptr(base), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_combine")
+
+
+def nvfp4_combine_backward(dout, rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k, used_rows,
+                           drows, dweight, workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_combine_backward(_ptr(dout), _ptr(rows), rows_dtype, n_rows, cols, _ptr(slot_row),
+                                       _ptr(weight), tokens, k, _ptr(used_rows), _ptr(drows), _ptr(dweight),
+                                       _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_combine_backward")
+
+
+def nvfp4_gemv(x, ldx, rows, q, sf, g, N, K, out_dtype, D, ldd, stream=None) -> None:
+    _check(_lib.nvfp4_gemv(_ptr(x), ldx, rows, _ptr(q), _ptr(sf), _ptr(g), N, K, out_dtype, _ptr(D), ldd,
+                           _stream(stream)), "nvfp4_gemv")
+
+
+def nvfp4_grouped_gemv(G, group_offsets, total_rows, x, ldx, src_rows, row_index, q, sf, g, N, K, out_dtype,
+                       D, ldd, workspace=None, ws_bytes=0, stream=None) -> None:
+    _check(_lib.nvfp4_grouped_gemv(G, _ptr(group_offsets), total_rows, _ptr(x), ldx, src_rows,
+                                   _ptr(row_index), _ptr(q), _ptr(sf), _ptr(g), N, K, out_dtype, _ptr(D),
+                                   ldd, _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_grouped_gemv")
+
+
+def nvfp4_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols))
+
+
+def nvfp4_route_workspace_size(tokens: int, experts: int) -> int:
+    return int(_lib.nvfp4_route_workspace_size(tokens, experts))
+
+
+def nvfp4_combine_backward_workspace_size(n_rows: int) -> int:
+    return int(_lib.nvfp4_combine_backward_workspace_size(n_rows))
 
 
 def nvfp4_workspace_status(workspace, stream=None) -> int:
@@ -475,3 +583,301 @@ def gather_rows(t: NVFP4Tensor, row_index, group_offsets=None, workspace=None, s
     nvfp4_gather_rows(t.q, t.sf, t.rows, t.k, row_index, rows, group_offsets, G, q, sf, ws,
                       ws.numel(), stream)
     return NVFP4Tensor(q, sf, t.g, rows, t.k, NVFP4_SF_MMA)
+
+
+# ------------------------------------------------- the MoE block around the experts' products
+@dataclass
+class Routing:
+    """What ``route`` gives: the experts and weights of each token's slots, and the order of the
+    routed rows that ``gather_rows``, ``grouped_gemm``, ``grouped_gemv`` and ``combine`` read."""
+    expert: object         # int32 [tokens, top_k], -1 = no expert
+    weight: object         # f32 [tokens, top_k]
+    group_offsets: object  # int32 [experts + 1]
+    row_index: object      # int32 [tokens * top_k]: the token of each routed row
+    slot_row: object       # int32 [tokens, top_k]: the row of each slot, -1 = none
+    params: RouteParams
+
+
+def _need(ok, message: str) -> None:
+    if not ok:
+        raise ValueError(message)
+
+
+def _one_device(name: str, *tensors):
+    """The device of the tensors: one CUDA device, the current one (the calls launch there)."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: CUDA tensors expected, got {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensors on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _dtype_code(name: str, t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return NVFP4_OUT_BF16
+    if t.dtype == torch.float32:
+        return NVFP4_OUT_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _rows_of(name: str, t, rows: Optional[int], cols: Optional[int]):
+    """A bf16 matrix with contiguous rows; returns its row stride in elements."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name} must be a bfloat16 matrix, got {t.dtype} {tuple(t.shape)}")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: [{rows}, {cols}] expected, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # the stride of a single row is never used, and torch leaves it arbitrary
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _flat(name: str, t, dtype, *shape) -> None:
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _torch_stream(stream):
+    import torch
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
+def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, y: bool = True, mx: bool = False,
+            mx_sf_layout: int = NVFP4_SF_ROWMAJOR, amax: bool = False, rstd: bool = False, stream=None):
+    """Root-mean-square norm of x + residual (bf16 [rows, cols]) times weight (bf16 or f32 [cols]).
+
+    Returns a dict: 'h' the sum in bf16 (x itself without a residual), 'y' the norm in bf16, 'mx' its MXFP8
+    (codes, e8m0) for ``mx_gemm``, 'amax' max |y| ([1], for ``quantize``'s amax), 'rstd' [rows] for
+    ``rmsnorm_backward``; None for what was not asked for."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return rmsnorm(x, weight, residual, eps, y=y, mx=mx, mx_sf_layout=mx_sf_layout, amax=amax,
+                           rstd=rstd)
+    dev = _one_device("rmsnorm", x, weight, residual)
+    ldx = _rows_of("rmsnorm: x", x, None, None)
+    rows, cols = x.shape
+    wdt = _dtype_code("rmsnorm: weight", weight)
+    _flat("rmsnorm: weight", weight, weight.dtype, cols)
+    _need(y or mx, "rmsnorm: neither y nor mx asked for")
+    _need(y or not amax, "rmsnorm: amax is that of y")
+    h, ldr = x, 0
+    if residual is not None:
+        ldr = _rows_of("rmsnorm: residual", residual, rows, cols)
+        h = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    out = {"h": h, "y": None, "mx": None, "amax": None, "rstd": None}
+    if y:
+        out["y"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    mq = ms = None
+    if mx:
+        mq = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        ms = (torch.empty(mxfp8_sf_mma_bytes(rows, cols), dtype=torch.uint8, device=dev)
+              if mx_sf_layout == NVFP4_SF_MMA else
+              torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev))
+        out["mx"] = (mq, ms)
+    if amax:
+        out["amax"] = torch.empty(1, dtype=torch.float32, device=dev)
+    if rstd:
+        out["rstd"] = torch.empty(rows, dtype=torch.float32, device=dev)
+    nvfp4_rmsnorm(x, ldx, residual, ldr, weight, wdt, eps, rows, cols, h if residual is not None else None,
+                  cols, out["y"], cols, out["rstd"], out["amax"], mq, ms, mx_sf_layout)
+    return out
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, workspace=None, stream=None):
+    """(dx, dweight) of ``rmsnorm`` from the gradients of its y and (dh, optional) of its h.  dx is the
+    gradient of x and of residual; dweight (in weight's dtype) is None where not asked for."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return rmsnorm_backward(dy, h, weight, rstd, dh, dweight=dweight, workspace=workspace)
+    dev = _one_device("rmsnorm_backward", dy, h, weight, rstd, dh, workspace)
+    ldy = _rows_of("rmsnorm_backward: dy", dy, None, None)
+    rows, cols = dy.shape
+    ldh = _rows_of("rmsnorm_backward: h", h, rows, cols)
+    lddh = _rows_of("rmsnorm_backward: dh", dh, rows, cols) if dh is not None else 0
+    wdt = _dtype_code("rmsnorm_backward: weight", weight)
+    _flat("rmsnorm_backward: weight", weight, weight.dtype, cols)
+    _flat("rmsnorm_backward: rstd", rstd, torch.float32, rows)
+    dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    dw = ws = None
+    if dweight:
+        dw = torch.empty_like(weight)
+        ws = workspace if workspace is not None else _workspace(
+            dev, nvfp4_rmsnorm_backward_workspace_size(rows, cols))
+    nvfp4_rmsnorm_backward(dy, ldy, h, ldh, dh, lddh, weight, wdt, rstd, rows, cols, dx, cols, dw, ws,
+                           ws.numel() if ws is not None else 0)
+    return dx, dw
+
+
+def _logits_of(name: str, logits):
+    dt = _dtype_code(f"{name}: logits", logits)
+    _need(logits.dim() == 2, f"{name}: logits [tokens, experts] expected")
+    _need(logits.shape[1] <= 1 or logits.stride(1) == 1, f"{name}: rows of logits must be contiguous")
+    return dt, logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+
+
+def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: int = 1,
+          topk_groups: Optional[int] = None, group_top: int = 2, renormalize: bool = True,
+          scale: float = 1.0, workspace=None, stream=None) -> Routing:
+    """Experts and weights of each token (logits [tokens, experts], bf16 or f32), and the order of the routed
+    rows.  bias (f32 [experts]) steers the choice only; ``topk_groups`` of ``groups`` expert groups, ranked by
+    the sum of their ``group_top`` best scores, may be chosen from.  Logits at or below bf16's lowest finite
+    value mask their experts; slots without an expert have expert -1, weight 0 and row -1."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return route(logits, top_k, score=score, bias=bias, groups=groups, topk_groups=topk_groups,
+                         group_top=group_top, renormalize=renormalize, scale=scale, workspace=workspace)
+    dev = _one_device("route", logits, bias, workspace)
+    dt, ld = _logits_of("route", logits)
+    tokens, experts = logits.shape
+    if bias is not None:
+        _flat("route: bias", bias, torch.float32, experts)
+    _need(top_k >= 1, "route: top_k must be at least 1")
+    p = RouteParams(top_k, score, groups, groups if topk_groups is None else topk_groups, group_top,
+                    1 if renormalize else 0, scale)
+    i32 = dict(dtype=torch.int32, device=dev)
+    r = Routing(torch.empty((tokens, top_k), **i32),
+                torch.empty((tokens, top_k), dtype=torch.float32, device=dev),
+                torch.empty(experts + 1, **i32), torch.empty(tokens * top_k, **i32),
+                torch.empty((tokens, top_k), **i32), p)
+    ws = workspace
+    if ws is None:
+        n = nvfp4_route_workspace_size(tokens, experts)
+        ws = _workspace(dev, n) if n > 256 else None
+    nvfp4_route(logits, dt, ld, bias, tokens, experts, p, r.expert, r.weight, r.group_offsets, r.row_index,
+                r.slot_row, ws, ws.numel() if ws is not None else 0)
+    return r
+
+
+def route_backward(dweight, logits, routing: Routing, *, stream=None):
+    """The logits' gradient (their dtype) from that of ``routing.weight`` (f32 [tokens, top_k])."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return route_backward(dweight, logits, routing)
+    dev = _one_device("route_backward", dweight, logits, routing.expert)
+    dt, ld = _logits_of("route_backward", logits)
+    tokens, experts = logits.shape
+    k = routing.params.top_k
+    _flat("route_backward: dweight", dweight, torch.float32, tokens, k)
+    _flat("route_backward: expert", routing.expert, torch.int32, tokens, k)
+    d = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
+    nvfp4_route_backward(dweight, logits, dt, ld, routing.expert, tokens, experts, routing.params, d, experts)
+    return d
+
+
+def _combine_args(name: str, rows, slot_row, weight):
+    import torch
+    dt = _dtype_code(f"{name}: rows", rows)
+    _need(rows.dim() == 2 and rows.is_contiguous(), f"{name}: contiguous rows [n, cols] expected")
+    _need(slot_row.dim() == 2, f"{name}: slot_row [tokens, k] expected")
+    tokens, k = slot_row.shape
+    _flat(f"{name}: slot_row", slot_row, torch.int32, tokens, k)
+    _flat(f"{name}: weight", weight, torch.float32, tokens, k)
+    return dt, rows.shape[0], rows.shape[1], tokens, k
+
+
+def combine(rows, slot_row, weight, base=None, *, workspace=None, stream=None):
+    """out[t] = base[t] + sum_j weight[t, j] * rows[slot_row[t, j]], bf16 [tokens, cols]; rows bf16 or f32,
+    slots with a negative row left out.  ``workspace`` (256 bytes, optional) receives the status word."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return combine(rows, slot_row, weight, base, workspace=workspace)
+    dev = _one_device("combine", rows, slot_row, weight, base, workspace)
+    dt, n, cols, tokens, k = _combine_args("combine", rows, slot_row, weight)
+    if base is not None:
+        _flat("combine: base", base, torch.bfloat16, tokens, cols)
+    out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
+    nvfp4_combine(rows, dt, n, cols, slot_row, weight, tokens, k, base, out, workspace,
+                  workspace.numel() if workspace is not None else 0)
+    return out
+
+
+def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, workspace=None, stream=None):
+    """(drows, dweight) of ``combine`` (the base's gradient is dout).  With the routing's ``group_offsets``
+    the rows behind its last one get a zero gradient; without, every row that no slot names does."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return combine_backward(dout, rows, slot_row, weight, group_offsets, workspace=workspace)
+    dev = _one_device("combine_backward", dout, rows, slot_row, weight, group_offsets, workspace)
+    dt, n, cols, tokens, k = _combine_args("combine_backward", rows, slot_row, weight)
+    _flat("combine_backward: dout", dout, torch.bfloat16, tokens, cols)
+    used = None
+    if group_offsets is not None:
+        _need(group_offsets.dim() == 1 and group_offsets.numel() >= 2,
+              "combine_backward: group_offsets [groups + 1] expected")
+        _flat("combine_backward: group_offsets", group_offsets, torch.int32, group_offsets.numel())
+        used = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
+    make = torch.empty_like if used is not None else torch.zeros_like
+    drows = make(rows)
+    dweight = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+    ws = workspace if workspace is not None else _workspace(dev, nvfp4_combine_backward_workspace_size(n))
+    nvfp4_combine_backward(dout, rows, dt, n, cols, slot_row, weight, tokens, k, used, drows, dweight, ws,
+                           ws.numel())
+    return drows, dweight
+
+
+def _gemv_out(name: str, out_dtype: int, rows: int, N: int, out, dev):
+    import torch
+    dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
+    if out is None:
+        return torch.empty((rows, N), dtype=dt, device=dev), N
+    _need(out.dtype == dt and tuple(out.shape) == (rows, N) and (N <= 1 or out.stride(1) == 1),
+          f"{name}: out {dt} [{rows}, {N}] with contiguous rows expected")
+    _need(rows <= 1 or out.stride(0) >= N, f"{name}: rows of out overlap")
+    return out, out.stride(0) if rows > 1 else N
+
+
+def gemv(x, w: NVFP4Tensor, out_dtype: int = NVFP4_OUT_BF16, out=None, *, stream=None):
+    """D = x W^T of a few bf16 rows x [rows, K] and an NVFP4 matrix [N, K] (tiled scales): ``gemm`` for
+    single tokens, x not quantised."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return gemv(x, w, out_dtype, out)
+    dev = _one_device("gemv", x, w.q, w.sf, w.g, out)
+    ldx = _rows_of("gemv: x", x, None, w.k)
+    _need(w.sf_layout == NVFP4_SF_MMA, "gemv: w must have tiled scales (NVFP4_SF_MMA)")
+    _flat("gemv: w.q", w.q, torch.uint8, w.rows, w.k // 2)
+    _need(w.sf.is_contiguous() and w.sf.numel() >= nvfp4_sf_mma_bytes(w.rows, w.k), "gemv: w.sf too small")
+    out, ldd = _gemv_out("gemv", out_dtype, x.shape[0], w.rows, out, dev)
+    nvfp4_gemv(x, ldx, x.shape[0], w.q, w.sf, w.g, w.rows, w.k, out_dtype, out, ldd)
+    return out
+
+
+def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtype: int = NVFP4_OUT_BF16,
+                 out=None, *, workspace=None, stream=None):
+    """``gemv`` with one matrix per group: row i of D (in group e by group_offsets) is row row_index[i] of x
+    (row i without row_index) times matrix e; qb [G, N, K/2], sfb tiled per matrix, gb [G]."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return grouped_gemv(group_offsets, x, qb, sfb, gb, N, row_index, out_dtype, out,
+                                workspace=workspace)
+    dev = _one_device("grouped_gemv", x, group_offsets, qb, sfb, gb, row_index, out, workspace)
+    ldx = _rows_of("grouped_gemv: x", x, None, None)
+    K, G = x.shape[1], group_offsets.numel() - 1
+    _flat("grouped_gemv: group_offsets", group_offsets, torch.int32, G + 1)
+    _flat("grouped_gemv: qb", qb, torch.uint8, G, N, K // 2)
+    _flat("grouped_gemv: gb", gb, torch.float32, G)
+    _need(sfb.is_contiguous() and sfb.numel() >= G * nvfp4_sf_mma_bytes(N, K), "grouped_gemv: sfb too small")
+    rows = x.shape[0]
+    if row_index is not None:
+        rows = row_index.numel()
+        _flat("grouped_gemv: row_index", row_index, torch.int32, rows)
+    out, ldd = _gemv_out("grouped_gemv", out_dtype, rows, N, out, dev)
+    nvfp4_grouped_gemv(G, group_offsets, rows, x, ldx, x.shape[0], row_index, qb, sfb, gb, N, K, out_dtype,
+                       out, ldd, workspace, workspace.numel() if workspace is not None else 0)
+    return out

@@ -13,14 +13,15 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4.so")
-SOURCES = ["quantize.cu", "gemm.cu", "mxfp4.cu", "moe_comm.cu"]
+SOURCES = ["quantize.cu", "gemm.cu", "mxfp4.cu", "moe_comm.cu", "norm.cu", "route.cu", "combine.cu",
+           "gemv.cu"]
 HEADERS = ["common.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
-    "-Xptxas", "-v",
+    "-Xptxas", "-v", "--threads", "0",
 ]
 
 

@@ -1,0 +1,259 @@
+// combine.cu -- the weighted sum of a token's expert rows, and its gradients.
+//
+//   out[t] = base[t] + sum_j weight[t][j] * rows[slot_row[t][j]]
+//   drows[slot_row[t][j]] = weight[t][j] * dout[t]
+//   dweight[t][j] = <dout[t], rows[slot_row[t][j]]>        (dbase = dout)
+//
+// FP32 sums in slot order, one rounding to bf16 at the end; slots with a
+// negative row are left out.  All three are one pass over the data.
+#include "common.cuh"
+
+#include <algorithm>
+
+namespace nvfp4 {
+namespace {
+
+template <bool F32>
+struct RowVec;  // eight elements of a row
+template <>
+struct RowVec<false> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void* rows, int64_t vec) { v = static_cast<const uint4*>(rows)[vec]; }
+    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+    static __device__ __forceinline__ void store(void* rows, int64_t vec, const float (&f)[8])
+    {
+        static_cast<uint4*>(rows)[vec] = pack8(f);
+    }
+};
+template <>
+struct RowVec<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* rows, int64_t vec)
+    {
+        a = static_cast<const float4*>(rows)[2 * vec];
+        b = static_cast<const float4*>(rows)[2 * vec + 1];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(void* rows, int64_t vec, const float (&f)[8])
+    {
+        static_cast<float4*>(rows)[2 * vec] = make_float4(f[0], f[1], f[2], f[3]);
+        static_cast<float4*>(rows)[2 * vec + 1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+// A slot's row, -1 for none; an index past the rows is reported and left out.
+__device__ __forceinline__ int32_t slot_of(const int32_t* slot_row, int64_t slot, int64_t n_rows, uint32_t* status)
+{
+    const int32_t r = slot_row[slot];
+    if (r >= n_rows) {
+        record_status(status, NVFP4_ERR_INDEX);
+        return -1;
+    }
+    return r < 0 ? -1 : r;
+}
+
+// One thread = 8 columns of a token; four slots' loads in flight.
+template <bool F32>
+__global__ void __launch_bounds__(256) combine_kernel(const void* rows, int64_t n_rows, int64_t nvec,
+                                                      const int32_t* slot_row, const float* weight, int64_t tokens,
+                                                      int k, const uint4* base, uint4* out, uint32_t* status)
+{
+    for (int64_t u = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; u < tokens * nvec;
+         u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t t = u / nvec, c = u - t * nvec;
+        float acc[8];
+        if (base) {
+            unpack8(base[u], acc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+        }
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            int32_t r[4];
+            RowVec<F32> v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[j] = j0 + j < k ? slot_of(slot_row, t * k + j0 + j, n_rows, status) : -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r[j] >= 0) v[j].load(rows, r[j] * nvec + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (r[j] < 0) continue;
+                const float w = weight[t * k + j0 + j];
+                float f[8];
+                v[j].get(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+            }
+        }
+        out[u] = pack8(acc);
+    }
+}
+
+// One CTA of W warps per token; each thread keeps the products' sums of four
+// slots over its columns.  A row named by a second slot is reported and left
+// alone (`seen`, one bit a row, cleared by the call): its gradient would be a
+// sum that two slots write.
+template <bool F32>
+__global__ void __launch_bounds__(256) combine_backward_kernel(
+    const uint4* dout, const void* rows, int64_t n_rows, int nvec, const int32_t* slot_row, const float* weight,
+    int64_t tokens, int k, const int32_t* used_rows, void* drows, float* dweight, uint32_t* seen, uint32_t* status)
+{
+    __shared__ float s_dot[4][8];
+    __shared__ int32_t s_row[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            __syncthreads();
+            if (threadIdx.x < 4) {
+                const int j = threadIdx.x;
+                int32_t r = j0 + j < k ? slot_of(slot_row, t * k + j0 + j, n_rows, status) : -1;
+                if (r >= 0 && (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31)) & 1u) {
+                    record_status(status, NVFP4_ERR_INDEX);
+                    r = -1;
+                }
+                s_row[j] = r;
+            }
+            __syncthreads();
+            int32_t r[4];
+            float w[4], dot[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[j] = s_row[j];
+                w[j] = r[j] >= 0 ? weight[t * k + j0 + j] : 0.0f;
+                dot[j] = 0.0f;
+            }
+            for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+                RowVec<F32> v[4];
+                const uint4 dv = dout[t * nvec + c];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r[j] >= 0) v[j].load(rows, static_cast<int64_t>(r[j]) * nvec + c);
+                float d[8];
+                unpack8(dv, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (r[j] < 0) continue;
+                    float f[8];
+                    v[j].get(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot[j] = fmaf(d[i], f[i], dot[j]);
+                        f[i] = w[j] * d[i];
+                    }
+                    RowVec<F32>::store(drows, static_cast<int64_t>(r[j]) * nvec + c, f);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+                if (lane == 0) s_dot[j][warp] = dot[j];
+            }
+            __syncthreads();
+            if (threadIdx.x < 4 && j0 + threadIdx.x < k) {
+                float sum = 0.0f;
+                for (int i = 0; i < warps; ++i) sum += s_dot[threadIdx.x][i];
+                dweight[t * k + j0 + threadIdx.x] = sum;
+            }
+        }
+    }
+    if (used_rows) {  // rows that belong to no slot
+        const int64_t first = max(*used_rows, 0);
+        const float zero[8] = {};
+        for (int64_t u = first * nvec + blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; u < n_rows * nvec;
+             u += static_cast<int64_t>(gridDim.x) * blockDim.x)
+            RowVec<F32>::store(drows, u, zero);
+    }
+}
+
+constexpr size_t kCombineWorkspaceHead = 256;
+
+nvfp4_status combine_common(const void* rows, int rows_dtype, int64_t n_rows, int64_t cols, const int32_t* slot_row,
+                            const float* weight, int64_t tokens, int k)
+{
+    if (rows_dtype != NVFP4_OUT_F32 && rows_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_INVALID_ARG;
+    if (k < 1 || k > 64) return NVFP4_ERR_INVALID_ARG;
+    if (n_rows < 0 || n_rows > 0x7fffffffll || tokens < 0 || cols <= 0 || cols % 8 || cols > (1ll << 30))
+        return NVFP4_ERR_SHAPE;
+    if ((n_rows > 0 && !rows) || (tokens > 0 && (!slot_row || !weight))) return NVFP4_ERR_INVALID_ARG;
+    if (off16(rows) || (reinterpret_cast<uintptr_t>(slot_row) & 3u) || (reinterpret_cast<uintptr_t>(weight) & 3u))
+        return NVFP4_ERR_ALIGN;
+    return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" nvfp4_status nvfp4_combine(const void* rows, int rows_dtype, int64_t n_rows, int64_t cols,
+                                      const int32_t* slot_row, const float* weight, int64_t tokens, int k,
+                                      const void* base_bf16, void* out_bf16, void* workspace, size_t ws_bytes,
+                                      void* stream)
+{
+    if (const nvfp4_status s = combine_common(rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k)) return s;
+    if (tokens > 0 && !out_bf16) return NVFP4_ERR_INVALID_ARG;
+    if (off16(base_bf16) || off16(out_bf16)) return NVFP4_ERR_ALIGN;
+    if (workspace && (ws_bytes < 16 || off16(workspace))) return NVFP4_ERR_WORKSPACE;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    const int sms = sm100_sms(dev);
+    if (!sms) return NVFP4_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint32_t* status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
+    if (status && cudaMemsetAsync(status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (tokens == 0) return NVFP4_OK;
+    const int64_t nvec = cols / 8;
+    const int grid = static_cast<int>(std::min<int64_t>((tokens * nvec + 255) / 256, static_cast<int64_t>(sms) * 8));
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, st>>>(rows, n_rows, nvec, slot_row, weight, tokens, k,
+                                     static_cast<const uint4*>(base_bf16), static_cast<uint4*>(out_bf16), status);
+    };
+    rows_dtype == NVFP4_OUT_F32 ? go(combine_kernel<true>) : go(combine_kernel<false>);
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+extern "C" size_t nvfp4_combine_backward_workspace_size(int64_t n_rows)
+{
+    return kCombineWorkspaceHead + (n_rows > 0 ? static_cast<size_t>((n_rows + 31) / 32) * 4 : 0);
+}
+
+extern "C" nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void* rows, int rows_dtype,
+                                               int64_t n_rows, int64_t cols, const int32_t* slot_row,
+                                               const float* weight, int64_t tokens, int k, const int32_t* used_rows,
+                                               void* drows, float* dweight, void* workspace, size_t ws_bytes,
+                                               void* stream)
+{
+    if (const nvfp4_status s = combine_common(rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k)) return s;
+    if ((tokens > 0 && (!dout_bf16 || !dweight)) || (n_rows > 0 && !drows)) return NVFP4_ERR_INVALID_ARG;
+    if (off16(dout_bf16) || off16(drows) || (reinterpret_cast<uintptr_t>(dweight) & 3u) ||
+        (reinterpret_cast<uintptr_t>(used_rows) & 3u))
+        return NVFP4_ERR_ALIGN;
+    if (!workspace || off16(workspace) || ws_bytes < nvfp4_combine_backward_workspace_size(n_rows))
+        return NVFP4_ERR_WORKSPACE;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    const int sms = sm100_sms(dev);
+    if (!sms) return NVFP4_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(workspace, 0, nvfp4_combine_backward_workspace_size(n_rows), st) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+    if (tokens == 0 && (n_rows == 0 || !used_rows)) return NVFP4_OK;
+    const int nvec = static_cast<int>(cols / 8);
+    const int threads = std::min(256, std::max(1, (nvec + 31) / 32) * 32);
+    const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tokens, 1), static_cast<int64_t>(sms) * 8));
+    uint32_t* status = static_cast<uint32_t*>(workspace) + 2;
+    uint32_t* seen = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kCombineWorkspaceHead);
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, threads, 0, st>>>(static_cast<const uint4*>(dout_bf16), rows, n_rows, nvec, slot_row, weight,
+                                         tokens, k, used_rows, drows, dweight, seen, status);
+    };
+    rows_dtype == NVFP4_OUT_F32 ? go(combine_backward_kernel<true>) : go(combine_backward_kernel<false>);
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}

@@ -12,6 +12,8 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <mutex>
+
 #include "nvfp4.h"
 
 #if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ < 1000)
@@ -452,6 +454,26 @@ __device__ __forceinline__ float bf16_hi(uint32_t packed)
     return __uint_as_float(packed & 0xFFFF0000u);
 }
 
+// Eight bf16 values of a 16-byte vector <-> floats (pack8 rounds to nearest even).
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
+{
+    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z);
+    f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
 // E4M3 round-to-nearest-even, saturating to +-448; returns the byte.
 __device__ __forceinline__ uint32_t e4m3_rne_sat(float v)
 {
@@ -543,5 +565,22 @@ __host__ __device__ __forceinline__ int64_t sf_mma_offset(int64_t r, int64_t b, 
     const int64_t atom = (r >> 7) * (k16 >> 2) + (b >> 2);
     return atom * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3);
 }
+
+// SM count of an sm_100 device, 0 for any other (host).
+inline int sm100_sms(int dev)
+{
+    static int sms[64];
+    static std::once_flag flags[64];
+    std::call_once(flags[dev & 63], [dev]() {
+        int major = 0, n = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess && major == 10 &&
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+            sms[dev & 63] = n;
+    });
+    return sms[dev & 63];
+}
+
+// Not on a 16-byte boundary.
+inline bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 }  // namespace nvfp4

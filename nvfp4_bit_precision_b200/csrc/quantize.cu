@@ -1674,4 +1674,4 @@ extern "C" const char* nvfp4_status_string(nvfp4_status s)
     return "unknown status";
 }
 
-extern "C" int nvfp4_version(void) { return 200; }
+extern "C" int nvfp4_version(void) { return 300; }
