@@ -21,13 +21,25 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kGemvThreads = 256;
-constexpr int kGemvWarps = kGemvThreads / 32;
-constexpr int kUnitRows = 64;   // weight rows of a unit: 16 rows of each 32 of a 128-row scale block
-constexpr int kChunk = 128;     // columns of a step, 32 per lane
-constexpr int kTokStride = 68;  // floats per token in the reduction buffer (64 rows, padded off the banks)
+constexpr int kGemvWarps = 16;
+constexpr int kStep = 256;               // columns of a step, 64 per lane
+constexpr int kStageBytes = 2048 + 256;  // a 16-row tile's codes and scales
+constexpr int kRedStride = 20;           // floats per token of a tile's sums (16 rows, off the banks)
 constexpr int kMaxGemvGroups = 256;
+constexpr int kMaxSegments = 16;         // segments whose x rows are in shared memory together
+constexpr size_t kGemvSmem = 216 * 1024;  // (and less than 11 KB that is not dynamic)
 
+// Steps in a warp's ring, all but one copied ahead.
+#ifndef GS
+#define GS 3
+#endif
+__host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? GS : 2; }
+
+// Most (x row, step) pairs in shared memory, 512 bytes each, and per warp.
+__host__ __device__ constexpr int max_x_pairs(int nt)
+{
+    return static_cast<int>((kGemvSmem - kGemvWarps * (ring_stages(nt) * kStageBytes + 2 * 4 * 8 * nt * kRedStride)) / 512);
+}
 struct GemvArgs {
     const uint16_t* x;
     int64_t ldx;
@@ -41,7 +53,11 @@ struct GemvArgs {
     const float* g;
     int64_t n, k;
     int64_t sf_bytes;              // scale bytes of one matrix
+    int tiles, steps;              // 16-row tiles of a matrix, 256-column steps of a row
+    int seg_rows;                  // most x rows of a segment
+    int x_rows;                    // x rows that shared memory holds
     void* out;
+    int out_f32;
     int64_t ldd;
     uint32_t* status;
 };
@@ -62,13 +78,18 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// The two E4M3 scales of 32 elements, each in both halves of a register.
-__device__ __forceinline__ void scale_pair(uint32_t two, uint32_t& first, uint32_t& second)
+// The E4M3 scales of four 16-blocks, each in both halves of a register.
+__device__ __forceinline__ void four_scales(uint32_t word, uint32_t (&s)[4])
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-    first = __byte_perm(h, 0, 0x1010);
-    second = __byte_perm(h, 0, 0x3232);
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(word));
+    s[0] = __byte_perm(lo, 0, 0x1010);
+    s[1] = __byte_perm(lo, 0, 0x3232);
+    s[2] = __byte_perm(hi, 0, 0x1010);
+    s[3] = __byte_perm(hi, 0, 0x3232);
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -80,199 +101,426 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_once(const void* p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
-// Lane (r, t) = (lane / 4, lane % 4) of a warp holds, of each 16-row tile, rows
-// r and r + 8, and of each 128-column step the 32 columns from 32 t on: one
-// 16-byte load of codes a row.  The columns' order inside a matrix instruction
-// does not matter as long as both operands agree, so a code word's pairs go in
-// as they lie.  The tiles of a unit are rows 32 i + 16 h + 0..15 (i < 4) of a
-// 128-row block, whose scales one 16-byte load a lane row holds.
-template <int NT, bool F32>
-__global__ void __launch_bounds__(kGemvThreads, NT == 1 ? 2 : 1) gemv_kernel(const GemvArgs a)
+// Asynchronous copies to shared memory; zeros where there is nothing to read.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
 {
-    extern __shared__ float s_red[];  // [warps][8 NT tokens][kTokStride]
-    __shared__ int s_first[kMaxGemvGroups], s_rows[kMaxGemvGroups];
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// Work is cut into 16-row weight tiles; tile 8 b + u of a matrix is rows
+// 128 b + 32 i + 4 u + 0..3 (i < 4), whose scales of 64 columns lie together.  A
+// segment is a matrix with up to seg_rows of its x rows; all segments have the
+// same number of tiles, and the CTAs take equal runs of the list of all (segment,
+// tile) pairs.  A CTA brings the x rows of the segments it works on into shared
+// memory as FP16, in the order in which lanes read them; its warps take equal
+// runs of the tiles' 256-column steps.  A tile that lies inside one warp's run is
+// stored by that warp; of a tile that several runs share, the warp with its first
+// step adds the sums in warp order.
+//
+// Lane (r, t) = (lane / 4, lane % 4) works on rows r and r + 8 of a tile (row m is
+// i = m / 4, row m % 4 of its four) and, of each step, on the 64 columns from 64 t
+// on: two 16-byte vectors of codes and four scale bytes a row.  The columns' order
+// inside a matrix instruction does not matter as long as both operands agree, so
+// a code word's pairs go in as they lie.  Each warp copies its steps into a ring
+// of its own, some steps ahead and into the next tile too, in whole 64-byte runs
+// of a row, and waits for no other warp.
+template <int NT>
+__global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs a)
+{
+    constexpr int kStages = ring_stages(NT);
+    constexpr int kRed = 8 * NT * kRedStride;  // floats of a tile's sums
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    __shared__ int s_first[kMaxGemvGroups], s_rows[kMaxGemvGroups], s_end[kMaxGemvGroups];
     __shared__ int16_t s_group[kMaxGemvGroups];
-    __shared__ int s_active;
+    __shared__ int s_seg_e[kMaxSegments], s_seg_row[kMaxSegments], s_seg_n[kMaxSegments], s_seg_x[kMaxSegments + 1];
+    __shared__ int s_run[4];  // this CTA's tiles [0, 1) of the list, segments in shared memory, tile of the first one
+    __shared__ uint4 s_zero[4];
+    // of each x row in shared memory: its row of x (-1 for a bad index), its place in
+    // s_x, the bytes from one of its pieces to the next, its matrix; its largest magnitude
+    // (bf16 bits)
+    __shared__ int4 s_x_row[kMaxSegments * 8 * NT];
+    __shared__ uint32_t s_top[kMaxSegments * 8 * NT];
+    __shared__ float s_scale[kMaxSegments * 8 * NT];  // the factor on its sums: its own power of two, the matrix's g
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
-    // groups that have rows, in order
+    const int tiles = a.tiles, steps = a.steps;
+    uint8_t* const my_ring = s_dyn + warp * kStages * kStageBytes;
+    const uint32_t ring = smem_addr(my_ring);
+    float* const s_sums = reinterpret_cast<float*>(s_dyn + kGemvWarps * kStages * kStageBytes);  // [2][warps][kRed]
+    float* const my_head = s_sums + warp * kRed;                        // sums of a tile that an earlier warp began
+    float* const my_sums = s_sums + (kGemvWarps + warp) * kRed;         // sums of a tile that this one began
+    uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_sums + 2 * kGemvWarps * kRed);
+
+    int active = 0;  // (warp 0) groups that have rows
     if (warp == 0) {
-        int active = 0;
-        for (int e0 = 0; e0 < a.groups; e0 += 32) {
-            const int e = e0 + lane;
-            int64_t lo = 0, hi = 0;
-            if (e < a.groups) {
-                lo = a.group_offsets ? a.group_offsets[e] : 0;
-                hi = a.group_offsets ? a.group_offsets[e + 1] : a.rows;
-                lo = min(max(lo, static_cast<int64_t>(0)), a.rows);
-                hi = min(hi, a.rows);
+        // those groups in order, with the segments up to and with each
+        int before = 0;
+        const int rows = static_cast<int>(a.rows);
+        if (!a.group_offsets) {
+            active = 1;
+            before = (rows + a.seg_rows - 1) / a.seg_rows;
+            if (lane == 0) s_group[0] = 0, s_first[0] = 0, s_rows[0] = rows, s_end[0] = before;
+        } else {
+            int lo = lane < a.groups ? a.group_offsets[lane] : 0;
+            const int last = a.group_offsets[a.groups];
+#pragma unroll 1
+            for (int e0 = 0; e0 < a.groups; e0 += 32) {
+                const int e = e0 + lane;
+                const int next = e + 32 < a.groups ? a.group_offsets[e + 32] : last;  // in flight over this turn
+                int hi = __shfl_down_sync(0xffffffffu, lo, 1);
+                const int beyond = __shfl_sync(0xffffffffu, next, 0);
+                if (lane == 31) hi = beyond;
+                if (e + 1 == a.groups) hi = last;
+                const int first = min(max(lo, 0), rows), count = e < a.groups ? min(hi, rows) - first : 0;
+                const unsigned has = __ballot_sync(0xffffffffu, count > 0);
+                int segs = count > 0 ? (count + a.seg_rows - 1) / a.seg_rows : 0;
+#pragma unroll 1
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, segs, d);
+                    if (lane >= d) segs += v;
+                }
+                if (count > 0) {
+                    const int at = active + __popc(has & ((1u << lane) - 1));
+                    s_group[at] = static_cast<int16_t>(e);
+                    s_first[at] = first;
+                    s_rows[at] = count;
+                    s_end[at] = before + segs;
+                }
+                active += __popc(has);
+                before += __shfl_sync(0xffffffffu, segs, 31);
+                lo = next;
             }
-            const unsigned has = __ballot_sync(0xffffffffu, hi > lo);
-            if (hi > lo) {
-                const int at = active + __popc(has & ((1u << lane) - 1));
-                s_group[at] = static_cast<int16_t>(e);
-                s_first[at] = static_cast<int>(lo);
-                s_rows[at] = static_cast<int>(hi - lo);
-            }
-            active += __popc(has);
         }
-        if (lane == 0) s_active = active;
+        const int all = before * tiles, b = blockIdx.x, each = all / gridDim.x, more = all % gridDim.x;
+        if (lane == 0) {
+            s_run[0] = b * each + min(b, more);
+            s_run[1] = s_run[0] + each + (b < more ? 1 : 0);
+        }
+        __syncwarp();
+    } else if (warp == 1 && lane < 4) {
+        s_zero[lane] = make_uint4(0, 0, 0, 0);
     }
-    __syncthreads();
-    const int tiles = static_cast<int>((a.n + 127) / 128) * 2;
-    const int64_t units = static_cast<int64_t>(s_active) * tiles;
-    const int chunks = static_cast<int>((a.k + kChunk - 1) / kChunk);
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int which = static_cast<int>(u / tiles), tile = static_cast<int>(u - static_cast<int64_t>(which) * tiles);
-        const int64_t e = s_group[which];
-        const int64_t n0 = static_cast<int64_t>(tile >> 1) * 128 + (tile & 1) * 16;  // first row of tile 0
-        const uint8_t* q = a.q + (e * a.n + n0) * (a.k / 2);
-        const uint8_t* sf = a.sf + e * a.sf_bytes + static_cast<int64_t>(tile >> 1) * (a.k / 64) * 512 + (tile & 1) * 256;
-        const float gs = a.g[e];
-        for (int tok0 = 0; tok0 < s_rows[which]; tok0 += 8 * NT) {
-            const int toks = min(8 * NT, s_rows[which] - tok0);
-            const int64_t row0 = s_first[which] + static_cast<int64_t>(tok0);
-            const uint16_t* xr[NT];
-#pragma unroll
-            for (int b = 0; b < NT; ++b) {
-                xr[b] = nullptr;
-                if (8 * b + r < toks) {
-                    int64_t src = row0 + 8 * b + r;
-                    if (a.row_index) src = a.row_index[src];
-                    if (src < 0 || src >= a.src_rows)
+#pragma unroll 1
+    for (int f0 = -1;;) {
+        if (warp == 0) {
+            if (f0 < 0) f0 = s_run[0];
+            const int f1 = s_run[1];
+            // the segments from f0's on whose rows fit
+            const int seg0 = f0 / tiles, want = f1 > f0 ? (f1 - 1) / tiles - seg0 + 1 : 0;
+            int e = 0, row = 0, n = 0;
+            if (lane < min(want, kMaxSegments)) {
+                int g = 0;
+#pragma unroll 1
+                for (int step = 128; step; step >>= 1)  // groups whose segments all lie before
+                    if (g + step <= active && s_end[g + step - 1] <= seg0 + lane) g += step;
+                const int part = seg0 + lane - (g ? s_end[g - 1] : 0);
+                e = s_group[g];
+                row = s_first[g] + part * a.seg_rows;
+                n = min(a.seg_rows, s_rows[g] - part * a.seg_rows);
+            }
+            int upto = n;
+#pragma unroll 1
+            for (int d = 1; d < kMaxSegments; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += v;
+            }
+            const int fit = __popc(__ballot_sync(0xffffffffu, n > 0 && upto <= a.x_rows));
+            if (lane < kMaxSegments) {
+                s_seg_e[lane] = e, s_seg_row[lane] = row, s_seg_n[lane] = n;
+                s_seg_x[lane + 1] = upto;
+            }
+            if (lane == 0) s_run[2] = fit, s_run[3] = f0 - seg0 * tiles, s_seg_x[0] = 0;
+            __syncwarp();
+#pragma unroll 1
+            for (int xr = lane; xr < s_seg_x[fit]; xr += 32) {
+                int s = 0;
+                while (s_seg_x[s + 1] <= xr) ++s;
+                int src = s_seg_row[s] + xr - s_seg_x[s];
+                if (a.row_index) {
+                    src = a.row_index[src];
+                    if (src < 0 || src >= a.src_rows) {
                         record_status(a.status, NVFP4_ERR_INDEX);
-                    else
-                        xr[b] = a.x + src * a.ldx;
+                        src = -1;
+                    }
+                }
+                const int x0 = s_seg_x[s];
+                s_x_row[xr] = make_int4(src, x0 * steps * 512 + (xr - x0) * 64, s_seg_n[s] * 64, s_seg_e[s]);
+                s_top[xr] = 0;
+            }
+        }
+        __syncthreads();
+        if (f0 < 0) f0 = s_run[0];
+        const int segs = s_run[2], f1 = s_run[1], tile0 = s_run[3];
+        if (f0 >= f1) return;
+        const int fe = min(f1, f0 - tile0 + segs * tiles);
+
+        // this warp's run of steps: items [j0, j1) of the (fe - f0) tiles' steps
+        const int items = (fe - f0) * steps;
+        const auto run_start = [&](int w) { return (items / kGemvWarps) * w + min(w, items % kGemvWarps); };
+        const int j0 = run_start(warp), j1 = run_start(warp + 1);
+        const int skip = j0 / steps, first_step = j0 - skip * steps;
+        int seg = 0, tile = tile0 + skip;
+        while (tile >= tiles) tile -= tiles, ++seg;
+
+        // A row's 128 bytes of a step are eight vectors; vector v of row r lies at
+        // place v ^ (r & 1), so that lanes reading vectors 2 t or 2 t + 1 of two rows
+        // meet eight different ones.
+        int left = j1 - j0, pc = first_step, pslot = 0, pseg = seg, ptile = tile;
+        bool aimed = false, have0 = false, have8 = false;
+        const uint8_t *pq = nullptr, *ps = nullptr;
+        const int64_t row_bytes = a.k / 2, next8 = 64 * row_bytes;  // from row m to row m + 8: i + 2
+        const uint32_t put = ring + r * 128 + (t ^ (r & 1)) * 16;
+        const auto copy_step = [&]() {
+            if (left > 0) {
+                if (!aimed) {
+                    const int64_t e = s_seg_e[pseg], block = ptile >> 3;
+                    const int u = ptile & 7;
+                    const int64_t n0 = block * 128 + 32 * (r >> 2) + 4 * u + (r & 3);
+                    have0 = n0 < a.n;
+                    have8 = n0 + 64 < a.n;
+                    pq = a.q + (e * a.n + n0) * row_bytes + 16 * t + pc * (kStep / 2);
+                    ps = a.sf + e * a.sf_bytes + block * (a.k / 64) * 512 + (lane & 15) / 4 * 512 +
+                         (4 * u + (lane & 3)) * 16 + static_cast<int64_t>(pc) * 2048;
+                    aimed = true;
+                }
+                const uint32_t dst = put + pslot * kStageBytes;
+                const int k = pc * kStep + 32 * t;
+                const bool in0 = k < a.k, in1 = k + 128 < a.k;
+                copy16_async(dst, in0 && have0 ? pq : a.q, in0 && have0);
+                copy16_async(dst + 64, in1 && have0 ? pq + 64 : a.q, in1 && have0);
+                copy16_async(dst + 1024, in0 && have8 ? pq + next8 : a.q, in0 && have8);
+                copy16_async(dst + 1088, in1 && have8 ? pq + next8 + 64 : a.q, in1 && have8);
+                if (lane < 16) {
+                    const bool in = pc * kStep + 64 * (lane >> 2) < a.k;
+                    copy16_async(ring + pslot * kStageBytes + 2048 + lane * 16, in ? ps : a.sf, in);
+                }
+                --left;
+                pq += kStep / 2;
+                ps += 2048;
+                if (++pc == steps) {
+                    pc = 0;
+                    aimed = false;
+                    if (++ptile == tiles) ptile = 0, ++pseg;
                 }
             }
-            float acc[4][NT][4];
+            pslot = pslot + 1 == kStages ? 0 : pslot + 1;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int s = 0; s < kStages - 1; ++s) copy_step();
+
+        // x rows of the segments as FP16, each at the power of two that brings its
+        // largest magnitude to [2^14, 2^15): of segment s (n rows) and a step, [8
+        // pieces][n][4 lanes t] vectors of 16 bytes.  A warp takes the steps warp, warp
+        // + 16, ... of each row; lane (r, t) brings piece r of the columns that lanes t
+        // read, and converts it in place once the largest magnitude is known.
+        const int x_rows = s_seg_x[segs];
+        float g = 0.0f;  // of the x row that is this thread's index
+        if (static_cast<int>(threadIdx.x) < x_rows) g = a.g[s_x_row[threadIdx.x].w];
+        const auto next = [&](int& xr, int& c) {
+            c += kGemvWarps;
+            if (c >= steps) c = warp, ++xr;
+        };
+        if (warp < steps) {
+            constexpr int kAhead = 4;  // loads in flight together
+            int xr = 0, c = warp;
+#pragma unroll 1
+            while (xr < x_rows) {
+                uint4 v[kAhead];
+                int at[kAhead], of[kAhead];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kAhead; ++i) {
+                    const int4 row = s_x_row[min(xr, x_rows - 1)];
+                    const int k = c * kStep + 64 * t + 8 * r;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (row.x >= 0 && k < a.k) v[i] = *reinterpret_cast<const uint4*>(a.x + row.x * a.ldx + k);
+                    at[i] = row.y + (c * 8 + r) * row.z + t * 16;
+                    of[i] = xr;
+                    next(xr, c);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (of[i] >= x_rows) break;
+                    *reinterpret_cast<uint4*>(s_x + at[i]) = v[i];
+                    const uint32_t m = __vmaxu2(
+                        __vimax3_u16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu), v[i].w & 0x7FFF7FFFu);
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+                    if (lane == 0) atomicMax(&s_top[of[i]], top);
+                }
+            }
+        }
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < x_rows) {
+            const uint32_t ex = s_top[threadIdx.x] >> 7;
+            s_scale[threadIdx.x] = (ex < 255 ? __uint_as_float((max(ex, 15u) - 14u) << 23) : 1.0f) * g;
+        }
+        if (warp < steps) {
+            int xr = 0, c = warp;
+#pragma unroll 2
+            while (xr < x_rows) {
+                const int4 row = s_x_row[xr];
+                uint4* const at = reinterpret_cast<uint4*>(s_x + t * 16 + row.y + (c * 8 + r) * row.z);
+                const uint32_t ex = s_top[xr] >> 7;  // exponent field of the largest magnitude
+                const float up = ex < 255 ? __uint_as_float((268u - max(ex, 15u)) << 23) : 1.0f;
+                float f[8];
+                unpack8(*at, f);
+                __half2 h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mul2(f[2 * j], f[2 * j + 1], f[2 * j], f[2 * j + 1], up, up);
+                    h[j] = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+                }
+                *at = *reinterpret_cast<const uint4*>(h);
+                next(xr, c);
+            }
+        }
+        if (j0 == j1)  // an empty run adds nothing to the tile that goes past it
+            for (int i = lane; i < kRed; i += 32) my_head[i] = 0.0f;
+        __syncthreads();
+
+        int slot = 0, c = first_step;
+        bool begun = first_step == 0, open = false;  // the tile was begun by this warp; its run ends inside it
+        float acc[NT][4];
+        const uint8_t* xp[NT];  // this lane's x vectors: piece p of step c at xp + (8 c + p) * xstep
+        int xstep[NT];
+        bool fresh = true;
+        const auto store = [&](int tok, int m, float v) {
+            const int64_t n = static_cast<int64_t>(tile >> 3) * 128 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
+            if (tok >= s_seg_n[seg] || n >= a.n) return;
+            v *= s_scale[s_seg_x[seg] + tok];
+            const int64_t at = (s_seg_row[seg] + tok) * a.ldd + n;
+            if (a.out_f32)
+                static_cast<float*>(a.out)[at] = v;
+            else
+                static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+        };
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j) {
+            if (fresh) {
+                const int n = s_seg_n[seg];
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    const bool is = 8 * b + r < n;
+                    xstep[b] = is ? n * 64 : 0;
+                    xp[b] = is ? s_x + s_seg_x[seg] * steps * 512 + (8 * b + r) * 64 + t * 16
+                               : reinterpret_cast<const uint8_t*>(s_zero + t);
+                    xp[b] += c * 8 * xstep[b];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+                }
+                fresh = false;
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();  // this step has come for every lane, and every lane is done with the last one
+            copy_step();
+            const uint8_t* const stage = my_ring + slot * kStageBytes;
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            uint4 code[2][2];
+            uint32_t sc[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* const row = stage + h * 1024 + r * 128 + t * 32;
+                code[h][0] = *reinterpret_cast<const uint4*>(row + (r & 1) * 16);
+                code[h][1] = *reinterpret_cast<const uint4*>(row + 16 - (r & 1) * 16);
+                four_scales(*reinterpret_cast<const uint32_t*>(stage + 2048 + t * 64 + (r & 3) * 16 + ((r >> 2) + 2 * h) * 4),
+                            sc[h]);
+            }
+            float part[2][NT][4];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[0][b][i] = part[1][b][i] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                uint4 x[NT];
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    x[b] = *reinterpret_cast<const uint4*>(xp[b]);
+                    xp[b] += xstep[b];
+                }
+                uint32_t v[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4& cw = code[h][p >> 2];
+                    e2m1x8_f16((p & 3) == 0 ? cw.x : (p & 3) == 1 ? cw.y : (p & 3) == 2 ? cw.z : cw.w, v[h]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[h][i] = mul_f16x2(v[h][i], sc[h][p >> 1]);
+                }
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    mma_16816(part[0][b], v[0][0], v[1][0], v[0][1], v[1][1], x[b].x, x[b].y);
+                    mma_16816(part[1][b], v[0][2], v[1][2], v[0][3], v[1][3], x[b].z, x[b].w);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[b][i] += part[0][b][i] + part[1][b][i];
+            if (++c < steps && j + 1 < j1) continue;
+            // the tile or the run ends: columns 2 t and 2 t + 1 of the sums are tokens
+            // 8 b + 2 t, 8 b + 2 t + 1
+            open = begun && c < steps;
+            if (begun && !open) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][b][j] = 0.0f;
-            for (int c = warp; c < chunks; c += kGemvWarps) {
-                const int64_t k0 = static_cast<int64_t>(c) * kChunk + 32 * t;
-                const bool in = k0 < a.k;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                uint4 code[4][2], sc[2];
+                    for (int i = 0; i < 4; ++i) store(8 * b + 2 * t + (i & 1), r + 8 * (i >> 1), acc[b][i]);
+            } else {
+                float* const to = begun ? my_sums : my_head;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool have = in && n0 + 32 * i < a.n;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        code[i][h] = have ? load_once(q + (32 * i + r + 8 * h) * (a.k / 2) + k0 / 2) : zero;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    sc[h] = in ? load_once(sf + (k0 / 64) * 512 + (r + 8 * h) * 16) : zero;
-                // x: 32 columns of token 8 b + r, scaled into FP16's range
-                uint32_t xf[NT][16];
-                float back[NT];
-#pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 v = in && xr[b] ? *reinterpret_cast<const uint4*>(xr[b] + k0 + 8 * j) : zero;
-                        xf[b][4 * j] = v.x, xf[b][4 * j + 1] = v.y, xf[b][4 * j + 2] = v.z, xf[b][4 * j + 3] = v.w;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) m = __vmaxu2(m, xf[b][j] & 0x7FFF7FFFu);
-                    m = max(m & 0xFFFFu, m >> 16);
-                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    const uint32_t ex = m >> 7;  // exponent field of the largest magnitude
-                    const bool finite = ex < 255;
-                    const uint32_t low = max(ex, 15u);
-                    const float up = finite ? __uint_as_float((268u - low) << 23) : 1.0f;
-                    back[b] = finite ? __uint_as_float((low - 14u) << 23) : 1.0f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const __half2 h = __floats2half2_rn(bf16_lo(xf[b][j]) * up, bf16_hi(xf[b][j]) * up);
-                        xf[b][j] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                }
-                float part[4][NT][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int b = 0; b < NT; ++b)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[i][b][j] = 0.0f;
-                    uint32_t s[2][2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t w = i == 0 ? sc[h].x : i == 1 ? sc[h].y : i == 2 ? sc[h].z : sc[h].w;
-                        scale_pair(w >> (16 * (t & 1)), s[h][0], s[h][1]);
-                    }
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t p[2][4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4& cw = code[i][h];
-                            e2m1x8_f16(w == 0 ? cw.x : w == 1 ? cw.y : w == 2 ? cw.z : cw.w, p[h]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) p[h][j] = mul_f16x2(p[h][j], s[h][w >> 1]);
-                        }
-#pragma unroll
-                        for (int b = 0; b < NT; ++b) {
-                            mma_16816(part[i][b], p[0][0], p[1][0], p[0][1], p[1][1], xf[b][4 * w], xf[b][4 * w + 1]);
-                            mma_16816(part[i][b], p[0][2], p[1][2], p[0][3], p[1][3], xf[b][4 * w + 2],
-                                      xf[b][4 * w + 3]);
-                        }
-                    }
-                }
-                // columns 2 t and 2 t + 1 of a sum are tokens 8 b + 2 t, 8 b + 2 t + 1
-#pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    const float even = __shfl_sync(0xffffffffu, back[b], 8 * t);
-                    const float odd = __shfl_sync(0xffffffffu, back[b], 8 * t + 4);
+                for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[i][b][j] = fmaf(part[i][b][j], (j & 1) ? odd : even, acc[i][b][j]);
-                }
+                        to[(8 * b + 2 * t + (i & 1)) * kRedStride + r + 8 * (i >> 1)] = acc[b][i];
             }
-            // the warps' sums, in warp order
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s_red[(warp * 8 * NT + 8 * b + 2 * t + (j & 1)) * kTokStride + 16 * i + r + 8 * (j >> 1)] =
-                            acc[i][b][j];
-            __syncthreads();
-            for (int o = threadIdx.x; o < toks * kUnitRows; o += kGemvThreads) {
-                const int tok = o / kUnitRows, row = o % kUnitRows;
-                const int64_t n = n0 + 32 * (row >> 4) + (row & 15);
-                if (n >= a.n) continue;
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kGemvWarps; ++w) v += s_red[(w * 8 * NT + tok) * kTokStride + row];
-                v *= gs;
-                const int64_t at = (row0 + tok) * a.ldd + n;
-                if (F32)
-                    static_cast<float*>(a.out)[at] = v;
-                else
-                    static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+            if (j + 1 < j1) {
+                c = 0;
+                if (++tile == tiles) tile = 0, ++seg;
+                begun = fresh = true;
             }
-            __syncthreads();
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        if (open) {  // this warp's sums and those of the warps that went on with the tile
+            const int end = j1 - c + steps;  // the item behind the tile's last
+            int others = 0;
+            while (run_start(warp + others + 1) < end) ++others;
+            for (int o = lane; o < 16 * s_seg_n[seg]; o += 32) {
+                const int at = (o >> 4) * kRedStride + (o & 15);
+                float v = my_sums[at];
+                for (int w = 1; w <= others; ++w) v += my_head[w * kRed + at];
+                store(o >> 4, o & 15, v);
+            }
+        }
+        if (fe == f1) return;
+        __syncthreads();  // the next segments' rows take the place of these
+        f0 = fe;
     }
+}
+
+template <int NT>
+nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
+{
+    constexpr size_t fixed = kGemvWarps * (ring_stages(NT) * kStageBytes + 2 * sizeof(float) * 8 * NT * kRedStride);
+    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
+    if (steps > max_x_pairs(NT)) return NVFP4_ERR_SHAPE;                      // one row does not fit
+    if (a.rows * tiles * steps > 0x7fffffffll) return NVFP4_ERR_SHAPE;        // indexes are 31-bit on the device
+    const int64_t fit = max_x_pairs(NT) / steps;
+    a.tiles = static_cast<int>(tiles), a.steps = static_cast<int>(steps);
+    a.seg_rows = static_cast<int>(std::min<int64_t>(8 * NT, fit));
+    a.x_rows = static_cast<int>(std::min<int64_t>(fit, std::min<int64_t>(a.rows, 8 * NT * kMaxSegments)));
+    static bool raised[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (!raised[dev & 63]) {
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(gemv_kernel<NT>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvSmem)) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        raised[dev & 63] = true;
+    }
+    const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
+    gemv_kernel<NT><<<grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, size_t ws_bytes, void* stream)
@@ -298,18 +546,10 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
     if (a.status && cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (a.rows == 0) return NVFP4_OK;
     a.sf_bytes = static_cast<int64_t>(nvfp4_sf_mma_bytes(a.n, a.k));
-    const int64_t tiles = (a.n + 127) / 128 * 2;
     // two 8-token columns once a matrix is expected to meet more than 8 rows
     const bool two = a.rows > 8 * static_cast<int64_t>(a.groups);
-    const int64_t units = tiles * std::min<int64_t>(a.groups, a.rows);
-    const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(sms) * (two ? 1 : 2)));
-    const size_t smem = sizeof(float) * kGemvWarps * (two ? 16 : 8) * kTokStride;
-    const auto go = [&](auto kernel) { kernel<<<grid, kGemvThreads, smem, st>>>(a); };
-    if (out_dtype == NVFP4_OUT_F32)
-        two ? go(gemv_kernel<2, true>) : go(gemv_kernel<1, true>);
-    else
-        two ? go(gemv_kernel<2, false>) : go(gemv_kernel<1, false>);
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    a.out_f32 = out_dtype == NVFP4_OUT_F32;
+    return two ? start_gemv<2>(a, sms, st) : start_gemv<1>(a, sms, st);
 }
 
 }  // namespace

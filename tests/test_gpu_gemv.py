@@ -1,9 +1,9 @@
 """Few-token products with NVFP4 matrices against float64 products of the same values.
 
 Tolerance.  An accumulation of 16 products by the tensor cores may truncate each of its 17 additions:
-17 * 2^-23 of the magnitudes; a warp's 128 columns are 8 of them in a row, then come one product-and-sum
-per 128 columns it takes (one in 8 of them), 8 sums over the warps and the product with g.  x is exact or
-within 2^-40 of its 128 columns' largest magnitude."""
+17 * 2^-23 of the magnitudes; of 256 columns two chains of 8 of them run side by side, then come two sums
+for every 256 columns, up to 16 over the warps and the products with the scales.  x is exact or within
+2^-40 of its row's largest magnitude."""
 import numpy as np
 import pytest
 
@@ -28,10 +28,8 @@ def f64(t):
 
 def bound(x, w, ref, f32):
     k = x.shape[1]
-    c = (8 * 17 + -(-k // 1024) + 16) * 2.0 ** -23
-    pad = np.zeros((x.shape[0], -(-k // 128) * 128))
-    pad[:, :k] = np.abs(x)
-    top = np.repeat(pad.reshape(x.shape[0], -1, 128).max(2), 128, 1)[:, :k]
+    c = (8 * 17 + 2 * -(-k // 256) + 19) * 2.0 ** -23
+    top = np.abs(x).max(1, keepdims=True) * np.ones_like(x)
     return c * (np.abs(x) @ np.abs(w).T) + 2.0 ** -40 * (top @ np.abs(w).T) + (0 if f32 else 2.0 ** -8) * np.abs(ref) + 1e-44
 
 
@@ -169,6 +167,45 @@ def test_grouped(counts, gather, k, f32):
         w = R.nvfp4_matrix(*mats[e % few])
         ref = xs[s] @ w.T
         assert np.all(np.abs(got[s] - ref) <= bound(xs[s], w, ref, f32))
+
+
+@pytest.mark.parametrize("G,n,k", [(40, 1024, 1152), (64, 512, 320), (6, 4096, 704), (3, 2176, 2560)])
+def test_many_tiles(G, n, k):
+    """CTAs and warps that begin and end inside tiles and segments; a matrix with more rows than fit at once."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(G)
+    counts = rng.integers(0, 4, G)
+    counts[0], counts[G // 2] = 21, 9
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    mats = [R.random_nvfp4(rng, n, k) for _ in range(3)]
+    x = bits(rng, (off[-1], k))
+    qb = torch.from_numpy(np.stack([mats[e % 3][0] for e in range(G)])).cuda()
+    sfb = torch.from_numpy(np.concatenate([R.tile(mats[e % 3][1]) for e in range(G)])).cuda()
+    gb = torch.tensor([mats[e % 3][2] for e in range(G)], dtype=torch.float32, device="cuda")
+    y = nv.grouped_gemv(torch.from_numpy(off).cuda(), to_dev(x), qb, sfb, gb, n, None, nv.NVFP4_OUT_F32)
+    again = nv.grouped_gemv(torch.from_numpy(off).cuda(), to_dev(x), qb, sfb, gb, n, None, nv.NVFP4_OUT_F32)
+    assert torch.equal(y, again)
+    got, w = f64(y), [R.nvfp4_matrix(*m) for m in mats]
+    for e in range(G):
+        if counts[e]:
+            s = slice(off[e], off[e + 1])
+            ref = val(x[s]) @ w[e % 3].T
+            assert np.all(np.abs(got[s] - ref) <= bound(val(x[s]), w[e % 3], ref, True))
+
+
+@pytest.mark.parametrize("rows,k", [(3, 20480), (9, 12288), (2, 45056)])
+def test_long_rows(rows, k):
+    """Rows of which few fit into shared memory at a time."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(k)
+    q, sf, g = R.random_nvfp4(rng, 272, k)
+    x = bits(rng, (rows, k))
+    y = nv.gemv(to_dev(x), upload(nv, q, sf, g), nv.NVFP4_OUT_F32)
+    w = R.nvfp4_matrix(q, sf, g)
+    ref = val(x) @ w.T
+    assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
 
 
 def test_grouped_rows_outside_groups_and_bad_indexes():
