@@ -21,6 +21,8 @@ import os
 from dataclasses import dataclass
 from typing import Optional
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
@@ -175,7 +177,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -598,6 +600,8 @@ class Routing:
     params: RouteParams
 
 
+# The calls below serve single tokens too, where the kernel takes a few microseconds: their checks read
+# each property once, and they hand addresses to the library without further wrapping.
 def _need(ok, message: str) -> None:
     if not ok:
         raise ValueError(message)
@@ -605,49 +609,57 @@ def _need(ok, message: str) -> None:
 
 def _one_device(name: str, *tensors):
     """The device of the tensors: one CUDA device, the current one (the calls launch there)."""
-    import torch
-    dev = tensors[0].device
+    first = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: CUDA tensors expected, got {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensors on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
+        if t is not None and t.get_device() != first:
+            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if first < 0:
+        raise ValueError(f"{name}: CUDA tensors expected, got {tensors[0].device}")
+    current = torch.cuda.current_device()
+    if first != current:
+        raise ValueError(f"{name}: tensors on cuda:{first}, but the current device is cuda:{current}")
+    return tensors[0].device
+
+
+def _raw_stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _matrix(dev, dtype, rows: int, cols: int):
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
 
 
 def _dtype_code(name: str, t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return NVFP4_OUT_BF16
-    if t.dtype == torch.float32:
+    if dt is torch.float32:
         return NVFP4_OUT_F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    raise ValueError(f"{name} must be bfloat16 or float32, got {dt}")
 
 
-def _rows_of(name: str, t, rows: Optional[int], cols: Optional[int]):
+def _rows_of(name: str, t, rows=None, cols=None):
     """A bf16 matrix with contiguous rows; returns its row stride in elements."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 2:
-        raise ValueError(f"{name} must be a bfloat16 matrix, got {t.dtype} {tuple(t.shape)}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name}: [{rows}, {cols}] expected, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 2:
+        raise ValueError(f"{name} must be a bfloat16 matrix, got {t.dtype} {tuple(shape)}")
+    n, c = shape
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name}: [{rows}, {cols}] expected, got {tuple(shape)}")
+    if t.is_contiguous():  # (the stride of a single row is never used, and torch leaves it arbitrary)
+        return c
+    if c > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    # the stride of a single row is never used, and torch leaves it arbitrary
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if n > 1 else c
 
 
 def _flat(name: str, t, dtype, *shape) -> None:
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
 
 
-def _torch_stream(stream):
-    import torch
-    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+def _on(stream):
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, y: bool = True, mx: bool = False,
@@ -656,58 +668,62 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, y: bool = True, mx: 
 
     Returns a dict: 'h' the sum in bf16 (x itself without a residual), 'y' the norm in bf16, 'mx' its MXFP8
     (codes, e8m0) for ``mx_gemm``, 'amax' max |y| ([1], for ``quantize``'s amax), 'rstd' [rows] for
-    ``rmsnorm_backward``; None for what was not asked for."""
-    import torch
+    ``rmsnorm_backward``; None for what was not asked for.  With ``stream`` the outputs belong to it."""
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return rmsnorm(x, weight, residual, eps, y=y, mx=mx, mx_sf_layout=mx_sf_layout, amax=amax,
                            rstd=rstd)
     dev = _one_device("rmsnorm", x, weight, residual)
-    ldx = _rows_of("rmsnorm: x", x, None, None)
+    ldx = _rows_of("rmsnorm: x", x)
     rows, cols = x.shape
     wdt = _dtype_code("rmsnorm: weight", weight)
     _flat("rmsnorm: weight", weight, weight.dtype, cols)
-    _need(y or mx, "rmsnorm: neither y nor mx asked for")
-    _need(y or not amax, "rmsnorm: amax is that of y")
-    h, ldr = x, 0
+    if not y:
+        _need(mx, "rmsnorm: neither y nor mx asked for")
+        _need(not amax, "rmsnorm: amax is that of y")
+    out = {"h": x, "y": None, "mx": None, "amax": None, "rstd": None}
+    res = h = yp = mq = ms = ap = rp = None
+    ldr = 0
     if residual is not None:
         ldr = _rows_of("rmsnorm: residual", residual, rows, cols)
-        h = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    out = {"h": h, "y": None, "mx": None, "amax": None, "rstd": None}
+        res = residual.data_ptr()
+        out["h"] = _matrix(dev, torch.bfloat16, rows, cols)
+        h = out["h"].data_ptr()
     if y:
-        out["y"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    mq = ms = None
+        out["y"] = _matrix(dev, torch.bfloat16, rows, cols)
+        yp = out["y"].data_ptr()
     if mx:
-        mq = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-        ms = (torch.empty(mxfp8_sf_mma_bytes(rows, cols), dtype=torch.uint8, device=dev)
-              if mx_sf_layout == NVFP4_SF_MMA else
-              torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev))
-        out["mx"] = (mq, ms)
+        q = _matrix(dev, torch.uint8, rows, cols)
+        s = (torch.empty(mxfp8_sf_mma_bytes(rows, cols), dtype=torch.uint8, device=dev)
+             if mx_sf_layout == NVFP4_SF_MMA else _matrix(dev, torch.uint8, rows, cols // 32))
+        out["mx"] = (q, s)
+        mq, ms = q.data_ptr(), s.data_ptr()
     if amax:
         out["amax"] = torch.empty(1, dtype=torch.float32, device=dev)
+        ap = out["amax"].data_ptr()
     if rstd:
         out["rstd"] = torch.empty(rows, dtype=torch.float32, device=dev)
-    nvfp4_rmsnorm(x, ldx, residual, ldr, weight, wdt, eps, rows, cols, h if residual is not None else None,
-                  cols, out["y"], cols, out["rstd"], out["amax"], mq, ms, mx_sf_layout)
+        rp = out["rstd"].data_ptr()
+    _check(_lib.nvfp4_rmsnorm(x.data_ptr(), ldx, res, ldr, weight.data_ptr(), wdt, eps, rows, cols, h, cols,
+                              yp, cols, rp, ap, mq, ms, mx_sf_layout, _raw_stream(dev)), "nvfp4_rmsnorm")
     return out
 
 
 def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, workspace=None, stream=None):
     """(dx, dweight) of ``rmsnorm`` from the gradients of its y and (dh, optional) of its h.  dx is the
     gradient of x and of residual; dweight (in weight's dtype) is None where not asked for."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return rmsnorm_backward(dy, h, weight, rstd, dh, dweight=dweight, workspace=workspace)
     dev = _one_device("rmsnorm_backward", dy, h, weight, rstd, dh, workspace)
-    ldy = _rows_of("rmsnorm_backward: dy", dy, None, None)
+    ldy = _rows_of("rmsnorm_backward: dy", dy)
     rows, cols = dy.shape
     ldh = _rows_of("rmsnorm_backward: h", h, rows, cols)
     lddh = _rows_of("rmsnorm_backward: dh", dh, rows, cols) if dh is not None else 0
     wdt = _dtype_code("rmsnorm_backward: weight", weight)
     _flat("rmsnorm_backward: weight", weight, weight.dtype, cols)
     _flat("rmsnorm_backward: rstd", rstd, torch.float32, rows)
-    dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    dx = _matrix(dev, torch.bfloat16, rows, cols)
     dw = ws = None
     if dweight:
         dw = torch.empty_like(weight)
@@ -720,9 +736,12 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, work
 
 def _logits_of(name: str, logits):
     dt = _dtype_code(f"{name}: logits", logits)
-    _need(logits.dim() == 2, f"{name}: logits [tokens, experts] expected")
-    _need(logits.shape[1] <= 1 or logits.stride(1) == 1, f"{name}: rows of logits must be contiguous")
-    return dt, logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    shape = logits.shape
+    _need(len(shape) == 2, f"{name}: logits [tokens, experts] expected")
+    if logits.is_contiguous():
+        return dt, shape[1]
+    _need(shape[1] <= 1 or logits.stride(1) == 1, f"{name}: rows of logits must be contiguous")
+    return dt, logits.stride(0) if shape[0] > 1 else shape[1]
 
 
 def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: int = 1,
@@ -732,9 +751,8 @@ def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: 
     rows.  bias (f32 [experts]) steers the choice only; ``topk_groups`` of ``groups`` expert groups, ranked by
     the sum of their ``group_top`` best scores, may be chosen from.  Logits at or below bf16's lowest finite
     value mask their experts; slots without an expert have expert -1, weight 0 and row -1."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return route(logits, top_k, score=score, bias=bias, groups=groups, topk_groups=topk_groups,
                          group_top=group_top, renormalize=renormalize, scale=scale, workspace=workspace)
     dev = _one_device("route", logits, bias, workspace)
@@ -745,25 +763,28 @@ def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: 
     _need(top_k >= 1, "route: top_k must be at least 1")
     p = RouteParams(top_k, score, groups, groups if topk_groups is None else topk_groups, group_top,
                     1 if renormalize else 0, scale)
-    i32 = dict(dtype=torch.int32, device=dev)
-    r = Routing(torch.empty((tokens, top_k), **i32),
-                torch.empty((tokens, top_k), dtype=torch.float32, device=dev),
-                torch.empty(experts + 1, **i32), torch.empty(tokens * top_k, **i32),
-                torch.empty((tokens, top_k), **i32), p)
-    ws = workspace
-    if ws is None:
+    i32 = torch.int32
+    r = Routing(_matrix(dev, i32, tokens, top_k), _matrix(dev, torch.float32, tokens, top_k),
+                torch.empty(experts + 1, dtype=i32, device=dev),
+                torch.empty(tokens * top_k, dtype=i32, device=dev), _matrix(dev, i32, tokens, top_k), p)
+    wp, n = None, 0
+    if workspace is None:
         n = nvfp4_route_workspace_size(tokens, experts)
-        ws = _workspace(dev, n) if n > 256 else None
-    nvfp4_route(logits, dt, ld, bias, tokens, experts, p, r.expert, r.weight, r.group_offsets, r.row_index,
-                r.slot_row, ws, ws.numel() if ws is not None else 0)
+        if n > 256:
+            workspace = _workspace(dev, n)
+    if workspace is not None:
+        wp, n = workspace.data_ptr(), workspace.numel()
+    _check(_lib.nvfp4_route(logits.data_ptr(), dt, ld, bias.data_ptr() if bias is not None else None, tokens,
+                            experts, ctypes.byref(p), r.expert.data_ptr(), r.weight.data_ptr(),
+                            r.group_offsets.data_ptr(), r.row_index.data_ptr(), r.slot_row.data_ptr(), wp, n,
+                            _raw_stream(dev)), "nvfp4_route")
     return r
 
 
 def route_backward(dweight, logits, routing: Routing, *, stream=None):
     """The logits' gradient (their dtype) from that of ``routing.weight`` (f32 [tokens, top_k])."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return route_backward(dweight, logits, routing)
     dev = _one_device("route_backward", dweight, logits, routing.expert)
     dt, ld = _logits_of("route_backward", logits)
@@ -771,45 +792,47 @@ def route_backward(dweight, logits, routing: Routing, *, stream=None):
     k = routing.params.top_k
     _flat("route_backward: dweight", dweight, torch.float32, tokens, k)
     _flat("route_backward: expert", routing.expert, torch.int32, tokens, k)
-    d = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
+    d = _matrix(dev, logits.dtype, tokens, experts)
     nvfp4_route_backward(dweight, logits, dt, ld, routing.expert, tokens, experts, routing.params, d, experts)
     return d
 
 
 def _combine_args(name: str, rows, slot_row, weight):
-    import torch
     dt = _dtype_code(f"{name}: rows", rows)
-    _need(rows.dim() == 2 and rows.is_contiguous(), f"{name}: contiguous rows [n, cols] expected")
-    _need(slot_row.dim() == 2, f"{name}: slot_row [tokens, k] expected")
-    tokens, k = slot_row.shape
-    _flat(f"{name}: slot_row", slot_row, torch.int32, tokens, k)
-    _flat(f"{name}: weight", weight, torch.float32, tokens, k)
-    return dt, rows.shape[0], rows.shape[1], tokens, k
+    shape, slots = rows.shape, slot_row.shape
+    _need(len(shape) == 2 and rows.is_contiguous(), f"{name}: contiguous rows [n, cols] expected")
+    _need(len(slots) == 2, f"{name}: slot_row [tokens, k] expected")
+    _flat(f"{name}: slot_row", slot_row, torch.int32, *slots)
+    _flat(f"{name}: weight", weight, torch.float32, *slots)
+    return dt, shape[0], shape[1], slots[0], slots[1]
 
 
 def combine(rows, slot_row, weight, base=None, *, workspace=None, stream=None):
     """out[t] = base[t] + sum_j weight[t, j] * rows[slot_row[t, j]], bf16 [tokens, cols]; rows bf16 or f32,
     slots with a negative row left out.  ``workspace`` (256 bytes, optional) receives the status word."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return combine(rows, slot_row, weight, base, workspace=workspace)
     dev = _one_device("combine", rows, slot_row, weight, base, workspace)
     dt, n, cols, tokens, k = _combine_args("combine", rows, slot_row, weight)
+    bp = wp = None
     if base is not None:
         _flat("combine: base", base, torch.bfloat16, tokens, cols)
-    out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
-    nvfp4_combine(rows, dt, n, cols, slot_row, weight, tokens, k, base, out, workspace,
-                  workspace.numel() if workspace is not None else 0)
+        bp = base.data_ptr()
+    nb = 0
+    if workspace is not None:
+        wp, nb = workspace.data_ptr(), workspace.numel()
+    out = _matrix(dev, torch.bfloat16, tokens, cols)
+    _check(_lib.nvfp4_combine(rows.data_ptr(), dt, n, cols, slot_row.data_ptr(), weight.data_ptr(), tokens, k,
+                              bp, out.data_ptr(), wp, nb, _raw_stream(dev)), "nvfp4_combine")
     return out
 
 
 def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, workspace=None, stream=None):
     """(drows, dweight) of ``combine`` (the base's gradient is dout).  With the routing's ``group_offsets``
     the rows behind its last one get a zero gradient; without, every row that no slot names does."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return combine_backward(dout, rows, slot_row, weight, group_offsets, workspace=workspace)
     dev = _one_device("combine_backward", dout, rows, slot_row, weight, group_offsets, workspace)
     dt, n, cols, tokens, k = _combine_args("combine_backward", rows, slot_row, weight)
@@ -820,9 +843,8 @@ def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, worksp
               "combine_backward: group_offsets [groups + 1] expected")
         _flat("combine_backward: group_offsets", group_offsets, torch.int32, group_offsets.numel())
         used = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
-    make = torch.empty_like if used is not None else torch.zeros_like
-    drows = make(rows)
-    dweight = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+    drows = torch.empty_like(rows) if used is not None else torch.zeros_like(rows)
+    dweight = _matrix(dev, torch.float32, tokens, k)
     ws = workspace if workspace is not None else _workspace(dev, nvfp4_combine_backward_workspace_size(n))
     nvfp4_combine_backward(dout, rows, dt, n, cols, slot_row, weight, tokens, k, used, drows, dweight, ws,
                            ws.numel())
@@ -830,11 +852,10 @@ def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, worksp
 
 
 def _gemv_out(name: str, out_dtype: int, rows: int, N: int, out, dev):
-    import torch
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
     if out is None:
-        return torch.empty((rows, N), dtype=dt, device=dev), N
-    _need(out.dtype == dt and tuple(out.shape) == (rows, N) and (N <= 1 or out.stride(1) == 1),
+        return _matrix(dev, dt, rows, N), N
+    _need(out.dtype is dt and out.shape == (rows, N) and (N <= 1 or out.stride(1) == 1),
           f"{name}: out {dt} [{rows}, {N}] with contiguous rows expected")
     _need(rows <= 1 or out.stride(0) >= N, f"{name}: rows of out overlap")
     return out, out.stride(0) if rows > 1 else N
@@ -843,17 +864,19 @@ def _gemv_out(name: str, out_dtype: int, rows: int, N: int, out, dev):
 def gemv(x, w: NVFP4Tensor, out_dtype: int = NVFP4_OUT_BF16, out=None, *, stream=None):
     """D = x W^T of a few bf16 rows x [rows, K] and an NVFP4 matrix [N, K] (tiled scales): ``gemm`` for
     single tokens, x not quantised."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return gemv(x, w, out_dtype, out)
-    dev = _one_device("gemv", x, w.q, w.sf, w.g, out)
-    ldx = _rows_of("gemv: x", x, None, w.k)
+    q, sf, g, N, K = w.q, w.sf, w.g, w.rows, w.k
+    dev = _one_device("gemv", x, q, sf, g, out)
+    ldx = _rows_of("gemv: x", x, None, K)
+    rows = x.shape[0]
     _need(w.sf_layout == NVFP4_SF_MMA, "gemv: w must have tiled scales (NVFP4_SF_MMA)")
-    _flat("gemv: w.q", w.q, torch.uint8, w.rows, w.k // 2)
-    _need(w.sf.is_contiguous() and w.sf.numel() >= nvfp4_sf_mma_bytes(w.rows, w.k), "gemv: w.sf too small")
-    out, ldd = _gemv_out("gemv", out_dtype, x.shape[0], w.rows, out, dev)
-    nvfp4_gemv(x, ldx, x.shape[0], w.q, w.sf, w.g, w.rows, w.k, out_dtype, out, ldd)
+    _flat("gemv: w.q", q, torch.uint8, N, K // 2)
+    _need(sf.is_contiguous() and sf.numel() >= nvfp4_sf_mma_bytes(N, K), "gemv: w.sf too small")
+    out, ldd = _gemv_out("gemv", out_dtype, rows, N, out, dev)
+    _check(_lib.nvfp4_gemv(x.data_ptr(), ldx, rows, q.data_ptr(), sf.data_ptr(), g.data_ptr(), N, K, out_dtype,
+                           out.data_ptr(), ldd, _raw_stream(dev)), "nvfp4_gemv")
     return out
 
 
@@ -861,23 +884,27 @@ def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtyp
                  out=None, *, workspace=None, stream=None):
     """``gemv`` with one matrix per group: row i of D (in group e by group_offsets) is row row_index[i] of x
     (row i without row_index) times matrix e; qb [G, N, K/2], sfb tiled per matrix, gb [G]."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(_torch_stream(stream)):
+        with _on(stream):
             return grouped_gemv(group_offsets, x, qb, sfb, gb, N, row_index, out_dtype, out,
                                 workspace=workspace)
     dev = _one_device("grouped_gemv", x, group_offsets, qb, sfb, gb, row_index, out, workspace)
-    ldx = _rows_of("grouped_gemv: x", x, None, None)
-    K, G = x.shape[1], group_offsets.numel() - 1
+    ldx = _rows_of("grouped_gemv: x", x)
+    src, K = x.shape
+    G = group_offsets.numel() - 1
     _flat("grouped_gemv: group_offsets", group_offsets, torch.int32, G + 1)
     _flat("grouped_gemv: qb", qb, torch.uint8, G, N, K // 2)
     _flat("grouped_gemv: gb", gb, torch.float32, G)
     _need(sfb.is_contiguous() and sfb.numel() >= G * nvfp4_sf_mma_bytes(N, K), "grouped_gemv: sfb too small")
-    rows = x.shape[0]
+    rows, ip, wp, nb = src, None, None, 0
     if row_index is not None:
         rows = row_index.numel()
         _flat("grouped_gemv: row_index", row_index, torch.int32, rows)
+        ip = row_index.data_ptr()
+    if workspace is not None:
+        wp, nb = workspace.data_ptr(), workspace.numel()
     out, ldd = _gemv_out("grouped_gemv", out_dtype, rows, N, out, dev)
-    nvfp4_grouped_gemv(G, group_offsets, rows, x, ldx, x.shape[0], row_index, qb, sfb, gb, N, K, out_dtype,
-                       out, ldd, workspace, workspace.numel() if workspace is not None else 0)
+    _check(_lib.nvfp4_grouped_gemv(G, group_offsets.data_ptr(), rows, x.data_ptr(), ldx, src, ip,
+                                   qb.data_ptr(), sfb.data_ptr(), gb.data_ptr(), N, K, out_dtype,
+                                   out.data_ptr(), ldd, wp, nb, _raw_stream(dev)), "nvfp4_grouped_gemv")
     return out

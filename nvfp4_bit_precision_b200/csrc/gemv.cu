@@ -30,10 +30,7 @@ constexpr int kMaxSegments = 16;         // segments whose x rows are in shared 
 constexpr size_t kGemvSmem = 216 * 1024;  // (and less than 11 KB that is not dynamic)
 
 // Steps in a warp's ring, all but one copied ahead.
-#ifndef GS
-#define GS 3
-#endif
-__host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? GS : 2; }
+__host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? 3 : 2; }
 
 // Most (x row, step) pairs in shared memory, 512 bytes each, and per warp.
 __host__ __device__ constexpr int max_x_pairs(int nt)
@@ -56,6 +53,7 @@ struct GemvArgs {
     int tiles, steps;              // 16-row tiles of a matrix, 256-column steps of a row
     int seg_rows;                  // most x rows of a segment
     int x_rows;                    // x rows that shared memory holds
+    int each, more;                // one matrix's tiles over the CTAs: each, and one more for the first CTAs
     void* out;
     int out_f32;
     int64_t ldd;
@@ -152,7 +150,23 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_sums + 2 * kGemvWarps * kRed);
 
     int active = 0;  // (warp 0) groups that have rows
-    if (warp == 0) {
+    const bool one = !a.group_offsets && a.rows <= a.seg_rows;  // one matrix, one segment
+    if (one) {
+        const int rows = static_cast<int>(a.rows), xr = threadIdx.x;
+        if (xr < rows) {
+            s_x_row[xr] = make_int4(xr, xr * 64, rows * 64, 0);
+            s_top[xr] = 0;
+        }
+        if (xr < 4) s_zero[xr] = make_uint4(0, 0, 0, 0);
+        if (xr == 0) {
+            const int b = blockIdx.x;
+            s_run[0] = s_run[3] = b * a.each + min(b, a.more);
+            s_run[1] = s_run[0] + a.each + (b < a.more ? 1 : 0);
+            s_run[2] = 1;
+            s_seg_e[0] = s_seg_row[0] = s_seg_x[0] = 0;
+            s_seg_n[0] = s_seg_x[1] = rows;
+        }
+    } else if (warp == 0) {
         // those groups in order, with the segments up to and with each
         int before = 0;
         const int rows = static_cast<int>(a.rows);
@@ -202,7 +216,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     }
 #pragma unroll 1
     for (int f0 = -1;;) {
-        if (warp == 0) {
+        if (warp == 0 && !one) {
             if (f0 < 0) f0 = s_run[0];
             const int f1 = s_run[1];
             // the segments from f0's on whose rows fit
@@ -306,26 +320,25 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             pslot = pslot + 1 == kStages ? 0 : pslot + 1;
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-#pragma unroll 1
-        for (int s = 0; s < kStages - 1; ++s) copy_step();
-
         // x rows of the segments as FP16, each at the power of two that brings its
         // largest magnitude to [2^14, 2^15): of segment s (n rows) and a step, [8
-        // pieces][n][4 lanes t] vectors of 16 bytes.  A warp takes the steps warp, warp
-        // + 16, ... of each row; lane (r, t) brings piece r of the columns that lanes t
-        // read, and converts it in place once the largest magnitude is known.
+        // pieces][n][4 lanes t] vectors of 16 bytes.  A warp takes the (row, step) pairs
+        // warp, warp + 16, ... in row order; lane (r, t) brings piece r of the columns
+        // that lanes t read, and converts it in place once the largest magnitude is known.
         const int x_rows = s_seg_x[segs];
         float g = 0.0f;  // of the x row that is this thread's index
         if (static_cast<int>(threadIdx.x) < x_rows) g = a.g[s_x_row[threadIdx.x].w];
         const auto next = [&](int& xr, int& c) {
             c += kGemvWarps;
-            if (c >= steps) c = warp, ++xr;
+            while (c >= steps) c -= steps, ++xr;
         };
-        if (warp < steps) {
-            constexpr int kAhead = 4;  // loads in flight together
-            int xr = 0, c = warp;
+        {
+            constexpr int kAhead = 4 * NT;  // loads in flight together
+            int xr = 0, c = warp - kGemvWarps;
+            next(xr, c);
+            bool primed = false;
 #pragma unroll 1
-            while (xr < x_rows) {
+            do {
                 uint4 v[kAhead];
                 int at[kAhead], of[kAhead];
 #pragma unroll
@@ -333,10 +346,15 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     const int4 row = s_x_row[min(xr, x_rows - 1)];
                     const int k = c * kStep + 64 * t + 8 * r;
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (row.x >= 0 && k < a.k) v[i] = *reinterpret_cast<const uint4*>(a.x + row.x * a.ldx + k);
+                    if (xr < x_rows && row.x >= 0 && k < a.k) v[i] = *reinterpret_cast<const uint4*>(a.x + row.x * a.ldx + k);
                     at[i] = row.y + (c * 8 + r) * row.z + t * 16;
                     of[i] = xr;
                     next(xr, c);
+                }
+                if (!primed) {  // the first weights, behind the first x
+#pragma unroll 1
+                    for (int s = 0; s < kStages - 1; ++s) copy_step();
+                    primed = true;
                 }
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
@@ -347,15 +365,16 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
                     if (lane == 0) atomicMax(&s_top[of[i]], top);
                 }
-            }
+            } while (xr < x_rows);
         }
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < x_rows) {
             const uint32_t ex = s_top[threadIdx.x] >> 7;
             s_scale[threadIdx.x] = (ex < 255 ? __uint_as_float((max(ex, 15u) - 14u) << 23) : 1.0f) * g;
         }
-        if (warp < steps) {
-            int xr = 0, c = warp;
+        {
+            int xr = 0, c = warp - kGemvWarps;
+            next(xr, c);
 #pragma unroll 2
             while (xr < x_rows) {
                 const int4 row = s_x_row[xr];
@@ -519,6 +538,7 @@ nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
         raised[dev & 63] = true;
     }
     const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
+    a.each = a.tiles / grid, a.more = a.tiles % grid;
     gemv_kernel<NT><<<grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -181,6 +181,9 @@ def test_one_device_refuses_the_wrong_current_device(nv, monkeypatch):
         def __init__(self, d):
             self.device = torch.device(d)
 
+        def get_device(self):
+            return self.device.index
+
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     assert nv._one_device("op", T("cuda:0"), None, T("cuda:0")).index == 0
     with pytest.raises(ValueError, match="current device"):
