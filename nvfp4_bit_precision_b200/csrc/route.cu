@@ -34,6 +34,7 @@ struct RouteArgs {
     const float* bias;
     int64_t tokens;
     int experts, top_k, groups, topk_groups, group_top;
+    int group_lanes;        // lanes of a group where that is a power of two whole lanes, else 0
     int softmax, renorm;
     float scale;
     int32_t* expert;
@@ -42,7 +43,8 @@ struct RouteArgs {
     int32_t* row_index;
     int32_t* slot_row;
     uint32_t* status;
-    int32_t* hist;          // [CTAs, experts]
+    int32_t* hist;          // [CTAs, hist_ld]
+    int hist_ld;            // experts up to a power of two, at least 4
     int64_t tokens_per_cta;
 };
 
@@ -170,9 +172,43 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
     }
     if (a.groups > 1) {
         const int size = a.experts / a.groups;
-        K mine = 0;         // lane g: group g's key
+        K mine = 0;         // lane g (or the first of its lanes): group g's key
         float mine_err = 0.0f;
-        for (int g = 0; g < a.groups; ++g) {
+        if (a.group_lanes) {
+            // a group is group_lanes whole lanes: each lane's two best, then merged
+            // pairwise within the group's lanes
+            K best = 0, second = 0;
+            float e1 = 0.0f, e2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                if (key[i] > best)
+                    second = best, e2 = e1, best = key[i], e1 = err[i];
+                else if (key[i] > second)
+                    second = key[i], e2 = err[i];
+            }
+#pragma unroll 1
+            for (int d = 1; d < a.group_lanes; d <<= 1) {
+                const K ob = __shfl_xor_sync(kFull, best, d), os = __shfl_xor_sync(kFull, second, d);
+                const float o1 = __shfl_xor_sync(kFull, e1, d), o2 = __shfl_xor_sync(kFull, e2, d);
+                if (ob > best) {
+                    const bool keep = best > os;
+                    second = keep ? best : os, e2 = keep ? e1 : o2;
+                    best = ob, e1 = o1;
+                } else if (ob > second) {
+                    second = ob, e2 = o1;
+                }
+            }
+            if (best && lane % a.group_lanes == 0 && lane < a.groups * a.group_lanes) {
+                S sum = best == 1 ? static_cast<S>(NAN) : value_of(best);
+                mine_err = e1;
+                if (a.group_top == 2 && second) {
+                    sum += second == 1 ? static_cast<S>(NAN) : value_of(second);
+                    mine_err += e2;
+                }
+                mine = ordered(sum);
+                mine_err += fabsf(static_cast<float>(sum)) * 0x1p-23f;
+            }
+        } else for (int g = 0; g < a.groups; ++g) {
             S sum = 0;
             float sum_err = 0.0f;
             bool any = false;
@@ -222,8 +258,8 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int g = (lane * EPL + i) / size;
-            if (g >= a.groups || !((kept >> g) & 1)) key[i] = 0;
+            const int g = a.group_lanes ? lane & -a.group_lanes : (lane * EPL + i) / size;
+            if (g >= 32 || !((kept >> g) & 1)) key[i] = 0;
         }
     }
     id = -1;
@@ -358,6 +394,11 @@ __device__ int block_prefix(const int* count, int* off, int n, int* warp_total)
     return total;
 }
 
+// Programmatic dependent launch: the second kernel may start while the first
+// still runs, and waits here until all of it is done and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One warp per token.  SINGLE: one CTA, which also places the rows; otherwise
 // each CTA counts its tokens' experts into its row of a.hist.
 template <int EPL, bool BF16, bool SINGLE>
@@ -370,9 +411,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0u;
     __syncthreads();
     const int64_t t0 = blockIdx.x * a.tokens_per_cta, t1 = min(t0 + a.tokens_per_cta, a.tokens);
+    if constexpr (!SINGLE) let_next_kernel_start();
+    float next[EPL];  // the following token's logits, on their way
+    if (t0 + warp < t1) load_logits<EPL, BF16>(a.logits, a.ld, t0 + warp, lane, a.experts, next);
     for (int64_t t = t0 + warp; t < t1; t += warps) {
         float l[EPL];
-        load_logits<EPL, BF16>(a.logits, a.ld, t, lane, a.experts, l);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = next[i];
+        if (t + warps < t1) load_logits<EPL, BF16>(a.logits, a.ld, t + warps, lane, a.experts, next);
         int id;
         float logit;
         bool close;
@@ -410,8 +456,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
         for (int64_t r = total + threadIdx.x; r < a.tokens * a.top_k; r += blockDim.x) a.row_index[r] = -1;
         place_rows(a, 0, a.tokens * a.top_k, s_off, s_cnt);
     } else {
-        for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-            a.hist[static_cast<int64_t>(blockIdx.x) * a.experts + e] = s_count[e];
+        for (int e = threadIdx.x; e < a.hist_ld; e += blockDim.x)
+            a.hist[blockIdx.x * a.hist_ld + e] = e < a.experts ? s_count[e] : 0;
     }
 }
 
@@ -427,15 +473,26 @@ __global__ void __launch_bounds__(kPlanThreads) route_plan_kernel(const RouteArg
     int* s_warp = s_off + E + 1;      // [32]
     int* s_cnt = s_warp + 32;         // [warps, E]
     const int b = blockIdx.x;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int all = 0, before = 0;
-        for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-            const int n = a.hist[static_cast<int64_t>(c) * E + e];
-            all += n;
-            if (c < b) before += n;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = s_before[e] = 0;
+    __syncthreads();
+    wait_for_previous_kernel();
+    {
+        // four experts a thread, the CTAs' rows over the threads that share them
+        const int vecs = a.hist_ld / 4, v = threadIdx.x % vecs;
+        int4 all = make_int4(0, 0, 0, 0), before = all;
+#pragma unroll 4
+        for (int c = threadIdx.x / vecs; c < static_cast<int>(gridDim.x); c += kPlanThreads / vecs) {
+            const int4 n = reinterpret_cast<const int4*>(a.hist)[c * vecs + v];
+            all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+            if (c < b) before.x += n.x, before.y += n.y, before.z += n.z, before.w += n.w;
         }
-        s_count[e] = all;
-        s_before[e] = before;
+        const int n_all[4] = {all.x, all.y, all.z, all.w}, n_before[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * v + i < E) {
+                if (n_all[i]) atomicAdd(&s_count[4 * v + i], n_all[i]);
+                if (n_before[i]) atomicAdd(&s_before[4 * v + i], n_before[i]);
+            }
     }
     __syncthreads();
     const int total = block_prefix(s_count, s_off, E, s_warp);
@@ -540,6 +597,13 @@ size_t route_smem(int experts, bool single, bool plan)
     return sizeof(int) * experts;
 }
 
+int hist_stride(int experts)
+{
+    int n = 4;
+    while (n < experts) n *= 2;
+    return n;
+}
+
 int route_ctas(int64_t tokens, int sms)
 {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((tokens + 31) / 32, std::min(sms, 160))));
@@ -566,7 +630,7 @@ using namespace nvfp4;
 extern "C" size_t nvfp4_route_workspace_size(int64_t tokens, int experts)
 {
     if (tokens <= kSingleTokens || experts <= 0) return kRouteWorkspaceHead;
-    return kRouteWorkspaceHead + sizeof(int32_t) * static_cast<size_t>(route_ctas(tokens, 160)) * experts;
+    return kRouteWorkspaceHead + sizeof(int32_t) * static_cast<size_t>(route_ctas(tokens, 160)) * hist_stride(experts);
 }
 
 extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,
@@ -605,6 +669,10 @@ extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_
     a.status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
     const int ctas = single ? 1 : route_ctas(tokens, sms);
     a.tokens_per_cta = (tokens + ctas - 1) / ctas;
+    a.hist_ld = hist_stride(experts);
+    const int per_lane = experts <= 32 ? 1 : experts <= 64 ? 2 : experts <= 128 ? 4 : experts <= 256 ? 8 : 16;
+    const int size = experts / a.groups, lanes = size / per_lane;
+    a.group_lanes = size % per_lane == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     a.hist = single ? nullptr : reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kRouteWorkspaceHead);
     const size_t smem = route_smem(experts, single, false);
     bool ok = true;
@@ -625,8 +693,16 @@ extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_
     else NVFP4_ROUTE(16);
 #undef NVFP4_ROUTE
     if (!ok || cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
-    if (!single)
-        route_plan_kernel<<<ctas, kPlanThreads, route_smem(experts, false, true), st>>>(a);
+    if (!single) {
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas), cfg.blockDim = dim3(kPlanThreads);
+        cfg.dynamicSmemBytes = route_smem(experts, false, true), cfg.stream = st;
+        cfg.attrs = &early, cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, route_plan_kernel, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
