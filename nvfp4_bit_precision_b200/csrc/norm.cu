@@ -19,7 +19,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kMaxCols = 32768;  // 1024 threads x 4 vectors of 8 elements
-constexpr int max_threads(int per) { return per == 4 ? 1024 : 256 * per; }
+constexpr int kNormThreads = 1024;
 
 struct NormArgs {
     const uint4* x;
@@ -35,7 +35,7 @@ struct NormArgs {
     int64_t rows, padded_rows;
     int nvec;                    // 16-byte vectors per row
     float eps;
-    int mx_tiled;
+    int mx_tiled, w32;
 };
 
 template <bool W32>
@@ -68,15 +68,77 @@ __device__ __forceinline__ T block_sum(T v, T* s)
     return t;
 }
 
-// One CTA per row, V 16-byte vectors (8 elements) per thread held in registers
-// between the statistic and the output: every tensor is read and written once.
-template <int V, bool W32>
-__global__ void __launch_bounds__(max_threads(V)) rmsnorm_kernel(const NormArgs a)
+// Sum over the block in warp order, the same value in every thread.  `s` holds
+// two rows of one float per warp, used in turn (`turn` flips), so that one barrier
+// a sum is enough.
+__device__ __forceinline__ float block_sum_turn(float v, float (*s)[32], int& turn)
 {
-    __shared__ float s_sum[32];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    float* const row = s[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) row[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.0f;
+    for (int w = 0; w < warps; w += 4) {  // (the places past the last warp are zero)
+        const float4 q = *reinterpret_cast<const float4*>(row + w);
+        t += (q.x + q.y) + (q.z + q.w);
+    }
+    return t;
+}
+
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
+        "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// bf16(a + b), one rounding: the FP32 sum rounded to bf16 is the same number (it
+// is exact unless one addend is below 2^-16 of the other, far from any midpoint).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+constexpr int kOutY = 1, kOutMx = 2;
+
+// One CTA per row at a time, V 16-byte vectors (8 elements) per thread held in
+// registers between the statistic and the output: every tensor is read and written
+// once.  The weight stays in registers over the CTA's rows (read again for V = 4,
+// whose registers it would not fit).
+template <int V, bool RES, int OUT>
+__global__ void __launch_bounds__(kNormThreads) rmsnorm_kernel(const NormArgs a)
+{
+    __shared__ __align__(16) float s_sum[2][32];
     __shared__ double s_wide[32];
+    constexpr bool kKeepW = V <= 2;
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) s_sum[i >> 5][i & 31] = 0.0f;
+    __syncthreads();
+    const auto weight = [&](int v, float (&w)[8]) {
+        if (v >= a.nvec) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+        } else if (a.w32) {
+            load_weight<true>(a.weight, v, w);
+        } else {
+            load_weight<false>(a.weight, v, w);
+        }
+    };
+    float w[kKeepW ? V : 1][8];
+    if constexpr (kKeepW) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) weight(threadIdx.x + i * blockDim.x, w[i]);
+    }
+    const float cols = static_cast<float>(8 * a.nvec);
     float top = 0.0f;  // largest |y| as stored
     bool nan = false;
+    int turn = 0;
     for (int64_t row = blockIdx.x; row < a.padded_rows; row += gridDim.x) {
         if (row >= a.rows) {  // padding rows of the tiled scale layout: zero bytes
             for (int g = threadIdx.x; g < a.nvec / 16; g += blockDim.x)
@@ -84,40 +146,38 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_kernel(const NormArgs 
             continue;
         }
         uint4 h[V];
-        float sum = 0.0f;
+        const uint4* const px = a.x + row * a.ldx + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            h[i] = v < a.nvec ? a.x[row * a.ldx + v] : make_uint4(0, 0, 0, 0);
+            const bool in = static_cast<int>(threadIdx.x + i * blockDim.x) < a.nvec;
+            h[i] = in ? px[i * blockDim.x] : make_uint4(0, 0, 0, 0);
         }
-        if (a.residual) {
+        if constexpr (RES) {
+            const uint4* const pr = a.residual + row * a.ldr + threadIdx.x;
             uint4 r[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int v = threadIdx.x + i * blockDim.x;
-                r[i] = v < a.nvec ? a.residual[row * a.ldr + v] : make_uint4(0, 0, 0, 0);
+                const bool in = static_cast<int>(threadIdx.x + i * blockDim.x) < a.nvec;
+                r[i] = in ? pr[i * blockDim.x] : make_uint4(0, 0, 0, 0);
             }
+            uint4* const ph = a.h + row * a.ldh + threadIdx.x;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int v = threadIdx.x + i * blockDim.x;
-                float f[8], g[8];
-                unpack8(h[i], f);
-                unpack8(r[i], g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += g[j];
-                h[i] = pack8(f);
-                if (v < a.nvec) a.h[row * a.ldh + v] = h[i];
+                h[i].x = add_bf16x2(h[i].x, r[i].x), h[i].y = add_bf16x2(h[i].y, r[i].y);
+                h[i].z = add_bf16x2(h[i].z, r[i].z), h[i].w = add_bf16x2(h[i].w, r[i].w);
+                if (static_cast<int>(threadIdx.x + i * blockDim.x) < a.nvec) ph[i * blockDim.x] = h[i];
             }
         }
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[8];
             unpack8(h[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+            for (int j = 0; j < 8; j += 2) fma2(s0, s1, f[j], f[j + 1], f[j], f[j + 1]);
         }
-        sum = block_sum(sum, s_sum);
-        float rstd = __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(8 * a.nvec)) + a.eps);
+        const float sum = block_sum_turn(s0 + s1, s_sum, turn);
+        float rstd = __frsqrt_rn(__fdiv_rn(sum, cols) + a.eps);
         if (!(sum < 0x1p120f) || (sum < 0x1p-100f && a.eps < 0x1p-100f)) {
             // squares out of FP32's range (the whole row's CTA takes this branch)
             double wide = 0.0;
@@ -136,17 +196,16 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_kernel(const NormArgs 
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
             const bool in = v < a.nvec;
-            float f[8], w[8];
+            float f[8];
             unpack8(h[i], f);
-            if (in) {
-                load_weight<W32>(a.weight, v, w);
-            } else {
+            if constexpr (!kKeepW) weight(v, w[0]);
+            const float* const wi = w[kKeepW ? i : 0];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+            for (int j = 0; j < 8; j += 2) {
+                mul2(f[j], f[j + 1], f[j], f[j + 1], rstd, rstd);
+                mul2(f[j], f[j + 1], f[j], f[j + 1], wi[j], wi[j + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
-            if (a.y) {
+            if constexpr ((OUT & kOutY) != 0) {
                 const uint4 p = pack8(f);
                 if (in) a.y[row * a.ldy + v] = p;
                 if (a.amax) {
@@ -159,26 +218,27 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_kernel(const NormArgs 
                     }
                 }
             }
-            if (a.mx_q) {
+            if constexpr ((OUT & kOutMx) != 0) {
                 // four lanes hold a 32-element block; nvec is a multiple of 4, so a
                 // block's lanes are all inside the row or all outside
                 float m = absmax3(absmax3(f[0], f[1], f[2]), absmax3(f[3], f[4], f[5]), absmax3(f[6], f[7], 0.0f));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                // floor(log2 m) - 8, at least -127: from the exponent field (0 and
-                // subnormal m have field 0)
-                const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 135, -127);
-                const float inv = __uint_as_float(e == -127 ? 0x7F000000u : static_cast<uint32_t>(127 - e) << 23);
-                uint32_t byte = static_cast<uint32_t>(e + 127);
+                // floor(log2 m) - 8, at least -127, from the exponent field (0 and
+                // subnormal m have field 0): the byte is the field - 8, at least 0
+                const uint32_t byte = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(m) >> 23) - 8, 0));
+                const float inv = __uint_as_float((254u - byte) << 23);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) mul2(f[j], f[j + 1], f[j], f[j + 1], inv, inv);
                 uint2 c;
-                c.x = e4m3x2_rne_sat(f[1] * inv, f[0] * inv) | e4m3x2_rne_sat(f[3] * inv, f[2] * inv) << 16;
-                c.y = e4m3x2_rne_sat(f[5] * inv, f[4] * inv) | e4m3x2_rne_sat(f[7] * inv, f[6] * inv) << 16;
+                c.x = e4m3x2_rne_sat(f[1], f[0]) | e4m3x2_rne_sat(f[3], f[2]) << 16;
+                c.y = e4m3x2_rne_sat(f[5], f[4]) | e4m3x2_rne_sat(f[7], f[6]) << 16;
                 if (in) a.mx_q[row * a.nvec + v] = c;
                 if (a.mx_tiled) {  // nvec is a multiple of 16: one word of four scales per 16 lanes
-                    byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 8;
-                    byte |= __shfl_down_sync(0xffffffffu, byte, 8) << 16;
+                    uint32_t four = byte | __shfl_down_sync(0xffffffffu, byte, 4) << 8;
+                    four |= __shfl_down_sync(0xffffffffu, four, 8) << 16;
                     if (in && (v & 15) == 0)
-                        *reinterpret_cast<uint32_t*>(a.mx_sf + sf_mma_offset(row, v / 4, a.nvec / 4)) = byte;
+                        *reinterpret_cast<uint32_t*>(a.mx_sf + sf_mma_offset(row, v / 4, a.nvec / 4)) = four;
                 } else if (in && (v & 3) == 0) {
                     a.mx_sf[row * (a.nvec / 4) + v / 4] = static_cast<uint8_t>(byte);
                 }
@@ -187,7 +247,7 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_kernel(const NormArgs 
     }
     if (a.amax) {
         if (nan) top = __uint_as_float(0x7FC00000u);
-        uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         if ((threadIdx.x & 31) == 0) atomicMax(a.amax, t);
     }
 }
@@ -200,6 +260,7 @@ struct NormBackArgs {
     const float* rstd;
     uint4* dx;
     float* partial;   // [gridDim.x, cols]; NULL = dw not wanted
+    uint32_t* status;
     int64_t lddy, ldh, lddh, lddx;
     int64_t rows;
     int nvec;
@@ -208,9 +269,14 @@ struct NormBackArgs {
 // One CTA per row at a time; the columns' dy * n sums stay in registers over
 // all the CTA's rows and go out once, as one row of `partial`.
 template <int V, bool W32>
-__global__ void __launch_bounds__(max_threads(V)) rmsnorm_backward_kernel(const NormBackArgs a)
+__global__ void __launch_bounds__(kNormThreads) rmsnorm_backward_kernel(const NormBackArgs a)
 {
-    __shared__ float s_sum[32];
+    __shared__ __align__(16) float s_sum[2][32];
+    int turn = 0;
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) s_sum[i >> 5][i & 31] = 0.0f;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0u;
+    __syncthreads();
+    let_next_kernel_start();
     float dw[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -244,7 +310,7 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_backward_kernel(const 
                 }
             }
         }
-        const float c = __fdiv_rn(block_sum(sum, s_sum), static_cast<float>(8 * a.nvec));
+        const float c = __fdiv_rn(block_sum_turn(sum, s_sum, turn), static_cast<float>(8 * a.nvec));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
@@ -270,36 +336,52 @@ __global__ void __launch_bounds__(max_threads(V)) rmsnorm_backward_kernel(const 
     }
 }
 
-// dw[c] = sum over the parts, 32 columns per CTA, its 8 warps over the parts in
-// a fixed order.
+// dw[c] = sum over the parts, 32 columns per CTA: eight lanes hold a part's 32
+// columns, 128 of them take the parts in turn, and their sums meet in shared
+// memory in a fixed order.  Launched early (see wait_for_previous_kernel).
 template <bool W32>
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* partial, int parts, int cols, void* dw)
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* partial, int parts, int cols, void* dw)
 {
-    __shared__ float s[8][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float v = 0.0f;
-    if (c < cols)
-        for (int p = warp; p < parts; p += 8) v += partial[static_cast<int64_t>(p) * cols + c];
-    s[warp][lane] = v;
+    __shared__ __align__(16) float s[128][36];
+    const int v = threadIdx.x & 7, p0 = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + 4 * v;
+    float4 t = make_float4(0, 0, 0, 0);
+    wait_for_previous_kernel();
+    if (c < cols) {
+#pragma unroll 4
+        for (int p = p0; p < parts; p += 128) {
+            const float4 q = *reinterpret_cast<const float4*>(partial + static_cast<int64_t>(p) * cols + c);
+            t.x += q.x, t.y += q.y, t.z += q.z, t.w += q.w;
+        }
+    }
+    *reinterpret_cast<float4*>(&s[p0][4 * v]) = t;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        float t = 0.0f;
+    // warp w adds rows 4 w .. 4 w + 3, then the first warp the 32 results
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float four = (s[4 * warp][lane] + s[4 * warp + 1][lane]) + (s[4 * warp + 2][lane] + s[4 * warp + 3][lane]);
+    __syncthreads();
+    s[warp][lane] = four;
+    __syncthreads();
+    const int col = blockIdx.x * 32 + lane;
+    if (warp == 0 && col < cols) {
+        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[i][lane];
+        for (int i = 0; i < 32; ++i) sum += s[i][lane];
         if (W32)
-            static_cast<float*>(dw)[c] = t;
+            static_cast<float*>(dw)[col] = sum;
         else
-            static_cast<__nv_bfloat16*>(dw)[c] = __float2bfloat16_rn(t);
+            static_cast<__nv_bfloat16*>(dw)[col] = __float2bfloat16_rn(sum);
     }
 }
 
-// Threads and vectors per thread of a row of nvec vectors.
-void row_shape(int nvec, int* threads, int* per)
-{
-    *per = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
-    *threads = ((nvec + *per - 1) / *per + 31) / 32 * 32;
-}
+// Vectors per thread of a row of nvec vectors, and its threads.  Two, at up to
+// 1024 threads (2^26 elements at 512 to 8192 columns: 80 to 93 us forward, 97 to
+// 115 us backward; one: 96 to 170 and 107 to 155 us; four: 81 to 100 and 126 to
+// 157 us); four for longer rows, and for the MXFP8 output of many rows from 2056
+// columns on, whose arithmetic gains most from few threads per row (4096 to 8192
+// columns: 81 to 83 us against 87 to 93).
+int row_vectors(int nvec) { return nvec <= 2 * kNormThreads ? 2 : 4; }
+int row_threads(int nvec, int per) { return ((nvec + per - 1) / per + 31) / 32 * 32; }
 
 constexpr size_t kNormWorkspaceHead = 256;
 
@@ -307,8 +389,7 @@ constexpr size_t kNormWorkspaceHead = 256;
 constexpr int kMaxSms = 160;
 int backward_grid(int64_t rows, int64_t cols, int sms)
 {
-    int threads, per;
-    row_shape(static_cast<int>(cols / 8), &threads, &per);
+    const int nvec = static_cast<int>(cols / 8), threads = row_threads(nvec, row_vectors(nvec));
     return static_cast<int>(std::min<int64_t>(
         rows, static_cast<int64_t>(std::min(sms, kMaxSms)) * std::max(1, 1024 / threads)));
 }
@@ -357,14 +438,28 @@ extern "C" nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ldx, const voi
     a.rows = rows, a.nvec = static_cast<int>(cols / 8), a.eps = eps;
     a.mx_tiled = mx_q && mx_sf_layout == NVFP4_SF_MMA;
     a.padded_rows = a.mx_tiled ? (rows + 127) / 128 * 128 : rows;
-    int threads, per;
-    row_shape(a.nvec, &threads, &per);
-    const int grid = static_cast<int>(std::min<int64_t>(a.padded_rows, static_cast<int64_t>(sms) * std::max(1, 2048 / threads)));
-    const bool w32 = weight_dtype == NVFP4_OUT_F32;
-    const auto go = [&](auto kernel) { kernel<<<grid, threads, 0, st>>>(a); };
-    if (per == 1) w32 ? go(rmsnorm_kernel<1, true>) : go(rmsnorm_kernel<1, false>);
-    else if (per == 2) w32 ? go(rmsnorm_kernel<2, true>) : go(rmsnorm_kernel<2, false>);
-    else w32 ? go(rmsnorm_kernel<4, true>) : go(rmsnorm_kernel<4, false>);
+    int per = row_vectors(a.nvec);
+    if (mx_q && a.nvec > 256 && rows > sms) per = 4;
+    const int threads = row_threads(a.nvec, per);
+    a.w32 = weight_dtype == NVFP4_OUT_F32;
+    const int out = (y_bf16 ? kOutY : 0) | (mx_q ? kOutMx : 0);
+    const auto go = [&](auto kernel) {
+        int fit = 1;  // CTAs per SM: one wave of them takes all rows
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, reinterpret_cast<const void*>(kernel), threads, 0);
+        const int grid = static_cast<int>(std::min<int64_t>(a.padded_rows, static_cast<int64_t>(sms) * std::max(fit, 1)));
+        kernel<<<grid, threads, 0, st>>>(a);
+    };
+#define NVFP4_NORM(V, RES)                                                               \
+    out == kOutY ? go(rmsnorm_kernel<V, RES, kOutY>)                                     \
+                 : out == kOutMx ? go(rmsnorm_kernel<V, RES, kOutMx>) : go(rmsnorm_kernel<V, RES, kOutY | kOutMx>)
+    if (residual_bf16) {
+        if (per == 2) NVFP4_NORM(2, true);
+        else NVFP4_NORM(4, true);
+    } else {
+        if (per == 2) NVFP4_NORM(2, false);
+        else NVFP4_NORM(4, false);
+    }
+#undef NVFP4_NORM
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
@@ -397,10 +492,9 @@ extern "C" nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy
     if (!sms) return NVFP4_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool w32 = weight_dtype == NVFP4_OUT_F32;
-    if (workspace && ws_bytes >= 16 &&
-        cudaMemsetAsync(static_cast<uint32_t*>(workspace) + 2, 0, 4, st) != cudaSuccess)
-        return NVFP4_ERR_CUDA;
+    uint32_t* const status = workspace && ws_bytes >= 16 ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
     if (rows == 0) {
+        if (status && cudaMemsetAsync(status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
         if (dweight && cudaMemsetAsync(dweight, 0, cols * (w32 ? 4 : 2), st) != cudaSuccess) return NVFP4_ERR_CUDA;
         return NVFP4_OK;
     }
@@ -410,21 +504,19 @@ extern "C" nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy
     a.dx = static_cast<uint4*>(dx_bf16);
     a.partial = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kNormWorkspaceHead) : nullptr;
     a.lddy = lddy / 8, a.ldh = ldh / 8, a.lddh = lddh / 8, a.lddx = lddx / 8;
-    a.rows = rows, a.nvec = static_cast<int>(cols / 8);
-    int threads, per;
-    row_shape(a.nvec, &threads, &per);
+    a.rows = rows, a.nvec = static_cast<int>(cols / 8), a.status = status;
+    const int per = row_vectors(a.nvec), threads = row_threads(a.nvec, per);
     const int grid = backward_grid(rows, cols, sms);
     const auto go = [&](auto kernel) { kernel<<<grid, threads, 0, st>>>(a); };
-    if (per == 1) w32 ? go(rmsnorm_backward_kernel<1, true>) : go(rmsnorm_backward_kernel<1, false>);
-    else if (per == 2) w32 ? go(rmsnorm_backward_kernel<2, true>) : go(rmsnorm_backward_kernel<2, false>);
+    if (per == 2) w32 ? go(rmsnorm_backward_kernel<2, true>) : go(rmsnorm_backward_kernel<2, false>);
     else w32 ? go(rmsnorm_backward_kernel<4, true>) : go(rmsnorm_backward_kernel<4, false>);
     if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dweight) {
-        const int blocks = static_cast<int>((cols + 31) / 32);
-        if (w32)
-            rmsnorm_dw_kernel<true><<<blocks, 256, 0, st>>>(a.partial, grid, static_cast<int>(cols), dweight);
-        else
-            rmsnorm_dw_kernel<false><<<blocks, 256, 0, st>>>(a.partial, grid, static_cast<int>(cols), dweight);
+        const dim3 blocks(static_cast<unsigned>((cols + 31) / 32));
+        const float* const partial = a.partial;
+        if (launch_early(w32 ? rmsnorm_dw_kernel<true> : rmsnorm_dw_kernel<false>, blocks, dim3(1024), 0, st, partial,
+                         grid, static_cast<int>(cols), dweight) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -394,11 +394,6 @@ __device__ int block_prefix(const int* count, int* off, int n, int* warp_total)
     return total;
 }
 
-// Programmatic dependent launch: the second kernel may start while the first
-// still runs, and waits here until all of it is done and its writes are visible.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // One warp per token.  SINGLE: one CTA, which also places the rows; otherwise
 // each CTA counts its tokens' experts into its row of a.hist.
 template <int EPL, bool BF16, bool SINGLE>
@@ -694,14 +689,9 @@ extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_
 #undef NVFP4_ROUTE
     if (!ok || cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!single) {
-        cudaLaunchAttribute early;
-        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(ctas), cfg.blockDim = dim3(kPlanThreads);
-        cfg.dynamicSmemBytes = route_smem(experts, false, true), cfg.stream = st;
-        cfg.attrs = &early, cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, route_plan_kernel, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+        if (launch_early(route_plan_kernel, dim3(ctas), dim3(kPlanThreads), route_smem(experts, false, true), st, a) !=
+            cudaSuccess)
+            return NVFP4_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
