@@ -190,3 +190,31 @@ def test_one_device_refuses_the_wrong_current_device(nv, monkeypatch):
         nv._one_device("op", T("cuda:1"), T("cuda:1"))
     with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
         nv._one_device("op", T("cuda:0"), T("cuda:1"))
+
+
+def test_autograd_forms_refuse():
+    """moe's functions check before they launch; a captured gradient is refused (with a stand-in for capture)."""
+    import torch
+    from nvfp4_bit_precision_b200 import moe
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensors expected"):
+        moe.rms_norm(x, x[0])
+    with pytest.raises(ValueError, match="differ"):
+        moe.rms_norm(x, x[0], x[:1])
+    with pytest.raises(ValueError, match="CUDA tensors expected"):
+        moe.moe_route(torch.zeros((2, 8)), 2)
+    assert moe.RMSNorm(64).weight.dtype == torch.bfloat16
+
+
+def test_captured_gradients_refused_on_the_host(monkeypatch):
+    import torch
+    from nvfp4_bit_precision_b200 import moe
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    x = torch.zeros((2, 64), dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(RuntimeError, match="CUDA graph"):
+        moe.rms_norm(x, x[0])
+    with pytest.raises(RuntimeError, match="CUDA graph"):
+        moe.moe_route(torch.zeros((2, 8), requires_grad=True), 2)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors expected"):
+        moe.rms_norm(x, x[0])
