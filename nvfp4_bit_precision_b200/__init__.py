@@ -17,6 +17,7 @@ with torch and call the C functions.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -327,6 +328,7 @@ def nvfp4_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
     return int(_lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols))
 
 
+@functools.lru_cache(maxsize=1024)
 def nvfp4_route_workspace_size(tokens: int, experts: int) -> int:
     return int(_lib.nvfp4_route_workspace_size(tokens, experts))
 
@@ -615,7 +617,7 @@ def _one_device(name: str, *tensors):
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if first < 0:
         raise ValueError(f"{name}: CUDA tensors expected, got {tensors[0].device}")
-    current = torch.cuda.current_device()
+    current = torch._C._cuda_getDevice()
     if first != current:
         raise ValueError(f"{name}: tensors on cuda:{first}, but the current device is cuda:{current}")
     return tensors[0].device

@@ -52,6 +52,7 @@ struct GemvArgs {
     int64_t sf_bytes;              // scale bytes of one matrix
     int tiles, steps;              // 16-row tiles of a matrix, 256-column steps of a row
     int seg_rows;                  // most x rows of a segment
+    int whole;                     // no tile or step reaches past the matrix
     int x_rows;                    // x rows that shared memory holds
     int each, more;                // one matrix's tiles over the CTAs: each, and one more for the first CTAs
     void* out;
@@ -105,6 +106,20 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 load_shared(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
 // Work is cut into 16-row weight tiles; tile 8 b + u of a matrix is rows
 // 128 b + 32 i + 4 u + 0..3 (i < 4), whose scales of 64 columns lie together.  A
 // segment is a matrix with up to seg_rows of its x rows; all segments have the
@@ -280,46 +295,74 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // place v ^ (r & 1), so that lanes reading vectors 2 t or 2 t + 1 of two rows
         // meet eight different ones.
         int left = j1 - j0, pc = first_step, pslot = 0, pseg = seg, ptile = tile;
-        bool aimed = false, have0 = false, have8 = false;
-        const uint8_t *pq = nullptr, *ps = nullptr;
-        const int64_t row_bytes = a.k / 2, next8 = 64 * row_bytes;  // from row m to row m + 8: i + 2
-        const uint32_t put = ring + r * 128 + (t ^ (r & 1)) * 16;
+        bool have0 = true, have8 = true;  // rows r and r + 8 lie in the matrix
+        const int64_t row_bytes = a.k / 2;
+        const uint8_t *tq = nullptr, *ts = nullptr;                  // this lane's first codes (row r), scales of the tile
+        const uint8_t *pq = nullptr, *pq8 = nullptr, *ps = nullptr;  // those of the step
+        const auto rows_there = [&]() {
+            if (a.whole) return;
+            const int64_t n = static_cast<int64_t>(ptile >> 3) * 128 + 32 * (r >> 2) + 4 * (ptile & 7) + (r & 3);
+            have0 = n < a.n;
+            have8 = n + 64 < a.n;
+        };
+        const auto aim = [&]() {  // at tile ptile of segment pseg
+            const int64_t e = s_seg_e[pseg], block = ptile >> 3;
+            const int u = ptile & 7;
+            tq = a.q + (e * a.n + block * 128 + 32 * (r >> 2) + 4 * u + (r & 3)) * row_bytes + 16 * t;
+            ts = a.sf + e * a.sf_bytes + block * (a.k / 64) * 512 + (lane & 15) / 4 * 512 + (4 * u + (lane & 3)) * 16;
+            rows_there();
+        };
+        const auto at_step = [&]() {
+            pq = tq + pc * (kStep / 2);
+            pq8 = pq + 64 * row_bytes;  // from row m to row m + 8: i + 2
+            ps = ts + static_cast<int64_t>(pc) * 2048;
+        };
+        if (left > 0) {
+            aim();
+            at_step();
+        }
+        const uint32_t put = ring + r * 128 + (t ^ (r & 1)) * 16, put_sc = ring + 2048 + (lane & 15) * 16;
         const auto copy_step = [&]() {
             if (left > 0) {
-                if (!aimed) {
-                    const int64_t e = s_seg_e[pseg], block = ptile >> 3;
-                    const int u = ptile & 7;
-                    const int64_t n0 = block * 128 + 32 * (r >> 2) + 4 * u + (r & 3);
-                    have0 = n0 < a.n;
-                    have8 = n0 + 64 < a.n;
-                    pq = a.q + (e * a.n + n0) * row_bytes + 16 * t + pc * (kStep / 2);
-                    ps = a.sf + e * a.sf_bytes + block * (a.k / 64) * 512 + (lane & 15) / 4 * 512 +
-                         (4 * u + (lane & 3)) * 16 + static_cast<int64_t>(pc) * 2048;
-                    aimed = true;
-                }
-                const uint32_t dst = put + pslot * kStageBytes;
-                const int k = pc * kStep + 32 * t;
-                const bool in0 = k < a.k, in1 = k + 128 < a.k;
-                copy16_async(dst, in0 && have0 ? pq : a.q, in0 && have0);
-                copy16_async(dst + 64, in1 && have0 ? pq + 64 : a.q, in1 && have0);
-                copy16_async(dst + 1024, in0 && have8 ? pq + next8 : a.q, in0 && have8);
-                copy16_async(dst + 1088, in1 && have8 ? pq + next8 + 64 : a.q, in1 && have8);
-                if (lane < 16) {
-                    const bool in = pc * kStep + 64 * (lane >> 2) < a.k;
-                    copy16_async(ring + pslot * kStageBytes + 2048 + lane * 16, in ? ps : a.sf, in);
+                const uint32_t dst = put + pslot * kStageBytes, dst_sc = put_sc + pslot * kStageBytes;
+                if (a.whole) {
+                    copy16_async(dst, pq);
+                    copy16_async(dst + 64, pq + 64);
+                    copy16_async(dst + 1024, pq8);
+                    copy16_async(dst + 1088, pq8 + 64);
+                    if (lane < 16) copy16_async(dst_sc, ps);
+                } else {
+                    const int k = pc * kStep + 32 * t;
+                    const bool in0 = k < a.k, in1 = k + 128 < a.k;
+                    copy16_async(dst, in0 && have0 ? pq : a.q, in0 && have0);
+                    copy16_async(dst + 64, in1 && have0 ? pq + 64 : a.q, in1 && have0);
+                    copy16_async(dst + 1024, in0 && have8 ? pq8 : a.q, in0 && have8);
+                    copy16_async(dst + 1088, in1 && have8 ? pq8 + 64 : a.q, in1 && have8);
+                    const bool in = pc * kStep + 64 * ((lane & 15) >> 2) < a.k;
+                    if (lane < 16) copy16_async(dst_sc, in ? ps : a.sf, in);
                 }
                 --left;
                 pq += kStep / 2;
+                pq8 += kStep / 2;
                 ps += 2048;
-                if (++pc == steps) {
+                if (++pc == steps && left > 0) {
                     pc = 0;
-                    aimed = false;
-                    if (++ptile == tiles) ptile = 0, ++pseg;
+                    if (++ptile == tiles) {
+                        ptile = 0, ++pseg;
+                        aim();
+                    } else {  // four rows on, or the next 128-row block
+                        const bool next_block = (ptile & 7) == 0;
+                        tq += (next_block ? 100 : 4) * row_bytes;
+                        ts += next_block ? (a.k / 64) * 512 - 448 : 64;
+                        rows_there();
+                    }
+                    at_step();
                 }
             }
             pslot = pslot + 1 == kStages ? 0 : pslot + 1;
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+
         // x rows of the segments as FP16, each at the power of two that brings its
         // largest magnitude to [2^14, 2^15): of segment s (n rows) and a step, [8
         // pieces][n][4 lanes t] vectors of 16 bytes.  A warp takes the (row, step) pairs
@@ -400,35 +443,44 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         int slot = 0, c = first_step;
         bool begun = first_step == 0, open = false;  // the tile was begun by this warp; its run ends inside it
         float acc[NT][4];
-        const uint8_t* xp[NT];  // this lane's x vectors: piece p of step c at xp + (8 c + p) * xstep
-        int xstep[NT];
-        bool fresh = true;
+        // of the segment: this lane's x vectors, piece p of step c at x0 + (8 c + p) *
+        // xstep; the factors on the sums of tokens 8 b + 2 t + 0, 1, and which are there
+        uint32_t x0[NT], xp[NT], xstep[NT];
+        float factor[NT][2];
+        bool there[NT][2];
+        int64_t row0 = 0;
+        const auto enter = [&]() {
+            const int n = s_seg_n[seg], first = s_seg_x[seg];
+            row0 = s_seg_row[seg];
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                const bool is = 8 * b + r < n;
+                xstep[b] = is ? n * 64 : 0;
+                x0[b] = is ? smem_addr(s_x) + first * steps * 512 + (8 * b + r) * 64 + t * 16 : smem_addr(s_zero + t);
+                xp[b] = x0[b] + c * 8 * xstep[b];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = 8 * b + 2 * t + i;
+                    there[b][i] = tok < n;
+                    factor[b][i] = tok < n ? s_scale[first + tok] : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+            }
+        };
+        // a value of token tok to weight row m of the tile
         const auto store = [&](int tok, int m, float v) {
             const int64_t n = static_cast<int64_t>(tile >> 3) * 128 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
-            if (tok >= s_seg_n[seg] || n >= a.n) return;
-            v *= s_scale[s_seg_x[seg] + tok];
-            const int64_t at = (s_seg_row[seg] + tok) * a.ldd + n;
+            if (n >= a.n) return;
+            const int64_t at = (row0 + tok) * a.ldd + n;
             if (a.out_f32)
                 static_cast<float*>(a.out)[at] = v;
             else
                 static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
         };
+        if (j0 < j1) enter();
 #pragma unroll 1
         for (int j = j0; j < j1; ++j) {
-            if (fresh) {
-                const int n = s_seg_n[seg];
-#pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    const bool is = 8 * b + r < n;
-                    xstep[b] = is ? n * 64 : 0;
-                    xp[b] = is ? s_x + s_seg_x[seg] * steps * 512 + (8 * b + r) * 64 + t * 16
-                               : reinterpret_cast<const uint8_t*>(s_zero + t);
-                    xp[b] += c * 8 * xstep[b];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
-                }
-                fresh = false;
-            }
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();  // this step has come for every lane, and every lane is done with the last one
             copy_step();
@@ -444,17 +496,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 four_scales(*reinterpret_cast<const uint32_t*>(stage + 2048 + t * 64 + (r & 3) * 16 + ((r >> 2) + 2 * h) * 4),
                             sc[h]);
             }
-            float part[2][NT][4];
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[0][b][i] = part[1][b][i] = 0.0f;
+            float part[2][NT][4] = {};
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
                 uint4 x[NT];
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
-                    x[b] = *reinterpret_cast<const uint4*>(xp[b]);
+                    x[b] = load_shared(xp[b]);
                     xp[b] += xstep[b];
                 }
                 uint32_t v[2][4];
@@ -483,7 +531,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) store(8 * b + 2 * t + (i & 1), r + 8 * (i >> 1), acc[b][i]);
+                    for (int i = 0; i < 4; ++i)
+                        if (there[b][i & 1])
+                            store(8 * b + 2 * t + (i & 1), r + 8 * (i >> 1), acc[b][i] * factor[b][i & 1]);
             } else {
                 float* const to = begun ? my_sums : my_head;
 #pragma unroll
@@ -494,8 +544,18 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             }
             if (j + 1 < j1) {
                 c = 0;
-                if (++tile == tiles) tile = 0, ++seg;
-                begun = fresh = true;
+                begun = true;
+                if (++tile == tiles) {
+                    tile = 0, ++seg;
+                    enter();
+                } else {
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        xp[b] = x0[b];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+                    }
+                }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -508,7 +568,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 const int at = (o >> 4) * kRedStride + (o & 15);
                 float v = my_sums[at];
                 for (int w = 1; w <= others; ++w) v += my_head[w * kRed + at];
-                store(o >> 4, o & 15, v);
+                store(o >> 4, o & 15, v * s_scale[s_seg_x[seg] + (o >> 4)]);
             }
         }
         if (fe == f1) return;
@@ -538,6 +598,7 @@ nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
         raised[dev & 63] = true;
     }
     const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
+    a.whole = a.n % 128 == 0 && a.k % kStep == 0;
     a.each = a.tiles / grid, a.more = a.tiles % grid;
     gemv_kernel<NT><<<grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

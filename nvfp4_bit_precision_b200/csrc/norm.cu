@@ -443,12 +443,10 @@ extern "C" nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ldx, const voi
     const int threads = row_threads(a.nvec, per);
     a.w32 = weight_dtype == NVFP4_OUT_F32;
     const int out = (y_bf16 ? kOutY : 0) | (mx_q ? kOutMx : 0);
-    const auto go = [&](auto kernel) {
-        int fit = 1;  // CTAs per SM: one wave of them takes all rows
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, reinterpret_cast<const void*>(kernel), threads, 0);
-        const int grid = static_cast<int>(std::min<int64_t>(a.padded_rows, static_cast<int64_t>(sms) * std::max(fit, 1)));
-        kernel<<<grid, threads, 0, st>>>(a);
-    };
+    // one wave of CTAs takes all rows: as many as 64 registers a thread leave room for
+    const int fit = std::max(1, 1024 / threads);
+    const int grid = static_cast<int>(std::min<int64_t>(a.padded_rows, static_cast<int64_t>(sms) * fit));
+    const auto go = [&](auto kernel) { kernel<<<grid, threads, 0, st>>>(a); };
 #define NVFP4_NORM(V, RES)                                                               \
     out == kOutY ? go(rmsnorm_kernel<V, RES, kOutY>)                                     \
                  : out == kOutMx ? go(rmsnorm_kernel<V, RES, kOutMx>) : go(rmsnorm_kernel<V, RES, kOutY | kOutMx>)

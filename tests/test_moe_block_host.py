@@ -184,7 +184,7 @@ def test_one_device_refuses_the_wrong_current_device(nv, monkeypatch):
         def get_device(self):
             return self.device.index
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     assert nv._one_device("op", T("cuda:0"), None, T("cuda:0")).index == 0
     with pytest.raises(ValueError, match="current device"):
         nv._one_device("op", T("cuda:1"), T("cuda:1"))
