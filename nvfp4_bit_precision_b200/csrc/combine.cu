@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* rows, int64_t 
                                                       const int32_t* slot_row, const float* weight, int64_t tokens,
                                                       int k, const uint4* base, uint4* out, uint32_t* status)
 {
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     for (int64_t u = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; u < tokens * nvec;
          u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t t = u / nvec, c = u - t * nvec;
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
     __shared__ float s_dot[4][8];
     __shared__ int32_t s_row[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    let_next_kernel_start();
     for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
         for (int j0 = 0; j0 < k; j0 += 4) {
             __syncthreads();
@@ -211,12 +214,13 @@ extern "C" nvfp4_status nvfp4_combine(const void* rows, int rows_dtype, int64_t 
     if (tokens == 0) return NVFP4_OK;
     const int64_t nvec = cols / 8;
     const int grid = static_cast<int>(std::min<int64_t>((tokens * nvec + 255) / 256, static_cast<int64_t>(sms) * 8));
+    cudaError_t err = cudaSuccess;
     const auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, st>>>(rows, n_rows, nvec, slot_row, weight, tokens, k,
-                                     static_cast<const uint4*>(base_bf16), static_cast<uint4*>(out_bf16), status);
+        err = launch_early(!status, kernel, grid, 256, 0, st, rows, n_rows, nvec, slot_row, weight, tokens, k,
+                           static_cast<const uint4*>(base_bf16), static_cast<uint4*>(out_bf16), status);
     };
     rows_dtype == NVFP4_OUT_F32 ? go(combine_kernel<true>) : go(combine_kernel<false>);
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 extern "C" size_t nvfp4_combine_backward_workspace_size(int64_t n_rows)

@@ -587,23 +587,26 @@ inline bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u)
 // while the one before it in the stream still runs (its launch is then hidden), and
 // calls wait_for_previous_kernel before it touches anything the other writes: all
 // of the other kernel is done by then and its writes are visible.  The earlier
-// kernel's let_next_kernel_start only says when the start may come.
+// kernel's let_next_kernel_start only says when the start may come; it comes once
+// all of that kernel's CTAs have said so, so none of them is kept from starting.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// (`early` false: an ordinary launch, as after a memset, which is no kernel.)
 template <typename... Params, typename... Args>
-inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                Args... args)
+inline cudaError_t launch_early(bool early, void (*kernel)(Params...), int64_t grid, int block, size_t smem,
+                                cudaStream_t stream, Args... args)
 {
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = stream;
-    cfg.attrs = &early, cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid)), cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+    cfg.attrs = &attr, cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     float* const my_sums = s_sums + (kGemvWarps + warp) * kRed;         // sums of a tile that this one began
     uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_sums + 2 * kGemvWarps * kRed);
 
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     int active = 0;  // (warp 0) groups that have rows
     const bool one = !a.group_offsets && a.rows <= a.seg_rows;  // one matrix, one segment
     if (one) {
@@ -600,7 +602,8 @@ nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
     const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
     a.whole = a.n % 128 == 0 && a.k % kStep == 0;
     a.each = a.tiles / grid, a.more = a.tiles % grid;
-    gemv_kernel<NT><<<grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st>>>(a);
+    if (launch_early(!a.status, gemv_kernel<NT>, grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st, a) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 

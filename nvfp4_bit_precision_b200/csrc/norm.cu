@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_kernel(const NormArgs a)
     __shared__ __align__(16) float s_sum[2][32];
     __shared__ double s_wide[32];
     constexpr bool kKeepW = V <= 2;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     for (int i = threadIdx.x; i < 64; i += blockDim.x) s_sum[i >> 5][i & 31] = 0.0f;
     __syncthreads();
     const auto weight = [&](int v, float (&w)[8]) {
@@ -274,9 +276,10 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_backward_kernel(const No
     __shared__ __align__(16) float s_sum[2][32];
     int turn = 0;
     for (int i = threadIdx.x; i < 64; i += blockDim.x) s_sum[i >> 5][i & 31] = 0.0f;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0u;
     __syncthreads();
-    let_next_kernel_start();
     float dw[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* partial, 
     const int c = blockIdx.x * 32 + 4 * v;
     float4 t = make_float4(0, 0, 0, 0);
     wait_for_previous_kernel();
+    let_next_kernel_start();
     if (c < cols) {
 #pragma unroll 4
         for (int p = p0; p < parts; p += 128) {
@@ -446,7 +450,8 @@ extern "C" nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ldx, const voi
     // one wave of CTAs takes all rows: as many as 64 registers a thread leave room for
     const int fit = std::max(1, 1024 / threads);
     const int grid = static_cast<int>(std::min<int64_t>(a.padded_rows, static_cast<int64_t>(sms) * fit));
-    const auto go = [&](auto kernel) { kernel<<<grid, threads, 0, st>>>(a); };
+    cudaError_t err = cudaSuccess;
+    const auto go = [&](auto kernel) { err = launch_early(!amax_out, kernel, grid, threads, 0, st, a); };
 #define NVFP4_NORM(V, RES)                                                               \
     out == kOutY ? go(rmsnorm_kernel<V, RES, kOutY>)                                     \
                  : out == kOutMx ? go(rmsnorm_kernel<V, RES, kOutMx>) : go(rmsnorm_kernel<V, RES, kOutY | kOutMx>)
@@ -458,7 +463,7 @@ extern "C" nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ldx, const voi
         else NVFP4_NORM(4, false);
     }
 #undef NVFP4_NORM
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 extern "C" size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols)
@@ -505,15 +510,15 @@ extern "C" nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy
     a.rows = rows, a.nvec = static_cast<int>(cols / 8), a.status = status;
     const int per = row_vectors(a.nvec), threads = row_threads(a.nvec, per);
     const int grid = backward_grid(rows, cols, sms);
-    const auto go = [&](auto kernel) { kernel<<<grid, threads, 0, st>>>(a); };
+    cudaError_t err = cudaSuccess;
+    const auto go = [&](auto kernel) { err = launch_early(true, kernel, grid, threads, 0, st, a); };
     if (per == 2) w32 ? go(rmsnorm_backward_kernel<2, true>) : go(rmsnorm_backward_kernel<2, false>);
     else w32 ? go(rmsnorm_backward_kernel<4, true>) : go(rmsnorm_backward_kernel<4, false>);
-    if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (err != cudaSuccess || cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dweight) {
-        const dim3 blocks(static_cast<unsigned>((cols + 31) / 32));
         const float* const partial = a.partial;
-        if (launch_early(w32 ? rmsnorm_dw_kernel<true> : rmsnorm_dw_kernel<false>, blocks, dim3(1024), 0, st, partial,
-                         grid, static_cast<int>(cols), dweight) != cudaSuccess)
+        if (launch_early(true, w32 ? rmsnorm_dw_kernel<true> : rmsnorm_dw_kernel<false>, (cols + 31) / 32, 1024, 0, st,
+                         partial, grid, static_cast<int>(cols), dweight) != cudaSuccess)
             return NVFP4_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

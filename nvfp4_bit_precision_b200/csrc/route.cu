@@ -401,12 +401,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
 {
     extern __shared__ int s_dyn[];
     int* s_count = s_dyn;  // [experts]
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) s_count[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0u;
     __syncthreads();
     const int64_t t0 = blockIdx.x * a.tokens_per_cta, t1 = min(t0 + a.tokens_per_cta, a.tokens);
-    if constexpr (!SINGLE) let_next_kernel_start();
     float next[EPL];  // the following token's logits, on their way
     if (t0 + warp < t1) load_logits<EPL, BF16>(a.logits, a.ld, t0 + warp, lane, a.experts, next);
     for (int64_t t = t0 + warp; t < t1; t += warps) {
@@ -471,6 +472,7 @@ __global__ void __launch_bounds__(kPlanThreads) route_plan_kernel(const RouteArg
     for (int e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = s_before[e] = 0;
     __syncthreads();
     wait_for_previous_kernel();
+    let_next_kernel_start();
     {
         // four experts a thread, the CTAs' rows over the threads that share them
         const int vecs = a.hist_ld / 4, v = threadIdx.x % vecs;
@@ -523,6 +525,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackArgs
 {
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     for (int64_t t = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); t < a.tokens; t += warps) {
         int id = -1;
         float g = 0.0f, l = 0.0f;
@@ -675,7 +679,7 @@ extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_
         if (smem > 48 * 1024)
             ok = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
-        if (ok) kernel<<<ctas, kRouteThreads, smem, st>>>(a);
+        if (ok) ok = launch_early(true, kernel, ctas, kRouteThreads, smem, st, a) == cudaSuccess;
     };
     const bool h = logits_dtype == NVFP4_OUT_BF16;
 #define NVFP4_ROUTE(EPL)                                                                          \
@@ -689,7 +693,7 @@ extern "C" nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_
 #undef NVFP4_ROUTE
     if (!ok || cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!single) {
-        if (launch_early(route_plan_kernel, dim3(ctas), dim3(kPlanThreads), route_smem(experts, false, true), st, a) !=
+        if (launch_early(true, route_plan_kernel, ctas, kPlanThreads, route_smem(experts, false, true), st, a) !=
             cudaSuccess)
             return NVFP4_ERR_CUDA;
     }
@@ -716,12 +720,13 @@ extern "C" nvfp4_status nvfp4_route_backward(const float* dweight, const void* l
                     p->renormalize, p->scale, dlogits, ldd};
     const int grid = static_cast<int>(std::min<int64_t>((tokens + 7) / 8, static_cast<int64_t>(sms) * 8));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto go = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(a); };
+    cudaError_t err = cudaSuccess;
+    const auto go = [&](auto kernel) { err = launch_early(true, kernel, grid, 256, 0, st, a); };
     const bool h = logits_dtype == NVFP4_OUT_BF16;
     if (experts <= 32) h ? go(route_backward_kernel<1, true>) : go(route_backward_kernel<1, false>);
     else if (experts <= 64) h ? go(route_backward_kernel<2, true>) : go(route_backward_kernel<2, false>);
     else if (experts <= 128) h ? go(route_backward_kernel<4, true>) : go(route_backward_kernel<4, false>);
     else if (experts <= 256) h ? go(route_backward_kernel<8, true>) : go(route_backward_kernel<8, false>);
     else h ? go(route_backward_kernel<16, true>) : go(route_backward_kernel<16, false>);
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
