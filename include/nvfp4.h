@@ -457,7 +457,7 @@ typedef struct {
     float scale;      /* factor on the weights                                      */
 } nvfp4_route_params;
 
-/* Workspace bytes nvfp4_route needs (none for up to 128 tokens). */
+/* Workspace bytes nvfp4_route needs; up to 256 means that it may be left out. */
 size_t nvfp4_route_workspace_size(int64_t tokens, int experts);
 
 /*
@@ -536,9 +536,10 @@ nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void* rows, int
  *   D[i][j] = g * sum_k x[i][k] * (e2m1(q_jk) * e4m3(sf(j, k/16)))
  * x [rows, ldx] bf16, not quantised; q [N, K/2], sf and g as nvfp4_gemm's B
  * (NVFP4_SF_MMA layout).  Sums are FP32, in a fixed order.  D [rows, ldd] FP32 or
- * bf16 (RNE).  Any number of rows; meant for up to about 32, since the matrix is
- * read again for every 16.  N a multiple of 16, K of 64, ldx >= K of 8;
- * x, q, sf 16-byte aligned.
+ * bf16 (RNE).  Any number of rows; meant for up to about 32: the matrix is read
+ * again for every 8 or 16 rows, and for fewer where K is long (shared memory holds
+ * 45056 x values).  N a multiple of 16, K of 64 and at most 45056, ldx >= K of 8;
+ * rows * N * K below about 2^43 (NVFP4_ERR_SHAPE); x, q, sf 16-byte aligned.
  */
 nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t ldx, int64_t rows, const uint8_t* q,
                         const uint8_t* sf, const float* g, int64_t N, int64_t K, int out_dtype,

@@ -10,8 +10,14 @@
 // scores order it.  Without bias and groups that is the order of the logits
 // themselves, which both score functions keep.  Otherwise FP32 scores are
 // compared, each with a bound on its error; a token whose choice hangs on a
-// difference within those bounds is chosen again from scores in FP64 (about one
-// token in a thousand).  Equal scores go to the lower index.
+// difference within those bounds is chosen again from scores in FP64 (a few tokens
+// in a thousand).  Equal scores go to the lower index.
+//
+// What bounds it: at 16384 tokens of 64 experts the logits are 4.2 MB (0.6 us), and
+// the call takes 13 us on the device: a warp per token, whose serial work (loads,
+// four rounds of maximum and ballot, the weights) and whose code's first run from a
+// cold instruction cache are the time; the row order adds 4 us in a second launch
+// that starts early.  Splitting a token over more lanes does not shorten the rounds.
 #include "common.cuh"
 
 #include <algorithm>
@@ -24,7 +30,11 @@ constexpr int kMaxTopK = 32;   // lane j of a warp holds slot j
 constexpr int kMaxRouteGroups = 32;
 constexpr int kRouteThreads = 1024;
 constexpr int kPlanThreads = 512;
-constexpr int kSingleTokens = 128;  // up to here one CTA does the whole call
+// Up to here one CTA does the whole call in one launch, which the host feels.  On
+// the device, one CTA against two launches: 8 tokens 5.4 us against 5.8 (64 experts)
+// and 9.9 against 10.5 (256, biased, in groups); 32 tokens 6.2 against 5.9 and 15.5
+// against 10.6; 128 tokens 12.0 against 6.1 and 49 against 16.
+constexpr int kSingleTokens = 16;
 constexpr size_t kRouteWorkspaceHead = 256;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -85,6 +95,12 @@ __device__ __forceinline__ T warp_sum(T v)
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
     return v;
 }
+
+// exp and 1 / x for the FP32 scores, whose errors choose() bounds, and in FP64.
+__device__ __forceinline__ float score_exp(float v) { return __expf(v); }
+__device__ __forceinline__ double score_exp(double v) { return exp(v); }
+__device__ __forceinline__ float score_reciprocal(float v) { return __fdividef(1.0f, v); }
+__device__ __forceinline__ double score_reciprocal(double v) { return 1.0 / v; }
 
 template <typename S> struct KeyOf;
 template <> struct KeyOf<float> { using type = uint32_t; };
@@ -148,25 +164,30 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             if (l[i] <= kMaskedLogit)
                 s[i] = 0;
             else if (a.softmax)
-                s[i] = exp(static_cast<S>(l[i]) - top);
+                s[i] = score_exp(static_cast<S>(l[i]) - top);
             else
-                s[i] = static_cast<S>(1) / (static_cast<S>(1) + exp(-static_cast<S>(l[i])));
+                s[i] = score_reciprocal(static_cast<S>(1) + score_exp(-static_cast<S>(l[i])));
             if (a.softmax) total += s[i];
         }
-        if (a.softmax) total = warp_sum(total);
+        if (a.softmax) total = score_reciprocal(warp_sum(total));
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane * EPL + i;
-            if (a.softmax) s[i] /= total;
+            if (a.softmax) s[i] *= total;
             const S v = s[i] + (a.bias && e < a.experts ? static_cast<S>(a.bias[e]) : static_cast<S>(0));
             key[i] = l[i] <= kMaskedLogit ? 0 : ordered(v);
-            // FP32: 2 ulp of exp and |l - top| half ulps of its argument, at most 16
-            // additions deep in the total, one rounding each in the quotient and the
-            // bias's addition; half as much again on top
+            // FP32.  __expf is off by (2 + 1.16 |x|) ulp, 2^-22 + |x| 2^-22.8 of its
+            // value.  Sigmoid: that times 1 - s, and the sum's and quotient's roundings.
+            // Softmax: that and the argument's rounding for the term; in the total the
+            // terms' errors are weighted by the scores, whose mean |x| is at most ln 512,
+            // and 25 additions follow one another: 2^-18.6; then two products.  Both: the
+            // bias's addition.
             err[i] = 0.0f;
             if (F32) {
-                const float d = a.softmax ? fabsf(static_cast<float>(l[i] - top)) : 0.0f;
-                err[i] = static_cast<float>(s[i]) * (0x1p-19f + d * 0x1p-23f) + fabsf(static_cast<float>(v)) * 0x1p-23f;
+                const float sf = static_cast<float>(s[i]);
+                const float rel = a.softmax ? 0x1p-18f + fabsf(static_cast<float>(l[i] - top)) * 0x1p-22f
+                                            : 0x1p-21f + (1.0f - sf) * (1.0f + fabsf(l[i])) * 0x1p-22f;
+                err[i] = sf * rel + fabsf(static_cast<float>(v)) * 0x1p-23f;
             }
         }
     }
@@ -605,7 +626,7 @@ int hist_stride(int experts)
 
 int route_ctas(int64_t tokens, int sms)
 {
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((tokens + 31) / 32, std::min(sms, 160))));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((tokens + 7) / 8, std::min(sms, 160))));
 }
 
 nvfp4_status route_common(const void* logits, int logits_dtype, int64_t ld, int64_t tokens, int experts, int top_k,
