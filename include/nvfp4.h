@@ -512,15 +512,17 @@ nvfp4_status nvfp4_combine(const void* rows, int rows_dtype, int64_t n_rows, int
                            const void* base_bf16, void* out_bf16, void* workspace, size_t ws_bytes,
                            void* stream);
 
-/* Workspace bytes nvfp4_combine_backward needs (the status word, a bit a row). */
+/* Workspace bytes of nvfp4_combine_backward (the status word, a bit a row). */
 size_t nvfp4_combine_backward_workspace_size(int64_t n_rows);
 
 /*
  * nvfp4_combine_backward -- gradients of nvfp4_combine:
  *   drows[slot_row[t][j]] = weight[t][j] * dout[t]      (rows_dtype)
  *   dweight[t][j] = <dout[t], rows[slot_row[t][j]]>     (FP32; 0 for left-out slots)
- * Each row belongs to one slot at most, as nvfp4_route's do: a row that a second
- * slot names is reported (NVFP4_ERR_INDEX) and that slot left out.  used_rows
+ * Each row belongs to one slot at most, as nvfp4_route's do.  With a workspace
+ * that is checked: a slot whose row another has named, or past n_rows, is left out
+ * and reported (NVFP4_ERR_INDEX); without one the gradient of a row that two slots
+ * name is unspecified.  used_rows
  * (device int32, group_offsets + experts of nvfp4_route): the rows from
  * *used_rows on are zeroed; NULL: rows that no slot names are left as they were.
  */

@@ -304,7 +304,7 @@ def nvfp4_combine(rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k, b
 
 
 def nvfp4_combine_backward(dout, rows, rows_dtype, n_rows, cols, slot_row, weight, tokens, k, used_rows,
-                           drows, dweight, workspace, ws_bytes, stream=None) -> None:
+                           drows, dweight, workspace=None, ws_bytes=0, stream=None) -> None:
     _check(_lib.nvfp4_combine_backward(_ptr(dout), _ptr(rows), rows_dtype, n_rows, cols, _ptr(slot_row),
                                        _ptr(weight), tokens, k, _ptr(used_rows), _ptr(drows), _ptr(dweight),
                                        _ptr(workspace), ws_bytes, _stream(stream)),
@@ -832,7 +832,9 @@ def combine(rows, slot_row, weight, base=None, *, workspace=None, stream=None):
 
 def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, workspace=None, stream=None):
     """(drows, dweight) of ``combine`` (the base's gradient is dout).  With the routing's ``group_offsets``
-    the rows behind its last one get a zero gradient; without, every row that no slot names does."""
+    the rows behind its last one get a zero gradient; without, every row that no slot names does.  Each row
+    belongs to one slot at most, as a routing's do; a ``workspace`` of
+    ``nvfp4_combine_backward_workspace_size(n)`` bytes has that checked and receives the status word."""
     if stream is not None:
         with _on(stream):
             return combine_backward(dout, rows, slot_row, weight, group_offsets, workspace=workspace)
@@ -847,9 +849,8 @@ def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, worksp
         used = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
     drows = torch.empty_like(rows) if used is not None else torch.zeros_like(rows)
     dweight = _matrix(dev, torch.float32, tokens, k)
-    ws = workspace if workspace is not None else _workspace(dev, nvfp4_combine_backward_workspace_size(n))
-    nvfp4_combine_backward(dout, rows, dt, n, cols, slot_row, weight, tokens, k, used, drows, dweight, ws,
-                           ws.numel())
+    nvfp4_combine_backward(dout, rows, dt, n, cols, slot_row, weight, tokens, k, used, drows, dweight, workspace,
+                           workspace.numel() if workspace is not None else 0)
     return drows, dweight
 
 

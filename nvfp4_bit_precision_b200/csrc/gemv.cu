@@ -9,11 +9,26 @@
 //  - a code pair becomes two FP16 values in one conversion, and one packed
 //    multiply by the block scale gives e2m1 * e4m3 (6 significant bits, between
 //    2^-10 and 2688 or zero): exact in FP16;
-//  - x is brought into FP16's range by a power of two per token and 128
-//    columns, its largest magnitude to [2^14, 2^15): exact for values down to
-//    2^-32 of that largest one, and off by at most 2^-40 of it below;
-//  - products and their sums are FP32; each 128 columns' sum is scaled back and
-//    added in FP32.
+//  - x is brought into FP16's range by a power of two per row, its largest
+//    magnitude to [2^14, 2^15): exact for values down to 2^-32 of that largest one,
+//    and off by at most 2^-40 of it below;
+//  - products and their sums are FP32; the tensor cores' sums of 256 columns are
+//    added in FP32, and the total is scaled back.
+//
+// What bounds it.  Bytes, with what comes before the first of them: a plain read of
+// as many bytes takes 12.1 us (59 MB) and 20.6 us (133 MB) a launch here.  One row x
+// 20480 x 5120 (59 MB) 16.2 us; 32 tokens' rows through four experts of 4096 x 1536
+// each (about 43 experts, 150 MB) 37 us; eight tokens' through 1536 x 4096 (60 MB)
+// 22 us, of which 4 us pass before the routing has been read and the first weights
+// are asked for.  13 rows x 4096 x 4096: 12.5 us, 6 of them bringing the rows into
+// each SM's shared memory.  Steps on the way, at the one row: warps of 64 matrix
+// rows loading into registers 24.9 us; a copy ring and 16-row tiles in equal runs
+// 18.1 us; the first weights asked for behind x instead of before it, and no group
+// scan for a single matrix, 15.7 us.  Decoding by shifts and masks into bf16 (15
+// integer operations per eight codes against four conversions) ran at 37 codes a
+// clock and SM with the matrix instructions, below the 41 that HBM delivers; the
+// conversions run at 65.  Asking for a CTA's later tiles ahead by bulk prefetches
+// into L2 was slower (one row: 16.9 to 19.4 us): x waits behind them.
 #include "common.cuh"
 
 #include <algorithm>
@@ -27,16 +42,17 @@ constexpr int kStageBytes = 2048 + 256;  // a 16-row tile's codes and scales
 constexpr int kRedStride = 20;           // floats per token of a tile's sums (16 rows, off the banks)
 constexpr int kMaxGemvGroups = 256;
 constexpr int kMaxSegments = 16;         // segments whose x rows are in shared memory together
-constexpr size_t kGemvSmem = 216 * 1024;  // (and less than 11 KB that is not dynamic)
+constexpr size_t kGemvSmem = 216 * 1024;  // dynamic; 11 KB more are not, of 227 KB in all
 
 // Steps in a warp's ring, all but one copied ahead.
 __host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? 3 : 2; }
 
-// Most (x row, step) pairs in shared memory, 512 bytes each, and per warp.
+// Most (x row, step) pairs in shared memory, 512 bytes each.
 __host__ __device__ constexpr int max_x_pairs(int nt)
 {
     return static_cast<int>((kGemvSmem - kGemvWarps * (ring_stages(nt) * kStageBytes + 2 * 4 * 8 * nt * kRedStride)) / 512);
 }
+
 struct GemvArgs {
     const uint16_t* x;
     int64_t ldx;
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     // (bf16 bits)
     __shared__ int4 s_x_row[kMaxSegments * 8 * NT];
     __shared__ uint32_t s_top[kMaxSegments * 8 * NT];
-    __shared__ float s_scale[kMaxSegments * 8 * NT];  // the factor on its sums: its own power of two, the matrix's g
+    __shared__ float2 s_scale[kMaxSegments * 8 * NT];  // the factors on its sums: the matrix's g, its own power of two
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
     const int tiles = a.tiles, steps = a.steps;
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < x_rows) {
             const uint32_t ex = s_top[threadIdx.x] >> 7;
-            s_scale[threadIdx.x] = (ex < 255 ? __uint_as_float((max(ex, 15u) - 14u) << 23) : 1.0f) * g;
+            s_scale[threadIdx.x] = make_float2(g, ex < 255 ? __uint_as_float((max(ex, 15u) - 14u) << 23) : 1.0f);
         }
         {
             int xr = 0, c = warp - kGemvWarps;
@@ -448,7 +464,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // of the segment: this lane's x vectors, piece p of step c at x0 + (8 c + p) *
         // xstep; the factors on the sums of tokens 8 b + 2 t + 0, 1, and which are there
         uint32_t x0[NT], xp[NT], xstep[NT];
-        float factor[NT][2];
+        float2 factor[NT][2];
         bool there[NT][2];
         int64_t row0 = 0;
         const auto enter = [&]() {
@@ -464,14 +480,16 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 for (int i = 0; i < 2; ++i) {
                     const int tok = 8 * b + 2 * t + i;
                     there[b][i] = tok < n;
-                    factor[b][i] = tok < n ? s_scale[first + tok] : 0.0f;
+                    factor[b][i] = tok < n ? s_scale[first + tok] : make_float2(0.0f, 0.0f);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
             }
         };
-        // a value of token tok to weight row m of the tile
-        const auto store = [&](int tok, int m, float v) {
+        // a sum of token tok to weight row m of the tile (g first: the power of two
+        // may leave few bits to a product of both factors)
+        const auto store = [&](int tok, int m, float v, float2 by) {
+            v = v * by.x * by.y;
             const int64_t n = static_cast<int64_t>(tile >> 3) * 128 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
             if (n >= a.n) return;
             const int64_t at = (row0 + tok) * a.ldd + n;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (there[b][i & 1])
-                            store(8 * b + 2 * t + (i & 1), r + 8 * (i >> 1), acc[b][i] * factor[b][i & 1]);
+                            store(8 * b + 2 * t + (i & 1), r + 8 * (i >> 1), acc[b][i], factor[b][i & 1]);
             } else {
                 float* const to = begun ? my_sums : my_head;
 #pragma unroll
@@ -570,7 +588,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 const int at = (o >> 4) * kRedStride + (o & 15);
                 float v = my_sums[at];
                 for (int w = 1; w <= others; ++w) v += my_head[w * kRed + at];
-                store(o >> 4, o & 15, v * s_scale[s_seg_x[seg] + (o >> 4)]);
+                store(o >> 4, o & 15, v, s_scale[s_seg_x[seg] + (o >> 4)]);
             }
         }
         if (fe == f1) return;

@@ -89,6 +89,20 @@ def test_range_of_x():
     assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
 
 
+def test_small_x_and_g():
+    """x near the smallest numbers under a small g: the result keeps FP32's precision where it is a normal number."""
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(17)
+    q, sf, _ = R.random_nvfp4(rng, 128, 256)
+    for g, exponent in ((2.0 ** -20, -100), (2.0 ** -30, -110), (2.0 ** -3, -124)):
+        x = W.f32_to_bf16_bits((rng.standard_normal((3, 256)) * 2.0 ** exponent * 2.0 ** 14).astype(np.float32))
+        w = R.nvfp4_matrix(q, sf, np.float32(g))
+        ref = val(x) @ w.T
+        y = nv.gemv(to_dev(x), upload(nv, q, sf, np.float32(g)), nv.NVFP4_OUT_F32)
+        # (the two products' roundings are half of 2^-149 where they leave the normal numbers)
+        assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
+
+
 def test_non_finite_tokens_stay_alone():
     import torch
     import nvfp4_bit_precision_b200 as nv

@@ -95,7 +95,8 @@ def test_combine_argument_errors(nv):
         return nv._lib.nvfp4_combine_backward(dout, rows, dt, n, cols, slot, w, t, k, used, dr, dw, ws, wn, None)
     assert back(dout=None) == ARG and back(dr=None) == ARG and back(dw=None) == ARG
     assert back(cols=4) == SHAPE and back(dr=FAKE + 4) == ALIGN and back(used=FAKE + 1) == ALIGN
-    assert back(ws=None) == WORKSPACE and back(wn=256) == WORKSPACE
+    assert back(ws=FAKE + 8) == WORKSPACE and back(wn=256) == WORKSPACE
+    assert back(ws=None, wn=0) not in (ARG, SHAPE, ALIGN, WORKSPACE)   # the check is optional (no GPU here)
     assert nv.nvfp4_combine_backward_workspace_size(33) == 256 + 8
 
 
