@@ -53,6 +53,26 @@ __host__ __device__ constexpr int max_x_pairs(int nt)
     return static_cast<int>((kGemvSmem - kGemvWarps * (ring_stages(nt) * kStageBytes + 2 * 4 * 8 * nt * kRedStride)) / 512);
 }
 
+// Division of 0 <= n < 2^31 by a number known on the host.  With 2^s >= d and
+// m = floor(2^(31 + s) / d) + 1, n m / 2^(31 + s) exceeds n / d by at most
+// n / 2^(31 + s) < 2^-s <= 1 / d, too little to reach the next whole number.
+struct Divisor {
+    uint32_t m = 0;
+    int shift = 0, d = 1;
+    Divisor() = default;
+    explicit Divisor(int by) : d(by)
+    {
+        int s = 0;
+        while ((1ll << s) < by) ++s;
+        m = static_cast<uint32_t>((1ull << (31 + s)) / static_cast<uint64_t>(by) + 1);
+        shift = 31 + s;
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> shift);
+    }
+};
+
 struct GemvArgs {
     const uint16_t* x;
     int64_t ldx;
@@ -70,6 +90,7 @@ struct GemvArgs {
     int seg_rows;                  // most x rows of a segment
     int whole;                     // no tile or step reaches past the matrix
     int x_rows;                    // x rows that shared memory holds
+    Divisor by_tiles, by_steps, by_seg_rows, by_grid;
     int each, more;                // one matrix's tiles over the CTAs: each, and one more for the first CTAs
     void* out;
     int out_f32;
@@ -205,7 +226,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         const int rows = static_cast<int>(a.rows);
         if (!a.group_offsets) {
             active = 1;
-            before = (rows + a.seg_rows - 1) / a.seg_rows;
+            before = a.by_seg_rows(rows - 1) + 1;
             if (lane == 0) s_group[0] = 0, s_first[0] = 0, s_rows[0] = rows, s_end[0] = before;
         } else {
             int lo = lane < a.groups ? a.group_offsets[lane] : 0;
@@ -220,8 +241,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 if (e + 1 == a.groups) hi = last;
                 const int first = min(max(lo, 0), rows), count = e < a.groups ? min(hi, rows) - first : 0;
                 const unsigned has = __ballot_sync(0xffffffffu, count > 0);
-                int segs = count > 0 ? (count + a.seg_rows - 1) / a.seg_rows : 0;
-#pragma unroll 1
+                int segs = count > 0 ? a.by_seg_rows(count - 1) + 1 : 0;
+#pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, segs, d);
                     if (lane >= d) segs += v;
@@ -238,7 +259,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 lo = next;
             }
         }
-        const int all = before * tiles, b = blockIdx.x, each = all / gridDim.x, more = all % gridDim.x;
+        const int all = before * tiles, b = blockIdx.x, each = a.by_grid(all), more = all - each * static_cast<int>(gridDim.x);
         if (lane == 0) {
             s_run[0] = b * each + min(b, more);
             s_run[1] = s_run[0] + each + (b < more ? 1 : 0);
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             if (f0 < 0) f0 = s_run[0];
             const int f1 = s_run[1];
             // the segments from f0's on whose rows fit
-            const int seg0 = f0 / tiles, want = f1 > f0 ? (f1 - 1) / tiles - seg0 + 1 : 0;
+            const int seg0 = a.by_tiles(f0), want = f1 > f0 ? a.by_tiles(f1 - 1) - seg0 + 1 : 0;
             int e = 0, row = 0, n = 0;
             if (lane < min(want, kMaxSegments)) {
                 int g = 0;
@@ -305,7 +326,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         const int items = (fe - f0) * steps;
         const auto run_start = [&](int w) { return (items / kGemvWarps) * w + min(w, items % kGemvWarps); };
         const int j0 = run_start(warp), j1 = run_start(warp + 1);
-        const int skip = j0 / steps, first_step = j0 - skip * steps;
+        const int skip = a.by_steps(j0), first_step = j0 - skip * steps;
         int seg = 0, tile = tile0 + skip;
         while (tile >= tiles) tile -= tiles, ++seg;
 
@@ -618,6 +639,8 @@ nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
         raised[dev & 63] = true;
     }
     const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
+    a.by_tiles = Divisor(a.tiles), a.by_steps = Divisor(a.steps), a.by_seg_rows = Divisor(a.seg_rows);
+    a.by_grid = Divisor(grid);
     a.whole = a.n % 128 == 0 && a.k % kStep == 0;
     a.each = a.tiles / grid, a.more = a.tiles % grid;
     if (launch_early(!a.status, gemv_kernel<NT>, grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st, a) != cudaSuccess)
