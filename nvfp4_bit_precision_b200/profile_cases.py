@@ -9,6 +9,11 @@
     python -m nvfp4_bit_precision_b200.profile_cases mxfp4 ROWS COLS [--warm W]
     python -m nvfp4_bit_precision_b200.profile_cases dispatch TOKENS HIDDEN [--warm W]
     python -m nvfp4_bit_precision_b200.profile_cases combine TOKENS HIDDEN [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases norm ROWS COLS [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases norm-backward ROWS COLS [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases route TOKENS EXPERTS [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases weighted-combine TOKENS HIDDEN [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases gemv ROWS N K [--warm W]
 
 Each runs W untimed launches of the case, then one more, on synthetic operands
 (codes and in-range scale bytes drawn on the device; bf16 inputs ~N(0, 1e-3)),
@@ -174,10 +179,61 @@ def _combine(nv, torch, tokens, hidden, warm):
     return ws
 
 
+def _bf16(torch, shape, std, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+
+def _norm(nv, torch, rows, cols, warm):
+    """The norm of x + residual as MXFP8 with tiled scales."""
+    x, r, w = (_bf16(torch, s, 1.0, i) for i, s in enumerate(((rows, cols), (rows, cols), (cols,))))
+    for _ in range(warm + 1):
+        nv.rmsnorm(x, w, r, y=False, mx=True, mx_sf_layout=nv.NVFP4_SF_MMA)
+
+
+def _norm_backward(nv, torch, rows, cols, warm):
+    """The norm's gradients, with one of the sum coming in."""
+    x, dy, dh, w = (_bf16(torch, s, 1.0, i) for i, s in enumerate(((rows, cols),) * 3 + ((cols,),)))
+    rstd = nv.rmsnorm(x, w, rstd=True)["rstd"]
+    for _ in range(warm + 1):
+        nv.rmsnorm_backward(dy, x, w, rstd, dh)
+
+
+def _route(nv, torch, tokens, experts, warm):
+    """Softmax routing to four experts, renormalised."""
+    logits = _bf16(torch, (tokens, experts), 1.5, 0).float()
+    for _ in range(warm + 1):
+        nv.route(logits, min(4, experts))
+
+
+def _weighted_combine(nv, torch, tokens, hidden, warm):
+    """The weighted sum of four bf16 rows per token, in random order."""
+    rows = _bf16(torch, (4 * tokens, hidden), 1.0, 0)
+    slot = torch.randperm(4 * tokens, device="cuda").to(torch.int32).reshape(tokens, 4)
+    w = torch.full((tokens, 4), 0.25, device="cuda")
+    for _ in range(warm + 1):
+        nv.combine(rows, slot, w)
+
+
+def _gemv(nv, torch, rows, N, K, warm):
+    """A few bf16 rows times an NVFP4 matrix."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    w = nv.NVFP4Tensor(torch.randint(0, 256, (N, K // 2), generator=g, **u8),
+                       torch.randint(0x30, 0x40, (nv.nvfp4_sf_mma_bytes(N, K),), generator=g, **u8),
+                       torch.ones(1, device="cuda"), N, K, nv.NVFP4_SF_MMA)
+    x = _bf16(torch, (rows, K), 1.0, 0)
+    for _ in range(warm + 1):
+        nv.gemv(x, w)
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["gemm", "mxfp8-gemm", "grouped-gemm", "quant-grad", "quant-act",
-                                         "quant-weight", "mxfp4", "dispatch", "combine"])
+                                         "quant-weight", "mxfp4", "dispatch", "combine", "norm",
+                                         "norm-backward", "route", "weighted-combine", "gemv"])
     ap.add_argument("dims", type=int, nargs="+")
     ap.add_argument("--warm", type=int, default=3)
     args = ap.parse_args(argv)
@@ -200,6 +256,12 @@ def main(argv=None) -> int:
         ws = _dispatch(nv, torch, *args.dims[:2], args.warm)
     elif args.case == "combine":
         ws = _combine(nv, torch, *args.dims[:2], args.warm)
+    elif args.case == "gemv":
+        ws = _gemv(nv, torch, *args.dims[:3], args.warm)
+    elif args.case in ("norm", "norm-backward", "route", "weighted-combine"):
+        case = {"norm": _norm, "norm-backward": _norm_backward, "route": _route,
+                "weighted-combine": _weighted_combine}[args.case]
+        ws = case(nv, torch, *args.dims[:2], args.warm)
     else:
         ws = _mxfp4(nv, torch, *args.dims[:2], args.warm)
     torch.cuda.synchronize()
