@@ -29,6 +29,8 @@
  *    are written to a status word in the workspace, which every call that is
  *    given a workspace clears first; nvfp4_workspace_status() synchronises the
  *    stream and returns the word of the last call that used that workspace.
+ *  - A workspace serves one call at a time: calls that may overlap on the GPU
+ *    (other streams, other captured graphs) take one each.
  *  - Matrices are row-major.  "Rowwise" quantisation blocks 16 consecutive
  *    elements along a row; "columnwise" quantises the transpose, so its codes
  *    are [cols, rows/2] and its 16-blocks run down a column of the input.

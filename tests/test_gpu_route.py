@@ -47,8 +47,8 @@ def check(l, bf16, top_k, softmax=True, bias=None, groups=1, topk_groups=1, grou
     return r, x, ids
 
 
-SHAPES = [(1, 1, 1), (1, 8, 8), (2, 5, 3), (31, 33, 4), (127, 64, 4), (128, 64, 4), (129, 64, 4), (300, 60, 6),
-          (515, 256, 8), (257, 160, 32), (40, 300, 7), (140, 512, 12)]
+SHAPES = [(1, 1, 1), (1, 8, 8), (2, 5, 3), (16, 64, 4), (17, 64, 4), (31, 33, 4), (127, 64, 4), (128, 64, 4), (129, 64, 4), (300, 60, 6),
+          (515, 256, 8), (1185, 24, 3), (257, 160, 32), (40, 300, 7), (140, 512, 12)]
 
 
 @pytest.mark.parametrize("tokens,experts,top_k", SHAPES)
