@@ -469,13 +469,15 @@ size_t nvfp4_route_workspace_size(int64_t tokens, int experts);
  *   logits [tokens, ld] of logits_dtype; s = softmax or sigmoid of a token's
  *   logits.  The top_k experts are chosen by s + bias (bias [experts] FP32 or
  *   NULL, it steers the choice only) among the topk_groups groups whose
- *   group_top best s + bias sum highest; ties go to the lower index, and the
- *   comparison is that of the exact scores.  weight = scale * s, divided by the
- *   sum of the chosen s with renormalize.
+ *   group_top best s + bias sum highest; ties go to the lower index.  Without
+ *   bias and groups the logits themselves are compared; otherwise scores are
+ *   told apart as far as FP64 does.  weight = scale * s, divided by the sum of
+ *   the chosen s with renormalize.
  * A logit at or below bf16's lowest finite value (-3.3895e38; FP32's lowest and
  * -inf among them) masks its expert.  Where fewer than top_k experts are left,
- * the remaining slots have expert -1, weight 0 and row -1.  A NaN logit ranks
- * last.
+ * the remaining slots have expert -1, weight 0 and row -1.  A NaN ranks last: the
+ * logit where logits are compared, the score otherwise (a NaN logit makes all of
+ * a token's softmax scores NaN).
  * Outputs: expert, weight [tokens, top_k], by falling rank; group_offsets
  * [experts + 1]; row_index [tokens * top_k]: the token of each routed row, rows
  * in expert order and by (token, slot) within an expert, -1 behind the last row

@@ -180,14 +180,15 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             // value.  Sigmoid: that times 1 - s, and the sum's and quotient's roundings.
             // Softmax: that and the argument's rounding for the term; in the total the
             // terms' errors are weighted by the scores, whose mean |x| is at most ln 512,
-            // and 25 additions follow one another: 2^-18.6; then two products.  Both: the
-            // bias's addition.
+            // and 21 additions follow one another: 2^-18.4; then a quotient and a product.
+            // Both: the bias's addition, and numbers below the smallest normal one, which
+            // may come out as zero.
             err[i] = 0.0f;
             if (F32) {
                 const float sf = static_cast<float>(s[i]);
                 const float rel = a.softmax ? 0x1p-18f + fabsf(static_cast<float>(l[i] - top)) * 0x1p-22f
                                             : 0x1p-21f + (1.0f - sf) * (1.0f + fabsf(l[i])) * 0x1p-22f;
-                err[i] = sf * rel + fabsf(static_cast<float>(v)) * 0x1p-23f;
+                err[i] = sf * rel + fabsf(static_cast<float>(v)) * 0x1p-23f + 0x1p-125f;
             }
         }
     }

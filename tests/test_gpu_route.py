@@ -151,6 +151,17 @@ def test_far_negative_logits_keep_their_ratio():
     check(l, False, 4, True)
 
 
+@pytest.mark.parametrize("softmax", [True, False])
+def test_scores_near_the_smallest_numbers(softmax):
+    """Groups ranked by scores that FP32 flushes to zero, or almost."""
+    rng = np.random.default_rng(24)
+    l = np.full((60, 16), -87.0, dtype=np.float32) - np.float32(4.0) * rng.random((60, 16)).astype(np.float32)
+    if softmax:
+        l[:, 5] = 0.0
+    check(l, False, 4, softmax, groups=4, topk_groups=2)
+    check(l, False, 4, softmax, groups=4, topk_groups=2, group_top=1)
+
+
 def gradients(x, l, r, ids, softmax, renorm, scale, bf16):
     import torch
     import nvfp4_bit_precision_b200 as nv
