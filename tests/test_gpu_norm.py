@@ -120,6 +120,25 @@ def test_amax_skips_the_quantisers_pass():
         np.testing.assert_array_equal(host(a), host(b))
 
 
+def test_sums_of_any_bit_patterns():
+    """h is the FP32 sum rounded to bf16 for any finite numbers: every exponent, subnormals, overflow, signed zeros,
+    addends of one size, 2^-7 to 2^-18 apart, and of any."""
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(16)
+    x = rng.integers(0, 1 << 16, (512, 4096)).astype(np.uint16)
+    r = rng.integers(0, 1 << 16, (512, 4096)).astype(np.uint16)
+    x[:, :256] &= 0x80FF                                             # subnormals and the smallest normal numbers
+    r[:, :256] &= 0x80FF
+    far = (x[:, 256:2048].astype(np.int32) & 0x7F80) - (rng.integers(0, 19, (512, 1792)) << 7)
+    r[:, 256:2048] = (r[:, 256:2048] & 0x807F) | np.maximum(far, 0).astype(np.uint16)
+    for b in (x, r):
+        b[(b & 0x7F80) == 0x7F80] &= 0x807F                          # no infinities and NaN
+    h = host(nv.rmsnorm(to_dev(x), to_dev(bits(rng, 4096)), to_dev(r))["h"])
+    with np.errstate(over="ignore"):
+        want = W.f32_to_bf16_bits(W.bf16_bits_to_f32(x) + W.bf16_bits_to_f32(r))
+    np.testing.assert_array_equal(h, want)
+
+
 def test_extremes():
     """Rows of zeros, of one value, of subnormals and of large values; NaN and inf stay in their rows."""
     import torch
