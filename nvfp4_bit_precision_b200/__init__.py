@@ -324,6 +324,7 @@ def nvfp4_grouped_gemv(G, group_offsets, total_rows, x, ldx, src_rows, row_index
            "nvfp4_grouped_gemv")
 
 
+@functools.lru_cache(maxsize=1024)
 def nvfp4_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
     return int(_lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols))
 
@@ -726,13 +727,18 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, work
     _flat("rmsnorm_backward: weight", weight, weight.dtype, cols)
     _flat("rmsnorm_backward: rstd", rstd, torch.float32, rows)
     dx = _matrix(dev, torch.bfloat16, rows, cols)
-    dw = ws = None
+    dw = wp = dwp = None
+    nb = 0
     if dweight:
         dw = torch.empty_like(weight)
-        ws = workspace if workspace is not None else _workspace(
-            dev, nvfp4_rmsnorm_backward_workspace_size(rows, cols))
-    nvfp4_rmsnorm_backward(dy, ldy, h, ldh, dh, lddh, weight, wdt, rstd, rows, cols, dx, cols, dw, ws,
-                           ws.numel() if ws is not None else 0)
+        if workspace is None:
+            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_size(rows, cols), dtype=torch.uint8,
+                                    device=dev)
+        dwp, wp, nb = dw.data_ptr(), workspace.data_ptr(), workspace.numel()
+    _check(_lib.nvfp4_rmsnorm_backward(dy.data_ptr(), ldy, h.data_ptr(), ldh,
+                                       dh.data_ptr() if dh is not None else None, lddh, weight.data_ptr(), wdt,
+                                       rstd.data_ptr(), rows, cols, dx.data_ptr(), cols, dwp, wp, nb,
+                                       _raw_stream(dev)), "nvfp4_rmsnorm_backward")
     return dx, dw
 
 
@@ -773,7 +779,7 @@ def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: 
     if workspace is None:
         n = nvfp4_route_workspace_size(tokens, experts)
         if n > 256:
-            workspace = _workspace(dev, n)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     if workspace is not None:
         wp, n = workspace.data_ptr(), workspace.numel()
     _check(_lib.nvfp4_route(logits.data_ptr(), dt, ld, bias.data_ptr() if bias is not None else None, tokens,
@@ -795,7 +801,9 @@ def route_backward(dweight, logits, routing: Routing, *, stream=None):
     _flat("route_backward: dweight", dweight, torch.float32, tokens, k)
     _flat("route_backward: expert", routing.expert, torch.int32, tokens, k)
     d = _matrix(dev, logits.dtype, tokens, experts)
-    nvfp4_route_backward(dweight, logits, dt, ld, routing.expert, tokens, experts, routing.params, d, experts)
+    _check(_lib.nvfp4_route_backward(dweight.data_ptr(), logits.data_ptr(), dt, ld, routing.expert.data_ptr(),
+                                     tokens, experts, ctypes.byref(routing.params), d.data_ptr(), experts,
+                                     _raw_stream(dev)), "nvfp4_route_backward")
     return d
 
 
@@ -849,8 +857,12 @@ def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, worksp
         used = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
     drows = torch.empty_like(rows) if used is not None else torch.zeros_like(rows)
     dweight = _matrix(dev, torch.float32, tokens, k)
-    nvfp4_combine_backward(dout, rows, dt, n, cols, slot_row, weight, tokens, k, used, drows, dweight, workspace,
-                           workspace.numel() if workspace is not None else 0)
+    wp, nb = None, 0
+    if workspace is not None:
+        wp, nb = workspace.data_ptr(), workspace.numel()
+    _check(_lib.nvfp4_combine_backward(dout.data_ptr(), rows.data_ptr(), dt, n, cols, slot_row.data_ptr(),
+                                       weight.data_ptr(), tokens, k, used, drows.data_ptr(), dweight.data_ptr(),
+                                       wp, nb, _raw_stream(dev)), "nvfp4_combine_backward")
     return drows, dweight
 
 
