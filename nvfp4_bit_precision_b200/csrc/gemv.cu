@@ -17,10 +17,10 @@
 //
 // What bounds it.  Bytes, with what comes before the first of them: a plain read of
 // as many bytes takes 12.1 us (59 MB) and 20.6 us (133 MB) a launch here.  One row x
-// 20480 x 5120 (59 MB) 16.2 us; 32 tokens' rows through four experts of 4096 x 1536
-// each (about 43 experts, 150 MB) 37 us; eight tokens' through 1536 x 4096 (60 MB)
-// 22 us, of which 4 us pass before the routing has been read and the first weights
-// are asked for.  13 rows x 4096 x 4096: 12.5 us, 6 of them bringing the rows into
+// 20480 x 5120 (59 MB) 15.6 us; 32 tokens' rows through four experts of 4096 x 1536
+// each (about 43 experts, 150 MB) 36 us; eight tokens' through 1536 x 4096 (60 MB)
+// 21 us, of which 3 us pass before the routing has been read and the first weights
+// are asked for.  13 rows x 4096 x 4096: 12 us, 6 of them bringing the rows into
 // each SM's shared memory.  Steps on the way, at the one row: warps of 64 matrix
 // rows loading into registers 24.9 us; a copy ring and 16-row tiles in equal runs
 // 18.1 us; the first weights asked for behind x instead of before it, and no group
@@ -42,7 +42,7 @@ constexpr int kStageBytes = 2048 + 256;  // a 16-row tile's codes and scales
 constexpr int kRedStride = 20;           // floats per token of a tile's sums (16 rows, off the banks)
 constexpr int kMaxGemvGroups = 256;
 constexpr int kMaxSegments = 16;         // segments whose x rows are in shared memory together
-constexpr size_t kGemvSmem = 216 * 1024;  // dynamic; 11 KB more are not, of 227 KB in all
+constexpr size_t kGemvSmem = 216 * 1024;  // dynamic; 11.2 KB more are not, of 227 KB in all
 
 // Steps in a warp's ring, all but one copied ahead.
 __host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? 3 : 2; }
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ int s_first[kMaxGemvGroups], s_rows[kMaxGemvGroups], s_end[kMaxGemvGroups];
     __shared__ int16_t s_group[kMaxGemvGroups];
+    __shared__ int2 s_count[kGemvWarps];
     __shared__ int s_seg_e[kMaxSegments], s_seg_row[kMaxSegments], s_seg_n[kMaxSegments], s_seg_x[kMaxSegments + 1];
     __shared__ int s_run[4];  // this CTA's tiles [0, 1) of the list, segments in shared memory, tile of the first one
     __shared__ uint4 s_zero[4];
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
 
     wait_for_previous_kernel();
     let_next_kernel_start();
-    int active = 0;  // (warp 0) groups that have rows
+    int active = 0;  // groups that have rows
     const bool one = !a.group_offsets && a.rows <= a.seg_rows;  // one matrix, one segment
     if (one) {
         const int rows = static_cast<int>(a.rows), xr = threadIdx.x;
@@ -220,53 +221,48 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             s_seg_e[0] = s_seg_row[0] = s_seg_x[0] = 0;
             s_seg_n[0] = s_seg_x[1] = rows;
         }
-    } else if (warp == 0) {
-        // those groups in order, with the segments up to and with each
-        int before = 0;
-        const int rows = static_cast<int>(a.rows);
-        if (!a.group_offsets) {
-            active = 1;
-            before = a.by_seg_rows(rows - 1) + 1;
-            if (lane == 0) s_group[0] = 0, s_first[0] = 0, s_rows[0] = rows, s_end[0] = before;
-        } else {
-            int lo = lane < a.groups ? a.group_offsets[lane] : 0;
-            const int last = a.group_offsets[a.groups];
-#pragma unroll 1
-            for (int e0 = 0; e0 < a.groups; e0 += 32) {
-                const int e = e0 + lane;
-                const int next = e + 32 < a.groups ? a.group_offsets[e + 32] : last;  // in flight over this turn
-                int hi = __shfl_down_sync(0xffffffffu, lo, 1);
-                const int beyond = __shfl_sync(0xffffffffu, next, 0);
-                if (lane == 31) hi = beyond;
-                if (e + 1 == a.groups) hi = last;
-                const int first = min(max(lo, 0), rows), count = e < a.groups ? min(hi, rows) - first : 0;
-                const unsigned has = __ballot_sync(0xffffffffu, count > 0);
-                int segs = count > 0 ? a.by_seg_rows(count - 1) + 1 : 0;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, segs, d);
-                    if (lane >= d) segs += v;
-                }
-                if (count > 0) {
-                    const int at = active + __popc(has & ((1u << lane) - 1));
-                    s_group[at] = static_cast<int16_t>(e);
-                    s_first[at] = first;
-                    s_rows[at] = count;
-                    s_end[at] = before + segs;
-                }
-                active += __popc(has);
-                before += __shfl_sync(0xffffffffu, segs, 31);
-                lo = next;
-            }
+    } else {
+        // those groups in order, with the segments up to and with each: thread e looks
+        // at group e, its warp counts, and the warps' counts are added up
+        static_assert(kMaxGemvGroups <= 32 * kGemvWarps, "a thread for each group");
+        const int rows = static_cast<int>(a.rows), e = threadIdx.x;
+        int lo = 0, hi = 0;
+        if (a.group_offsets) {
+            if (e < a.groups) lo = a.group_offsets[e], hi = a.group_offsets[e + 1];
+        } else if (e == 0) {
+            hi = rows;
         }
-        const int all = before * tiles, b = blockIdx.x, each = a.by_grid(all), more = all - each * static_cast<int>(gridDim.x);
-        if (lane == 0) {
+        const int first = min(max(lo, 0), rows), count = min(hi, rows) - first;
+        const unsigned has = __ballot_sync(0xffffffffu, count > 0);
+        int upto = count > 0 ? a.by_seg_rows(count - 1) + 1 : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (lane == 31) s_count[warp] = make_int2(upto, __popc(has));
+        if (e < 4) s_zero[e] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        int at = __popc(has & ((1u << lane) - 1)), all = 0;
+#pragma unroll
+        for (int w = 0; w < kMaxGemvGroups / 32; ++w) {
+            const int2 n = s_count[w];
+            if (w < warp) upto += n.x, at += n.y;
+            all += n.x, active += n.y;
+        }
+        if (count > 0) {
+            s_group[at] = static_cast<int16_t>(e);
+            s_first[at] = first;
+            s_rows[at] = count;
+            s_end[at] = upto;
+        }
+        if (e == 0) {
+            all *= tiles;
+            const int b = blockIdx.x, each = a.by_grid(all), more = all - each * static_cast<int>(gridDim.x);
             s_run[0] = b * each + min(b, more);
             s_run[1] = s_run[0] + each + (b < more ? 1 : 0);
         }
-        __syncwarp();
-    } else if (warp == 1 && lane < 4) {
-        s_zero[lane] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
     }
 #pragma unroll 1
     for (int f0 = -1;;) {
