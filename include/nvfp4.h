@@ -543,8 +543,8 @@ nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void* rows, int
  * x [rows, ldx] bf16, not quantised; q [N, K/2], sf and g as nvfp4_gemm's B
  * (NVFP4_SF_MMA layout).  Sums are FP32, in a fixed order.  D [rows, ldd] FP32 or
  * bf16 (RNE).  Any number of rows; meant for up to about 32: the matrix is read
- * again for every 8 or 16 rows, and for fewer where K is long (shared memory holds
- * 45056 x values).  N a multiple of 16, K of 64 and at most 45056, ldx >= K of 8;
+ * again for every 8 or 16 rows, and for fewer where K is long and that costs less
+ * than going over x in parts.  N a multiple of 16, K of 64 and at most 45056, ldx >= K of 8;
  * rows * N * K below about 2^43 (NVFP4_ERR_SHAPE); x, q, sf 16-byte aligned.
  */
 nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t ldx, int64_t rows, const uint8_t* q,

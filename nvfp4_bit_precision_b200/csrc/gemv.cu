@@ -20,8 +20,9 @@
 // 20480 x 5120 (59 MB) 15.6 us; 32 tokens' rows through four experts of 4096 x 1536
 // each (about 43 experts, 150 MB) 36 us; eight tokens' through 1536 x 4096 (60 MB)
 // 21 us, of which 3 us pass before the routing has been read and the first weights
-// are asked for.  13 rows x 4096 x 4096: 12 us, 6 of them bringing the rows into
-// each SM's shared memory.  Steps on the way, at the one row: warps of 64 matrix
+// are asked for.  At more rows it is bringing x into each SM's shared memory, a row
+// about as dear as a 16-row tile: 13 rows x 4096 x 4096 11 us, 32 rows x 5120 x 20480
+// 75 us.  Steps on the way, at the one row: warps of 64 matrix
 // rows loading into registers 24.9 us; a copy ring and 16-row tiles in equal runs
 // 18.1 us; the first weights asked for behind x instead of before it, and no group
 // scan for a single matrix, 15.7 us.  Decoding by shifts and masks into bf16 (15
@@ -47,10 +48,20 @@ constexpr size_t kGemvSmem = 216 * 1024;  // dynamic; 11.2 KB more are not, of 2
 // Steps in a warp's ring, all but one copied ahead.
 __host__ __device__ constexpr int ring_stages(int nt) { return nt == 1 ? 3 : 2; }
 
-// Most (x row, step) pairs in shared memory, 512 bytes each.
-__host__ __device__ constexpr int max_x_pairs(int nt)
+// Bytes of the rings and of the tiles' sums that warps hand on.
+__host__ __device__ constexpr size_t gemv_fixed(int nt)
 {
-    return static_cast<int>((kGemvSmem - kGemvWarps * (ring_stages(nt) * kStageBytes + 2 * 4 * 8 * nt * kRedStride)) / 512);
+    return kGemvWarps * (ring_stages(nt) * kStageBytes + 2 * sizeof(float) * 8 * nt * kRedStride);
+}
+
+// Tiles whose sums over several panels a CTA keeps, and the bytes of one.
+constexpr int kPanelTiles = 24;
+__host__ __device__ constexpr size_t tile_sum_bytes(int nt) { return sizeof(float) * 16 * 8 * nt; }
+
+// Most (x row, step) pairs in shared memory, 512 bytes each.
+__host__ __device__ constexpr int max_x_pairs(int nt, bool panels)
+{
+    return static_cast<int>((kGemvSmem - gemv_fixed(nt) - (panels ? kPanelTiles * tile_sum_bytes(nt) : 0)) / 512);
 }
 
 // Division of 0 <= n < 2^31 by a number known on the host.  With 2^s >= d and
@@ -90,8 +101,10 @@ struct GemvArgs {
     int seg_rows;                  // most x rows of a segment
     int whole;                     // no tile or step reaches past the matrix
     int x_rows;                    // x rows that shared memory holds
-    Divisor by_tiles, by_steps, by_seg_rows, by_grid;
-    int each, more;                // one matrix's tiles over the CTAs: each, and one more for the first CTAs
+    int panel_steps;               // steps of x in shared memory at a time: all, or a panel of them
+    Divisor by_tiles, by_steps, by_seg_rows;
+    Divisor by_grid;               // CTAs; of one matrix those of a segment
+    int each, more;                // one matrix's tiles over them: each, and one more for the first CTAs
     void* out;
     int out_f32;
     int64_t ldd;
@@ -174,7 +187,10 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at)
 // a code word's pairs go in as they lie.  Each warp copies its steps into a ring
 // of its own, some steps ahead and into the next tile too, in whole 64-byte runs
 // of a row, and waits for no other warp.
-template <int NT>
+//
+// With PANELS (one matrix), x comes in panels of columns: the CTA goes over at most
+// kPanelTiles tiles panel by panel and keeps their sums in shared memory.
+template <int NT, bool PANELS>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs a)
 {
     constexpr int kStages = ring_stages(NT);
@@ -200,25 +216,28 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     float* const s_sums = reinterpret_cast<float*>(s_dyn + kGemvWarps * kStages * kStageBytes);  // [2][warps][kRed]
     float* const my_head = s_sums + warp * kRed;                        // sums of a tile that an earlier warp began
     float* const my_sums = s_sums + (kGemvWarps + warp) * kRed;         // sums of a tile that this one began
-    uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_sums + 2 * kGemvWarps * kRed);
+    float* const s_acc = s_sums + 2 * kGemvWarps * kRed;  // with panels: [kPanelTiles][8 NT][16]
+    uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_acc) + (PANELS ? kPanelTiles * tile_sum_bytes(NT) : 0);
+    const int panel_steps = PANELS ? a.panel_steps : steps;
 
     wait_for_previous_kernel();
     let_next_kernel_start();
     int active = 0;  // groups that have rows
-    const bool one = !a.group_offsets && a.rows <= a.seg_rows;  // one matrix, one segment
+    const bool one = !a.group_offsets;  // one matrix: a CTA has tiles of one segment
     if (one) {
-        const int rows = static_cast<int>(a.rows), xr = threadIdx.x;
+        const int part = a.by_grid(blockIdx.x), b = blockIdx.x - part * a.by_grid.d, first = part * a.seg_rows;
+        const int rows = min(a.seg_rows, static_cast<int>(a.rows) - first), xr = threadIdx.x;
         if (xr < rows) {
-            s_x_row[xr] = make_int4(xr, xr * 64, rows * 64, 0);
+            s_x_row[xr] = make_int4(first + xr, xr * 64, rows * 64, 0);
             s_top[xr] = 0;
         }
         if (xr < 4) s_zero[xr] = make_uint4(0, 0, 0, 0);
         if (xr == 0) {
-            const int b = blockIdx.x;
             s_run[0] = s_run[3] = b * a.each + min(b, a.more);
             s_run[1] = s_run[0] + a.each + (b < a.more ? 1 : 0);
             s_run[2] = 1;
-            s_seg_e[0] = s_seg_row[0] = s_seg_x[0] = 0;
+            s_seg_e[0] = s_seg_x[0] = 0;
+            s_seg_row[0] = first;
             s_seg_n[0] = s_seg_x[1] = rows;
         }
     } else {
@@ -227,11 +246,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         static_assert(kMaxGemvGroups <= 32 * kGemvWarps, "a thread for each group");
         const int rows = static_cast<int>(a.rows), e = threadIdx.x;
         int lo = 0, hi = 0;
-        if (a.group_offsets) {
-            if (e < a.groups) lo = a.group_offsets[e], hi = a.group_offsets[e + 1];
-        } else if (e == 0) {
-            hi = rows;
-        }
+        if (e < a.groups) lo = a.group_offsets[e], hi = a.group_offsets[e + 1];
         const int first = min(max(lo, 0), rows), count = min(hi, rows) - first;
         const unsigned has = __ballot_sync(0xffffffffu, count > 0);
         int upto = count > 0 ? a.by_seg_rows(count - 1) + 1 : 0;
@@ -314,15 +329,20 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         }
         __syncthreads();
         if (f0 < 0) f0 = s_run[0];
-        const int segs = s_run[2], f1 = s_run[1], tile0 = s_run[3];
+        // (with PANELS `one` holds; without the test here the loop over the steps came out a
+        // sixth slower: 32 rows x 5120 x 20480 87 us against 75)
+        const int segs = s_run[2], f1 = s_run[1], tile0 = PANELS && one ? f0 : s_run[3];
         if (f0 >= f1) return;
-        const int fe = min(f1, f0 - tile0 + segs * tiles);
+        const int fe = min(min(f1, f0 - tile0 + segs * tiles), PANELS ? f0 + kPanelTiles : f1);
 
+#pragma unroll 1
+        for (int p0 = 0;;) {
+        const int psteps = PANELS ? min(panel_steps, steps - p0) : steps;
         // this warp's run of steps: items [j0, j1) of the (fe - f0) tiles' steps
-        const int items = (fe - f0) * steps;
+        const int items = (fe - f0) * psteps;
         const auto run_start = [&](int w) { return (items / kGemvWarps) * w + min(w, items % kGemvWarps); };
         const int j0 = run_start(warp), j1 = run_start(warp + 1);
-        const int skip = a.by_steps(j0), first_step = j0 - skip * steps;
+        const int skip = psteps == panel_steps ? a.by_steps(j0) : j0 / psteps, first_step = j0 - skip * psteps;
         int seg = 0, tile = tile0 + skip;
         while (tile >= tiles) tile -= tiles, ++seg;
 
@@ -348,9 +368,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             rows_there();
         };
         const auto at_step = [&]() {
-            pq = tq + pc * (kStep / 2);
+            pq = tq + (p0 + pc) * (kStep / 2);
             pq8 = pq + 64 * row_bytes;  // from row m to row m + 8: i + 2
-            ps = ts + static_cast<int64_t>(pc) * 2048;
+            ps = ts + static_cast<int64_t>(p0 + pc) * 2048;
         };
         if (left > 0) {
             aim();
@@ -367,20 +387,20 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     copy16_async(dst + 1088, pq8 + 64);
                     if (lane < 16) copy16_async(dst_sc, ps);
                 } else {
-                    const int k = pc * kStep + 32 * t;
+                    const int k = (p0 + pc) * kStep + 32 * t;
                     const bool in0 = k < a.k, in1 = k + 128 < a.k;
                     copy16_async(dst, in0 && have0 ? pq : a.q, in0 && have0);
                     copy16_async(dst + 64, in1 && have0 ? pq + 64 : a.q, in1 && have0);
                     copy16_async(dst + 1024, in0 && have8 ? pq8 : a.q, in0 && have8);
                     copy16_async(dst + 1088, in1 && have8 ? pq8 + 64 : a.q, in1 && have8);
-                    const bool in = pc * kStep + 64 * ((lane & 15) >> 2) < a.k;
+                    const bool in = (p0 + pc) * kStep + 64 * ((lane & 15) >> 2) < a.k;
                     if (lane < 16) copy16_async(dst_sc, in ? ps : a.sf, in);
                 }
                 --left;
                 pq += kStep / 2;
                 pq8 += kStep / 2;
                 ps += 2048;
-                if (++pc == steps && left > 0) {
+                if (++pc == psteps && left > 0) {
                     pc = 0;
                     if (++ptile == tiles) {
                         ptile = 0, ++pseg;
@@ -408,7 +428,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         if (static_cast<int>(threadIdx.x) < x_rows) g = a.g[s_x_row[threadIdx.x].w];
         const auto next = [&](int& xr, int& c) {
             c += kGemvWarps;
-            while (c >= steps) c -= steps, ++xr;
+            while (c >= psteps) c -= psteps, ++xr;
         };
         {
             constexpr int kAhead = 4 * NT;  // loads in flight together
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     const int4 row = s_x_row[min(xr, x_rows - 1)];
-                    const int k = c * kStep + 64 * t + 8 * r;
+                    const int k = (p0 + c) * kStep + 64 * t + 8 * r;
                     v[i] = make_uint4(0, 0, 0, 0);
                     if (xr < x_rows && row.x >= 0 && k < a.k) v[i] = *reinterpret_cast<const uint4*>(a.x + row.x * a.ldx + k);
                     at[i] = row.y + (c * 8 + r) * row.z + t * 16;
@@ -474,6 +494,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         if (j0 == j1)  // an empty run adds nothing to the tile that goes past it
             for (int i = lane; i < kRed; i += 32) my_head[i] = 0.0f;
         __syncthreads();
+        if (PANELS && static_cast<int>(threadIdx.x) < x_rows) s_top[threadIdx.x] = 0;  // for the next panel
 
         int slot = 0, c = first_step;
         bool begun = first_step == 0, open = false;  // the tile was begun by this warp; its run ends inside it
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             for (int b = 0; b < NT; ++b) {
                 const bool is = 8 * b + r < n;
                 xstep[b] = is ? n * 64 : 0;
-                x0[b] = is ? smem_addr(s_x) + first * steps * 512 + (8 * b + r) * 64 + t * 16 : smem_addr(s_zero + t);
+                x0[b] = is ? smem_addr(s_x) + first * panel_steps * 512 + (8 * b + r) * 64 + t * 16 : smem_addr(s_zero + t);
                 xp[b] = x0[b] + c * 8 * xstep[b];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -507,6 +528,14 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // may leave few bits to a product of both factors)
         const auto store = [&](int tok, int m, float v, float2 by) {
             v = v * by.x * by.y;
+            if (PANELS) {
+                float* const sum = s_acc + ((tile - tile0) * 8 * NT + tok) * 16 + m;
+                if (p0 > 0) v += *sum;
+                if (p0 + psteps < steps) {
+                    *sum = v;
+                    return;
+                }
+            }
             const int64_t n = static_cast<int64_t>(tile >> 3) * 128 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
             if (n >= a.n) return;
             const int64_t at = (row0 + tok) * a.ldd + n;
@@ -560,10 +589,10 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[b][i] += part[0][b][i] + part[1][b][i];
-            if (++c < steps && j + 1 < j1) continue;
+            if (++c < psteps && j + 1 < j1) continue;
             // the tile or the run ends: columns 2 t and 2 t + 1 of the sums are tokens
             // 8 b + 2 t, 8 b + 2 t + 1
-            open = begun && c < steps;
+            open = begun && c < psteps;
             if (begun && !open) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
@@ -598,7 +627,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
         if (open) {  // this warp's sums and those of the warps that went on with the tile
-            const int end = j1 - c + steps;  // the item behind the tile's last
+            const int end = j1 - c + psteps;  // the item behind the tile's last
             int others = 0;
             while (run_start(warp + others + 1) < end) ++others;
             for (int o = lane; o < 16 * s_seg_n[seg]; o += 32) {
@@ -608,38 +637,72 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 store(o >> 4, o & 15, v, s_scale[s_seg_x[seg] + (o >> 4)]);
             }
         }
-        if (fe == f1) return;
-        __syncthreads();  // the next segments' rows take the place of these
+        if (fe == f1 && (!PANELS || p0 + psteps == steps)) return;
+        __syncthreads();  // the next panel or the next segments' rows take the place of these
+        if (!PANELS || (p0 += psteps) == steps) break;
+        }
         f0 = fe;
     }
 }
 
-template <int NT>
-nvfp4_status start_gemv(GemvArgs a, int sms, cudaStream_t st)
+// One matrix: even segments of at most `fit` rows, each with as many CTAs.  Bringing a
+// row of x costs a CTA about as much as a tile, so a CTA has tiles of one segment
+// alone, and `cost`, its tiles and rows, is what a form's time goes by.  5120 x 20480 at
+// 17 rows: 59 us so, 100 us with the tiles of all segments in equal runs; 512 x 20480 at
+// 8 rows, 4 segments: 13 us, 27 us with a CTA for each tile of one segment.
+struct Plan {
+    int seg_rows = 1, ctas = 1;
+    int64_t cost = INT64_MAX;
+    Plan() = default;
+    Plan(int64_t rows, int64_t tiles, int64_t fit, int sms)
+    {
+        const int64_t segments = (rows + fit - 1) / fit;
+        seg_rows = static_cast<int>((rows + segments - 1) / segments);
+        for (int wave = 1; wave <= 4; ++wave) {
+            const int64_t n = std::min(tiles, wave * sms / segments);
+            const int64_t c = n ? wave * ((tiles + n - 1) / n + seg_rows) : INT64_MAX;
+            if (c < cost) cost = c, ctas = static_cast<int>(n);
+        }
+    }
+};
+
+template <int NT, bool PANELS>
+nvfp4_status start_gemv(GemvArgs a, const Plan& plan, int sms, cudaStream_t st)
 {
-    constexpr size_t fixed = kGemvWarps * (ring_stages(NT) * kStageBytes + 2 * sizeof(float) * 8 * NT * kRedStride);
-    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
-    if (steps > max_x_pairs(NT)) return NVFP4_ERR_SHAPE;                      // one row does not fit
-    if (a.rows * tiles * steps > 0x7fffffffll) return NVFP4_ERR_SHAPE;        // indexes are 31-bit on the device
-    const int64_t fit = max_x_pairs(NT) / steps;
-    a.tiles = static_cast<int>(tiles), a.steps = static_cast<int>(steps);
-    a.seg_rows = static_cast<int>(std::min<int64_t>(8 * NT, fit));
-    a.x_rows = static_cast<int>(std::min<int64_t>(fit, std::min<int64_t>(a.rows, 8 * NT * kMaxSegments)));
+    const int64_t tiles = a.tiles, steps = a.steps;
+    int64_t grid;
+    if (a.group_offsets) {
+        const int64_t fit = max_x_pairs(NT, false) / steps;
+        a.seg_rows = static_cast<int>(std::min<int64_t>(8 * NT, fit));
+        a.x_rows = static_cast<int>(std::min<int64_t>(fit, std::min<int64_t>(a.rows, 8 * NT * kMaxSegments)));
+        // (no more segments than one unfinished for each group, and the full ones)
+        grid = std::min<int64_t>(sms, tiles * (std::min<int64_t>(a.groups, a.rows) + a.rows / a.seg_rows));
+        a.by_grid = Divisor(static_cast<int>(grid));
+    } else {
+        a.seg_rows = a.x_rows = plan.seg_rows;
+        grid = plan.ctas * ((a.rows + plan.seg_rows - 1) / plan.seg_rows);
+        a.by_grid = Divisor(plan.ctas);
+        a.each = a.tiles / plan.ctas, a.more = a.tiles % plan.ctas;
+    }
+    a.panel_steps = a.steps;
+    if (PANELS) {
+        const int64_t most = max_x_pairs(NT, true) / a.x_rows, count = (steps + most - 1) / most;
+        a.panel_steps = static_cast<int>((steps + count - 1) / count);
+    }
+    const size_t smem = gemv_fixed(NT) + (PANELS ? kPanelTiles * tile_sum_bytes(NT) : 0) +
+                        static_cast<size_t>(a.panel_steps) * 512 * a.x_rows;
     static bool raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!raised[dev & 63]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(gemv_kernel<NT>),
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(gemv_kernel<NT, PANELS>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvSmem)) != cudaSuccess)
             return NVFP4_ERR_CUDA;
         raised[dev & 63] = true;
     }
-    const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * std::min<int64_t>(a.groups, a.rows)));
-    a.by_tiles = Divisor(a.tiles), a.by_steps = Divisor(a.steps), a.by_seg_rows = Divisor(a.seg_rows);
-    a.by_grid = Divisor(grid);
+    a.by_tiles = Divisor(a.tiles), a.by_steps = Divisor(a.panel_steps), a.by_seg_rows = Divisor(a.seg_rows);
     a.whole = a.n % 128 == 0 && a.k % kStep == 0;
-    a.each = a.tiles / grid, a.more = a.tiles % grid;
-    if (launch_early(!a.status, gemv_kernel<NT>, grid, 32 * kGemvWarps, fixed + steps * 512 * a.x_rows, st, a) != cudaSuccess)
+    if (launch_early(!a.status, gemv_kernel<NT, PANELS>, static_cast<int>(grid), 32 * kGemvWarps, smem, st, a) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
@@ -667,17 +730,30 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
     if (a.status && cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (a.rows == 0) return NVFP4_OK;
     a.sf_bytes = static_cast<int64_t>(nvfp4_sf_mma_bytes(a.n, a.k));
-    // 16 columns of x at a time where that saves a third of the passes over a matrix
-    // (4096 x 4096: 9 rows 10.8 us against 12.8, 24 rows 16.3 against 20.7, but 16 rows,
-    // two passes either way, 16.4 against 12.6; 1 row 7.1 against 6.1)
-    const int64_t steps = (a.k + kStep - 1) / kStep, mean = (a.rows + a.groups - 1) / a.groups;
-    const auto passes = [&](int nt) {
-        const int64_t at_once = std::min<int64_t>(8 * nt, std::max<int64_t>(1, max_x_pairs(nt) / steps));
-        return (mean + at_once - 1) / at_once;
-    };
-    const bool two = 3 * passes(2) <= 2 * passes(1);
     a.out_f32 = out_dtype == NVFP4_OUT_F32;
-    return two ? start_gemv<2>(a, sms, st) : start_gemv<1>(a, sms, st);
+    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
+    if (steps > max_x_pairs(1, false)) return NVFP4_ERR_SHAPE;          // one row does not fit
+    if (a.rows * tiles * steps > 0x7fffffffll) return NVFP4_ERR_SHAPE;  // indexes are 31-bit on the device
+    a.tiles = static_cast<int>(tiles), a.steps = static_cast<int>(steps);
+    const auto at_once = [&](int nt) { return std::min<int64_t>(8 * nt, max_x_pairs(nt, false) / steps); };
+    if (a.group_offsets) {
+        // 16 columns of x at a time where that saves a third of the passes over a matrix
+        // (16 experts of 4096 x 1536: 9 rows each 24 us against 29, 32 rows 40 against 49, but
+        // 8 rows 23.5 against 21.3; of 1536 x 4096, 16 rows, two passes either way, 44 against 38)
+        const int64_t mean = (a.rows + a.groups - 1) / a.groups;
+        const auto passes = [&](int nt) { return (mean + at_once(nt) - 1) / at_once(nt); };
+        const bool two = 3 * passes(2) <= 2 * passes(1);
+        return two ? start_gemv<2, false>(a, Plan(), sms, st) : start_gemv<1, false>(a, Plan(), sms, st);
+    }
+    // The form that costs least; a tile or a row costs a twentieth more with panels, where
+    // loads wait at each panel's start, and a fifth more with 16 columns of x.  (5120 x
+    // 20480: 4 rows 31 us, with panels 34; 16 rows 85 and 57, with 16 columns 109.  2048 x
+    // 24576, 8 rows: 36 us with 16 columns, 45 with panels, 47 without either.)
+    const Plan one(a.rows, tiles, at_once(1), sms), two(a.rows, tiles, at_once(2), sms);
+    const Plan panels(a.rows, tiles, 8, sms);
+    if (20 * one.cost <= std::min(24 * two.cost, 21 * panels.cost)) return start_gemv<1, false>(a, one, sms, st);
+    if (24 * two.cost <= 21 * panels.cost) return start_gemv<2, false>(a, two, sms, st);
+    return start_gemv<1, true>(a, panels, sms, st);
 }
 
 }  // namespace

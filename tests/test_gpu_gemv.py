@@ -239,3 +239,117 @@ def test_grouped_rows_outside_groups_and_bad_indexes():
     assert bool((out[3:] == 7).all()) and bool((out[1:3] == 0).all())
     one = nv.gemv(x[2:3], nv.NVFP4Tensor(qb[0], sfb, gb, 128, 128, nv.NVFP4_SF_MMA), nv.NVFP4_OUT_F32)
     assert torch.equal(out[:1], one)
+
+
+# Rows of which not all fit go in panels of columns.  The bound above holds for them: a panel's chain of sums is
+# shorter than the whole row's by two for every 256 columns of the others, and the panels' sums add one each.
+
+@pytest.mark.parametrize("rows", [4, 8, 9, 13, 16, 17, 24, 33])
+@pytest.mark.parametrize("n,k", [(16, 45056), (272, 5888), (144, 11328), (2448, 8256)])
+def test_panels(rows, n, k):
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(rows + k)
+    q, sf, g = R.random_nvfp4(rng, n, k, extreme=True)
+    x = bits(rng, (rows, k))
+    wide = torch.full((rows + 1, n + 16), 5.0, device="cuda")
+    y = nv.gemv(to_dev(x), upload(nv, q, sf, g), nv.NVFP4_OUT_F32, wide[:rows, :n])
+    w = R.nvfp4_matrix(q, sf, g)
+    ref = val(x) @ w.T
+    assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
+    assert bool((wide[rows] == 5).all()) and bool((wide[:, n:] == 5).all())
+    half = nv.gemv(to_dev(x), upload(nv, q, sf, g), nv.NVFP4_OUT_BF16)
+    assert np.all(np.abs(f64(half) - ref) <= bound(val(x), w, ref, False))
+
+
+def test_panels_of_different_size():
+    """Columns of one panel far larger or smaller than the others', panels of zeros, small and large g."""
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(21)
+    n, k = 128, 12288
+    q, sf, _ = R.random_nvfp4(rng, n, k)
+    v = rng.standard_normal((8, k))
+    v[0, :512] *= 2.0 ** 90
+    v[1, -512:] *= 2.0 ** 90
+    v[2] *= 2.0 ** 110
+    v[3] *= 2.0 ** -100
+    v[4, 256:] = 0
+    v[5, :-256] = 0
+    v[6] = 0
+    x = W.f32_to_bf16_bits(v.astype(np.float32))
+    for g in (2.0 ** -20, 2.0 ** -3):
+        w = R.nvfp4_matrix(q, sf, np.float32(g))
+        ref = val(x) @ w.T
+        y = f64(nv.gemv(to_dev(x), upload(nv, q, sf, np.float32(g)), nv.NVFP4_OUT_F32))
+        assert np.all(np.abs(y - ref) <= bound(val(x), w, ref, True))
+        assert (y[6] == 0).all()
+
+
+def test_panels_non_finite_tokens_stay_alone():
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(22)
+    n, k = 128, 12288
+    q, sf, g = R.random_nvfp4(rng, n, k)
+    x = bits(rng, (8, k))
+    clean = f64(nv.gemv(to_dev(x), upload(nv, q, sf, g)))
+    x[1, 3], x[3, 6000], x[6, k - 1] = 0x7F80, 0x7FC0, 0xFF80
+    y = f64(nv.gemv(to_dev(x), upload(nv, q, sf, g)))
+    np.testing.assert_array_equal(y[[0, 2, 4, 5, 7]], clean[[0, 2, 4, 5, 7]])
+    assert np.isnan(y[3]).all() and not np.isfinite(y[[1, 6]]).any()
+
+
+@pytest.mark.parametrize("rows", [8, 13])
+def test_panels_more_tiles_than_sums_kept(rows):
+    """So many matrix rows that a multiprocessor goes over the panels more than once."""
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(23)
+    k, copies = 5888, 470
+    q, sf, g = R.random_nvfp4(rng, 128, k)
+    x = bits(rng, (rows, k))
+    y = f64(nv.gemv(to_dev(x), upload(nv, np.tile(q, (copies, 1)), np.tile(sf, (copies, 1)), g), nv.NVFP4_OUT_F32))
+    w = R.nvfp4_matrix(q, sf, g)
+    ref = val(x) @ w.T
+    assert np.all(np.abs(y.reshape(rows, copies, 128) - ref[:, None]) <= bound(val(x), w, ref, True)[:, None])
+
+
+@pytest.mark.parametrize("counts", [[9, 0, 17, 8], [33], [0, 40, 1, 30]])
+def test_panels_grouped(counts):
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(sum(counts))
+    G, n, k, total = len(counts), 256, 8256, sum(counts)
+    mats = [R.random_nvfp4(rng, n, k) for _ in range(G)]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    src = bits(rng, (11, k))
+    idx = rng.integers(0, 11, total + 2).astype(np.int32)
+    out = torch.full((total + 2, n), 7.0, device="cuda")
+    nv.grouped_gemv(torch.from_numpy(off).cuda(), to_dev(src), torch.from_numpy(np.stack([m[0] for m in mats])).cuda(),
+                    torch.from_numpy(np.concatenate([R.tile(m[1]).reshape(-1) for m in mats])).cuda(),
+                    torch.tensor([m[2] for m in mats], dtype=torch.float32, device="cuda"), n,
+                    torch.from_numpy(idx).cuda(), nv.NVFP4_OUT_F32, out)
+    got = f64(out)
+    assert (got[total:] == 7).all()
+    for e in range(G):
+        s = slice(off[e], off[e + 1])
+        xe, w = val(src[idx[s]]), R.nvfp4_matrix(*mats[e])
+        if len(xe):
+            ref = xe @ w.T
+            assert np.all(np.abs(got[s] - ref) <= bound(xe, w, ref, True))
+
+
+def test_panels_are_repeatable_in_a_graph():
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(24)
+    q, sf, g = R.random_nvfp4(rng, 2048, 8256)
+    x, w = to_dev(bits(rng, (8, 8256))), upload(nv, q, sf, g)
+    first = nv.gemv(x, w, nv.NVFP4_OUT_F32)
+    out = torch.empty_like(first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.gemv(x, w, nv.NVFP4_OUT_F32, out)
+    for _ in range(5):
+        out.fill_(3.0)
+        graph.replay()
+        assert torch.equal(out, first)
