@@ -739,7 +739,8 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
     if (a.group_offsets) {
         // 16 columns of x at a time where that saves a third of the passes over a matrix
         // (16 experts of 4096 x 1536: 9 rows each 24 us against 29, 32 rows 40 against 49, but
-        // 8 rows 23.5 against 21.3; of 1536 x 4096, 16 rows, two passes either way, 44 against 38)
+        // 8 rows 23.5 against 21.3; of 1536 x 4096, 16 rows, two passes either way, 44 against
+        // 38, and 9 rows, where the rule loses, 34 against 31.5)
         const int64_t mean = (a.rows + a.groups - 1) / a.groups;
         const auto passes = [&](int nt) { return (mean + at_once(nt) - 1) / at_once(nt); };
         const bool two = 3 * passes(2) <= 2 * passes(1);

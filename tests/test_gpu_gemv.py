@@ -353,3 +353,15 @@ def test_panels_are_repeatable_in_a_graph():
         out.fill_(3.0)
         graph.replay()
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("rows,n,k", [(5003, 48, 128), (1301, 16, 5888), (700, 128, 1024), (300, 1040, 320)])
+def test_more_segments_than_multiprocessors(rows, n, k):
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(rows)
+    q, sf, g = R.random_nvfp4(rng, n, k)
+    x = bits(rng, (rows, k))
+    y = nv.gemv(to_dev(x), upload(nv, q, sf, g), nv.NVFP4_OUT_F32)
+    w = R.nvfp4_matrix(q, sf, g)
+    ref = val(x) @ w.T
+    assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
