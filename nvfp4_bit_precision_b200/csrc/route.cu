@@ -88,6 +88,8 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v)
         __reduce_max_sync(kFull, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
+// Largest float of the warp, none of them NaN.
+__device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kFull, ordered(v))); }
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v)
 {
@@ -128,9 +130,17 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t ld, int6
 }
 
 // The k best experts of one token, lane j returning slot j's expert (-1: none
-// left) and its logit.  Lane i holds the EPL experts from i * EPL on.  With
-// float scores, `close` says that the choice hangs on less than the scores'
-// error bounds.
+// left) and its logit.  Lane i holds the EPL experts from i * EPL on.
+//
+// With float scores, `close` says that the choice hangs on less than the scores'
+// error bounds.  Those differ from expert to expert (a score that a bias cancels
+// has a far larger one than a small score under a small bias), so that each of the
+// chosen is compared with all that rank behind it, not with the next alone: its
+// score less its bound has to exceed their largest score plus bound.  For groups,
+// whose rank is a sum of their best scores, every member's bound is taken to be
+// the group's largest: the n-th best exact score is then within that bound of the
+// n-th best FP32 score, whichever members they belong to.  (Groups that are ranked
+// one after the other take the token's largest bound, which saves a reduction each.)
 template <typename S, int EPL>
 __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL], int lane, int& id, float& logit,
                                        bool& close)
@@ -138,7 +148,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
     using K = typename KeyOf<S>::type;
     constexpr bool F32 = sizeof(S) == 4;
     K key[EPL];
-    float err[EPL];
+    float err[EPL], largest = 0.0f;
     close = false;
     const bool by_logit = !a.bias && a.groups == 1;
     if (by_logit) {
@@ -184,13 +194,23 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             // Both: the bias's addition, and numbers below the smallest normal one, which
             // may come out as zero.
             err[i] = 0.0f;
-            if (F32) {
+            if (F32 && key[i]) {
                 const float sf = static_cast<float>(s[i]);
                 const float rel = a.softmax ? 0x1p-18f + fabsf(static_cast<float>(l[i] - top)) * 0x1p-22f
                                             : 0x1p-21f + (1.0f - sf) * (1.0f + fabsf(l[i])) * 0x1p-22f;
                 err[i] = sf * rel + fabsf(static_cast<float>(v)) * 0x1p-23f + 0x1p-125f;
             }
         }
+    }
+    if (F32 && !by_logit) {
+        // infinities and NaN have no bound: such a token is left to FP64, and all is finite below
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) most = max(most, __float_as_uint(err[i]));
+        most = warp_max(most);
+        close = most >= 0x7F800000u;
+        if (close) return;
+        largest = __uint_as_float(most);
     }
     if (a.groups > 1) {
         const int size = a.experts / a.groups;
@@ -200,41 +220,35 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             // a group is group_lanes whole lanes: each lane's two best, then merged
             // pairwise within the group's lanes
             K best = 0, second = 0;
-            float e1 = 0.0f, e2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 if (key[i] > best)
-                    second = best, e2 = e1, best = key[i], e1 = err[i];
+                    second = best, best = key[i];
                 else if (key[i] > second)
-                    second = key[i], e2 = err[i];
+                    second = key[i];
+                if (F32) mine_err = fmaxf(mine_err, err[i]);
             }
 #pragma unroll 1
             for (int d = 1; d < a.group_lanes; d <<= 1) {
                 const K ob = __shfl_xor_sync(kFull, best, d), os = __shfl_xor_sync(kFull, second, d);
-                const float o1 = __shfl_xor_sync(kFull, e1, d), o2 = __shfl_xor_sync(kFull, e2, d);
-                if (ob > best) {
-                    const bool keep = best > os;
-                    second = keep ? best : os, e2 = keep ? e1 : o2;
-                    best = ob, e1 = o1;
-                } else if (ob > second) {
-                    second = ob, e2 = o1;
-                }
+                if (F32) mine_err = fmaxf(mine_err, __shfl_xor_sync(kFull, mine_err, d));
+                second = max(max(second, os), min(best, ob));
+                best = max(best, ob);
             }
             if (best && lane % a.group_lanes == 0 && lane < a.groups * a.group_lanes) {
                 S sum = best == 1 ? static_cast<S>(NAN) : value_of(best);
-                mine_err = e1;
                 if (a.group_top == 2 && second) {
                     sum += second == 1 ? static_cast<S>(NAN) : value_of(second);
-                    mine_err += e2;
+                    mine_err *= 2.0f;
                 }
                 mine = ordered(sum);
                 mine_err += fabsf(static_cast<float>(sum)) * 0x1p-23f;
             }
         } else for (int g = 0; g < a.groups; ++g) {
             S sum = 0;
-            float sum_err = 0.0f;
             bool any = false;
             int taken = -1;
+            float sum_err = 0.0f;
             for (int n = 0; n < a.group_top; ++n) {
                 K m = 0;
 #pragma unroll
@@ -246,14 +260,13 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
                 if (best == 0) break;
                 const int src = __ffs(__ballot_sync(kFull, m == best)) - 1;
                 int at = -1;
-                float e_at = 0.0f;
 #pragma unroll
                 for (int i = EPL - 1; i >= 0; --i) {
                     const int e = lane * EPL + i;
-                    if (e >= g * size && e < (g + 1) * size && e != taken && key[i] == best) at = e, e_at = err[i];
+                    if (e >= g * size && e < (g + 1) * size && e != taken && key[i] == best) at = e;
                 }
                 taken = __shfl_sync(kFull, at, src);
-                sum_err += __shfl_sync(kFull, e_at, src);
+                sum_err += largest;
                 sum += best == 1 ? static_cast<S>(NAN) : value_of(best);
                 any = true;
             }
@@ -263,20 +276,21 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             }
         }
         unsigned kept = 0;
-        K last = 0;
-        float last_err = 0.0f;
-        for (int n = 0; n <= a.topk_groups; ++n) {
+        const K rank = mine;
+        for (int n = 0; n < a.topk_groups; ++n) {
             const K best = warp_max(mine);
             if (best == 0) break;
             const int src = __ffs(__ballot_sync(kFull, mine == best)) - 1;
-            const float e_best = __shfl_sync(kFull, mine_err, src);
-            if (n == a.topk_groups) {  // the best group left out
-                if (F32) close |= !(value_of(last) - value_of(best) > static_cast<S>(last_err + e_best));
-                break;
-            }
             kept |= 1u << src;
             if (lane == src) mine = 0;
-            last = best, last_err = e_best;
+        }
+        if (F32) {  // the kept groups' smallest value against the largest one left out
+            const float v = rank ? static_cast<float>(value_of(rank)) : 0.0f;
+            const bool in = (kept >> lane) & 1u;
+            const float least = -warp_max(in ? -__fsub_rd(v, mine_err) : -INFINITY);
+            const float most = warp_max(rank && !in ? __fadd_ru(v, mine_err) : -INFINITY);
+            close = !(least > most) && kept;
+            if (close) return;
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -286,10 +300,8 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
     }
     id = -1;
     logit = 0.0f;
-    K last = 0;
-    float last_err = 0.0f;
-    const int rounds = F32 && !by_logit ? a.top_k + 1 : a.top_k;
-    for (int j = 0; j < rounds; ++j) {
+    float score = 0.0f, bound = 0.0f;  // of slot j, lane j
+    for (int j = 0; j < a.top_k; ++j) {
         K m = key[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
@@ -309,12 +321,29 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
         const int e = src * EPL + __shfl_sync(kFull, at, src);
         const float lv = __shfl_sync(kFull, l_at, src);
         if (F32 && !by_logit) {
-            const float e_best = __shfl_sync(kFull, e_at, src);
-            if (j > 0) close |= !(value_of(last) - value_of(best) > static_cast<S>(last_err + e_best));
-            last = best, last_err = e_best;
-            if (j == a.top_k) break;
+            const float eb = __shfl_sync(kFull, e_at, src);
+            if (lane == j) score = static_cast<float>(value_of(best)), bound = eb;
         }
         if (lane == j) id = e, logit = lv;
+    }
+    if (F32 && !by_logit) {
+        // the largest score plus bound of all behind slot j: of the experts left, and of
+        // the later slots
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i]) most = fmaxf(most, __fadd_ru(static_cast<float>(value_of(key[i])), err[i]));
+        most = warp_max(most);
+        float upper = id >= 0 ? __fadd_ru(score, bound) : -INFINITY;  // of this slot, and then of it and the later ones
+        float later = __shfl_down_sync(kFull, upper, 1);
+        if (lane == 31) later = -INFINITY;
+#pragma unroll 1
+        for (int d = 1; d < a.top_k; d <<= 1) {
+            const float v = __shfl_down_sync(kFull, later, d);
+            if (lane + d < 32) later = fmaxf(later, v);
+        }
+        most = fmaxf(most, later);
+        close = __any_sync(kFull, id >= 0 && !(__fsub_rd(score, bound) > most));
     }
 }
 

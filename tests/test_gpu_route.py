@@ -234,3 +234,69 @@ def test_many_tokens():
     again = nv.route(x, 4)
     for a, b in ((r.expert, again.expert), (r.weight, again.weight), (r.row_index, again.row_index)):
         assert torch.equal(a, b)
+
+
+def cancelled(softmax, experts, where, small, rest):
+    """41 tokens with expert `where`'s score cancelled by its bias but for its rounding, the logit in steps of one
+    unit in the last place: the biased score is a small number that only the score's own digits tell, next to the
+    biases `small` {expert: value} of experts with scores of 1e-17 (whose FP32 errors are far smaller), all others
+    at the bias `rest`."""
+    l = np.full((41, experts), -40.0, dtype=np.float32)
+    l[:, where] = np.float32(0.4) + np.arange(-20, 21).astype(np.float32) * np.float32(2.0 ** -25)
+    l[:, experts - 1] = 0.0                      # (softmax: the other half of the sum)
+    bias = np.full(experts, rest, dtype=np.float32)
+    bias[where] = -np.float32(R.scores(l[20].astype(np.float64), softmax)[where])
+    for e, v in small.items():
+        bias[e] = v
+    return l, bias
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+def test_a_third_score_within_its_error(softmax):
+    """The best two FP32 scores are told apart by their own errors; a third one, with a larger error, is the best."""
+    l, bias = cancelled(softmax, 8, 2, {0: 2e-9, 1: 1e-9}, -4.0)
+    for k in (1, 2, 3):
+        check(l, False, k, softmax, bias, renorm=False)
+    l, bias = cancelled(softmax, 256, 200, {0: 2e-9, 1: 1e-9, 2: -1e-8}, -4.0)
+    for k in (1, 2, 5):
+        check(l, False, k, softmax, bias, renorm=False)
+
+
+def test_a_third_softmax_score_of_many():
+    """As above among 512 experts, the largest score not the winner of the FP32 order."""
+    l = np.full((2, 512), -100.0, dtype=np.float32)
+    l[:, 0], l[:, 1:16], l[:, 200:202] = 0.0, -16.54, -60.0
+    p = R.scores(l[0].astype(np.float64), True)[0]
+    bias = np.zeros(512, dtype=np.float32)
+    bias[200], bias[201] = p - 2.4e-7, p - 6.0e-7
+    check(l, False, 1, True, bias)
+    check(l, False, 2, True, bias)
+
+
+GROUPS = [(5, 4), (8, 4), (7, 3), (32, 4), (20, 5)]  # ranked by lanes, or one after the other
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("groups,size", GROUPS)
+def test_groups_within_a_third_ones_error(softmax, groups, size):
+    """Group 1 has the cancelled score, groups 0 and 2 values whose errors tell those two apart: it is left out, kept
+    last or kept first."""
+    a, b, c = 0, size, 2 * size
+    l, bias = cancelled(softmax, groups * size, b, {a: 2e-9, c: 1e-9}, -5.0)
+    for topk_groups in (1, 2):
+        check(l, False, 1, softmax, bias, groups, topk_groups, 1, renorm=False)
+    # sums of the best two: 2e-9, the cancelled one, 1e-9
+    l, bias = cancelled(softmax, groups * size, b, {a: 1e-9, a + 1: 1e-9, b + 1: 0.0, c: 5e-10, c + 1: 5e-10}, -5.0)
+    for topk_groups in (1, 2):
+        check(l, False, 2, softmax, bias, groups, topk_groups, 2, renorm=False)
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("groups,size", GROUPS)
+def test_a_member_of_a_group_within_its_error(softmax, groups, size):
+    """The group's best scores in FP32 are not its best ones: a member with a larger error is."""
+    b, c = size, 2 * size
+    l, bias = cancelled(softmax, groups * size, b, {b + 1: 2e-9, c: 2.5e-9}, -5.0)
+    check(l, False, 1, softmax, bias, groups, 1, 1, renorm=False)
+    l, bias = cancelled(softmax, groups * size, b, {b + 1: 2e-9, b + 2: 1e-9, c: 2.5e-9, c + 1: 1e-9}, -5.0)
+    check(l, False, 2, softmax, bias, groups, 1, 2, renorm=False)
