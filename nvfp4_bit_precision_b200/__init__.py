@@ -839,8 +839,8 @@ def combine(rows, slot_row, weight, base=None, *, workspace=None, stream=None):
 
 
 def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, workspace=None, stream=None):
-    """(drows, dweight) of ``combine`` (the base's gradient is dout).  With the routing's ``group_offsets``
-    the rows behind its last one get a zero gradient; without, every row that no slot names does.  Each row
+    """(drows, dweight) of ``combine`` (the base's gradient is dout).  Rows that no slot names get a zero gradient;
+    with the routing's ``group_offsets``, whose last rows few are, without a pass over all of them.  Each row
     belongs to one slot at most, as a routing's do; a ``workspace`` of
     ``nvfp4_combine_backward_workspace_size(n)`` bytes has that checked and receives the status word."""
     if stream is not None:

@@ -100,17 +100,76 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* rows, int64_t 
     }
 }
 
+// With used_rows every row of drows is defined: those that no slot names are zeroed
+// before the gradients are written.  Which rows slots name needs no memory of its
+// own: mark_rows_kernel leaves each slot's number at a place of the row it names, and
+// a row is named if the number found at its place is that of a slot with this row,
+// whatever bytes lay there before.  The places are dweight's, which is written later,
+// and for rows past its end the first bytes of the rows.  (Marks in the rows alone
+// take 4.5 us more at 65536 rows of 8 KB, whose pages and sectors are all touched.)
+struct Marks {
+    int32_t* place;   // dweight
+    int64_t places;
+    uint8_t* rows;    // drows
+    int64_t row_bytes;
+    __device__ __forceinline__ int32_t* of(int64_t r) const
+    {
+        return r < places ? place + r : reinterpret_cast<int32_t*>(rows + r * row_bytes);
+    }
+};
+
+__global__ void __launch_bounds__(256) mark_rows_kernel(const int32_t* slot_row, int64_t slots, int64_t n_rows, Marks marks)
+{
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    for (int64_t s = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; s < slots;
+         s += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int32_t r = slot_row[s];
+        if (r >= 0 && r < n_rows) *marks.of(r) = static_cast<int32_t>(s);
+    }
+}
+
+// A warp looks at `per` rows at a time, a lane at each, and zeroes those of them that
+// no slot names (from *used_rows on none does).  The gradients' kernel is not let in
+// before the end: its CTAs would crowd where room comes first (16384 tokens x 256,
+// top-4: 36 us in all against 23).
+//
+// The marks and this cost 4.5 us at 65536 rows, two launches: 184.1 -> 188.9 us with
+// the gradients at 4096 columns, 19 -> 23 us at 256, 3.2 -> 5.7 us at 256 rows.
+__global__ void __launch_bounds__(256) zero_unnamed_rows_kernel(const int32_t* slot_row, int64_t slots, int64_t n_rows,
+                                                                const int32_t* used_rows, int per, Marks marks)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    wait_for_previous_kernel();
+    const int64_t used = *used_rows;
+    for (int64_t r0 = warp * per; r0 < n_rows; r0 += warps * per) {
+        const int64_t r = r0 + lane;
+        bool unnamed = lane < per && r < n_rows;
+        if (unnamed && r < used) {
+            const int32_t s = *marks.of(r);
+            unnamed = !(s >= 0 && s < slots && slot_row[s] == r);
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, unnamed); left; left &= left - 1) {
+            uint4* const row = reinterpret_cast<uint4*>(marks.rows + (r0 + __ffs(left) - 1) * marks.row_bytes);
+            for (int64_t v = lane; v < marks.row_bytes / 16; v += 32) row[v] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 // What bounds it: HBM.  The gradients of the same tokens read dout and the rows and
-// write the rows' gradients once (1.21 GB): 181 us, 6.7 TB/s.
+// write the rows' gradients once (1.21 GB): 184 us, 6.6 TB/s.
 //
 // One CTA of W warps per token; each thread keeps the products' sums of four
-// slots over its columns.  With `seen` (one bit a row, cleared by the call) a slot
+// slots over its columns (bf16 rows within 64 registers: left to itself the compiler
+// took 59, and 1 us more).  With `seen` (one bit a row, cleared by the call) a slot
 // whose row an earlier one has named is reported and left out: the row's gradient
 // would be a sum that two slots write.
 template <bool F32>
-__global__ void __launch_bounds__(256) combine_backward_kernel(
+__global__ void __launch_bounds__(256, F32 ? 1 : 4) combine_backward_kernel(
     const uint4* dout, const void* rows, int64_t n_rows, int nvec, const int32_t* slot_row, const float* weight,
-    int64_t tokens, int k, const int32_t* used_rows, void* drows, float* dweight, uint32_t* seen, uint32_t* status)
+    int64_t tokens, int k, void* drows, float* dweight, uint32_t* seen, uint32_t* status)
 {
     __shared__ float s_dot[4][8];
     __shared__ int32_t s_row[4];
@@ -172,13 +231,6 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
                 dweight[t * k + j0 + threadIdx.x] = sum;
             }
         }
-    }
-    if (used_rows) {  // rows that belong to no slot
-        const int64_t first = max(*used_rows, 0);
-        const float zero[8] = {};
-        for (int64_t u = first * nvec + blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; u < n_rows * nvec;
-             u += static_cast<int64_t>(gridDim.x) * blockDim.x)
-            RowVec<F32>::store(drows, u, zero);
     }
 }
 
@@ -248,6 +300,11 @@ extern "C" nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void
         return NVFP4_ERR_ALIGN;
     if (workspace && (off16(workspace) || ws_bytes < nvfp4_combine_backward_workspace_size(n_rows)))
         return NVFP4_ERR_WORKSPACE;
+    const int64_t row_bytes = cols * (rows_dtype == NVFP4_OUT_F32 ? 4 : 2), slots = tokens * k;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(rows), to = reinterpret_cast<uintptr_t>(drows);
+    if (used_rows && (from < to ? to - from : from - to) < static_cast<uint64_t>(n_rows * row_bytes))
+        return NVFP4_ERR_INVALID_ARG;  // the marks would overwrite rows
+    if (used_rows && slots > 0x7fffffffll) return NVFP4_ERR_SHAPE;  // a mark is a slot's number
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     const int sms = sm100_sms(dev);
@@ -255,17 +312,35 @@ extern "C" nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (workspace && cudaMemsetAsync(workspace, 0, nvfp4_combine_backward_workspace_size(n_rows), st) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    if (tokens == 0 && (n_rows == 0 || !used_rows)) return NVFP4_OK;
+    cudaError_t err = cudaSuccess;
+    bool early = !workspace;
+    if (used_rows && n_rows > 0) {
+        const Marks marks{reinterpret_cast<int32_t*>(dweight), slots, static_cast<uint8_t*>(drows), row_bytes};
+        const auto ctas = [&](int64_t threads) {
+            return std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(sms) * 8);
+        };
+        if (slots > 0) {
+            err = launch_early(early, mark_rows_kernel, ctas(slots), 256, 0, st, slot_row, slots, n_rows, marks);
+            early = true;
+        }
+        const int64_t grid = ctas(n_rows * 32);
+        const int per = static_cast<int>(std::min<int64_t>((n_rows + grid * 8 - 1) / (grid * 8), 32));
+        if (err == cudaSuccess)
+            err = launch_early(early, zero_unnamed_rows_kernel, grid, 256, 0, st, slot_row, slots, n_rows, used_rows, per,
+                               marks);
+        early = true;
+        if (err != cudaSuccess) return NVFP4_ERR_CUDA;
+    }
+    if (tokens == 0) return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
     const int nvec = static_cast<int>(cols / 8);
     const int threads = std::min(256, std::max(1, (nvec + 31) / 32) * 32);
-    const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tokens, 1), static_cast<int64_t>(sms) * 8));
+    const int grid = static_cast<int>(std::min<int64_t>(tokens, static_cast<int64_t>(sms) * 8));
     uint32_t* const status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
     uint32_t* const seen =
         workspace ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kCombineWorkspaceHead) : nullptr;
-    cudaError_t err = cudaSuccess;
     const auto go = [&](auto kernel) {
-        err = launch_early(!workspace, kernel, grid, threads, 0, st, static_cast<const uint4*>(dout_bf16), rows, n_rows,
-                           nvec, slot_row, weight, tokens, k, used_rows, drows, dweight, seen, status);
+        err = launch_early(early, kernel, grid, threads, 0, st, static_cast<const uint4*>(dout_bf16), rows, n_rows, nvec,
+                           slot_row, weight, tokens, k, drows, dweight, seen, status);
     };
     rows_dtype == NVFP4_OUT_F32 ? go(combine_backward_kernel<true>) : go(combine_backward_kernel<false>);
     return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

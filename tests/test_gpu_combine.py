@@ -133,3 +133,81 @@ def test_no_tokens():
     assert bool((dr == 0).all()) and dw.shape == (0, 2)
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     assert bool((nv.combine_backward(rows[:0], rows, e, w, off)[0] == 0).all())
+
+
+@pytest.mark.parametrize("tokens,k,cols", [(3, 2, 8), (40, 4, 264), (700, 3, 64), (5000, 4, 128), (9, 4, 8200)])
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("checked", [True, False])
+def test_slots_dropped_after_routing(tokens, k, cols, f32, checked):
+    """Rows below the routing's last one whose slots were taken out, or that a bad index left out, get a zero
+    gradient, whatever the buffer held: here NaN, and numbers of slots that name other rows or none."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(tokens + cols)
+    rows, rd, slot, w = make(rng, tokens, k, cols, f32, 0.3)
+    n = tokens * k
+    slot[0, 0], slot[-1, -1] = 2147483647, -7
+    dout = bits(rng, (tokens, cols), 1e-2)
+    sd, wd, dd = torch.from_numpy(slot).cuda(), torch.from_numpy(w).cuda(), to_dev(dout)
+    off = torch.tensor([0, n // 2, n], dtype=torch.int32, device="cuda")
+    rr, rw = R.combine_backward(val(dout), rows, slot, w)
+    named = np.zeros(n, dtype=bool)
+    named[slot[(slot >= 0) & (slot < n)]] = True
+    assert not named.all()
+    ws = torch.empty(nv.nvfp4_combine_backward_workspace_size(n), dtype=torch.uint8, device="cuda") if checked else None
+    for fill in ("nan", "numbers"):
+        dr = torch.full_like(rd, float("nan"))
+        if fill == "numbers":  # a 64-bit number at the head of each row
+            head = dr.view(torch.int64).view(n, -1)
+            head[:, 0] = torch.from_numpy(rng.integers(-2, n + 2, n)).cuda()
+        dw = torch.full((tokens, k), float("nan"), device="cuda")
+        nv.nvfp4_combine_backward(dd, rd, nv.NVFP4_OUT_F32 if f32 else nv.NVFP4_OUT_BF16, n, cols, sd, wd, tokens, k,
+                                  off.data_ptr() + 8, dr, dw, ws, 0 if ws is None else ws.numel())
+        assert bool((dr[torch.from_numpy(~named).cuda()] == 0).all())
+        assert np.all(np.abs(f64(dr) - rr) <= ((0 if f32 else B) + U) * np.abs(rr) + 2.0 ** -134)
+        assert checked is False or nv.nvfp4_workspace_status(ws) == 8
+    spoil = torch.full_like(rd, float("nan"))
+    del spoil                                   # the wrapper's buffer is likely this memory
+    a, b = nv.combine_backward(dd, rd, sd, wd, off, workspace=ws)
+    assert torch.equal(a, dr) and torch.equal(b, dw)
+    a, b = nv.combine_backward(dd, rd, sd, wd)
+    assert torch.equal(a, dr) and torch.equal(b, dw)
+
+
+def test_rows_named_twice_and_dropped():
+    """The check and the zeroing together: the row two slots name has the gradient of one of them."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(8)
+    rd, dout = to_dev(bits(rng, (8, 64))), to_dev(bits(rng, (4, 64)))
+    slot = torch.tensor([[0, 1], [2, -1], [4, 5], [6, 1]], dtype=torch.int32, device="cuda")
+    w = torch.ones((4, 2), device="cuda")
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    ws = torch.empty(nv.nvfp4_combine_backward_workspace_size(8), dtype=torch.uint8, device="cuda")
+    spoil = torch.full_like(rd, float("nan"))
+    del spoil
+    dr, dw = nv.combine_backward(dout, rd, slot, w, off, workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 8
+    assert torch.equal(dr[[0, 2, 4, 5, 6]], dout[[0, 1, 2, 2, 3]]) and bool((dr[[3, 7]] == 0).all())
+    assert torch.equal(dr[1], dout[0]) or torch.equal(dr[1], dout[3])
+
+
+def test_gradients_of_a_routing_with_dropped_slots():
+    """Through autograd, with the slots past an expert's capacity taken out of the routing."""
+    import dataclasses
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    from nvfp4_bit_precision_b200.moe import moe_combine
+    rng = np.random.default_rng(9)
+    tokens, experts, cols, capacity = 300, 8, 256, 60
+    r = nv.route(torch.from_numpy(rng.standard_normal((tokens, experts)).astype(np.float32)).cuda(), 2)
+    first = r.group_offsets[r.expert.long()]
+    slot = torch.where(r.slot_row - first < capacity, r.slot_row, torch.full_like(r.slot_row, -1))
+    assert bool((slot < 0).any())
+    rows = to_dev(bits(rng, (2 * tokens, cols))).requires_grad_()
+    dout = to_dev(bits(rng, (tokens, cols)))
+    spoil = torch.full_like(rows, float("nan"))
+    del spoil
+    moe_combine(rows, dataclasses.replace(r, slot_row=slot)).backward(dout)
+    rr, _ = R.combine_backward(f64(dout), f64(rows.detach()), host(slot), host(r.weight))
+    assert np.all(np.abs(f64(rows.grad) - rr) <= (B + U) * np.abs(rr) + 2.0 ** -134)

@@ -219,3 +219,16 @@ def test_captured_gradients_refused_on_the_host(monkeypatch):
         moe.moe_route(torch.zeros((2, 8), requires_grad=True), 2)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors expected"):
         moe.rms_norm(x, x[0])
+
+
+def test_combine_backward_refuses_gradients_over_the_rows(nv):
+    """With used_rows the slots' numbers pass through drows before rows is read."""
+    def back(rows, dr, used=FAKE, dt=1):
+        return nv._lib.nvfp4_combine_backward(FAKE, rows, dt, 8, 64, FAKE, FAKE, 4, 2, used, dr, FAKE, None, 0, None)
+    at = 1 << 30
+    assert back(at, at) == ARG and back(at, at + 1008) == ARG and back(at + 1008, at) == ARG
+    assert back(at, at + 1024, dt=0) == ARG
+    import torch
+    if not torch.cuda.is_available():  # nothing is launched
+        for status in (back(at, at + 1024), back(at, at + 2048, dt=0), back(at, at, used=None)):
+            assert status not in (ARG, SHAPE, ALIGN, WORKSPACE)
