@@ -21,3 +21,14 @@ def orc():
     import oracle
     oracle.build()
     return oracle
+
+
+def pytest_collection_modifyitems(items):
+    """test_moe_block_host.py hands stand-in addresses to the library, some of them past its checks, where nothing
+    but the missing GPU keeps a kernel from being launched on them: it runs on machines without one only."""
+    host = [i for i in items if i.path.name == "test_moe_block_host.py"]
+    if host:
+        import torch
+        if torch.cuda.is_available():
+            for i in host:
+                i.add_marker(pytest.mark.skip(reason="stand-in addresses: needs a machine without a GPU"))

@@ -232,3 +232,22 @@ def test_combine_backward_refuses_gradients_over_the_rows(nv):
     if not torch.cuda.is_available():  # nothing is launched
         for status in (back(at, at + 1024), back(at, at + 2048, dt=0), back(at, at, used=None)):
             assert status not in (ARG, SHAPE, ALIGN, WORKSPACE)
+
+
+def test_stand_in_addresses_stay_off_a_gpu(monkeypatch):
+    import pathlib
+    import torch
+    import conftest
+
+    class Item:
+        def __init__(self, name):
+            self.path, self.marks = pathlib.Path(name), []
+
+        def add_marker(self, mark):
+            self.marks.append(mark.name)
+
+    for gpu in (True, False):
+        monkeypatch.setattr(torch.cuda, "is_available", lambda: gpu)
+        items = [Item(__file__), Item("tests/test_gpu_norm.py")]
+        conftest.pytest_collection_modifyitems(items)
+        assert [i.marks for i in items] == [["skip"] if gpu else [], []]
