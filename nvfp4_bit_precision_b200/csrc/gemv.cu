@@ -150,6 +150,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The exponent field by which a row of x is scaled, from its largest magnitude (bf16
+// bits).  With an infinity or a NaN in the row it is that of the largest finite
+// numbers: they, too, then fit into FP16, and a sum is infinite or NaN by those alone.
+__device__ __forceinline__ uint32_t x_exponent(uint32_t top) { return min(max(top >> 7, 15u), 254u); }
 
 // Asynchronous copies to shared memory; zeros where there is nothing to read.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
@@ -467,8 +471,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         }
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < x_rows) {
-            const uint32_t ex = s_top[threadIdx.x] >> 7;
-            s_scale[threadIdx.x] = make_float2(g, ex < 255 ? __uint_as_float((max(ex, 15u) - 14u) << 23) : 1.0f);
+            s_scale[threadIdx.x] = make_float2(g, __uint_as_float((x_exponent(s_top[threadIdx.x]) - 14u) << 23));
         }
         {
             int xr = 0, c = warp - kGemvWarps;
@@ -477,8 +480,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             while (xr < x_rows) {
                 const int4 row = s_x_row[xr];
                 uint4* const at = reinterpret_cast<uint4*>(s_x + t * 16 + row.y + (c * 8 + r) * row.z);
-                const uint32_t ex = s_top[xr] >> 7;  // exponent field of the largest magnitude
-                const float up = ex < 255 ? __uint_as_float((268u - max(ex, 15u)) << 23) : 1.0f;
+                const float up = __uint_as_float((268u - x_exponent(s_top[xr])) << 23);
                 float f[8];
                 unpack8(*at, f);
                 __half2 h[4];

@@ -365,3 +365,37 @@ def test_more_segments_than_multiprocessors(rows, n, k):
     w = R.nvfp4_matrix(q, sf, g)
     ref = val(x) @ w.T
     assert np.all(np.abs(f64(y) - ref) <= bound(val(x), w, ref, True))
+
+
+@pytest.mark.parametrize("rows,n,k", [(5, 128, 256), (13, 272, 512), (8, 128, 12288), (5, 2048, 64)])
+@pytest.mark.parametrize("grouped", [True, False])
+def test_infinities_beside_large_values(rows, n, k, grouped):
+    """An infinite entry decides its row's sums; the finite ones beside it, beyond FP16's range or not, do not make
+    them NaN.  Two infinities of opposite signs, and one under a weight of zero, do."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(k)
+    q, sf, g = R.random_nvfp4(rng, n, k)
+    q = (rng.integers(1, 8, (n, k // 2)) | rng.integers(1, 8, (n, k // 2)) << 4).astype(np.uint8)  # positive weights
+    q[::5, 3] = 0
+    if grouped and n % 128:
+        n, q, sf = 256, q[:256], sf[:256]
+    v = rng.standard_normal((rows, k))
+    v[0], v[1], v[2] = -np.abs(v[0]) * 2.0 ** 125, np.abs(v[1]) * 1e6, np.abs(v[2]) * 2.0 ** -120
+    v[0, k - 1], v[1, 6], v[2, 11] = np.inf, -np.inf, np.inf
+    v[3, 1], v[3, k - 2] = np.inf, -np.inf
+    x = W.f32_to_bf16_bits(v.astype(np.float32))
+    if grouped:
+        off = torch.tensor([0, 2, 2, rows], dtype=torch.int32, device="cuda")
+        y = nv.grouped_gemv(off, to_dev(x), torch.from_numpy(np.stack([q] * 3)).cuda(),
+                            torch.from_numpy(np.concatenate([R.tile(sf)] * 3)).cuda(),
+                            torch.full((3,), float(g), device="cuda"), n, None, nv.NVFP4_OUT_F32)
+    else:
+        y = nv.gemv(to_dev(x), upload(nv, q, sf, g), nv.NVFP4_OUT_F32)
+    w = R.nvfp4_matrix(q, sf, g)
+    with np.errstate(invalid="ignore"):
+        ref = val(x) @ w.T
+    assert (ref[0] == np.inf).all() and (ref[1, ::5] != ref[1, ::5]).all() and (ref[1, 1::5] == -np.inf).all()
+    np.testing.assert_array_equal(f64(y)[:4], ref[:4])
+    finite = np.abs(f64(y)[4:] - ref[4:]) <= bound(val(x)[4:], w, ref[4:], True)
+    assert finite.all()
