@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["quantize.cu", "gemm.cu", "mxfp4.cu", "moe_comm.cu", "norm.cu", "route.cu", "combine.cu",
            "gemv.cu"]
-HEADERS = ["common.cuh"]
+HEADERS = ["common.cuh", "gemv_plan.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

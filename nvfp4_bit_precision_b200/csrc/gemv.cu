@@ -31,6 +31,7 @@
 // conversions run at 65.  Asking for a CTA's later tiles ahead by bulk prefetches
 // into L2 was slower (one row: 16.9 to 19.4 us): x waits behind them.
 #include "common.cuh"
+#include "gemv_plan.h"
 
 #include <algorithm>
 
@@ -647,27 +648,6 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     }
 }
 
-// One matrix: even segments of at most `fit` rows, each with as many CTAs.  Bringing a
-// row of x costs a CTA about as much as a tile, so a CTA has tiles of one segment
-// alone, and `cost`, its tiles and rows, is what a form's time goes by.  5120 x 20480 at
-// 17 rows: 59 us so, 100 us with the tiles of all segments in equal runs; 512 x 20480 at
-// 8 rows, 4 segments: 13 us, 27 us with a CTA for each tile of one segment.
-struct Plan {
-    int seg_rows = 1, ctas = 1;
-    int64_t cost = INT64_MAX;
-    Plan() = default;
-    Plan(int64_t rows, int64_t tiles, int64_t fit, int sms)
-    {
-        const int64_t segments = (rows + fit - 1) / fit;
-        seg_rows = static_cast<int>((rows + segments - 1) / segments);
-        for (int wave = 1; wave <= 4; ++wave) {
-            const int64_t n = std::min(tiles, wave * sms / segments);
-            const int64_t c = n ? wave * ((tiles + n - 1) / n + seg_rows) : INT64_MAX;
-            if (c < cost) cost = c, ctas = static_cast<int>(n);
-        }
-    }
-};
-
 template <int NT, bool PANELS>
 nvfp4_status start_gemv(GemvArgs a, const Plan& plan, int sms, cudaStream_t st)
 {
@@ -748,15 +728,9 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
         const bool two = 3 * passes(2) <= 2 * passes(1);
         return two ? start_gemv<2, false>(a, Plan(), sms, st) : start_gemv<1, false>(a, Plan(), sms, st);
     }
-    // The form that costs least; a tile or a row costs a twentieth more with panels, where
-    // loads wait at each panel's start, and a fifth more with 16 columns of x.  (5120 x
-    // 20480: 4 rows 31 us, with panels 34; 16 rows 85 and 57, with 16 columns 109.  2048 x
-    // 24576, 8 rows: 36 us with 16 columns, 45 with panels, 47 without either.)
-    const Plan one(a.rows, tiles, at_once(1), sms), two(a.rows, tiles, at_once(2), sms);
-    const Plan panels(a.rows, tiles, 8, sms);
-    if (20 * one.cost <= std::min(24 * two.cost, 21 * panels.cost)) return start_gemv<1, false>(a, one, sms, st);
-    if (24 * two.cost <= 21 * panels.cost) return start_gemv<2, false>(a, two, sms, st);
-    return start_gemv<1, true>(a, panels, sms, st);
+    const Form form = cheapest_form(a.rows, tiles, at_once(1), at_once(2), sms);
+    if (form.panels) return start_gemv<1, true>(a, form.plan, sms, st);
+    return form.columns == 8 ? start_gemv<1, false>(a, form.plan, sms, st) : start_gemv<2, false>(a, form.plan, sms, st);
 }
 
 }  // namespace
