@@ -703,6 +703,11 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
         (reinterpret_cast<uintptr_t>(a.row_index) & 3u) || (reinterpret_cast<uintptr_t>(a.group_offsets) & 3u))
         return NVFP4_ERR_ALIGN;
     if (workspace && (ws_bytes < 16 || off16(workspace))) return NVFP4_ERR_WORKSPACE;
+    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
+    if (a.rows > 0) {
+        if (steps > max_x_pairs(1, false)) return NVFP4_ERR_SHAPE;            // one row does not fit
+        if (a.rows > 0x7fffffffll / (tiles * steps)) return NVFP4_ERR_SHAPE;  // indexes are 31-bit on the device
+    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     const int sms = sm100_sms(dev);
@@ -713,9 +718,6 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
     if (a.rows == 0) return NVFP4_OK;
     a.sf_bytes = static_cast<int64_t>(nvfp4_sf_mma_bytes(a.n, a.k));
     a.out_f32 = out_dtype == NVFP4_OUT_F32;
-    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
-    if (steps > max_x_pairs(1, false)) return NVFP4_ERR_SHAPE;          // one row does not fit
-    if (a.rows * tiles * steps > 0x7fffffffll) return NVFP4_ERR_SHAPE;  // indexes are 31-bit on the device
     a.tiles = static_cast<int>(tiles), a.steps = static_cast<int>(steps);
     const auto at_once = [&](int nt) { return std::min<int64_t>(8 * nt, max_x_pairs(nt, false) / steps); };
     if (a.group_offsets) {

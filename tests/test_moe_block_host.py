@@ -251,3 +251,17 @@ def test_stand_in_addresses_stay_off_a_gpu(monkeypatch):
         items = [Item(__file__), Item("tests/test_gpu_norm.py")]
         conftest.pytest_collection_modifyitems(items)
         assert [i.marks for i in items] == [["skip"] if gpu else [], []]
+
+
+def test_gemv_refuses_sizes_whose_product_overflows(nv):
+    """rows x tiles x steps past 2^31 and past 2^63 alike, before anything is asked of a device."""
+    def dense(rows, n, k):
+        return nv._lib.nvfp4_gemv(FAKE, k, rows, FAKE, FAKE, FAKE, n, k, 1, FAKE, n, None)
+
+    def grouped(rows, n, k):
+        return nv._lib.nvfp4_grouped_gemv(4, FAKE, rows, FAKE, k, rows, None, FAKE, FAKE, FAKE, n, k, 1, FAKE, n, None,
+                                          0, None)
+    for call in (dense, grouped):
+        for rows, n, k in ((2 ** 31 - 1, 2 ** 30, 45056), (2 ** 31 - 1, 2 ** 30, 64 * 512), (2 ** 31 - 1, 2 ** 30, 64),
+                           (2 ** 28, 128, 64), (2 ** 20, 2 ** 14, 1024), (1, 128, 45120 + 64)):
+            assert call(rows, n, k) == SHAPE, (rows, n, k)
