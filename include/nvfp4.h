@@ -441,7 +441,8 @@ size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
  *   dweight = sum over rows of dy * n        (NULL = not wanted).
  * dx is the gradient of x and of residual.  It may be dy or dh itself.  dweight
  * has weight_dtype; its sum is FP32 in a fixed order.  Shapes and alignment as
- * for nvfp4_rmsnorm.  The workspace is read only for dweight.
+ * for nvfp4_rmsnorm.  The workspace is needed for dweight; without it one may be
+ * given (16 bytes, 16-byte aligned), whose status word is then cleared.
  */
 nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy, const void* h_bf16,
                                     int64_t ldh, const void* dh_bf16, int64_t lddh,

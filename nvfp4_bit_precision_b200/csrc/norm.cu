@@ -499,7 +499,8 @@ extern "C" nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy
     if (off16(dy_bf16) || off16(h_bf16) || off16(dh_bf16) || off16(weight) || off16(dx_bf16) || off16(dweight) ||
         (reinterpret_cast<uintptr_t>(rstd) & 3u) || lddy % 8 || ldh % 8 || lddx % 8 || (dh_bf16 && lddh % 8))
         return NVFP4_ERR_ALIGN;
-    if (dweight && (!workspace || off16(workspace) || ws_bytes < nvfp4_rmsnorm_backward_workspace_size(rows, cols)))
+    if ((workspace && (off16(workspace) || ws_bytes < 16)) ||
+        (dweight && (!workspace || ws_bytes < nvfp4_rmsnorm_backward_workspace_size(rows, cols))))
         return NVFP4_ERR_WORKSPACE;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
@@ -507,7 +508,7 @@ extern "C" nvfp4_status nvfp4_rmsnorm_backward(const void* dy_bf16, int64_t lddy
     if (!sms) return NVFP4_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool w32 = weight_dtype == NVFP4_OUT_F32;
-    uint32_t* const status = workspace && ws_bytes >= 16 ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
+    uint32_t* const status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
     if (rows == 0) {
         if (status && cudaMemsetAsync(status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
         if (dweight && cudaMemsetAsync(dweight, 0, cols * (w32 ? 4 : 2), st) != cudaSuccess) return NVFP4_ERR_CUDA;

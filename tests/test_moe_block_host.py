@@ -265,3 +265,10 @@ def test_gemv_refuses_sizes_whose_product_overflows(nv):
         for rows, n, k in ((2 ** 31 - 1, 2 ** 30, 45056), (2 ** 31 - 1, 2 ** 30, 64 * 512), (2 ** 31 - 1, 2 ** 30, 64),
                            (2 ** 28, 128, 64), (2 ** 20, 2 ** 14, 1024), (1, 128, 45120 + 64)):
             assert call(rows, n, k) == SHAPE, (rows, n, k)
+
+
+@pytest.mark.parametrize("change", [dict(ws=FAKE + 2), dict(ws=FAKE + 4), dict(ws=FAKE + 8), dict(n=8), dict(n=0)])
+def test_norm_backward_checks_a_workspace_without_dweight(nv, change):
+    """Its status word is cleared whether or not dweight is asked for."""
+    assert back(nv, dw=None, **change) == WORKSPACE
+    assert back(nv, dw=None, rows=0, **change) == WORKSPACE
