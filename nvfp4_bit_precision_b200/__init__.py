@@ -661,6 +661,11 @@ def _flat(name: str, t, dtype, *shape) -> None:
         raise ValueError(f"{name}: contiguous {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
 
 
+def _bytes(name: str, t, least: int) -> None:
+    if t.element_size() != 1 or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name}: at least {least} contiguous bytes expected, got {t.dtype} {tuple(t.shape)}")
+
+
 def _on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
@@ -888,7 +893,8 @@ def gemv(x, w: NVFP4Tensor, out_dtype: int = NVFP4_OUT_BF16, out=None, *, stream
     rows = x.shape[0]
     _need(w.sf_layout == NVFP4_SF_MMA, "gemv: w must have tiled scales (NVFP4_SF_MMA)")
     _flat("gemv: w.q", q, torch.uint8, N, K // 2)
-    _need(sf.is_contiguous() and sf.numel() >= nvfp4_sf_mma_bytes(N, K), "gemv: w.sf too small")
+    _need(g.dtype is torch.float32 and g.numel() == 1, "gemv: w.g must be one float32 number")
+    _bytes("gemv: w.sf", sf, nvfp4_sf_mma_bytes(N, K))
     out, ldd = _gemv_out("gemv", out_dtype, rows, N, out, dev)
     _check(_lib.nvfp4_gemv(x.data_ptr(), ldx, rows, q.data_ptr(), sf.data_ptr(), g.data_ptr(), N, K, out_dtype,
                            out.data_ptr(), ldd, _raw_stream(dev)), "nvfp4_gemv")
@@ -910,7 +916,7 @@ def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtyp
     _flat("grouped_gemv: group_offsets", group_offsets, torch.int32, G + 1)
     _flat("grouped_gemv: qb", qb, torch.uint8, G, N, K // 2)
     _flat("grouped_gemv: gb", gb, torch.float32, G)
-    _need(sfb.is_contiguous() and sfb.numel() >= G * nvfp4_sf_mma_bytes(N, K), "grouped_gemv: sfb too small")
+    _bytes("grouped_gemv: sfb", sfb, G * nvfp4_sf_mma_bytes(N, K))
     rows, ip, wp, nb = src, None, None, 0
     if row_index is not None:
         rows = row_index.numel()

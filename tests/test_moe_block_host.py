@@ -272,3 +272,36 @@ def test_norm_backward_checks_a_workspace_without_dweight(nv, change):
     """Its status word is cleared whether or not dweight is asked for."""
     assert back(nv, dw=None, **change) == WORKSPACE
     assert back(nv, dw=None, rows=0, **change) == WORKSPACE
+
+
+def test_products_refuse_scales_of_other_types(nv, monkeypatch):
+    """The matrix scale is one FP32 number and the block scales are bytes; others would be read as if they were."""
+    import torch
+    monkeypatch.setattr(nv, "_one_device", lambda name, *t: t[0].device)
+    monkeypatch.setattr(nv, "_raw_stream", lambda dev: None)   # nothing gets as far as a launch
+    called = []
+    monkeypatch.setattr(nv, "_lib", type("Lib", (), {n: staticmethod(lambda *a: called.append(a) or 0)
+                                                    for n in ("nvfp4_gemv", "nvfp4_grouped_gemv")}
+                                         | {"nvfp4_sf_mma_bytes": nv._lib.nvfp4_sf_mma_bytes}))
+    x, q, sf = torch.zeros((1, 64), dtype=torch.bfloat16), torch.zeros((128, 32), dtype=torch.uint8), \
+        torch.zeros(512, dtype=torch.uint8)
+    off = torch.zeros(2, dtype=torch.int32)
+    dense = lambda g, s: nv.gemv(x, nv.NVFP4Tensor(q, s, g, 128, 64, nv.NVFP4_SF_MMA))
+    grouped = lambda g, s: nv.grouped_gemv(off, x, q[None], s, g, 128)
+    one = torch.ones(1)
+    for g in (one.bfloat16(), one.double(), one.half(), one.int(), torch.ones(0), torch.ones(2)):
+        with pytest.raises(ValueError, match="w.g"):
+            dense(g, sf)
+        with pytest.raises(ValueError, match="gb"):
+            grouped(g, sf)
+    for s in (sf.int(), sf.float(), sf.bfloat16()):
+        with pytest.raises(ValueError, match="w.sf"):
+            dense(one, s)
+        with pytest.raises(ValueError, match="sfb"):
+            grouped(one, s)
+    assert not called
+    for g, s in ((one, sf), (one, sf.view(torch.float8_e4m3fn)), (one, torch.zeros(2048, dtype=torch.int8))):
+        dense(g, s)
+        grouped(g, s)
+    dense(torch.tensor(1.0), sf)
+    assert len(called) == 7
