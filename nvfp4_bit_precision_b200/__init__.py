@@ -22,8 +22,6 @@ import os
 from dataclasses import dataclass
 from typing import Optional
 
-import torch
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
@@ -37,6 +35,18 @@ if _build.stale():
             raise ImportError(f"{LIB_PATH} is missing and could not be built: {exc}") from exc
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+class _Torch:
+    """torch, imported at its first use, when it takes this object's place: the C functions need addresses only."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 # ----------------------------------------------------------------- constants
 NVFP4_OK = 0

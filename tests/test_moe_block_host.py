@@ -305,3 +305,21 @@ def test_products_refuse_scales_of_other_types(nv, monkeypatch):
         grouped(g, s)
     dense(torch.tensor(1.0), sf)
     assert len(called) == 7
+
+
+def test_import_leaves_torch_to_first_use():
+    """Importing the package brings no torch along; the first call that needs it does."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys, nvfp4_bit_precision_b200 as nv\n"
+            "assert nv.nvfp4_version() >= 300 and nv.nvfp4_sf_mma_bytes(128, 64) == 512\n"
+            "assert nv.nvfp4_rmsnorm_backward_workspace_size(4, 256) > 256\n"
+            "assert 'torch' not in sys.modules\n"
+            "import torch\n"
+            "try:\n    nv.rmsnorm(torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(64))\n"
+            "except ValueError as e:\n    assert 'CUDA tensors expected' in str(e)\n"
+            "else:\n    raise AssertionError\n"
+            "assert nv._matrix(torch.device('cpu'), torch.uint8, 2, 3).shape == (2, 3) and nv.torch is torch\n")
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
