@@ -35,6 +35,15 @@ def _refuse_capture(name: str) -> None:
                            f"package's forward and backward calls")
 
 
+def _gradient(t):
+    """A gradient as the kernels read it: contiguous rows from a 16-byte boundary (a piece of a larger tensor may
+    begin anywhere)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -52,7 +61,7 @@ class _RMSNorm(torch.autograd.Function):
         if dy is None:  # only the sum was used
             dx, dw = dh, None
         else:
-            dx, dw = rmsnorm_backward(dy.contiguous(), h, weight, rstd, None if dh is None else dh.contiguous(),
+            dx, dw = rmsnorm_backward(_gradient(dy), h, weight, rstd, _gradient(dh),
                                       dweight=ctx.needs_input_grad[1])
         return dx, dw, dx if ctx.has_residual else None, None
 
@@ -97,7 +106,7 @@ class _Route(torch.autograd.Function):
     def backward(ctx, dweight, *_):
         _refuse_capture("moe_route")
         logits, expert = ctx.saved_tensors
-        return route_backward(dweight.contiguous(), logits, Routing(expert, None, None, None, None, ctx.params)), \
+        return route_backward(_gradient(dweight), logits, Routing(expert, None, None, None, None, ctx.params)), \
             None, None, None
 
 
@@ -125,7 +134,7 @@ class _Combine(torch.autograd.Function):
         rows, weight, slot_row, group_offsets = ctx.saved_tensors
         drows = dweight = None
         if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
-            drows, dweight = combine_backward(dout.contiguous(), rows, slot_row, weight, group_offsets)
+            drows, dweight = combine_backward(_gradient(dout), rows, slot_row, weight, group_offsets)
         return drows, dweight, None, None, dout if ctx.needs_input_grad[4] else None
 
 

@@ -277,3 +277,30 @@ def test_captured_gradients_are_refused(nv):
     g.replay()
     torch.cuda.synchronize()
     assert bool((y == 1).all())
+
+
+def test_gradients_that_begin_anywhere(nv):
+    """An upstream gradient that is a piece of a larger tensor, off the 16-byte boundary that the kernels read from."""
+    import torch
+    from nvfp4_bit_precision_b200.moe import moe_combine, moe_route, rms_norm
+    rng = np.random.default_rng(10)
+    leaf = lambda *s: to_dev(bits(rng, s)).requires_grad_()
+    x, res, w, rows, base = leaf(5, 128), leaf(5, 128), leaf(128), leaf(10, 128), leaf(5, 128)
+    logits = torch.from_numpy(rng.standard_normal((5, 8)).astype(np.float32)).cuda().requires_grad_()
+    leaves = (x, res, w, rows, base, logits)
+    head = torch.zeros(3, dtype=torch.bfloat16, device="cuda")
+    up = [to_dev(bits(rng, 3 + 5 * 128)) for _ in range(3)]
+
+    def grads(apart):
+        for t in leaves:
+            t.grad = None
+        y, h = rms_norm(x, w, res)
+        out = moe_combine(rows, moe_route(logits, 2), base)
+        if apart:
+            torch.autograd.backward([y, h, out], [u[3:].clone().view(5, 128) for u in up])
+        else:
+            torch.autograd.backward([torch.cat([head, t.reshape(-1)]) for t in (y, h, out)], up)
+        return [t.grad.clone() for t in leaves]
+
+    for a, b in zip(grads(True), grads(False)):
+        assert torch.equal(a, b)
