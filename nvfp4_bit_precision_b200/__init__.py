@@ -677,7 +677,9 @@ def _bytes(name: str, t, least: int) -> None:
 
 
 def _on(stream):
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):  # (ExternalStream(0) would be a new stream, not the default one)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, y: bool = True, mx: bool = False,

@@ -304,3 +304,20 @@ def test_gradients_that_begin_anywhere(nv):
 
     for a, b in zip(grads(True), grads(False)):
         assert torch.equal(a, b)
+
+
+def test_stream_numbers(nv, monkeypatch):
+    """A stream given as its address, 0 for the default stream as torch gives it."""
+    import torch
+    rng = np.random.default_rng(11)
+    x, w = to_dev(bits(rng, (4, 128))), to_dev(bits(rng, 128))
+    side = torch.cuda.Stream()
+    used, raw = [], nv._raw_stream
+    monkeypatch.setattr(nv, "_raw_stream", lambda dev: used.append(raw(dev)) or used[-1])
+    assert torch.cuda.default_stream().cuda_stream == 0
+    with torch.cuda.stream(side):
+        for s in (0, torch.cuda.default_stream(), side.cuda_stream, side, None):
+            nv.rmsnorm(x, w, stream=s)
+    nv.rmsnorm(x, w, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert used == [0, 0, side.cuda_stream, side.cuda_stream, side.cuda_stream, 0]
