@@ -483,7 +483,9 @@ size_t nvfp4_route_workspace_size(int64_t tokens, int experts);
  * [experts + 1]; row_index [tokens * top_k]: the token of each routed row, rows
  * in expert order and by (token, slot) within an expert, -1 behind the last row
  * (group_offsets[experts]); slot_row [tokens, top_k]: each slot's row.
- * tokens >= 0; 1 <= top_k <= experts / groups * topk_groups; experts <= 512.
+ * tokens >= 0; 1 <= top_k <= experts / groups * topk_groups; experts <= 512 (the
+ * calls that take group_offsets accept up to 256 groups; nvfp4_combine and
+ * mxfp8_combine read slot_row alone).
  */
 nvfp4_status nvfp4_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,
                          int64_t tokens, int experts, const nvfp4_route_params* p, int32_t* expert,
@@ -556,9 +558,9 @@ nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t ldx, int64_t rows, const uin
 /*
  * nvfp4_grouped_gemv -- nvfp4_gemv with one matrix per group, the form of
  * nvfp4_grouped_gemm for a few tokens: row i of D, in group e by group_offsets
- * (device int32 [G + 1], 1 <= G <= 256), is row row_index[i] of x [src_rows, ldx]
- * (NULL: row i) times matrix e.  q [G, N, K/2], sf [G] consecutive NVFP4_SF_MMA
- * blocks, g [G].  Rows behind group_offsets[G] are left as they were; an index
+ * (device int32 [G + 1], non-decreasing from 0, 1 <= G <= 256), is row row_index[i]
+ * of x [src_rows, ldx] (NULL: row i) times matrix e.  q [G, N, K/2], sf [G]
+ * consecutive NVFP4_SF_MMA blocks, g [G].  Rows behind group_offsets[G] are left as they were; an index
  * outside x gives a row of zeros and is reported in the optional workspace's
  * status word.  N a multiple of 128; otherwise as nvfp4_gemv.
  */

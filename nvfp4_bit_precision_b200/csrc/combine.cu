@@ -158,8 +158,10 @@ __global__ void __launch_bounds__(256) zero_unnamed_rows_kernel(const int32_t* s
     }
 }
 
-// What bounds it: HBM.  The gradients of the same tokens read dout and the rows and
-// write the rows' gradients once (1.21 GB): 184 us, 6.6 TB/s.
+// What bounds it: HBM at wide rows; the gradients of the same tokens read dout and the
+// rows and write the rows' gradients once (1.21 GB): 184 us, 6.6 TB/s.  At narrow ones
+// (one warp a token, eight an SM) it is a token's chain of slots, rows, sums and
+// barriers: 19 us at 256 columns, 75 MB.
 //
 // One CTA of W warps per token; each thread keeps the products' sums of four
 // slots over its columns (bf16 rows within 64 registers: left to itself the compiler

@@ -17,9 +17,9 @@
 //
 // What bounds it.  Bytes, with what comes before the first of them: a plain read of
 // as many bytes takes 12.1 us (59 MB) and 20.6 us (133 MB) a launch here.  One row x
-// 20480 x 5120 (59 MB) 15.6 us; 32 tokens' rows through four experts of 4096 x 1536
-// each (about 43 experts, 150 MB) 36 us; eight tokens' through 1536 x 4096 (60 MB)
-// 21 us, of which 3 us pass before the routing has been read and the first weights
+// 20480 x 5120 (59 MB) 16.0 us; 32 tokens' rows through four experts of 4096 x 1536
+// each (133 MB) 36 us; eight tokens' through 1536 x 4096 (60 MB)
+// 21.6 us, of which 3 us pass before the routing has been read and the first weights
 // are asked for.  At more rows it is bringing x into each SM's shared memory, a row
 // about as dear as a 16-row tile: 13 rows x 4096 x 4096 11 us, 32 rows x 5120 x 20480
 // 75 us.  Steps on the way, at the one row: warps of 64 matrix

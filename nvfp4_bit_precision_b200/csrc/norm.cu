@@ -395,7 +395,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* partial, 
 // 115 us backward; one: 96 to 170 and 107 to 155 us; four: 81 to 100 and 126 to
 // 157 us); four for longer rows, and for the MXFP8 output of many rows from 2056
 // columns on, whose arithmetic gains most from few threads per row (4096 to 8192
-// columns: 81 to 83 us against 87 to 93).
+// columns: 81 to 83 us against 87 to 93).  What the rule does not serve: below 512
+// columns a row is less than a warp's two vectors a lane (2^26 elements at 128 columns
+// 133 us forward, 192 us backward; at 256 73 and 105; at 512 49 and 84), and from
+// 16392 columns on the backward pass spills 284 to 312 bytes a thread (2^26 elements
+// at 16384 columns 102 us, at 32768 146).
 int row_vectors(int nvec) { return nvec <= 2 * kNormThreads ? 2 : 4; }
 int row_threads(int nvec, int per) { return ((nvec + per - 1) / per + 31) / 32 * 32; }
 
