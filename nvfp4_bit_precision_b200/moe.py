@@ -45,10 +45,15 @@ def _gradient(t):
 
 
 class _RMSNorm(torch.autograd.Function):
+    # x and residual come in their own shapes: views of their gradient, one for each, would be taken for tensors of
+    # their own, and two leaves would accumulate into the same memory
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
-        f = rmsnorm(x, weight, residual, eps, rstd=True)
-        ctx.save_for_backward(f["h"], weight, f["rstd"])
+        cols = x.shape[-1]
+        f = rmsnorm(x.reshape(-1, cols), weight, None if residual is None else residual.reshape(-1, cols), eps,
+                    rstd=True)
+        ctx.save_for_backward(x if residual is None else f["h"], weight, f["rstd"])
+        ctx.shape = x.shape
         ctx.has_residual = residual is not None
         ctx.set_materialize_grads(False)
         return (f["y"], f["h"]) if residual is not None else f["y"]
@@ -59,10 +64,11 @@ class _RMSNorm(torch.autograd.Function):
         _refuse_capture("rms_norm")
         h, weight, rstd = ctx.saved_tensors
         if dy is None:  # only the sum was used
-            dx, dw = dh, None
+            dx, dw = dh.clone(memory_format=torch.contiguous_format), None
         else:
-            dx, dw = rmsnorm_backward(_gradient(dy), h, weight, rstd, _gradient(dh),
+            dx, dw = rmsnorm_backward(_gradient(dy), h.reshape(-1, ctx.shape[-1]), weight, rstd, _gradient(dh),
                                       dweight=ctx.needs_input_grad[1])
+        dx = dx.view(ctx.shape)
         return dx, dw, dx if ctx.has_residual else None, None
 
 
@@ -70,12 +76,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     """Root-mean-square norm of x [..., cols] times weight [cols].  With a residual of x's shape: (y, h), the norm
     of h = x + residual and h itself; without: y.  x and residual bf16, weight bf16 or f32."""
     _refuse_captured_gradients("rms_norm", x, weight, residual)
-    cols = x.shape[-1]
     if residual is None:
-        return _RMSNorm.apply(x.reshape(-1, cols), weight, None, eps).reshape(x.shape)
+        return _RMSNorm.apply(x, weight, None, eps).reshape(x.shape)
     if residual.shape != x.shape:
         raise ValueError(f"rms_norm: residual {tuple(residual.shape)} and x {tuple(x.shape)} differ")
-    y, h = _RMSNorm.apply(x.reshape(-1, cols), weight, residual.reshape(-1, cols), eps)
+    y, h = _RMSNorm.apply(x, weight, residual, eps)
     return y.reshape(x.shape), h.reshape(x.shape)
 
 

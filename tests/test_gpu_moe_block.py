@@ -321,3 +321,57 @@ def test_stream_numbers(nv, monkeypatch):
     nv.rmsnorm(x, w, stream=torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert used == [0, 0, side.cuda_stream, side.cuda_stream, side.cuda_stream, 0]
+
+
+@pytest.mark.parametrize("shape", [(6, 128), (2, 3, 128), (128,)])
+def test_gradients_accumulate_apart(nv, shape):
+    """x and residual have one gradient, but two leaves do not share its memory: two backward passes give each of
+    them twice the gradient, and leave the tensors that were handed in as they were."""
+    import torch
+    from nvfp4_bit_precision_b200.moe import rms_norm
+    rng = np.random.default_rng(12)
+    x, res, w = (to_dev(bits(rng, s)).requires_grad_() for s in (shape, shape, 128))
+    dy, dh = to_dev(bits(rng, shape)), to_dev(bits(rng, shape))
+    kept = dh.clone()
+
+    def twice(outputs, grads):
+        out = []
+        for n in range(2):
+            y, h = rms_norm(x, w, res)
+            torch.autograd.backward([(y, h)[i] for i in outputs], grads)
+            out.append([t.grad.clone() for t in (x, res)])
+            assert x.grad.data_ptr() != res.grad.data_ptr()
+        x.grad = res.grad = w.grad = None
+        return out
+
+    for outputs, grads in (((0, 1), [dy, dh]), ((0,), [dy]), ((1,), [dh])):
+        (a, b), (a2, b2) = twice(outputs, grads)
+        assert torch.equal(a, b) and torch.equal(a2, 2 * a) and torch.equal(b2, 2 * b)   # (doubling is exact)
+        assert torch.equal(dh, kept)
+
+
+def test_norm_of_strided_inputs_and_changed_outputs(nv):
+    """Views with gaps go in and out; y may be changed in place, and a change of the sum or of x that the backward
+    pass reads is reported."""
+    import torch
+    from nvfp4_bit_precision_b200.moe import rms_norm
+    rng = np.random.default_rng(13)
+    wide, w = to_dev(bits(rng, (4, 6, 256))), to_dev(bits(rng, 128)).requires_grad_()
+    a, b = wide[:, ::2, :128], wide[:, 1::2, 128:]
+    xs, rs = (t.detach().clone().requires_grad_() for t in (a, b))
+    xv, rv = (torch.empty(4, 3, 256, dtype=torch.bfloat16, device="cuda")[..., :128].copy_(t).requires_grad_() for t in (a, b))
+    dy = to_dev(bits(rng, (4, 3, 128)))
+    for p, q in ((xs, rs), (xv, rv)):
+        y, h = rms_norm(p, w, q)
+        y.mul_(2.0)
+        torch.autograd.backward([y, h], [dy, dy])
+    assert torch.equal(xs.grad, xv.grad) and torch.equal(rs.grad, rv.grad) and torch.equal(xs.grad, rs.grad)
+    y, h = rms_norm(xs, w, rs)
+    h.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    y = rms_norm(xs, w)
+    with torch.no_grad():
+        xs.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
