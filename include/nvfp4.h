@@ -527,12 +527,14 @@ size_t nvfp4_combine_backward_workspace_size(int64_t n_rows);
  *   drows[slot_row[t][j]] = weight[t][j] * dout[t]      (rows_dtype)
  *   dweight[t][j] = <dout[t], rows[slot_row[t][j]]>     (FP32; 0 for left-out slots)
  * Each row belongs to one slot at most, as nvfp4_route's do.  With a workspace
- * that is checked: a slot whose row another has named, or past n_rows, is left out
- * and reported (NVFP4_ERR_INDEX); without one the gradient of a row that two slots
- * name is unspecified.  used_rows (device int32, group_offsets + experts of
- * nvfp4_route): rows that no slot names are zeroed, those from *used_rows on
- * without a look at the slots; drows may then not overlap rows
- * (NVFP4_ERR_INVALID_ARG).  NULL: rows that no slot names are left as they were.
+ * that is checked: a slot whose row another has named (which of the two is not
+ * determined), or past n_rows, is left out and reported (NVFP4_ERR_INDEX); without
+ * one the gradient of a row that two slots name is unspecified.  used_rows (device
+ * int32, group_offsets + experts of nvfp4_route): rows that no slot names are
+ * zeroed, those from *used_rows on without a look at the slots; tokens * k is then
+ * below 2^31.  NULL: rows that no slot names are left as they were.  drows may be
+ * rows and dweight weight; with used_rows not both, nor drows rows where n_rows
+ * exceeds tokens * k (NVFP4_ERR_INVALID_ARG).
  */
 nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void* rows, int rows_dtype,
                                     int64_t n_rows, int64_t cols, const int32_t* slot_row,

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* rows, int64_t 
 // own: mark_rows_kernel leaves each slot's number at a place of the row it names, and
 // a row is named if the number found at its place is that of a slot with this row,
 // whatever bytes lay there before.  The places are dweight's, which is written later,
-// and for rows past its end the first bytes of the rows.  (Marks in the rows alone
+// and for rows past its end (all rows where dweight is weight itself) the first bytes
+// of the rows.  (Marks in the rows alone
 // take 4.5 us more at 65536 rows of 8 KB, whose pages and sectors are all touched.)
 struct Marks {
     int32_t* place;   // dweight
@@ -251,6 +252,13 @@ nvfp4_status combine_common(const void* rows, int rows_dtype, int64_t n_rows, in
     return NVFP4_OK;
 }
 
+// Two arrays of as many bytes share some.
+bool overlap(const void* a, const void* b, int64_t bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x < y ? y - x : x - y) < static_cast<uint64_t>(bytes);
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -302,11 +310,11 @@ extern "C" nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void
         return NVFP4_ERR_ALIGN;
     if (workspace && (off16(workspace) || ws_bytes < nvfp4_combine_backward_workspace_size(n_rows)))
         return NVFP4_ERR_WORKSPACE;
-    const int64_t row_bytes = cols * (rows_dtype == NVFP4_OUT_F32 ? 4 : 2), slots = tokens * k;
-    const uintptr_t from = reinterpret_cast<uintptr_t>(rows), to = reinterpret_cast<uintptr_t>(drows);
-    if (used_rows && (from < to ? to - from : from - to) < static_cast<uint64_t>(n_rows * row_bytes))
-        return NVFP4_ERR_INVALID_ARG;  // the marks would overwrite rows
-    if (used_rows && slots > 0x7fffffffll) return NVFP4_ERR_SHAPE;  // a mark is a slot's number
+    const int64_t row_bytes = cols * (rows_dtype == NVFP4_OUT_F32 ? 4 : 2);
+    if (used_rows && tokens > 0x7fffffffll / k) return NVFP4_ERR_SHAPE;  // a mark is a slot's number
+    // marks go where nothing is still to be read: not over weights, and not over rows
+    const int64_t places = used_rows && !overlap(weight, dweight, tokens * k * 4) ? tokens * k : 0;
+    if (used_rows && n_rows > places && overlap(rows, drows, n_rows * row_bytes)) return NVFP4_ERR_INVALID_ARG;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     const int sms = sm100_sms(dev);
@@ -317,7 +325,8 @@ extern "C" nvfp4_status nvfp4_combine_backward(const void* dout_bf16, const void
     cudaError_t err = cudaSuccess;
     bool early = !workspace;
     if (used_rows && n_rows > 0) {
-        const Marks marks{reinterpret_cast<int32_t*>(dweight), slots, static_cast<uint8_t*>(drows), row_bytes};
+        const int64_t slots = tokens * k;
+        const Marks marks{reinterpret_cast<int32_t*>(dweight), places, static_cast<uint8_t*>(drows), row_bytes};
         const auto ctas = [&](int64_t threads) {
             return std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(sms) * 8);
         };

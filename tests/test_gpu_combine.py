@@ -211,3 +211,43 @@ def test_gradients_of_a_routing_with_dropped_slots():
     moe_combine(rows, dataclasses.replace(r, slot_row=slot)).backward(dout)
     rr, _ = R.combine_backward(f64(dout), f64(rows.detach()), host(slot), host(r.weight))
     assert np.all(np.abs(f64(rows.grad) - rr) <= (B + U) * np.abs(rr) + 2.0 ** -134)
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("what,spare", [("rows", 0), ("weight", 0), ("weight", 5)])
+def test_gradients_in_place(f32, what, spare):
+    """drows over rows, or dweight over weight, with slots left out and rows behind the last slot's."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(12)
+    tokens, k, cols = 50, 3, 136
+    rows, rd, slot, w = make(rng, tokens, k, cols, f32, 0.3)
+    n = tokens * k + spare
+    rd = torch.cat([rd, rd[:spare]])
+    dout = to_dev(bits(rng, (tokens, cols)))
+    sd, wd = torch.from_numpy(slot).cuda(), torch.from_numpy(w).cuda()
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    want = nv.combine_backward(dout, rd, sd, wd, off)
+    dr = rd.clone() if what == "rows" else torch.full_like(rd, float("nan"))
+    dw = wd.clone() if what == "weight" else torch.full_like(wd, float("nan"))
+    nv.nvfp4_combine_backward(dout, dr if what == "rows" else rd, nv.NVFP4_OUT_F32 if f32 else nv.NVFP4_OUT_BF16, n, cols,
+                              sd, dw if what == "weight" else wd, tokens, k, off.data_ptr() + 4, dr, dw)
+    assert torch.equal(dr, want[0]) and torch.equal(dw, want[1])
+
+
+def test_more_rows_than_slots():
+    """Rows past the places that dweight has for the slots' numbers, named and not."""
+    import torch
+    import nvfp4_bit_precision_b200 as nv
+    rng = np.random.default_rng(13)
+    rd, dout = to_dev(bits(rng, (1000, 64))), to_dev(bits(rng, (3, 64)))
+    slot = torch.tensor([[999, 2], [5, 600], [-1, 6]], dtype=torch.int32, device="cuda")
+    w = torch.ones((3, 2), device="cuda")
+    off = torch.tensor([0, 1000], dtype=torch.int32, device="cuda")
+    for poison in (float("nan"), 0.0):
+        spoil = torch.full_like(rd, poison)
+        del spoil
+        dr, dw = nv.combine_backward(dout, rd, slot, w, off)
+        ref = torch.zeros_like(rd)
+        ref[[999, 2, 5, 600, 6]] = dout[[0, 0, 1, 1, 2]]
+        assert torch.equal(dr, ref) and float(dw[2, 0]) == 0.0

@@ -222,15 +222,19 @@ def test_captured_gradients_refused_on_the_host(monkeypatch):
 
 
 def test_combine_backward_refuses_gradients_over_the_rows(nv):
-    """With used_rows the slots' numbers pass through drows before rows is read."""
-    def back(rows, dr, used=FAKE, dt=1):
-        return nv._lib.nvfp4_combine_backward(FAKE, rows, dt, 8, 64, FAKE, FAKE, 4, 2, used, dr, FAKE, None, 0, None)
-    at = 1 << 30
-    assert back(at, at) == ARG and back(at, at + 1008) == ARG and back(at + 1008, at) == ARG
-    assert back(at, at + 1024, dt=0) == ARG
+    """With used_rows the slots' numbers pass through drows, where dweight has no place for them, before rows is
+    read."""
+    at, w = 1 << 30, 1 << 34
+
+    def back(rows, dr, used=FAKE, dt=1, n=8, dw=1 << 35):
+        return nv._lib.nvfp4_combine_backward(FAKE, rows, dt, n, 64, FAKE, w, 4, 2, used, dr, dw, None, 0, None)
+    for more in (dict(n=9), dict(dw=w), dict(dw=w + 28), dict(dw=w - 28)):
+        assert back(at, at, **more) == ARG and back(at, at + 896, **more) == ARG and back(at + 896, at, **more) == ARG
+        assert back(at, at + 1152, dt=0, **more) == ARG
     import torch
     if not torch.cuda.is_available():  # nothing is launched
-        for status in (back(at, at + 1024), back(at, at + 2048, dt=0), back(at, at, used=None)):
+        for status in (back(at, at), back(at, at, used=None, n=9), back(at, at + 1152, n=9), back(at, at + 2304, dt=0, n=9),
+                       back(at, at + 1024, dw=w), back(at, at, dw=w + 32)):
             assert status not in (ARG, SHAPE, ALIGN, WORKSPACE)
 
 
@@ -323,3 +327,9 @@ def test_import_leaves_torch_to_first_use():
             "else:\n    raise AssertionError\n"
             "assert nv._matrix(torch.device('cpu'), torch.uint8, 2, 3).shape == (2, 3) and nv.torch is torch\n")
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+
+
+def test_combine_backward_counts_slots_in_31_bits(nv):
+    def back(t, used=FAKE, k=2):
+        return nv._lib.nvfp4_combine_backward(FAKE, FAKE, 1, 8, 64, FAKE, FAKE, t, k, used, 1 << 32, 1 << 35, None, 0, None)
+    assert back(1 << 30) == SHAPE and back((1 << 62) - 1) == SHAPE and back(1 << 28, k=8) == SHAPE
