@@ -191,7 +191,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const float (&l)[EPL]
             if (a.softmax) s[i] *= total;
             const S v = s[i] + (a.bias && e < a.experts ? static_cast<S>(a.bias[e]) : static_cast<S>(0));
             key[i] = l[i] <= kMaskedLogit ? 0 : ordered(v);
-            // FP32.  __expf is off by (2 + 1.16 |x|) ulp, 2^-22 + |x| 2^-22.8 of its
+            // FP32.  __expf is off by (2 + 1.173 |x|) ulp, 2^-22 + |x| 2^-22.7 of its
             // value.  Sigmoid: that times 1 - s, and the sum's and quotient's roundings.
             // Softmax: that and the argument's rounding for the term; in the total the
             // terms' errors are weighted by the scores, whose mean |x| is at most ln 512,
