@@ -572,6 +572,89 @@ nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, int64_t tot
                                 const float* g, int64_t N, int64_t K, int out_dtype, void* D,
                                 int64_t ldd, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * A paged cache of keys and values held in NVFP4 (asector, "NVFP4 and
+ * Blackwell": a local scale per 16-element block on top of one scale per
+ * tensor), blocks along the head dimension: codes q [2][pages][kv_heads]
+ * [page_size][dim / 2] and E4M3 bytes sf [2][pages][kv_heads][page_size]
+ * [dim / 16], the keys before the values.  amax [2] (device FP32): the largest
+ * magnitudes of keys and of values, which fix the two FP32 scales as in
+ * nvfp4_quantize with amax_in (g = amax / 2688; larger values saturate).  Token n
+ * of sequence s is token n % page_size of page table[s][n / page_size].
+ * dim 64, 128 or 256; page_size a power of two from 16 to 1024; q and sf 16-byte
+ * aligned.  nvfp4_dequantize reads keys or values as a row-major tensor of
+ * pages * kv_heads * page_size rows.
+ */
+typedef struct {
+    uint8_t* q;
+    uint8_t* sf;
+    const float* amax;
+    int64_t pages;
+    int kv_heads;
+    int page_size;
+    int dim;
+} nvfp4_kv_cache;
+
+/*
+ * nvfp4_kv_append -- keys and values of new tokens into a cache, keys and queries
+ * turned by their positions on the way.  (The pages name no attention; it is the
+ * step between the products that they quantise.)
+ *   k, v [tokens][kv_heads][dim] bf16 (ld: elements from token to token, hs: from
+ *   head to head; both multiples of 8), token t at place position[t] of sequence
+ *   sequence[t] (NULL: sequence t), device int32.  table [sequences][ldt >=
+ *   table_pages] device int32.
+ * With cos and sin (FP32 [angles][rot / 2], rows by position) the first rot
+ * elements of a head are turned: (a, b) -> (a cos - b sin, b cos + a sin) for the
+ * pairs (x[i], x[i + rot / 2]), or with neighbours = 1 (x[2 i], x[2 i + 1]), exact
+ * up to one rounding to bf16; the keys are then quantised as nvfp4_quantize does it.
+ * q [tokens][heads][dim] is turned likewise into q_out (which may be q, at the same
+ * strides); heads = 0 and NULL without queries.  Without cos, rot = 0.
+ * A token with a negative position or sequence is left out, its row of q_out as it
+ * was.  One whose sequence, place or page does not exist, or whose position is not
+ * below angles, is left out and reported in the optional workspace's status word
+ * (NVFP4_ERR_INDEX).  Of two tokens at one place, each block of 8 codes and each
+ * scale byte is one of theirs.  rot a multiple of 32; pointers 16-byte aligned
+ * (table, position and sequence 4).
+ */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k_bf16, int64_t ldk, int64_t hsk,
+                             const void* v_bf16, int64_t ldv, int64_t hsv, int64_t tokens,
+                             const int32_t* table, int64_t ldt, int64_t sequences,
+                             int64_t table_pages, const int32_t* position, const int32_t* sequence,
+                             const float* cos, const float* sin, int64_t angles, int rot,
+                             int neighbours, const void* q_bf16, int64_t ldq, int64_t hsq, int heads,
+                             void* q_out, int64_t ldo, int64_t hso, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* Workspace bytes of nvfp4_kv_attention; capacity = table_pages * page_size. */
+size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int heads, int kv_heads,
+                                         int dim, int64_t capacity);
+
+/*
+ * nvfp4_kv_attention -- attention of a few query tokens per sequence over a cache,
+ * the queries in bf16 (not quantised), the cached keys and values as they stand:
+ *   out[s][i][h] = sum_n p_n v_n,  p = softmax(scale <q[s][i][h], k_n>)
+ * over the tokens n that query i sees: those up to its own place lengths[s] -
+ * queries + i, of the window (0: all) last ones.  Query heads h belong to key head h
+ * / (heads / kv_heads).  q [sequences][queries][heads][dim] bf16 (strides in
+ * elements, multiples of 8); lengths device int32 [sequences], the queries' own
+ * tokens included; out contiguous bf16; lse (NULL: not wanted) FP32 [sequences]
+ * [queries][heads]: log sum_n exp(scale <q, k_n>).  A query that sees no token (as
+ * in a sequence of length 0) has out 0 and lse -inf.  Softmax and sums are FP32;
+ * the exponentials go into the product with v as FP16, 2^-12 off at most.
+ * The table is read up to a sequence's length.  A page outside the cache counts as
+ * zeros, a length outside 0..table_pages * page_size as the nearer end; both are
+ * reported in the workspace's status word (NVFP4_ERR_INDEX).  Meant for up to about
+ * 16 rows (queries * heads / kv_heads; 8 where dim is 256): the cache is read again
+ * for every so many.  Results do not depend on timing; they may depend on the other
+ * sequences of a call, by the places where a long one is cut.
+ */
+nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh,
+                                int64_t sequences, int queries, int heads,
+                                const nvfp4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                                int64_t table_pages, const int32_t* lengths, float scale,
+                                int64_t window, void* out_bf16, float* lse, void* workspace,
+                                size_t ws_bytes, void* stream);
+
 /* Synchronise `stream` and return the device status word of a workspace
  * (NVFP4_OK, NVFP4_ERR_TIMEOUT or NVFP4_ERR_INDEX); clears it. */
 nvfp4_status nvfp4_workspace_status(void* workspace, void* stream);

@@ -66,7 +66,8 @@ EXPORTED = [
     "mxfp8_combine", "nvfp4_gemm_cycles", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward",
     "nvfp4_rmsnorm_backward_workspace_size", "nvfp4_route", "nvfp4_route_backward",
     "nvfp4_route_workspace_size", "nvfp4_combine", "nvfp4_combine_backward",
-    "nvfp4_combine_backward_workspace_size", "nvfp4_gemv", "nvfp4_grouped_gemv",
+    "nvfp4_combine_backward_workspace_size", "nvfp4_gemv", "nvfp4_grouped_gemv", "nvfp4_kv_append",
+    "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size",
 ]
 
 
@@ -92,6 +93,15 @@ class RouteParams(ctypes.Structure):
         ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int),
         ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
         ("scale", ctypes.c_float),
+    ]
+
+
+class KVCacheView(ctypes.Structure):
+    """Mirror of ``nvfp4_kv_cache`` (include/nvfp4.h)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+        ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("dim", ctypes.c_int),
     ]
 
 
@@ -153,12 +163,20 @@ _lib.nvfp4_combine_backward_workspace_size.restype = _SZ
 _lib.nvfp4_gemv.argtypes = [_P, _I64, _I64, _P, _P, _P, _I64, _I64, _INT, _P, _I64, _P]
 _lib.nvfp4_grouped_gemv.argtypes = [_INT, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _INT, _P,
                                     _I64, _P, _SZ, _P]
+_lib.nvfp4_kv_append.argtypes = [ctypes.POINTER(KVCacheView), _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64,
+                                 _I64, _I64, _P, _P, _P, _P, _I64, _INT, _INT, _P, _I64, _I64, _INT, _P, _I64,
+                                 _I64, _P, _SZ, _P]
+_lib.nvfp4_kv_attention.argtypes = [_P, _I64, _I64, _I64, _I64, _INT, _INT, ctypes.POINTER(KVCacheView), _P, _I64,
+                                    _I64, _P, _F32, _I64, _P, _P, _P, _SZ, _P]
+_lib.nvfp4_kv_attention_workspace_size.argtypes = [_I64, _INT, _INT, _INT, _INT, _I64]
+_lib.nvfp4_kv_attention_workspace_size.restype = _SZ
 for _n in ("nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_quantize", "mxfp4_quantize",
            "nvfp4_dequantize", "nvfp4_gemm", "mxfp8_gemm", "mxfp4_gemm", "mxfp8_combine",
            "nvfp4_grouped_gemm", "nvfp4_gather_rows", "nvfp4_workspace_status",
            "nvfp4_quantize_noalloc_status", "nvfp4_gemm_cycles", "nvfp4_rmsnorm",
            "nvfp4_rmsnorm_backward", "nvfp4_route", "nvfp4_route_backward", "nvfp4_combine",
-           "nvfp4_combine_backward", "nvfp4_gemv", "nvfp4_grouped_gemv"):
+           "nvfp4_combine_backward", "nvfp4_gemv", "nvfp4_grouped_gemv", "nvfp4_kv_append",
+           "nvfp4_kv_attention"):
     getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -319,6 +337,27 @@ def nvfp4_combine_backward(dout, rows, rows_dtype, n_rows, cols, slot_row, weigh
                                        _ptr(weight), tokens, k, _ptr(used_rows), _ptr(drows), _ptr(dweight),
                                        _ptr(workspace), ws_bytes, _stream(stream)),
            "nvfp4_combine_backward")
+
+
+def nvfp4_kv_append(cache: KVCacheView, k, ldk, hsk, v, ldv, hsv, tokens, table, ldt, sequences, table_pages,
+                    position, sequence, cos, sin, angles, rot, neighbours, q, ldq, hsq, heads, q_out, ldo, hso,
+                    workspace=None, ws_bytes=0, stream=None) -> None:
+    _check(_lib.nvfp4_kv_append(ctypes.byref(cache), _ptr(k), ldk, hsk, _ptr(v), ldv, hsv, tokens, _ptr(table), ldt,
+                                sequences, table_pages, _ptr(position), _ptr(sequence), _ptr(cos), _ptr(sin), angles,
+                                rot, neighbours, _ptr(q), ldq, hsq, heads, _ptr(q_out), ldo, hso, _ptr(workspace),
+                                ws_bytes, _stream(stream)), "nvfp4_kv_append")
+
+
+def nvfp4_kv_attention(q, ldb, ldi, ldh, sequences, queries, heads, cache: KVCacheView, table, ldt, table_pages,
+                       lengths, scale, window, out, lse, workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_kv_attention(_ptr(q), ldb, ldi, ldh, sequences, queries, heads, ctypes.byref(cache),
+                                   _ptr(table), ldt, table_pages, _ptr(lengths), scale, window, _ptr(out), _ptr(lse),
+                                   _ptr(workspace), ws_bytes, _stream(stream)), "nvfp4_kv_attention")
+
+
+def nvfp4_kv_attention_workspace_size(sequences: int, queries: int, heads: int, kv_heads: int, dim: int,
+                                      capacity: int) -> int:
+    return _lib.nvfp4_kv_attention_workspace_size(sequences, queries, heads, kv_heads, dim, capacity)
 
 
 def nvfp4_gemv(x, ldx, rows, q, sf, g, N, K, out_dtype, D, ldd, stream=None) -> None:
@@ -941,3 +980,158 @@ def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtyp
                                    qb.data_ptr(), sfb.data_ptr(), gb.data_ptr(), N, K, out_dtype,
                                    out.data_ptr(), ldd, wp, nb, _raw_stream(dev)), "nvfp4_grouped_gemv")
     return out
+
+
+# ------------------------------------------------- the cache of a decoding step, and attention over it
+@dataclass
+class KVCache:
+    """A paged cache of keys and values in NVFP4, blocks along the head dimension: codes uint8 [2, pages, kv_heads,
+    page_size, dim/2] and E4M3 bytes uint8 [2, pages, kv_heads, page_size, dim/16], the keys first; amax f32 [2], the
+    largest magnitudes that keys and values are expected to have (larger ones saturate), and g = amax / 2688."""
+    q: object
+    sf: object
+    amax: object
+    g: object
+
+    def _half(self, which: int) -> NVFP4Tensor:
+        _, pages, heads, size, half = self.q.shape
+        rows = pages * heads * size
+        return NVFP4Tensor(self.q[which].view(rows, half), self.sf[which].view(rows, half // 8),
+                           self.g[which:which + 1], rows, 2 * half, NVFP4_SF_ROWMAJOR)
+
+    def keys(self) -> NVFP4Tensor:
+        """The keys as one matrix [pages * kv_heads * page_size, dim], a view (for ``dequantize``)."""
+        return self._half(0)
+
+    def values(self) -> NVFP4Tensor:
+        """The values, likewise."""
+        return self._half(1)
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, dim: int, amax_k: float = 2688.0, amax_v: float = 2688.0,
+             device=None) -> KVCache:
+    """A cache of zeros."""
+    dev = torch.device("cuda") if device is None else device
+    amax = torch.tensor([amax_k, amax_v], dtype=torch.float32)
+    # (2688 as a tensor: a division by a number may come out as a product with its reciprocal)
+    g = torch.where(amax > 0, amax / torch.full_like(amax, 2688.0), 1.0)
+    return KVCache(torch.zeros((2, pages, kv_heads, page_size, dim // 2), dtype=torch.uint8, device=dev),
+                   torch.zeros((2, pages, kv_heads, page_size, dim // 16), dtype=torch.uint8, device=dev),
+                   amax.to(dev), g.to(dev))
+
+
+def _cache_view(name: str, cache: KVCache) -> KVCacheView:
+    q, sf = cache.q, cache.sf
+    shape = q.shape
+    if len(shape) != 5 or shape[0] != 2:
+        raise ValueError(f"{name}: cache.q [2, pages, kv_heads, page_size, dim/2] expected, got {tuple(shape)}")
+    _flat(f"{name}: cache.q", q, torch.uint8, *shape)
+    _flat(f"{name}: cache.sf", sf, torch.uint8, 2, shape[1], shape[2], shape[3], shape[4] // 8)
+    _flat(f"{name}: cache.amax", cache.amax, torch.float32, 2)
+    return KVCacheView(q.data_ptr(), sf.data_ptr(), cache.amax.data_ptr(), shape[1], shape[2], shape[3], 2 * shape[4])
+
+
+def _table_of(name: str, table):
+    _need(table.dtype is torch.int32 and table.dim() == 2, f"{name}: int32 table [sequences, pages] expected")
+    n, pages = table.shape
+    if table.is_contiguous():
+        return n, pages, pages
+    _need(pages <= 1 or table.stride(1) == 1, f"{name}: rows of the table must be contiguous")
+    return n, pages, table.stride(0) if n > 1 else pages
+
+
+def _heads_of(name: str, t, tokens, heads, dim):
+    """A bf16 tensor [tokens, heads, dim] with contiguous heads; returns its strides in elements."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bfloat16 [tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
+    n, h, d = t.shape
+    if n != tokens or d != dim or (heads is not None and h != heads):
+        raise ValueError(f"{name}: [{tokens}, {heads or 'heads'}, {dim}] expected, got {tuple(t.shape)}")
+    _need(t.stride(2) == 1, f"{name}: heads must be contiguous")
+    return t.stride(0) if n > 1 else h * d, t.stride(1) if h > 1 else d
+
+
+def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None, sin=None, interleaved: bool = False,
+              q=None, q_out=None, workspace=None, stream=None):
+    """Keys and values of new tokens (bf16 [tokens, kv_heads, dim]) into the cache: token t at place ``position[t]`` of
+    sequence ``sequence[t]`` (sequence t without it), whose pages are ``table[sequence]`` (all int32).  With cos and
+    sin (f32 [angles, rot/2], rows by position) the first rot elements of the keys' heads are turned by their
+    position, pairs (i, i + rot/2) or with ``interleaved`` (2i, 2i + 1), and q's (bf16 [tokens, heads, dim]) into
+    ``q_out`` (a new tensor; q itself may be given), which is returned.  Tokens with a negative position or sequence are
+    left out (their rows of q_out too); tokens without a place in the cache are left out and reported in the optional
+    ``workspace`` (256 bytes)."""
+    if stream is not None:
+        with _on(stream):
+            return kv_append(cache, k, v, table, position, sequence, cos=cos, sin=sin, interleaved=interleaved, q=q,
+                             q_out=q_out, workspace=workspace)
+    dev = _one_device("kv_append", k, v, cache.q, cache.sf, cache.amax, table, position, sequence, cos, sin, q, q_out,
+                      workspace)
+    view = _cache_view("kv_append", cache)
+    tokens, dim = k.shape[0], view.dim
+    ldk, hsk = _heads_of("kv_append: k", k, tokens, view.kv_heads, dim)
+    ldv, hsv = _heads_of("kv_append: v", v, tokens, view.kv_heads, dim)
+    sequences, pages, ldt = _table_of("kv_append", table)
+    _flat("kv_append: position", position, torch.int32, tokens)
+    sp = cp = np = qp = op = wp = None
+    if sequence is not None:
+        _flat("kv_append: sequence", sequence, torch.int32, tokens)
+        sp = sequence.data_ptr()
+    angles = rot = heads = ldq = hsq = ldo = hso = nb = 0
+    if cos is not None or sin is not None:
+        _need(cos is not None and sin is not None and cos.dim() == 2, "kv_append: cos and sin [angles, rot/2] go together")
+        angles, rot = cos.shape[0], 2 * cos.shape[1]
+        _flat("kv_append: cos", cos, torch.float32, angles, rot // 2)
+        _flat("kv_append: sin", sin, torch.float32, angles, rot // 2)
+        cp, np = cos.data_ptr(), sin.data_ptr()
+    if q is not None:
+        _need(cp is not None, "kv_append: q is turned by cos and sin, which are missing")
+        heads = q.shape[1] if q.dim() == 3 else 0
+        ldq, hsq = _heads_of("kv_append: q", q, tokens, None, dim)
+        if q_out is None:
+            q_out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+        ldo, hso = _heads_of("kv_append: q_out", q_out, tokens, heads, dim)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    else:
+        _need(q_out is None, "kv_append: q_out without q")
+    if workspace is not None:
+        wp, nb = workspace.data_ptr(), workspace.numel()
+    _check(_lib.nvfp4_kv_append(ctypes.byref(view), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, tokens,
+                                table.data_ptr(), ldt, sequences, pages, position.data_ptr(), sp, cp, np, angles, rot,
+                                1 if interleaved else 0, qp, ldq, hsq, heads, op, ldo, hso, wp, nb, _raw_stream(dev)),
+           "nvfp4_kv_append")
+    return q_out
+
+
+def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = None, window: int = 0, lse: bool = False,
+                 workspace=None, stream=None):
+    """Attention of the last tokens of each sequence, q bf16 [sequences, queries, heads, dim], over the cache: query i
+    sees the cached tokens up to its own place lengths[s] - queries + i (lengths int32 [sequences], the queries' tokens
+    included), of them the ``window`` last ones (0: all).  Query heads share the kv heads in order; scale is 1 /
+    sqrt(dim) without one.  Returns bf16 [sequences, queries, heads, dim]; with ``lse`` also the logarithm of each
+    row's sum of exponentials, f32 [sequences, queries, heads].  Rows that see nothing are 0, their lse -inf.
+    ``workspace``: nvfp4_kv_attention_workspace_size bytes, which then hold the status word too."""
+    if stream is not None:
+        with _on(stream):
+            return kv_attention(q, cache, table, lengths, scale=scale, window=window, lse=lse, workspace=workspace)
+    dev = _one_device("kv_attention", q, cache.q, cache.sf, cache.amax, table, lengths, workspace)
+    view = _cache_view("kv_attention", cache)
+    if q.dtype is not torch.bfloat16 or q.dim() != 4 or q.shape[3] != view.dim:
+        raise ValueError(f"kv_attention: q bfloat16 [sequences, queries, heads, {view.dim}] expected, got {q.dtype} "
+                         f"{tuple(q.shape)}")
+    n, new, heads, dim = q.shape
+    _need(q.stride(3) == 1, "kv_attention: heads of q must be contiguous")
+    sequences, pages, ldt = _table_of("kv_attention", table)
+    _need(sequences == n, f"kv_attention: a table of {sequences} sequences for {n}")
+    _flat("kv_attention: lengths", lengths, torch.int32, n)
+    size = nvfp4_kv_attention_workspace_size(n, new, heads, view.kv_heads, dim, pages * view.page_size)
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    out = torch.empty((n, new, heads, dim), dtype=torch.bfloat16, device=dev)
+    sums = torch.empty((n, new, heads), dtype=torch.float32, device=dev) if lse else None
+    _check(_lib.nvfp4_kv_attention(q.data_ptr(), q.stride(0) if n > 1 else 0, q.stride(1) if new > 1 else 0,
+                                   q.stride(2) if heads > 1 else dim, n, new, heads, ctypes.byref(view),
+                                   table.data_ptr(), ldt, pages, lengths.data_ptr(),
+                                   dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                   sums.data_ptr() if lse else None, workspace.data_ptr(), workspace.numel(),
+                                   _raw_stream(dev)), "nvfp4_kv_attention")
+    return (out, sums) if lse else out

@@ -14,8 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["quantize.cu", "gemm.cu", "mxfp4.cu", "moe_comm.cu", "norm.cu", "route.cu", "combine.cu",
-           "gemv.cu"]
-HEADERS = ["common.cuh", "gemv_plan.h"]
+           "gemv.cu", "kv_append.cu", "kv_attention.cu"]
+HEADERS = ["common.cuh", "gemv_plan.h", "kv_cache.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

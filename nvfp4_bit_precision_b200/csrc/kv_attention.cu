@@ -1,0 +1,751 @@
+// kv_attention.cu -- attention of a few query tokens per sequence over a paged NVFP4
+// cache.
+//
+//   x_j = scale * <q, k_j>,  o = sum_j exp(x_j) v_j / sum_j exp(x_j),  lse = log sum_j exp(x_j)
+// over the cached tokens j that a query sees.  One pass over the cache with the running
+// maximum and sum of the softmax; work is split over the length, and the parts of a
+// head are joined by a second kernel.
+#include "kv_cache.cuh"
+
+#include <algorithm>
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kSlice = 32;                // tokens of a warp's step
+constexpr int kTile = kWarps * kSlice;    // tokens by which work is dealt out
+constexpr float kUp = 14.0f;              // exponentials are 2^14 at their largest: FP16 keeps those down to 2^-28 whole
+constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
+constexpr float kMinusInf = -__builtin_huge_valf();
+
+struct AttendArgs {
+    CacheView cache;
+    const uint16_t* q;
+    int64_t ldb, ldi, ldh;     // of q: from sequence to sequence, token to token, head to head, in elements
+    uint16_t* out;             // [sequences][queries][heads][dim]
+    float* lse;                // [sequences][queries][heads] or NULL
+    const int32_t* table;
+    int64_t ldt;
+    const int32_t* lengths;
+    int sequences, table_pages, queries, heads, group;
+    int rows, blocks, block_rows;  // rows (query, head of the group) of a key head, cut into blocks of so many
+    int window;
+    float scale;
+    int4* records;             // of each CTA: the item that it begins and others end (item, last CTA, -, whether)
+    float2* part_ml;           // [2 CTAs][block_rows] maximum and sum of a part
+    float* part_o;             // [2 CTAs][block_rows][dim]
+    uint32_t* status;
+};
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(two)));
+    return d;
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8x8 matrix of 16-bit numbers, a row in four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a sequence's rows see of it: tokens [begin, length), from a 32-token boundary, as tiles.
+struct Span {
+    int begin, length, tiles;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int seq)
+{
+    const int64_t most = static_cast<int64_t>(a.table_pages) << a.cache.page_shift;
+    int n = a.lengths[seq];
+    if (n < 0 || n > most) {
+        record_status(a.status, NVFP4_ERR_INDEX);
+        n = n < 0 ? 0 : static_cast<int>(most);
+    }
+    int begin = 0;
+    if (a.window > 0) begin = max(0, n - a.queries + 1 - a.window) & ~(kSlice - 1);
+    return {begin, n, max(1, (n - begin + kTile - 1) / kTile)};
+}
+
+template <int DIM, int NT>
+struct Shape {
+    static constexpr int kCodes = kSlice * DIM / 2, kScales = kSlice * DIM / 16;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kStages = DIM == 256 ? 2 : 3;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kRows = 8 * NT;
+    static_assert(kRing >= kRows * DIM * 4, "a warp's sums take its ring's place");
+    static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kRing;
+    static constexpr int kCtas = DIM == 128 && NT == 2 ? 3 : DIM == 256 ? 3 : 4;  // of a multiprocessor
+};
+
+template <int DIM, int NT>
+__global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_kernel(const AttendArgs a)
+{
+    using S = Shape<DIM, NT>;
+    constexpr int kSteps = DIM / 16;       // matrix instructions over the head dimension; 16-blocks of a token
+    constexpr int kLaneCodes = DIM / 8;    // bytes of a token's keys that a lane reads
+    constexpr int kRows = S::kRows;
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    __shared__ int s_sum[kWarps];
+    __shared__ int s_seq, s_rel;
+    __shared__ float2 s_ml[kWarps][kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane >> 2, t = lane & 3;
+    uint8_t* const my = s_dyn + warp * S::kRing;
+    const uint32_t ring = smem_addr(my);
+    const int items = a.cache.kv_heads * a.blocks;  // of a sequence
+
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    // All tiles of all items, sequence by sequence; this CTA's equal run of them, and
+    // where it begins: each thread adds up some sequences.
+    const int per = (a.sequences + 32 * kWarps - 1) / (32 * kWarps);
+    const int s0 = min(a.sequences, static_cast<int>(threadIdx.x) * per), s1 = min(a.sequences, s0 + per);
+    int mine = 0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) mine += span_of(a, s).tiles * items;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += s_sum[w];
+        all += s_sum[w];
+    }
+    const int ctas = gridDim.x, each = all / ctas, more = all - each * ctas;
+    int f = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), more);
+    const int f1 = f + each + (static_cast<int>(blockIdx.x) < more ? 1 : 0);
+    if (f >= upto - mine && f < upto) {
+        int s = s0, at = f - (upto - mine);
+#pragma unroll 1
+        for (;; ++s) {
+            const int n = span_of(a, s).tiles * items;
+            if (at < n) break;
+            at -= n;
+        }
+        s_seq = s, s_rel = at;
+    }
+    if (threadIdx.x == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    if (f >= f1) return;
+    int seq = s_seq, rel = s_rel;
+    float unused, gk, gv;
+    global_scales(a.cache.amax[0], unused, gk);
+    global_scales(a.cache.amax[1], unused, gv);
+
+#pragma unroll 1
+    while (f < f1) {
+        const Span span = span_of(a, seq);
+        const int item = rel / span.tiles, first_tile = rel - item * span.tiles;
+        const int take = min(span.tiles - first_tile, f1 - f);
+        const bool whole = take == span.tiles;
+        const int head = item / a.blocks, row0 = (item - head * a.blocks) * a.block_rows;
+        const int rows = min(a.block_rows, a.rows - row0);
+        const int begin = span.begin + first_tile * kTile, end = min(span.length, begin + take * kTile);
+        // this warp's slices
+        const int slices = (max(end - begin, 0) + kSlice - 1) / kSlice;
+        const int sl0 = slices * warp / kWarps, sl1 = slices * (warp + 1) / kWarps;
+        const int token0 = begin + sl0 * kSlice;
+
+        // Copies of a slice: codes and scales of 32 tokens' keys and values.  Pages of 32
+        // runs of 16 tokens are at hand at a time, one in each lane.
+        int page = -1, pages_from = 0;
+        const auto look_up = [&](int run) {  // this and the 31 runs of 16 tokens behind
+            const int index = (run + lane) >> (a.cache.page_shift - 4);
+            page = -1;
+            if ((run + lane) * 16 < end) {
+                page = a.table[seq * a.ldt + index];
+                if (page < 0 || page >= a.cache.pages) {
+                    record_status(a.status, NVFP4_ERR_INDEX);
+                    page = -1;
+                }
+            }
+            pages_from = run;
+        };
+        int next = sl0, put = 0;
+        const auto copy_slice = [&]() {
+            if (next < sl1) {
+                const int run = (begin + next * kSlice) / 16;
+                if (run - pages_from >= 32) look_up(run);
+                const uint32_t dst = ring + put * S::kStage;
+                const int in_page = (1 << a.cache.page_shift) - 1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int p = __shfl_sync(0xffffffffu, page, run + half - pages_from);
+                    const int64_t token = p < 0 ? 0
+                                                : ((static_cast<int64_t>(p) * a.cache.kv_heads + head) << a.cache.page_shift) +
+                                                      ((run + half) * 16 & in_page);
+                    const uint8_t* const q = a.cache.q + token * (DIM / 2);
+                    const uint8_t* const sf = a.cache.sf + token * (DIM / 16);
+                    // 16 tokens of DIM / 32 vectors of 16 codes' bytes each
+#pragma unroll
+                    for (int c = lane; c < DIM / 2; c += 32) {
+                        constexpr int kRow = DIM / 32;
+                        const int tok = c / kRow, col = c % kRow;
+                        // keys: rows in order; values: the even tokens of eight before the odd ones (see below)
+                        const int vtok = (tok & 8) | (tok & 1) << 2 | (tok & 6) >> 1;
+                        int kcol = col, vcol = col;
+                        if (DIM == 128) vcol ^= vtok & 2;
+                        if (DIM == 256) kcol ^= tok & 1, vcol ^= 2 * (vtok & 3);
+                        copy16_async(dst + half * (S::kCodes / 2) + (tok * kRow + kcol) * 16, q + c * 16, p >= 0);
+                        copy16_async(dst + S::kCodes + half * (S::kCodes / 2) + (vtok * kRow + vcol) * 16,
+                                     q + a.cache.half * (DIM / 2) + c * 16, p >= 0);
+                    }
+                    constexpr int kVecs = DIM / 16;  // 16 tokens' scales, in vectors
+                    const int c = lane % kVecs;
+                    if (lane < 2 * kVecs) {
+                        const bool v = lane >= kVecs;
+                        copy16_async(dst + 2 * S::kCodes + (v ? S::kScales : 0) + half * (S::kScales / 2) + c * 16,
+                                     sf + (v ? a.cache.half * (DIM / 16) : 0) + c * 16, p >= 0);
+                    }
+                }
+                ++next;
+            }
+            put = put + 1 == S::kStages ? 0 : put + 1;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if (sl0 < sl1) look_up(token0 / 16);
+#pragma unroll 1
+        for (int i = 0; i < S::kStages - 1; ++i) copy_slice();
+
+        // Queries as FP16, each row at the power of two that brings its largest magnitude
+        // to [2^14, 2^15) (as in the few-token products): of step s, lane (r, t) has row r's
+        // elements t DIM / 4 + 4 s + 0..3.
+        uint32_t qf[NT][kSteps][2];
+        float by[NT][2];       // factors on the products of rows 2 t, 2 t + 1: to base-2 logarithms
+        int from[NT][2], to[NT][2];  // tokens that those rows see
+        int all_from = 0, all_to = 0x7fffffff;
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+            const int row = 8 * b + r, i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
+            uint4 v[kSteps / 2];
+            uint32_t top = 0;
+#pragma unroll
+            for (int s = 0; s < kSteps / 2; ++s) {
+                v[s] = make_uint4(0, 0, 0, 0);
+                if (row < rows)
+                    v[s] = *reinterpret_cast<const uint4*>(a.q + seq * a.ldb + i * a.ldi + (head * a.group + h) * a.ldh +
+                                                           t * (DIM / 4) + 8 * s);
+                const uint32_t m = __vmaxu2(
+                    __vimax3_u16x2(v[s].x & 0x7FFF7FFFu, v[s].y & 0x7FFF7FFFu, v[s].z & 0x7FFF7FFFu), v[s].w & 0x7FFF7FFFu);
+                top = max(top, max(m & 0xFFFFu, m >> 16));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t ex = min(max(top >> 7, 15u), 254u);
+            const float up = __uint_as_float((268u - ex) << 23);
+#pragma unroll
+            for (int s = 0; s < kSteps / 2; ++s) {
+                float x[8];
+                unpack8(v[s], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 two = __floats2half2_rn(x[2 * j] * up, x[2 * j + 1] * up);
+                    qf[b][2 * s + j / 2][j & 1] = *reinterpret_cast<const uint32_t*>(&two);
+                }
+            }
+            // scale g log2(e), then the row's power of two
+            const float down = __uint_as_float((ex - 14u) << 23);
+            const float f2 = a.scale * gk * 1.44269502162933349609375f;
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+                by[b][i2] = f2 * __shfl_sync(0xffffffffu, down, (2 * t + i2) * 4);
+                const int n = 8 * b + 2 * t + i2;
+                const int last = span.length - a.queries + (row0 + min(n, rows - 1)) / a.group;
+                to[b][i2] = last + 1;
+                from[b][i2] = a.window > 0 ? max(0, last + 1 - a.window) : 0;
+            }
+        }
+        {   // what every row sees; rows are in the queries' order
+            const int low = span.length - a.queries + row0 / a.group;
+            const int high = span.length - a.queries + (row0 + rows - 1) / a.group;
+            all_to = low + 1;
+            all_from = a.window > 0 ? max(0, high + 1 - a.window) : 0;
+        }
+        float top[NT][2], sum[NT][2], o[NT][kSteps][4];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+            top[b][0] = top[b][1] = kMinusInf;
+            sum[b][0] = sum[b][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
+        }
+
+        int get = 0;
+#pragma unroll 1
+        for (int sl = sl0; sl < sl1; ++sl) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+            __syncwarp();  // this slice has come for every lane, and every lane is done with the last one
+            copy_slice();
+            const uint8_t* const stage = my + get * S::kStage;
+            get = get + 1 == S::kStages ? 0 : get + 1;
+            const int place = begin + sl * kSlice;  // of the first token
+            const bool edge = place < all_from || place + kSlice > min(all_to, end);
+
+            // x: 32 tokens x rows; lane (r, t): tokens r, r + 8 (+ 16), rows 2 t, 2 t + 1
+            float x[2][NT][4] = {};
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t code[2][kLaneCodes / 4], sc[2][DIM / 64];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int tok = 16 * m + 8 * h + r;
+                    const uint8_t* const row = stage + tok * (DIM / 2);
+                    if constexpr (DIM == 64) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(row + t * 8);
+                        code[h][0] = w.x, code[h][1] = w.y;
+                        const uint32_t two = e4m3x2_f16(stage[2 * S::kCodes + tok * 4 + t]);
+                        sc[h][0] = __byte_perm(two, 0, 0x1010);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < DIM / 128; ++v) {
+                            const int col = DIM == 256 ? (2 * t + v) ^ (r & 1) : t;
+                            const uint4 w = *reinterpret_cast<const uint4*>(row + col * 16);
+                            code[h][4 * v] = w.x, code[h][4 * v + 1] = w.y, code[h][4 * v + 2] = w.z, code[h][4 * v + 3] = w.w;
+                            const uint32_t two = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(
+                                stage + 2 * S::kCodes + tok * kSteps + t * (DIM / 64) + 2 * v));
+                            sc[h][2 * v] = __byte_perm(two, 0, 0x1010);
+                            sc[h][2 * v + 1] = __byte_perm(two, 0, 0x3232);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < kLaneCodes / 4; ++w) {
+                    uint32_t v[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        e2m1x8_f16(code[h][w], v[h]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[h][i] = mul_f16x2(v[h][i], sc[h][w / 2]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        mma_16816(x[m][b], v[0][0], v[1][0], v[0][1], v[1][1], qf[b][2 * w][0], qf[b][2 * w][1]);
+                        mma_16816(x[m][b], v[0][2], v[1][2], v[0][3], v[1][3], qf[b][2 * w + 1][0], qf[b][2 * w + 1][1]);
+                    }
+                }
+            }
+            uint32_t p[2][NT][2];  // exponentials, FP16: row r, tokens 2 t, 2 t + 1 (+ 8)
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                float high[2] = {kMinusInf, kMinusInf};
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& v = x[m][b][i];
+                        v *= by[b][i & 1];
+                        if (edge) {
+                            const int at = place + 16 * m + 8 * (i >> 1) + r;
+                            if (at < from[b][i & 1] || at >= min(to[b][i & 1], end)) v = kMinusInf;
+                        }
+                        high[i & 1] = fmaxf(high[i & 1], v);
+                    }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    high[0] = fmaxf(high[0], __shfl_xor_sync(0xffffffffu, high[0], d));
+                    high[1] = fmaxf(high[1], __shfl_xor_sync(0xffffffffu, high[1], d));
+                }
+                float base[2];
+                bool rises = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (high[i] > top[b][i]) rises = true;
+                }
+                if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float now = fmaxf(top[b][i], high[i]);
+                        const float less = now == top[b][i] ? 1.0f : exp2_fast(top[b][i] - now);  // (0 from nothing seen)
+                        top[b][i] = now;
+                        sum[b][i] *= less;
+#pragma unroll
+                        for (int s = 0; s < kSteps; ++s) o[b][s][i] *= less, o[b][s][2 + i] *= less;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) base[i] = top[b][i] == kMinusInf ? 0.0f : top[b][i] - kUp;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[m][b][i] = exp2_fast(x[m][b][i] - base[i & 1]);
+                        sum[b][i & 1] += x[m][b][i];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const __half2 two = __floats2half2_rn(x[m][b][2 * h], x[m][b][2 * h + 1]);
+                        p[m][b][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&two));
+                    }
+                }
+            }
+            // o += p v.  Lane (r, t) reads, of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the 16-block (half of
+            // one, two) number r: the pairs of tokens that an operand register holds are put
+            // together from two tokens' codes before these are converted.
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                constexpr int kWords = DIM / 128 > 0 ? DIM / 64 : 1;  // of a token, eight codes each
+                constexpr int kBlocks = DIM == 256 ? 2 : 1;
+                uint32_t code[4][kWords], byte[4][kBlocks];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = 16 * m + 8 * (j >> 1) + 2 * t + (j & 1);
+                    const int slot = 16 * m + 8 * (j >> 1) + 4 * (j & 1) + t;
+                    const uint8_t* const row = stage + S::kCodes + slot * (DIM / 2);
+                    if constexpr (DIM == 64) {
+                        code[j][0] = *reinterpret_cast<const uint32_t*>(row + r * 4);
+                        byte[j][0] = stage[2 * S::kCodes + S::kScales + tok * 4 + (r >> 1)];
+                    } else if constexpr (DIM == 128) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ (slot & 2)) * 16 + (r & 1) * 8));
+                        code[j][0] = w.x, code[j][1] = w.y;
+                        byte[j][0] = stage[2 * S::kCodes + S::kScales + tok * 8 + r];
+                    } else {
+                        const uint4 w = *reinterpret_cast<const uint4*>(row + (r ^ 2 * (slot & 3)) * 16);
+                        code[j][0] = w.x, code[j][1] = w.y, code[j][2] = w.z, code[j][3] = w.w;
+                        const uint32_t two =
+                            *reinterpret_cast<const uint16_t*>(stage + 2 * S::kCodes + S::kScales + tok * 16 + 2 * r);
+                        byte[j][0] = two & 0xFFu, byte[j][1] = two >> 8;
+                    }
+                }
+                if (edge) {
+                    // Tokens that no row sees count as zeros.  A scale that is NaN must not reach, as 0 x NaN,
+                    // rows that do not see its token: it goes to those that do here.
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) {
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = 8 * (j >> 1) + 2 * t + (j & 1);
+                            if (place + 16 * m + at >= end) byte[j][k] = 0;
+                            if ((byte[j][k] & 0x7Fu) == 0x7Fu) bad |= 1u << at, byte[j][k] = 0;
+                        }
+                        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+                        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+                        if (bad) {
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+#pragma unroll 1
+                                    for (int at = 0; at < 16; ++at) {
+                                        const int token = place + 16 * m + at;
+                                        if ((bad >> at & 1) && token >= from[b][i] && token < to[b][i]) {
+#pragma unroll
+                                            for (int s = k * (kSteps / kBlocks); s < (k + 1) * (kSteps / kBlocks); ++s)
+                                                o[b][s][i] = o[b][s][2 + i] = __int_as_float(0x7fffffff);
+                                        }
+                                    }
+                        }
+                    }
+                }
+                uint32_t sc[2][kBlocks];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) sc[h][k] = e4m3x2_f16(byte[2 * h][k] | byte[2 * h + 1][k] << 8);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    uint32_t even[2][4], odd[2][4];  // elements 2 i and 2 i + 1 of eight
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t one = code[2 * h][w], two = code[2 * h + 1][w];
+                        e2m1x8_f16((one & 0x0F0F0F0Fu) | ((two << 4) & 0xF0F0F0F0u), even[h]);
+                        e2m1x8_f16(((one >> 4) & 0x0F0F0F0Fu) | (two & 0xF0F0F0F0u), odd[h]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            even[h][i] = mul_f16x2(even[h][i], sc[h][w * kBlocks / kWords]);
+                            odd[h][i] = mul_f16x2(odd[h][i], sc[h][w * kBlocks / kWords]);
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_16816(o[b][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], p[m][b][0], p[m][b][1]);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+
+        // The warps' parts, joined: rows' sums of lane (r, t) are elements r DIM / 8.. of rows
+        // 2 t, 2 t + 1.
+        float* const s_o = reinterpret_cast<float*>(my);
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = sum[b][i];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                const int row = 8 * b + 2 * t + i;
+                if (r == 0) s_ml[warp][row] = make_float2(top[b][i], v);
+                if (sl0 < sl1) {
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+                        *reinterpret_cast<float2*>(s_o + row * DIM + r * (DIM / 8) + 2 * s) = make_float2(o[b][s][i], o[b][s][2 + i]);
+                }
+            }
+        __syncthreads();
+        const int slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
+        if (!whole && first_tile == 0 && threadIdx.x == 0) {
+            const int last = f + span.tiles - 1, cut = more * (each + 1);
+            a.records[blockIdx.x] = make_int4(item, last < cut ? last / (each + 1) : more + (last - cut) / each, seq, 1);
+        }
+#pragma unroll 1
+        for (int c = threadIdx.x; c < rows * (DIM / 4); c += 32 * kWarps) {
+            const int row = c / (DIM / 4), d = 4 * (c % (DIM / 4));
+            float high = kMinusInf;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) high = fmaxf(high, s_ml[w][row].x);
+            const float base = high == kMinusInf ? 0.0f : high;
+            float l = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (slices * w / kWarps == slices * (w + 1) / kWarps) continue;  // that warp had nothing to do
+                const float2 ml = s_ml[w][row];
+                const float part = exp2_fast(ml.x - base);
+                const float4 u = *reinterpret_cast<const float4*>(s_dyn + w * S::kRing + (row * DIM + d) * 4);
+                l += ml.y * part;
+                v.x += u.x * part, v.y += u.y * part, v.z += u.z * part, v.w += u.w * part;
+            }
+            if (whole) {
+                const float n = l == 0.0f ? 0.0f : gv / l;
+                const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
+                const int64_t at = (static_cast<int64_t>(seq) * a.queries + i) * a.heads + head * a.group + h;
+                *reinterpret_cast<uint2*>(a.out + at * DIM + d) = make_uint2(pack2(v.x * n, v.y * n), pack2(v.z * n, v.w * n));
+                if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+            } else {
+                *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * a.block_rows + row) * DIM + d) = v;
+                if (d == 0) a.part_ml[static_cast<int64_t>(slot) * a.block_rows + row] = make_float2(high, l);
+            }
+        }
+        f += take, rel += take;
+        if (rel == span.tiles * items) ++seq, rel = 0;
+        __syncthreads();  // the next part's slices take the sums' place
+    }
+}
+
+// The parts of the item that CTA `blockIdx.x` of the attention began and later ones ended.
+template <int DIM>
+__global__ void __launch_bounds__(256) join_kernel(const AttendArgs a)
+{
+    constexpr int kVecs = DIM / 4, kLanes = 256 / kVecs;
+    __shared__ float4 s_v[kLanes][kVecs];
+    __shared__ float s_l[kLanes];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int4 record = a.records[blockIdx.x];
+    const int row = blockIdx.y;
+    const int head = record.x / a.blocks, row0 = (record.x - head * a.blocks) * a.block_rows;
+    if (!record.w || row >= min(a.block_rows, a.rows - row0)) return;
+    const int parts = record.y - static_cast<int>(blockIdx.x) + 1;
+    const int lane = threadIdx.x / kVecs, d = threadIdx.x % kVecs;
+    const auto place = [&](int part) {
+        const int slot = part == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + part);
+        return static_cast<int64_t>(slot) * a.block_rows + row;
+    };
+    float high = kMinusInf;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) high = fmaxf(high, a.part_ml[place(i)].x);
+    const float base = high == kMinusInf ? 0.0f : high;
+    float l = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = lane; i < parts; i += kLanes) {
+        const float2 ml = a.part_ml[place(i)];
+        const float4 u = *reinterpret_cast<const float4*>(a.part_o + place(i) * DIM + 4 * d);
+        const float part = exp2_fast(ml.x - base);
+        l += ml.y * part;
+        v.x += u.x * part, v.y += u.y * part, v.z += u.z * part, v.w += u.w * part;
+    }
+    s_v[lane][d] = v;
+    if (d == 0) s_l[lane] = l;
+    __syncthreads();
+    if (lane > 0) return;
+#pragma unroll
+    for (int i = 1; i < kLanes; ++i) {
+        const float4 u = s_v[i][d];
+        l += s_l[i];
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    float unused, gv;
+    global_scales(a.cache.amax[1], unused, gv);
+    const float n = l == 0.0f ? 0.0f : gv / l;
+    const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
+    const int64_t at = (static_cast<int64_t>(record.z) * a.queries + i) * a.heads + head * a.group + h;
+    *reinterpret_cast<uint2*>(a.out + at * DIM + 4 * d) = make_uint2(pack2(v.x * n, v.y * n), pack2(v.z * n, v.w * n));
+    if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+}
+
+// Rows of a block and the CTAs of the attention.  (sms: at most as many multiprocessors)
+struct Cut {
+    int rows, blocks, block_rows;
+    int64_t ctas;
+};
+Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int64_t capacity, int sms)
+{
+    Cut c;
+    c.rows = queries * (heads / kv_heads);
+    const int most = dim == 256 || c.rows <= 8 ? 8 : 16;
+    c.blocks = (c.rows + most - 1) / most;
+    c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
+    const int wide = dim == 256 ? Shape<256, 1>::kCtas : most == 8 ? Shape<128, 1>::kCtas : dim == 128 ? Shape<128, 2>::kCtas : Shape<64, 2>::kCtas;
+    c.ctas = std::min<int64_t>(static_cast<int64_t>(sms) * wide,
+                               sequences * kv_heads * c.blocks * std::max<int64_t>(1, (capacity + kTile - 1) / kTile + 1));
+    return c;
+}
+
+constexpr int kMostSms = 192;  // of the workspace's size, which is known without a device
+
+template <int DIM, int NT>
+nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
+{
+    using S = Shape<DIM, NT>;
+    static bool raised[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (!raised[dev & 63]) {
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(attend_kernel<DIM, NT>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem)) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        raised[dev & 63] = true;
+    }
+    if (launch_early(false, attend_kernel<DIM, NT>, cut.ctas, 32 * kWarps, S::kSmem, st, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.ctas), static_cast<unsigned>(cut.block_rows)), cfg.blockDim = dim3(256);
+    cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+size_t workspace_bytes(int64_t ctas, int block_rows, int dim)
+{
+    return kHeadBytes + static_cast<size_t>(ctas) * (sizeof(int4) + 2 * static_cast<size_t>(block_rows) * (sizeof(float2) + 4 * dim)) + 16;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int heads, int kv_heads, int dim,
+                                                    int64_t capacity)
+{
+    if (sequences < 1 || queries < 1 || kv_heads < 1 || heads < kv_heads || capacity < 0 ||
+        (dim != 64 && dim != 128 && dim != 256) || queries > (1 << 20) || heads > 65536)
+        return kHeadBytes;
+    const Cut c = cut_of(std::min<int64_t>(sequences, 1 << 20), queries, heads, kv_heads, dim, std::min<int64_t>(capacity, 1ll << 31), kMostSms);
+    return workspace_bytes(c.ctas, c.block_rows, dim);
+}
+
+extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh, int64_t sequences,
+                                           int queries, int heads, const nvfp4_kv_cache* cache, const int32_t* table,
+                                           int64_t ldt, int64_t table_pages, const int32_t* lengths, float scale,
+                                           int64_t window, void* out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                                           void* stream)
+{
+    AttendArgs a{};
+    const nvfp4_status bad = check_cache(cache, &a.cache);
+    if (bad != NVFP4_OK) return bad;
+    const int dim = cache->dim, kv = cache->kv_heads;
+    if (sequences < 0 || sequences > (1 << 20) || queries < 1 || queries > (1 << 20) || heads < 1 || heads > 65536 || heads % kv ||
+        table_pages < 0 || table_pages > 0x7fffffffll || ldt < table_pages || window < 0)
+        return NVFP4_ERR_SHAPE;
+    if (!(scale == scale) || scale - scale != 0.0f) return NVFP4_ERR_INVALID_ARG;
+    if (sequences > 0 && (!q_bf16 || !out_bf16 || !lengths || (table_pages > 0 && !table))) return NVFP4_ERR_INVALID_ARG;
+    if (ldb < 0 || ldi < 0 || (heads > 1 && ldh < dim)) return NVFP4_ERR_SHAPE;
+    const int64_t capacity = table_pages * cache->page_size;
+    // (places in a sequence and the tiles of all are 31-bit numbers)
+    if (capacity > 0x7fffff00ll) return NVFP4_ERR_SHAPE;
+    if (off16(q_bf16) || off16(out_bf16) || ldb % 8 || ldi % 8 || ldh % 8 ||
+        ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(lse)) & 3u))
+        return NVFP4_ERR_ALIGN;
+    if (!workspace || off16(workspace) || ws_bytes < kHeadBytes) return NVFP4_ERR_WORKSPACE;
+    if (static_cast<int64_t>(queries) * (heads / kv) > (1 << 24)) return NVFP4_ERR_SHAPE;
+    if (sequences > 0) {
+        const Cut c = cut_of(sequences, queries, heads, kv, dim, capacity, 1);
+        if ((capacity / kTile + 2) > 0x7fffffffll / (sequences * kv) / c.blocks) return NVFP4_ERR_SHAPE;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    const int sms = sm100_sms(dev);
+    if (!sms) return NVFP4_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (sequences == 0) {
+        return cudaMemsetAsync(static_cast<uint8_t*>(workspace) + 8, 0, 4, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    }
+    const Cut cut = cut_of(sequences, queries, heads, kv, dim, capacity, std::min(sms, kMostSms));
+    if (ws_bytes < workspace_bytes(cut.ctas, cut.block_rows, dim)) return NVFP4_ERR_WORKSPACE;
+    a.q = static_cast<const uint16_t*>(q_bf16), a.ldb = ldb, a.ldi = ldi, a.ldh = ldh;
+    a.out = static_cast<uint16_t*>(out_bf16), a.lse = lse;
+    a.table = table, a.ldt = ldt, a.lengths = lengths;
+    a.sequences = static_cast<int>(sequences), a.table_pages = static_cast<int>(table_pages);
+    a.queries = queries, a.heads = heads, a.group = heads / kv;
+    a.rows = cut.rows, a.blocks = cut.blocks, a.block_rows = cut.block_rows;
+    a.window = static_cast<int>(std::min<int64_t>(window, 0x7fffffff));
+    a.scale = scale;
+    uint8_t* at = static_cast<uint8_t*>(workspace) + kHeadBytes;
+    a.records = reinterpret_cast<int4*>(at);
+    at += cut.ctas * sizeof(int4);
+    a.part_o = reinterpret_cast<float*>(at);
+    at += static_cast<size_t>(2 * cut.ctas) * cut.block_rows * dim * 4;
+    a.part_ml = reinterpret_cast<float2*>(at);
+    a.status = static_cast<uint32_t*>(workspace) + 2;
+    if (cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (dim == 256) return start<256, 1>(a, cut, st);
+    const bool one = cut.block_rows <= 8;
+    if (dim == 128) return one ? start<128, 1>(a, cut, st) : start<128, 2>(a, cut, st);
+    return one ? start<64, 1>(a, cut, st) : start<64, 2>(a, cut, st);
+}
