@@ -572,6 +572,34 @@ nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, int64_t tot
                                 const float* g, int64_t N, int64_t K, int out_dtype, void* D,
                                 int64_t ldd, void* workspace, size_t ws_bytes, void* stream);
 
+/* Workspace bytes of nvfp4_expert_mlp. */
+size_t nvfp4_expert_mlp_workspace_size(int64_t total_rows, int64_t hidden, int64_t ffn);
+
+/*
+ * nvfp4_expert_mlp -- the experts of a MoE layer for a few tokens (iitak,
+ * "Details": NVFP4 in the expert layers), their products as nvfp4_grouped_gemv's:
+ *   h_i = silu(x_r gate_e^T) * (x_r up_e^T), or max(x_r up_e^T, 0)^2 without a gate,
+ *   out[t] = base[t] + sum_j weight[t][j] * (h_i down_e^T),  i = slot_row[t][j]
+ * for routed row i of expert e, r = row_index[i] (all as nvfp4_route gives them).
+ * x [tokens, ldx] bf16; gate (all three pointers NULL: none) and up [G, ffn, hidden / 2],
+ * down [G, hidden, ffn / 2] with consecutive NVFP4_SF_MMA blocks and g [G]; base, out
+ * [tokens, hidden] bf16 (base NULL = 0; out may be base).  The products and what
+ * becomes of them are FP32; h is rounded to bf16, the x of the last product.
+ * Slots with a negative row are left out; a row_index outside x gives a row of
+ * zeros, a slot_row >= total_rows is left out, and both are reported in the
+ * workspace's status word.  hidden and ffn multiples of 128 and at most 45056,
+ * 1 <= G <= 256, 1 <= k <= 64; otherwise as nvfp4_grouped_gemv and nvfp4_combine.
+ */
+nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, int64_t total_rows,
+                              const void* x_bf16, int64_t ldx, int64_t tokens,
+                              const int32_t* row_index, const uint8_t* gate_q,
+                              const uint8_t* gate_sf, const float* gate_g, const uint8_t* up_q,
+                              const uint8_t* up_sf, const float* up_g, const uint8_t* down_q,
+                              const uint8_t* down_sf, const float* down_g, int64_t hidden,
+                              int64_t ffn, const int32_t* slot_row, const float* weight, int k,
+                              const void* base_bf16, void* out_bf16, void* workspace,
+                              size_t ws_bytes, void* stream);
+
 /*
  * A paged cache of keys and values held in NVFP4 (asector, "NVFP4 and
  * Blackwell": a local scale per 16-element block on top of one scale per

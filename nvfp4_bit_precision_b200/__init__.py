@@ -67,7 +67,8 @@ EXPORTED = [
     "nvfp4_rmsnorm_backward_workspace_size", "nvfp4_route", "nvfp4_route_backward",
     "nvfp4_route_workspace_size", "nvfp4_combine", "nvfp4_combine_backward",
     "nvfp4_combine_backward_workspace_size", "nvfp4_gemv", "nvfp4_grouped_gemv", "nvfp4_kv_append",
-    "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size",
+    "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size", "nvfp4_expert_mlp",
+    "nvfp4_expert_mlp_workspace_size",
 ]
 
 
@@ -170,13 +171,17 @@ _lib.nvfp4_kv_attention.argtypes = [_P, _I64, _I64, _I64, _I64, _INT, _INT, ctyp
                                     _I64, _P, _F32, _I64, _P, _P, _P, _SZ, _P]
 _lib.nvfp4_kv_attention_workspace_size.argtypes = [_I64, _INT, _INT, _INT, _INT, _I64]
 _lib.nvfp4_kv_attention_workspace_size.restype = _SZ
+_lib.nvfp4_expert_mlp.argtypes = [_INT, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64,
+                                  _P, _P, _INT, _P, _P, _P, _SZ, _P]
+_lib.nvfp4_expert_mlp_workspace_size.argtypes = [_I64, _I64, _I64]
+_lib.nvfp4_expert_mlp_workspace_size.restype = _SZ
 for _n in ("nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_quantize", "mxfp4_quantize",
            "nvfp4_dequantize", "nvfp4_gemm", "mxfp8_gemm", "mxfp4_gemm", "mxfp8_combine",
            "nvfp4_grouped_gemm", "nvfp4_gather_rows", "nvfp4_workspace_status",
            "nvfp4_quantize_noalloc_status", "nvfp4_gemm_cycles", "nvfp4_rmsnorm",
            "nvfp4_rmsnorm_backward", "nvfp4_route", "nvfp4_route_backward", "nvfp4_combine",
            "nvfp4_combine_backward", "nvfp4_gemv", "nvfp4_grouped_gemv", "nvfp4_kv_append",
-           "nvfp4_kv_attention"):
+           "nvfp4_kv_attention", "nvfp4_expert_mlp"):
     getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -337,6 +342,20 @@ def nvfp4_combine_backward(dout, rows, rows_dtype, n_rows, cols, slot_row, weigh
                                        _ptr(weight), tokens, k, _ptr(used_rows), _ptr(drows), _ptr(dweight),
                                        _ptr(workspace), ws_bytes, _stream(stream)),
            "nvfp4_combine_backward")
+
+
+def nvfp4_expert_mlp(G, group_offsets, total_rows, x, ldx, tokens, row_index, gate_q, gate_sf, gate_g, up_q, up_sf,
+                     up_g, down_q, down_sf, down_g, hidden, ffn, slot_row, weight, k, base, out, workspace, ws_bytes,
+                     stream=None) -> None:
+    _check(_lib.nvfp4_expert_mlp(G, _ptr(group_offsets), total_rows, _ptr(x), ldx, tokens, _ptr(row_index),
+                                 _ptr(gate_q), _ptr(gate_sf), _ptr(gate_g), _ptr(up_q), _ptr(up_sf), _ptr(up_g),
+                                 _ptr(down_q), _ptr(down_sf), _ptr(down_g), hidden, ffn, _ptr(slot_row), _ptr(weight),
+                                 k, _ptr(base), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)),
+           "nvfp4_expert_mlp")
+
+
+def nvfp4_expert_mlp_workspace_size(total_rows: int, hidden: int, ffn: int) -> int:
+    return _lib.nvfp4_expert_mlp_workspace_size(total_rows, hidden, ffn)
 
 
 def nvfp4_kv_append(cache: KVCacheView, k, ldk, hsk, v, ldv, hsv, tokens, table, ldt, sequences, table_pages,
@@ -979,6 +998,51 @@ def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtyp
     _check(_lib.nvfp4_grouped_gemv(G, group_offsets.data_ptr(), rows, x.data_ptr(), ldx, src, ip,
                                    qb.data_ptr(), sfb.data_ptr(), gb.data_ptr(), N, K, out_dtype,
                                    out.data_ptr(), ldd, wp, nb, _raw_stream(dev)), "nvfp4_grouped_gemv")
+    return out
+
+
+def expert_mlp(x, routing: Routing, up, down, gate=None, base=None, *, workspace=None, stream=None):
+    """The experts of a MoE layer for a few tokens x [tokens, hidden] bf16: each routed row through its expert's gate
+    and up matrices, silu(gate) * up (without a gate max(up, 0)^2), its down matrix, and the weighted sum per token
+    on top of base.  up, down and gate: ``moe.ExpertWeights`` (or the like: q, sf, g, n).  ``workspace``:
+    nvfp4_expert_mlp_workspace_size bytes, which then hold the status word too."""
+    if stream is not None:
+        with _on(stream):
+            return expert_mlp(x, routing, up, down, gate, base, workspace=workspace)
+    offsets, row_index, slot_row, weight = routing.group_offsets, routing.row_index, routing.slot_row, routing.weight
+    gates = (None, None, None) if gate is None else (gate.q, gate.sf, gate.g)
+    dev = _one_device("expert_mlp", x, offsets, row_index, slot_row, weight, up.q, up.sf, up.g, down.q, down.sf, down.g,
+                      *gates, base, workspace)
+    ldx = _rows_of("expert_mlp: x", x)
+    tokens, hidden = x.shape
+    G, ffn, rows = offsets.numel() - 1, up.n, row_index.numel()
+    _need(down.n == hidden, f"expert_mlp: down has {down.n} rows, x {hidden} columns")
+    _flat("expert_mlp: group_offsets", offsets, torch.int32, G + 1)
+    _flat("expert_mlp: row_index", row_index, torch.int32, rows)
+    _need(slot_row.dim() == 2, "expert_mlp: slot_row [tokens, top_k] expected")
+    k = slot_row.shape[1]
+    _flat("expert_mlp: slot_row", slot_row, torch.int32, tokens, k)
+    _flat("expert_mlp: weight", weight, torch.float32, tokens, k)
+    for name, w, n, cols in (("up", up, ffn, hidden), ("down", down, hidden, ffn), ("gate", gate, ffn, hidden)):
+        if w is not None:
+            _need(w.n == n, f"expert_mlp: {name} has {w.n} rows, {n} expected")
+            _flat(f"expert_mlp: {name}.q", w.q, torch.uint8, G, n, cols // 2)
+            _flat(f"expert_mlp: {name}.g", w.g, torch.float32, G)
+            _bytes(f"expert_mlp: {name}.sf", w.sf, G * nvfp4_sf_mma_bytes(n, cols))
+    bp = gp = gs = gg = None
+    if gate is not None:
+        gp, gs, gg = (t.data_ptr() for t in gates)
+    if base is not None:
+        _flat("expert_mlp: base", base, torch.bfloat16, tokens, hidden)
+        bp = base.data_ptr()
+    if workspace is None:
+        workspace = torch.empty(nvfp4_expert_mlp_workspace_size(rows, hidden, ffn), dtype=torch.uint8, device=dev)
+    out = _matrix(dev, torch.bfloat16, tokens, hidden)
+    _check(_lib.nvfp4_expert_mlp(G, offsets.data_ptr(), rows, x.data_ptr(), ldx, tokens, row_index.data_ptr(), gp, gs, gg,
+                                 up.q.data_ptr(), up.sf.data_ptr(), up.g.data_ptr(), down.q.data_ptr(),
+                                 down.sf.data_ptr(), down.g.data_ptr(), hidden, ffn, slot_row.data_ptr(),
+                                 weight.data_ptr(), k, bp, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 _raw_stream(dev)), "nvfp4_expert_mlp")
     return out
 
 

@@ -85,6 +85,9 @@ struct Divisor {
     }
 };
 
+// What becomes of the products.
+enum Epilogue { kProduct, kGated, kSquared };
+
 struct GemvArgs {
     const uint16_t* x;
     int64_t ldx;
@@ -96,6 +99,9 @@ struct GemvArgs {
     const uint8_t* q;
     const uint8_t* sf;
     const float* g;
+    const uint8_t* q2;             // kGated: the up matrices, q, sf and g being the gates
+    const uint8_t* sf2;
+    const float* g2;
     int64_t n, k;
     int64_t sf_bytes;              // scale bytes of one matrix
     int tiles, steps;              // 16-row tiles of a matrix, 256-column steps of a row
@@ -161,6 +167,10 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy8_async(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -195,9 +205,15 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at)
 //
 // With PANELS (one matrix), x comes in panels of columns: the CTA goes over at most
 // kPanelTiles tiles panel by panel and keeps their sums in shared memory.
-template <int NT, bool PANELS>
+//
+// kGated: a tile is eight rows of a gate matrix and the same eight of its up matrix,
+// of which the halves 64 h + 32 i + 4 u + 0..3 (i < 2) of a 128-row block have tiles 8 h +
+// u; lane (r, t) then has both products of row r, and silu(gate) * up leaves in their
+// place.  kSquared: the squared positive part of the product does.
+template <int NT, bool PANELS, int FORM>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs a)
 {
+    static_assert(FORM == kProduct || !PANELS, "experts have whole rows of x");
     constexpr int kStages = ring_stages(NT);
     constexpr int kRed = 8 * NT * kRedStride;  // floats of a tile's sums
     extern __shared__ __align__(16) uint8_t s_dyn[];
@@ -360,12 +376,20 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         const uint8_t *tq = nullptr, *ts = nullptr;                  // this lane's first codes (row r), scales of the tile
         const uint8_t *pq = nullptr, *pq8 = nullptr, *ps = nullptr;  // those of the step
         const auto rows_there = [&]() {
-            if (a.whole) return;
+            if (a.whole || FORM == kGated) return;  // (experts' matrices have whole 128-row blocks)
             const int64_t n = static_cast<int64_t>(ptile >> 3) * 128 + 32 * (r >> 2) + 4 * (ptile & 7) + (r & 3);
             have0 = n < a.n;
             have8 = n + 64 < a.n;
         };
         const auto aim = [&]() {  // at tile ptile of segment pseg
+            if constexpr (FORM == kGated) {
+                const int64_t e = s_seg_e[pseg], block = ptile >> 4;
+                const int u = ptile & 7, half = ptile >> 3 & 1;
+                tq = a.q + (e * a.n + block * 128 + 64 * half + 32 * (r >> 2) + 4 * u + (r & 3)) * row_bytes + 16 * t;
+                ts = (lane < 16 ? a.sf : a.sf2) + e * a.sf_bytes + block * (a.k / 64) * 512 + (lane & 15) / 4 * 512 +
+                     (4 * u + (lane & 3)) * 16 + 8 * half;
+                return;
+            }
             const int64_t e = s_seg_e[pseg], block = ptile >> 3;
             const int u = ptile & 7;
             tq = a.q + (e * a.n + block * 128 + 32 * (r >> 2) + 4 * u + (r & 3)) * row_bytes + 16 * t;
@@ -374,14 +398,15 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         };
         const auto at_step = [&]() {
             pq = tq + (p0 + pc) * (kStep / 2);
-            pq8 = pq + 64 * row_bytes;  // from row m to row m + 8: i + 2
+            pq8 = FORM == kGated ? pq + (a.q2 - a.q) : pq + 64 * row_bytes;  // from row m to row m + 8: i + 2
             ps = ts + static_cast<int64_t>(p0 + pc) * 2048;
         };
         if (left > 0) {
             aim();
             at_step();
         }
-        const uint32_t put = ring + r * 128 + (t ^ (r & 1)) * 16, put_sc = ring + 2048 + (lane & 15) * 16;
+        const uint32_t put = ring + r * 128 + (t ^ (r & 1)) * 16;
+        const uint32_t put_sc = ring + 2048 + (lane & 15) * 16 + (FORM == kGated && lane >= 16 ? 8 : 0);
         const auto copy_step = [&]() {
             if (left > 0) {
                 const uint32_t dst = put + pslot * kStageBytes, dst_sc = put_sc + pslot * kStageBytes;
@@ -390,7 +415,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     copy16_async(dst + 64, pq + 64);
                     copy16_async(dst + 1024, pq8);
                     copy16_async(dst + 1088, pq8 + 64);
-                    if (lane < 16) copy16_async(dst_sc, ps);
+                    if (FORM == kGated) copy8_async(dst_sc, ps, true);
+                    else if (lane < 16) copy16_async(dst_sc, ps);
                 } else {
                     const int k = (p0 + pc) * kStep + 32 * t;
                     const bool in0 = k < a.k, in1 = k + 128 < a.k;
@@ -399,7 +425,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     copy16_async(dst + 1024, in0 && have8 ? pq8 : a.q, in0 && have8);
                     copy16_async(dst + 1088, in1 && have8 ? pq8 + 64 : a.q, in1 && have8);
                     const bool in = (p0 + pc) * kStep + 64 * ((lane & 15) >> 2) < a.k;
-                    if (lane < 16) copy16_async(dst_sc, in ? ps : a.sf, in);
+                    if (FORM == kGated) copy8_async(dst_sc, in ? ps : a.sf, in);
+                    else if (lane < 16) copy16_async(dst_sc, in ? ps : a.sf, in);
                 }
                 --left;
                 pq += kStep / 2;
@@ -409,6 +436,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     pc = 0;
                     if (++ptile == tiles) {
                         ptile = 0, ++pseg;
+                        aim();
+                    } else if (FORM == kGated && (ptile & 7) == 0) {
                         aim();
                     } else {  // four rows on, or the next 128-row block
                         const bool next_block = (ptile & 7) == 0;
@@ -430,7 +459,11 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // that lanes t read, and converts it in place once the largest magnitude is known.
         const int x_rows = s_seg_x[segs];
         float g = 0.0f;  // of the x row that is this thread's index
-        if (static_cast<int>(threadIdx.x) < x_rows) g = a.g[s_x_row[threadIdx.x].w];
+        if (static_cast<int>(threadIdx.x) < x_rows) {
+            g = a.g[s_x_row[threadIdx.x].w];
+            if constexpr (FORM == kGated)  // (the up matrix's takes the matrix's place)
+                s_x_row[threadIdx.x].w = __float_as_int(a.g2[s_x_row[threadIdx.x].w]);
+        }
         const auto next = [&](int& xr, int& c) {
             c += kGemvWarps;
             while (c >= psteps) c -= psteps, ++xr;
@@ -506,6 +539,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // xstep; the factors on the sums of tokens 8 b + 2 t + 0, 1, and which are there
         uint32_t x0[NT], xp[NT], xstep[NT];
         float2 factor[NT][2];
+        float factor2[NT][2];
         bool there[NT][2];
         int64_t row0 = 0;
         const auto enter = [&]() {
@@ -522,6 +556,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     const int tok = 8 * b + 2 * t + i;
                     there[b][i] = tok < n;
                     factor[b][i] = tok < n ? s_scale[first + tok] : make_float2(0.0f, 0.0f);
+                    if constexpr (FORM == kGated) factor2[b][i] = tok < n ? __int_as_float(s_x_row[first + tok].w) : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
@@ -531,6 +566,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // may leave few bits to a product of both factors)
         const auto store = [&](int tok, int m, float v, float2 by) {
             v = v * by.x * by.y;
+            if constexpr (FORM == kSquared) {
+                v = v > 0.0f ? v * v : v == v ? 0.0f : v;
+            }
             if (PANELS) {
                 float* const sum = s_acc + ((tile - tile0) * 8 * NT + tok) * 16 + m;
                 if (p0 > 0) v += *sum;
@@ -546,6 +584,12 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                 static_cast<float*>(a.out)[at] = v;
             else
                 static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+        };
+        // silu(gate) * up of row m < 8 of a gated tile
+        const auto store_gated = [&](int tok, int m, float gate, float up, float2 by, float by2) {
+            const float z = gate * by.x * by.y, v = z / (1.0f + __expf(-z)) * (up * by2 * by.y);
+            const int64_t n = static_cast<int64_t>(tile >> 3) * 64 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
+            static_cast<__nv_bfloat16*>(a.out)[(row0 + tok) * a.ldd + n] = __float2bfloat16_rn(v);
         };
         if (j0 < j1) enter();
 #pragma unroll 1
@@ -596,7 +640,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             // the tile or the run ends: columns 2 t and 2 t + 1 of the sums are tokens
             // 8 b + 2 t, 8 b + 2 t + 1
             open = begun && c < psteps;
-            if (begun && !open) {
+            if (FORM == kGated && begun && !open) {
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (there[b][i]) store_gated(8 * b + 2 * t + i, r, acc[b][i], acc[b][2 + i], factor[b][i], factor2[b][i]);
+            } else if (begun && !open) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -633,11 +683,20 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             const int end = j1 - c + psteps;  // the item behind the tile's last
             int others = 0;
             while (run_start(warp + others + 1) < end) ++others;
+            if constexpr (FORM == kGated) {
+                for (int o = lane; o < 8 * s_seg_n[seg]; o += 32) {
+                    const int at = (o >> 3) * kRedStride + (o & 7), xr = s_seg_x[seg] + (o >> 3);
+                    float v = my_sums[at], u = my_sums[at + 8];
+                    for (int w = 1; w <= others; ++w) v += my_head[w * kRed + at], u += my_head[w * kRed + at + 8];
+                    store_gated(o >> 3, o & 7, v, u, s_scale[xr], __int_as_float(s_x_row[xr].w));
+                }
+            } else {
             for (int o = lane; o < 16 * s_seg_n[seg]; o += 32) {
                 const int at = (o >> 4) * kRedStride + (o & 15);
                 float v = my_sums[at];
                 for (int w = 1; w <= others; ++w) v += my_head[w * kRed + at];
                 store(o >> 4, o & 15, v, s_scale[s_seg_x[seg] + (o >> 4)]);
+            }
             }
         }
         if (fe == f1 && (!PANELS || p0 + psteps == steps)) return;
@@ -648,8 +707,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     }
 }
 
-template <int NT, bool PANELS>
-nvfp4_status start_gemv(GemvArgs a, const Plan& plan, int sms, cudaStream_t st)
+template <int NT, bool PANELS, int FORM = kProduct>
+nvfp4_status start_gemv(GemvArgs a, const Plan& plan, int sms, bool early, cudaStream_t st)
 {
     const int64_t tiles = a.tiles, steps = a.steps;
     int64_t grid;
@@ -677,21 +736,21 @@ nvfp4_status start_gemv(GemvArgs a, const Plan& plan, int sms, cudaStream_t st)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!raised[dev & 63]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(gemv_kernel<NT, PANELS>),
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(gemv_kernel<NT, PANELS, FORM>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvSmem)) != cudaSuccess)
             return NVFP4_ERR_CUDA;
         raised[dev & 63] = true;
     }
     a.by_tiles = Divisor(a.tiles), a.by_steps = Divisor(a.panel_steps), a.by_seg_rows = Divisor(a.seg_rows);
     a.whole = a.n % 128 == 0 && a.k % kStep == 0;
-    if (launch_early(!a.status, gemv_kernel<NT, PANELS>, static_cast<int>(grid), 32 * kGemvWarps, smem, st, a) != cudaSuccess)
+    if (launch_early(early, gemv_kernel<NT, PANELS, FORM>, static_cast<int>(grid), 32 * kGemvWarps, smem, st, a) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, size_t ws_bytes, void* stream)
+// What is wrong with the sizes and addresses of a call.
+nvfp4_status check_gemv(const GemvArgs& a, int out_dtype)
 {
-    GemvArgs a = in;
     if (!a.q || !a.sf || !a.g) return NVFP4_ERR_INVALID_ARG;
     if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_INVALID_ARG;
     if (a.rows < 0 || a.rows > 0x7fffffffll || a.n <= 0 || a.n % 16 || a.n > (1ll << 30) || a.k <= 0 || a.k % 64 ||
@@ -702,20 +761,18 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
         (reinterpret_cast<uintptr_t>(a.out) & (out_dtype == NVFP4_OUT_F32 ? 3u : 1u)) ||
         (reinterpret_cast<uintptr_t>(a.row_index) & 3u) || (reinterpret_cast<uintptr_t>(a.group_offsets) & 3u))
         return NVFP4_ERR_ALIGN;
-    if (workspace && (ws_bytes < 16 || off16(workspace))) return NVFP4_ERR_WORKSPACE;
-    const int64_t tiles = (a.n + 127) / 128 * 8, steps = (a.k + kStep - 1) / kStep;
+    const int64_t tiles = (a.n + 127) / 128 * (a.q2 ? 16 : 8), steps = (a.k + kStep - 1) / kStep;
     if (a.rows > 0) {
         if (steps > max_x_pairs(1, false)) return NVFP4_ERR_SHAPE;            // one row does not fit
         if (a.rows > 0x7fffffffll / (tiles * steps)) return NVFP4_ERR_SHAPE;  // indexes are 31-bit on the device
     }
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
-    const int sms = sm100_sms(dev);
-    if (!sms) return NVFP4_ERR_UNSUPPORTED;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    a.status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
-    if (a.status && cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
-    if (a.rows == 0) return NVFP4_OK;
+    return NVFP4_OK;
+}
+
+// The launch of a checked call with rows; early: behind a kernel, not a memset.
+nvfp4_status launch_rows(GemvArgs a, int out_dtype, int form, int sms, bool early, cudaStream_t st)
+{
+    const int64_t tiles = (a.n + 127) / 128 * (form == kGated ? 16 : 8), steps = (a.k + kStep - 1) / kStep;
     a.sf_bytes = static_cast<int64_t>(nvfp4_sf_mma_bytes(a.n, a.k));
     a.out_f32 = out_dtype == NVFP4_OUT_F32;
     a.tiles = static_cast<int>(tiles), a.steps = static_cast<int>(steps);
@@ -728,11 +785,30 @@ nvfp4_status launch_gemv(const GemvArgs& in, int out_dtype, void* workspace, siz
         const int64_t mean = (a.rows + a.groups - 1) / a.groups;
         const auto passes = [&](int nt) { return (mean + at_once(nt) - 1) / at_once(nt); };
         const bool two = 3 * passes(2) <= 2 * passes(1);
-        return two ? start_gemv<2, false>(a, Plan(), sms, st) : start_gemv<1, false>(a, Plan(), sms, st);
+        if (form == kGated)
+            return two ? start_gemv<2, false, kGated>(a, Plan(), sms, early, st) : start_gemv<1, false, kGated>(a, Plan(), sms, early, st);
+        if (form == kSquared)
+            return two ? start_gemv<2, false, kSquared>(a, Plan(), sms, early, st)
+                       : start_gemv<1, false, kSquared>(a, Plan(), sms, early, st);
+        return two ? start_gemv<2, false>(a, Plan(), sms, early, st) : start_gemv<1, false>(a, Plan(), sms, early, st);
     }
-    const Form form = cheapest_form(a.rows, tiles, at_once(1), at_once(2), sms);
-    if (form.panels) return start_gemv<1, true>(a, form.plan, sms, st);
-    return form.columns == 8 ? start_gemv<1, false>(a, form.plan, sms, st) : start_gemv<2, false>(a, form.plan, sms, st);
+    const Form one = cheapest_form(a.rows, tiles, at_once(1), at_once(2), sms);
+    if (one.panels) return start_gemv<1, true>(a, one.plan, sms, early, st);
+    return one.columns == 8 ? start_gemv<1, false>(a, one.plan, sms, early, st) : start_gemv<2, false>(a, one.plan, sms, early, st);
+}
+
+nvfp4_status launch_gemv(GemvArgs a, int out_dtype, void* workspace, size_t ws_bytes, void* stream)
+{
+    if (const nvfp4_status s = check_gemv(a, out_dtype)) return s;
+    if (workspace && (ws_bytes < 16 || off16(workspace))) return NVFP4_ERR_WORKSPACE;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    const int sms = sm100_sms(dev);
+    if (!sms) return NVFP4_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
+    if (a.status && cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return a.rows == 0 ? NVFP4_OK : launch_rows(a, out_dtype, kProduct, sms, !a.status, st);
 }
 
 }  // namespace
@@ -765,4 +841,62 @@ extern "C" nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, 
     a.group_offsets = group_offsets, a.groups = G, a.rows = total_rows;
     a.q = q, a.sf = sf, a.g = g, a.n = N, a.k = K, a.out = D, a.ldd = ldd;
     return launch_gemv(a, out_dtype, workspace, ws_bytes, stream);
+}
+
+namespace {
+constexpr size_t kMlpHead = 256;
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+}  // namespace
+
+extern "C" size_t nvfp4_expert_mlp_workspace_size(int64_t total_rows, int64_t hidden, int64_t ffn)
+{
+    if (total_rows < 1 || hidden < 1 || ffn < 1) return kMlpHead;
+    return kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 2) + static_cast<size_t>(total_rows) * hidden * 4;
+}
+
+extern "C" nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, int64_t total_rows, const void* x_bf16,
+                                         int64_t ldx, int64_t tokens, const int32_t* row_index, const uint8_t* gate_q,
+                                         const uint8_t* gate_sf, const float* gate_g, const uint8_t* up_q,
+                                         const uint8_t* up_sf, const float* up_g, const uint8_t* down_q,
+                                         const uint8_t* down_sf, const float* down_g, int64_t hidden, int64_t ffn,
+                                         const int32_t* slot_row, const float* weight, int k, const void* base_bf16,
+                                         void* out_bf16, void* workspace, size_t ws_bytes, void* stream)
+{
+    if (G < 1 || G > kMaxGemvGroups || !group_offsets || !gate_q != !gate_sf || !gate_q != !gate_g) return NVFP4_ERR_INVALID_ARG;
+    if (hidden % 128 || ffn % 128 || tokens < 0 || k < 1 || k > 64) return NVFP4_ERR_SHAPE;
+    if (total_rows > 0 && !row_index) return NVFP4_ERR_INVALID_ARG;
+    if (!slot_row || !weight || (tokens > 0 && !out_bf16)) return NVFP4_ERR_INVALID_ARG;
+    if (off16(gate_q) || off16(gate_sf) || (reinterpret_cast<uintptr_t>(gate_g) & 3u) || off16(base_bf16) || off16(out_bf16) ||
+        ((reinterpret_cast<uintptr_t>(slot_row) | reinterpret_cast<uintptr_t>(weight)) & 3u))
+        return NVFP4_ERR_ALIGN;
+    if (!workspace || off16(workspace) || ws_bytes < nvfp4_expert_mlp_workspace_size(total_rows, hidden, ffn))
+        return NVFP4_ERR_WORKSPACE;
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    GemvArgs up{};
+    up.x = static_cast<const uint16_t*>(x_bf16), up.ldx = ldx, up.src_rows = tokens, up.row_index = row_index;
+    up.group_offsets = group_offsets, up.groups = G, up.rows = total_rows;
+    up.q = up_q, up.sf = up_sf, up.g = up_g, up.n = ffn, up.k = hidden, up.out = ws + kMlpHead, up.ldd = ffn;
+    if (gate_q) up.q = gate_q, up.sf = gate_sf, up.g = gate_g, up.q2 = up_q, up.sf2 = up_sf, up.g2 = up_g;
+    if (gate_q && (!up_q || !up_sf || !up_g)) return NVFP4_ERR_INVALID_ARG;
+    if (off16(up_q) || off16(up_sf) || (reinterpret_cast<uintptr_t>(up_g) & 3u)) return NVFP4_ERR_ALIGN;
+    if (const nvfp4_status s = check_gemv(up, NVFP4_OUT_BF16)) return s;
+    GemvArgs down{};
+    down.x = static_cast<const uint16_t*>(up.out), down.ldx = ffn, down.src_rows = total_rows;
+    down.group_offsets = group_offsets, down.groups = G, down.rows = total_rows;
+    down.q = down_q, down.sf = down_sf, down.g = down_g, down.n = hidden, down.k = ffn, down.ldd = hidden;
+    down.out = ws + kMlpHead + round256(static_cast<size_t>(std::max<int64_t>(total_rows, 0)) * ffn * 2);
+    if (const nvfp4_status s = check_gemv(down, NVFP4_OUT_F32)) return s;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+    const int sms = sm100_sms(dev);
+    if (!sms) return NVFP4_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    up.status = static_cast<uint32_t*>(workspace) + 2;
+    if (cudaMemsetAsync(up.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (total_rows > 0) {
+        if (const nvfp4_status s = launch_rows(up, NVFP4_OUT_BF16, gate_q ? kGated : kSquared, sms, false, st)) return s;
+        if (const nvfp4_status s = launch_rows(down, NVFP4_OUT_F32, kProduct, sms, true, st)) return s;
+    }
+    return nvfp4_combine(down.out, NVFP4_OUT_F32, total_rows, hidden, slot_row, weight, tokens, k, base_bf16, out_bf16, nullptr, 0,
+                         stream);
 }

@@ -2,12 +2,12 @@
 
 ``rms_norm``, ``moe_route`` and ``moe_combine`` are the autograd forms of ``rmsnorm``, ``route`` and
 ``combine``: every arithmetic step runs in libnvfp4's kernels, this module only sequences the calls and keeps
-what the backward pass reads.  ``expert_gemv`` is the experts' forward pass for the few tokens of a decoding
-step, on the NVFP4 weights that ``grouped_gemm`` uses for many.
+what the backward pass reads.  ``expert_gemv`` and, with the activation inside, ``expert_mlp`` are the experts'
+forward pass for the few tokens of a decoding step, on the NVFP4 weights that ``grouped_gemm`` uses for many.
 
     y, h = rms_norm(x, norm_weight, residual)          # h: the residual stream
     r = moe_route(y.float() @ router.t(), top_k=4)     # experts, weights, the rows' order
-    out = expert_gemv(y, r, up, down, base=h)          # decoding; or, with gradients of rows and weights,
+    out = expert_mlp(y, r, up, down, gate, base=h)     # decoding; or, with gradients of rows and weights,
     out = moe_combine(rows, r, base=h)
 
 Gradients cannot be captured into a CUDA graph through these functions: a leaf whose gradient an eager graph
@@ -20,8 +20,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (NVFP4_OUT_BF16, NVFP4_OUT_F32, Routing, combine, combine_backward, grouped_gemv, rmsnorm,
-               rmsnorm_backward, route, route_backward)
+from . import (NVFP4_OUT_BF16, NVFP4_OUT_F32, Routing, combine, combine_backward, expert_mlp as _expert_mlp,
+               grouped_gemv, rmsnorm, rmsnorm_backward, route, route_backward)
 
 
 def _refuse_captured_gradients(name: str, *tensors) -> None:
@@ -172,3 +172,11 @@ def expert_gemv(x: torch.Tensor, routing: Routing, up: ExpertWeights, down: Expe
         h = activation(h)
     rows = grouped_gemv(routing.group_offsets, h, down.q, down.sf, down.g, down.n, None, NVFP4_OUT_F32)
     return combine(rows, routing.slot_row, routing.weight, base)
+
+
+@torch.no_grad()
+def expert_mlp(x: torch.Tensor, routing: Routing, up: ExpertWeights, down: ExpertWeights,
+               gate: ExpertWeights | None = None, base: torch.Tensor | None = None) -> torch.Tensor:
+    """``expert_gemv`` with the activation inside the products: silu(gate) * up, or max(up, 0)^2 without a gate.  The
+    whole forward pass of a few tokens' experts, for inference: no gradients."""
+    return _expert_mlp(x, routing, up, down, gate, base)
