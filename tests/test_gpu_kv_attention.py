@@ -1,0 +1,258 @@
+"""Attention over a paged NVFP4 cache against float64, with the bounds that kv_ref derives."""
+import numpy as np
+import pytest
+
+import kv_ref as K
+import workloads as W
+from gpu_util import cuda_available, host, to_dev
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="needs a CUDA device")]
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_bit_precision_b200 as nv
+    return nv
+
+
+def bits(rng, shape, std=1.0):
+    return W.f32_to_bf16_bits(rng.standard_normal(shape).astype(np.float32) * np.float32(std))
+
+
+def val(b):
+    return W.bf16_bits_to_f32(b).astype(np.float64)
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def i32(a):
+    return dev(np.asarray(a, dtype=np.int32))
+
+
+def filled(nv, rng, pages, kv, page, dim, amax=(8.0, 4.0), std=(1.0, 1.0)):
+    """A cache of normal numbers (quantised by the plain form) and the page's unused part of any finite bytes."""
+    c = nv.kv_cache(pages, kv, page, dim, *amax)
+    q, sf = np.empty(tuple(c.q.shape), np.uint8), np.empty(tuple(c.sf.shape), np.uint8)
+    for w in (0, 1):
+        q[w], sf[w] = K.quantise((rng.standard_normal((pages, kv, page, dim)) * std[w]).astype(np.float32), amax[w])
+    c.q.copy_(dev(q))
+    c.sf.copy_(dev(sf))
+    return c, q, sf
+
+
+def sequence_of(q, sf, g, table, length, page):
+    """One sequence's keys or values, float64 [kv, length, dim]."""
+    n = -(-length // page)
+    v = K.decode(q[table[:n]], sf[table[:n]], g)          # [pages, kv, page, dim]
+    return v.transpose(1, 0, 2, 3).reshape(v.shape[1], -1, v.shape[3])[:, :length]
+
+
+def check(nv, cache, q, sf, qb, table, lengths, page, window=0, scale=None, qd=None, td=None):
+    g = host(cache.g)
+    dim = qb.shape[3]
+    qd, td = to_dev(qb) if qd is None else qd, i32(table) if td is None else td
+    out, lse = nv.kv_attention(qd, cache, td, i32(lengths), window=window, scale=scale, lse=True)
+    only = nv.kv_attention(qd, cache, td, i32(lengths), window=window, scale=scale)
+    np.testing.assert_array_equal(host(only), host(out))
+    got, sums = val(host(out)), host(lse).astype(np.float64)
+    for s, n in enumerate(lengths):
+        k, v = (sequence_of(q[w], sf[w], g[w], table[s], n, page) for w in (0, 1))
+        ref, l, ob, lb = K.attend(val(qb[s]), k, v, n, np.float32(dim ** -0.5 if scale is None else scale).astype(np.float64), window)
+        assert np.all(np.abs(got[s] - ref) <= ob + 2.0 ** -8 * np.abs(ref)), (s, n, np.max(np.abs(got[s] - ref) / (ob + 2.0 ** -8 * np.abs(ref) + 1e-30)))
+        nothing = np.isneginf(l)
+        np.testing.assert_array_equal(np.isneginf(sums[s]), nothing)
+        assert np.all(np.abs(sums[s][~nothing] - l[~nothing]) <= lb[~nothing])
+        assert not got[s][nothing].any()
+    return out
+
+
+@pytest.mark.parametrize("dim,kv,group", [(128, 2, 4), (128, 1, 1), (128, 2, 5), (128, 1, 16), (128, 1, 17), (64, 3, 2), (64, 1, 9), (256, 2, 2),
+                                          (256, 1, 12)])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("new,window", [(1, 0), (3, 0), (1, 50), (4, 33)])
+def test_ragged(nv, dim, kv, group, page, new, window):
+    rng = np.random.default_rng(dim + 7 * kv + group + page + new + window)
+    lengths = [0, 1, 2, 15, 16, 17, 31, 33, 64, 127, 128, 129, 300, 517]
+    most = -(-517 // page)
+    pages = len(lengths) * most + 2
+    cache, q, sf = filled(nv, rng, pages, kv, page, dim)
+    table = rng.permutation(pages)[:len(lengths) * most].reshape(len(lengths), most)
+    check(nv, cache, q, sf, bits(rng, (len(lengths), new, kv * group, dim), 1.5), table, lengths, page, window)
+
+
+@pytest.mark.parametrize("n,lengths", [(1, [5000]), (3, [9000, 1, 700]), (200, None)])
+def test_cut_lengths(nv, n, lengths):
+    """Long sequences are cut into parts that several CTAs take; many short ones share a CTA."""
+    rng = np.random.default_rng(n)
+    dim, kv, page = 128, 2, 64
+    lengths = lengths or list(rng.integers(0, 260, n))
+    most = -(-max(lengths) // page)
+    pages = n * most
+    cache, q, sf = filled(nv, rng, pages, kv, page, dim)
+    table = rng.permutation(pages).reshape(n, most)
+    check(nv, cache, q, sf, bits(rng, (n, 1, 6, dim), 2.0), table, lengths, page)
+
+
+@pytest.mark.parametrize("n", [129, 300])
+def test_more_sequences_than_threads(nv, n):
+    rng = np.random.default_rng(n)
+    cache, q, sf = filled(nv, rng, n, 1, 16, 64)
+    table = rng.permutation(n)[:, None]
+    check(nv, cache, q, sf, bits(rng, (n, 1, 2, 64)), table, list(rng.integers(0, 17, n)), 16)
+
+
+@pytest.mark.parametrize("spread", [1.0, 30.0, 1e-20, 1e20])
+def test_sharp_and_flat(nv, spread):
+    """Scores from all but equal to one that takes all; queries of any size, each row on its own."""
+    rng = np.random.default_rng(9)
+    dim, page = 128, 32
+    cache, q, sf = filled(nv, rng, 40, 1, page, dim, (1e3, 1e-3), (100.0, 1e-4))
+    qb = bits(rng, (2, 1, 5, dim), 0.01)
+    qb[0, 0, 1] = 0
+    qb[1] = bits(rng, (1, 5, dim), 0.01 * spread)
+    scale = dim ** -0.5 if spread < 1e10 else 1e-21
+    check(nv, cache, q, sf, qb, rng.permutation(40).reshape(2, 20), [640, 601], page, scale=scale)
+
+
+def test_negative_scale_and_growing_scores(nv):
+    """The maximum rises with every token, then only falls."""
+    rng = np.random.default_rng(10)
+    dim, page, n = 64, 16, 800
+    cache, q, sf = filled(nv, rng, n // page, 1, page, dim, (64.0, 4.0))
+    ramp = np.linspace(0.0, 40.0, n).astype(np.float32)
+    k = np.zeros((n // page, 1, page, dim), np.float32)
+    k[:, 0, :, 0] = ramp.reshape(-1, page)
+    q[0], sf[0] = K.quantise(k, 64.0)
+    cache.q[0].copy_(dev(q[0]))
+    cache.sf[0].copy_(dev(sf[0]))
+    qb = np.zeros((1, 1, 2, dim), np.uint16)
+    qb[..., 0] = W.f32_to_bf16_bits(np.array([[[1.0, -1.0]]], np.float32))
+    for scale in (1.0, -1.0, 0.0):
+        check(nv, cache, q, sf, qb, np.arange(n // page)[None], [n], page, scale=scale)
+
+
+def test_strides(nv):
+    """Queries as a piece of a projection's output, a table as a piece of a larger one."""
+    import torch
+    rng = np.random.default_rng(11)
+    dim, page, kv, n, new, heads = 128, 32, 2, 5, 2, 6
+    cache, q, sf = filled(nv, rng, 30, kv, page, dim)
+    wide = bits(rng, (n, new, heads + 2 * kv, dim))
+    big = rng.permutation(30).reshape(5, 6)
+    check(nv, cache, q, sf, wide[:, :, :heads], big, [100, 3, 128, 77, 150], page, qd=to_dev(wide)[:, :, :heads],
+          td=torch.cat([i32(big), i32(np.full((5, 3), 99))], 1)[:, :6])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_masked_tokens_do_not_matter(nv, dim):
+    """NaN scales behind the end of a sequence, in its pages and in the table's other pages, before the window and
+    among the later of the query tokens: what does not see them stays as it was; what does is NaN."""
+    import torch
+    rng = np.random.default_rng(12 + dim)
+    page, kv, new, n = 32, 2, 3, 83
+    cache, q, sf = filled(nv, rng, 8, kv, page, dim)
+    table, qd = i32([[5, 2, 7, 1]]), to_dev(bits(rng, (1, new, 2 * kv, dim)))
+    for window in (0, 40):
+        want, wl = nv.kv_attention(qd, cache, table, i32([n]), window=window, lse=True)
+        bad = nv.KVCache(cache.q.clone(), cache.sf.clone(), cache.amax, cache.g)
+        for w in (0, 1):
+            bad.sf[w, 7, :, n - 64:] = 0x7F
+            bad.sf[w, [1, 0, 3, 4, 6]] = 0xFF
+            if window:
+                bad.sf[w, 5, :, :n - 2 - window] = 0x7F
+        got, gl = nv.kv_attention(qd, bad, table, i32([n]), window=window, lse=True)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        # the last token, seen by the last query alone: one block of its value
+        bad.sf[1, 7, 0, n - 1 - 64, 1] = 0x7F
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.equal(got[:, :2], want[:, :2]) and torch.equal(got[:, 2, 2:], want[:, 2, 2:])
+        nan = torch.isnan(got[0, 2, :2].float())
+        assert nan[:, 16:32].all() and not nan[:, :16].any() and not nan[:, 32:].any()
+        # and of its key: the whole row
+        bad.sf[1, 7, 0, n - 1 - 64, 1] = 1
+        bad.sf[0, 7, 1, n - 1 - 64, 0] = 0x7F
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.equal(got[:, :2], want[:, :2]) and torch.isnan(got[0, 2, 2:].float()).all()
+        # a value that all see
+        bad.sf[0, 7, 1, n - 1 - 64, 0] = 1
+        bad.sf[1, 2, 0, 20, 0] = 0x7F
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.isnan(got[0, :, :2, :16].float()).all() and not torch.isnan(got[0, :, 2:].float()).any()
+
+
+def test_non_finite_queries_stay_alone(nv):
+    import torch
+    rng = np.random.default_rng(13)
+    cache, q, sf = filled(nv, rng, 8, 1, 64, 128)
+    qd = to_dev(bits(rng, (2, 2, 4, 128)))
+    table, lengths = i32([[0, 1, 2, 3], [4, 5, 6, 7]]), i32([200, 256])
+    want = nv.kv_attention(qd, cache, table, lengths)
+    qd[0, 1, 2, 5] = float("nan")
+    qd[1, 0, 0, 7] = float("inf")
+    got = nv.kv_attention(qd, cache, table, lengths)
+    assert torch.isnan(got[0, 1, 2].float()).all() and torch.isnan(got[1, 0, 0].float()).all()
+    keep = torch.ones((2, 2, 4), dtype=torch.bool, device="cuda")
+    keep[0, 1, 2] = keep[1, 0, 0] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_bad_pages_and_lengths(nv):
+    """A page outside the cache counts as zeros, a length outside the table as its end; both are reported."""
+    import torch
+    rng = np.random.default_rng(14)
+    dim, page = 128, 32
+    cache, q, sf = filled(nv, rng, 6, 1, page, dim)
+    qd = to_dev(bits(rng, (2, 1, 4, dim)))
+    size = nv.nvfp4_kv_attention_workspace_size(2, 1, 4, 1, dim, 96)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    good = nv.kv_attention(qd, cache, i32([[0, 1, 2], [3, 4, 5]]), i32([96, 0]), workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 0
+    got = nv.kv_attention(qd, cache, i32([[0, 1, 2], [3, 4, 5]]), i32([2 ** 31 - 1, -7]), workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 8
+    assert torch.equal(got, good)
+    zero = nv.KVCache(torch.cat([cache.q, torch.zeros_like(cache.q[:, :1])], 1), torch.cat([cache.sf, torch.zeros_like(cache.sf[:, :1])], 1),
+                      cache.amax, cache.g)
+    want = nv.kv_attention(qd, zero, i32([[0, 6, 2], [3, 4, 6]]), i32([80, 96]), workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 0
+    for bad in (-1, 6, 2 ** 31 - 1, -2 ** 31):
+        got = nv.kv_attention(qd, cache, i32([[0, bad, 2], [3, 4, bad]]), i32([80, 96]), workspace=ws)
+        assert nv.nvfp4_workspace_status(ws) == 8
+        assert torch.equal(got, want)
+    # entries past a sequence's length are not read
+    got = nv.kv_attention(qd, cache, i32([[0, 1, -1], [3, 99, 99]]), i32([64, 32]), workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 0
+
+
+def test_no_sequences_and_no_pages(nv):
+    import torch
+    cache = nv.kv_cache(2, 1, 16, 64)
+    q = torch.zeros((0, 1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert nv.kv_attention(q, cache, torch.zeros((0, 3), dtype=torch.int32, device="cuda"), i32([])).shape == (0, 1, 2, 64)
+    q = torch.ones((3, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = nv.kv_attention(q, cache, torch.zeros((3, 0), dtype=torch.int32, device="cuda"), i32([0, 0, 0]), lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_same_results_again(nv):
+    """Twice, on another stream, captured and replayed, and two calls at once on two streams."""
+    import torch
+    rng = np.random.default_rng(15)
+    dim, page = 128, 64
+    cache, q, sf = filled(nv, rng, 80, 2, page, dim)
+    qd, table, lengths = to_dev(bits(rng, (2, 2, 10, dim))), i32(rng.permutation(80).reshape(2, 40)), i32([2560, 999])
+    want = nv.kv_attention(qd, cache, table, lengths)
+    assert torch.equal(nv.kv_attention(qd, cache, table, lengths), want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [nv.kv_attention(qd, cache, table, lengths, stream=streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = nv.kv_attention(qd, cache, table, lengths)
+    lengths.fill_(700)
+    graph.replay()
+    assert torch.equal(out, nv.kv_attention(qd, cache, table, lengths))
