@@ -209,9 +209,9 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.init()  # (returns at once where it has been)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -588,10 +588,11 @@ def mx4_gemm(qa, sfa, qb, sfb, out_dtype: int = NVFP4_OUT_BF16, out=None, amax_o
 
 
 def dequantize(t: NVFP4Tensor, out_dtype: int = NVFP4_OUT_F32, stream=None):
-    import torch
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
-    out = torch.empty((t.rows, t.k), dtype=dt, device=t.q.device)
-    nvfp4_dequantize(t.q, t.sf, t.g, t.rows, t.k, t.sf_layout, out_dtype, out, stream)
+    q = t.q
+    out = _matrix(q.device, dt, t.rows, t.k)
+    _check(_lib.nvfp4_dequantize(q.data_ptr(), _ptr(t.sf), _ptr(t.g), t.rows, t.k, t.sf_layout, out_dtype,
+                                 out.data_ptr(), _stream(stream)), "nvfp4_dequantize")
     return out
 
 
@@ -1010,40 +1011,54 @@ def expert_mlp(x, routing: Routing, up, down, gate=None, base=None, *, workspace
         with _on(stream):
             return expert_mlp(x, routing, up, down, gate, base, workspace=workspace)
     offsets, row_index, slot_row, weight = routing.group_offsets, routing.row_index, routing.slot_row, routing.weight
-    gates = (None, None, None) if gate is None else (gate.q, gate.sf, gate.g)
-    dev = _one_device("expert_mlp", x, offsets, row_index, slot_row, weight, up.q, up.sf, up.g, down.q, down.sf, down.g,
-                      *gates, base, workspace)
+    uq, us, ug, dq, ds, dg = up.q, up.sf, up.g, down.q, down.sf, down.g
+    gq, gs, gg = (None, None, None) if gate is None else (gate.q, gate.sf, gate.g)
+    dev = _one_device("expert_mlp", x, offsets, row_index, slot_row, weight, uq, us, ug, dq, ds, dg, gq, gs, gg, base,
+                      workspace)
     ldx = _rows_of("expert_mlp: x", x)
     tokens, hidden = x.shape
     G, ffn, rows = offsets.numel() - 1, up.n, row_index.numel()
-    _need(down.n == hidden, f"expert_mlp: down has {down.n} rows, x {hidden} columns")
-    _flat("expert_mlp: group_offsets", offsets, torch.int32, G + 1)
-    _flat("expert_mlp: row_index", row_index, torch.int32, rows)
-    _need(slot_row.dim() == 2, "expert_mlp: slot_row [tokens, top_k] expected")
+    i32, f32 = torch.int32, torch.float32
+    _flat("expert_mlp: group_offsets", offsets, i32, G + 1)
+    _flat("expert_mlp: row_index", row_index, i32, rows)
+    if slot_row.dim() != 2:
+        raise ValueError("expert_mlp: slot_row [tokens, top_k] expected")
     k = slot_row.shape[1]
-    _flat("expert_mlp: slot_row", slot_row, torch.int32, tokens, k)
-    _flat("expert_mlp: weight", weight, torch.float32, tokens, k)
-    for name, w, n, cols in (("up", up, ffn, hidden), ("down", down, hidden, ffn), ("gate", gate, ffn, hidden)):
-        if w is not None:
-            _need(w.n == n, f"expert_mlp: {name} has {w.n} rows, {n} expected")
-            _flat(f"expert_mlp: {name}.q", w.q, torch.uint8, G, n, cols // 2)
-            _flat(f"expert_mlp: {name}.g", w.g, torch.float32, G)
-            _bytes(f"expert_mlp: {name}.sf", w.sf, G * nvfp4_sf_mma_bytes(n, cols))
-    bp = gp = gs = gg = None
+    _flat("expert_mlp: slot_row", slot_row, i32, tokens, k)
+    _flat("expert_mlp: weight", weight, f32, tokens, k)
+    if down.n != hidden:
+        raise ValueError(f"expert_mlp: down has {down.n} rows, x {hidden} columns")
+    _experts_matrix("expert_mlp: up", uq, us, ug, G, ffn, hidden)
+    _experts_matrix("expert_mlp: down", dq, ds, dg, G, hidden, ffn)
+    bp = gp = gsp = ggp = None
     if gate is not None:
-        gp, gs, gg = (t.data_ptr() for t in gates)
+        if gate.n != ffn:
+            raise ValueError(f"expert_mlp: gate has {gate.n} rows, up {ffn}")
+        _experts_matrix("expert_mlp: gate", gq, gs, gg, G, ffn, hidden)
+        gp, gsp, ggp = gq.data_ptr(), gs.data_ptr(), gg.data_ptr()
     if base is not None:
         _flat("expert_mlp: base", base, torch.bfloat16, tokens, hidden)
         bp = base.data_ptr()
     if workspace is None:
         workspace = torch.empty(nvfp4_expert_mlp_workspace_size(rows, hidden, ffn), dtype=torch.uint8, device=dev)
     out = _matrix(dev, torch.bfloat16, tokens, hidden)
-    _check(_lib.nvfp4_expert_mlp(G, offsets.data_ptr(), rows, x.data_ptr(), ldx, tokens, row_index.data_ptr(), gp, gs, gg,
-                                 up.q.data_ptr(), up.sf.data_ptr(), up.g.data_ptr(), down.q.data_ptr(),
-                                 down.sf.data_ptr(), down.g.data_ptr(), hidden, ffn, slot_row.data_ptr(),
-                                 weight.data_ptr(), k, bp, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                 _raw_stream(dev)), "nvfp4_expert_mlp")
+    _check(_lib.nvfp4_expert_mlp(G, offsets.data_ptr(), rows, x.data_ptr(), ldx, tokens, row_index.data_ptr(), gp, gsp,
+                                 ggp, uq.data_ptr(), us.data_ptr(), ug.data_ptr(), dq.data_ptr(), ds.data_ptr(),
+                                 dg.data_ptr(), hidden, ffn, slot_row.data_ptr(), weight.data_ptr(), k, bp,
+                                 out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
+           "nvfp4_expert_mlp")
     return out
+
+
+def _experts_matrix(name: str, q, sf, g, G: int, n: int, k: int) -> None:
+    """One NVFP4 matrix [n, k] per expert, tiled scales."""
+    if q.shape != (G, n, k // 2) or q.dtype is not torch.uint8 or not q.is_contiguous():
+        raise ValueError(f"{name}.q: contiguous uint8 {(G, n, k // 2)} expected, got {q.dtype} {tuple(q.shape)}")
+    if g.shape != (G,) or g.dtype is not torch.float32 or not g.is_contiguous():
+        raise ValueError(f"{name}.g: contiguous float32 {(G,)} expected, got {g.dtype} {tuple(g.shape)}")
+    least = G * ((n + 127) // 128 * 128) * (k // 16)
+    if sf.numel() < least or sf.element_size() != 1 or not sf.is_contiguous():
+        raise ValueError(f"{name}.sf: at least {least} contiguous bytes expected, got {sf.dtype} {tuple(sf.shape)}")
 
 
 # ------------------------------------------------- the cache of a decoding step, and attention over it
@@ -1058,10 +1073,12 @@ class KVCache:
     g: object
 
     def _half(self, which: int) -> NVFP4Tensor:
-        _, pages, heads, size, half = self.q.shape
-        rows = pages * heads * size
-        return NVFP4Tensor(self.q[which].view(rows, half), self.sf[which].view(rows, half // 8),
-                           self.g[which:which + 1], rows, 2 * half, NVFP4_SF_ROWMAJOR)
+        q, sf, g = self.q, self.sf, self.g
+        _, pages, heads, size, half = q.shape
+        rows, blocks = pages * heads * size, half // 8
+        return NVFP4Tensor(q.as_strided((rows, half), (half, 1), q.storage_offset() + which * rows * half),
+                           sf.as_strided((rows, blocks), (blocks, 1), sf.storage_offset() + which * rows * blocks),
+                           g.as_strided((1,), (1,), g.storage_offset() + which), rows, 2 * half, NVFP4_SF_ROWMAJOR)
 
     def keys(self) -> NVFP4Tensor:
         """The keys as one matrix [pages * kv_heads * page_size, dim], a view (for ``dequantize``)."""
@@ -1085,19 +1102,26 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, dim: int, amax_k: float 
 
 
 def _cache_view(name: str, cache: KVCache) -> KVCacheView:
-    q, sf = cache.q, cache.sf
+    q, sf, amax = cache.q, cache.sf, cache.amax
+    u8 = torch.uint8
     shape = q.shape
-    if len(shape) != 5 or shape[0] != 2:
-        raise ValueError(f"{name}: cache.q [2, pages, kv_heads, page_size, dim/2] expected, got {tuple(shape)}")
-    _flat(f"{name}: cache.q", q, torch.uint8, *shape)
-    _flat(f"{name}: cache.sf", sf, torch.uint8, 2, shape[1], shape[2], shape[3], shape[4] // 8)
-    _flat(f"{name}: cache.amax", cache.amax, torch.float32, 2)
-    return KVCacheView(q.data_ptr(), sf.data_ptr(), cache.amax.data_ptr(), shape[1], shape[2], shape[3], 2 * shape[4])
+    if len(shape) != 5 or shape[0] != 2 or q.dtype is not u8 or not q.is_contiguous():
+        raise ValueError(f"{name}: cache.q contiguous uint8 [2, pages, kv_heads, page_size, dim/2] expected, got {q.dtype} "
+                         f"{tuple(shape)}")
+    _, pages, heads, size, half = shape
+    if sf.shape != (2, pages, heads, size, half // 8) or sf.dtype is not u8 or not sf.is_contiguous():
+        raise ValueError(f"{name}: cache.sf contiguous uint8 {(2, pages, heads, size, half // 8)} expected, got {sf.dtype} "
+                         f"{tuple(sf.shape)}")
+    if amax.shape != (2,) or amax.dtype is not torch.float32 or not amax.is_contiguous():
+        raise ValueError(f"{name}: cache.amax float32 [2] expected, got {amax.dtype} {tuple(amax.shape)}")
+    return KVCacheView(q.data_ptr(), sf.data_ptr(), amax.data_ptr(), pages, heads, size, 2 * half)
 
 
 def _table_of(name: str, table):
-    _need(table.dtype is torch.int32 and table.dim() == 2, f"{name}: int32 table [sequences, pages] expected")
-    n, pages = table.shape
+    shape = table.shape
+    if len(shape) != 2 or table.dtype is not torch.int32:
+        raise ValueError(f"{name}: int32 table [sequences, pages] expected, got {table.dtype} {tuple(shape)}")
+    n, pages = shape
     if table.is_contiguous():
         return n, pages, pages
     _need(pages <= 1 or table.stride(1) == 1, f"{name}: rows of the table must be contiguous")
@@ -1106,13 +1130,13 @@ def _table_of(name: str, table):
 
 def _heads_of(name: str, t, tokens, heads, dim):
     """A bf16 tensor [tokens, heads, dim] with contiguous heads; returns its strides in elements."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be bfloat16 [tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
-    n, h, d = t.shape
-    if n != tokens or d != dim or (heads is not None and h != heads):
-        raise ValueError(f"{name}: [{tokens}, {heads or 'heads'}, {dim}] expected, got {tuple(t.shape)}")
-    _need(t.stride(2) == 1, f"{name}: heads must be contiguous")
-    return t.stride(0) if n > 1 else h * d, t.stride(1) if h > 1 else d
+    if t.shape != (tokens, heads, dim) or t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: bfloat16 {(tokens, heads, dim)} expected, got {t.dtype} {tuple(t.shape)}")
+    ld, hs, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: heads must be contiguous")
+    # (the stride of a single row or head is never used, and torch leaves it arbitrary)
+    return ld if tokens > 1 else heads * dim, hs if heads > 1 else dim
 
 
 def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None, sin=None, interleaved: bool = False,
@@ -1150,9 +1174,9 @@ def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None,
     if q is not None:
         _need(cp is not None, "kv_append: q is turned by cos and sin, which are missing")
         heads = q.shape[1] if q.dim() == 3 else 0
-        ldq, hsq = _heads_of("kv_append: q", q, tokens, None, dim)
+        ldq, hsq = _heads_of("kv_append: q", q, tokens, heads, dim)
         if q_out is None:
-            q_out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty_strided((tokens, heads, dim), (heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
         ldo, hso = _heads_of("kv_append: q_out", q_out, tokens, heads, dim)
         qp, op = q.data_ptr(), q_out.data_ptr()
     else:
@@ -1179,23 +1203,32 @@ def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = 
             return kv_attention(q, cache, table, lengths, scale=scale, window=window, lse=lse, workspace=workspace)
     dev = _one_device("kv_attention", q, cache.q, cache.sf, cache.amax, table, lengths, workspace)
     view = _cache_view("kv_attention", cache)
-    if q.dtype is not torch.bfloat16 or q.dim() != 4 or q.shape[3] != view.dim:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != view.dim or q.dtype is not torch.bfloat16:
         raise ValueError(f"kv_attention: q bfloat16 [sequences, queries, heads, {view.dim}] expected, got {q.dtype} "
-                         f"{tuple(q.shape)}")
-    n, new, heads, dim = q.shape
-    _need(q.stride(3) == 1, "kv_attention: heads of q must be contiguous")
+                         f"{tuple(shape)}")
+    n, new, heads, dim = shape
+    ldb, ldi, ldh, one = q.stride()
+    if one != 1:
+        raise ValueError("kv_attention: heads of q must be contiguous")
     sequences, pages, ldt = _table_of("kv_attention", table)
-    _need(sequences == n, f"kv_attention: a table of {sequences} sequences for {n}")
+    if sequences != n:
+        raise ValueError(f"kv_attention: a table of {sequences} sequences for {n}")
     _flat("kv_attention: lengths", lengths, torch.int32, n)
-    size = nvfp4_kv_attention_workspace_size(n, new, heads, view.kv_heads, dim, pages * view.page_size)
     if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    out = torch.empty((n, new, heads, dim), dtype=torch.bfloat16, device=dev)
+        workspace = torch.empty(_attention_bytes(n, new, heads, view.kv_heads, dim, pages * view.page_size),
+                                dtype=torch.uint8, device=dev)
+    out = torch.empty_strided(shape, (new * heads * dim, heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
     sums = torch.empty((n, new, heads), dtype=torch.float32, device=dev) if lse else None
-    _check(_lib.nvfp4_kv_attention(q.data_ptr(), q.stride(0) if n > 1 else 0, q.stride(1) if new > 1 else 0,
-                                   q.stride(2) if heads > 1 else dim, n, new, heads, ctypes.byref(view),
-                                   table.data_ptr(), ldt, pages, lengths.data_ptr(),
+    # (strides over a single sequence, token or head are never used, and torch leaves them arbitrary)
+    _check(_lib.nvfp4_kv_attention(q.data_ptr(), ldb if n > 1 else 0, ldi if new > 1 else 0, ldh if heads > 1 else dim, n,
+                                   new, heads, ctypes.byref(view), table.data_ptr(), ldt, pages, lengths.data_ptr(),
                                    dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
                                    sums.data_ptr() if lse else None, workspace.data_ptr(), workspace.numel(),
                                    _raw_stream(dev)), "nvfp4_kv_attention")
     return (out, sums) if lse else out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(*sizes) -> int:
+    return _lib.nvfp4_kv_attention_workspace_size(*sizes)

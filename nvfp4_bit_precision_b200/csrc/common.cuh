@@ -393,6 +393,15 @@ __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, f
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// d = a b + d, each lane rounded once.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
+        "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // max(|a|, |b|, |c|) in one instruction (exact).
 __device__ __forceinline__ float absmax3(float a, float b, float c)
 {
@@ -555,6 +564,22 @@ __device__ __forceinline__ void global_scales(float amax, float& S, float& g)
     }
     S = s;
     g = __fdiv_rn(amax, 2688.0f);
+}
+
+// RN(a / 6) for a >= 0.  Markstein's corrected quotient (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Develop. 34(1), 1990): q0 = RN(a z) with z = RN(1/6), the
+// remainder a - 6 q0 exactly in one fused multiply-add, then RN(q0 + r z).
+// Checked against the IEEE division for every non-negative float: equal for
+// every a >= 2^-120; below that (quotients near the subnormal range) the
+// division itself is used.
+__device__ __forceinline__ float div6_rn(float a)
+{
+    if (a < 7.52316384526264005100e-37f) return __fdiv_rn(a, 6.0f);  // 2^-120
+    const float z = 0.16666667163372039794921875f;                    // RN(1/6)
+    const float q0 = __fmul_rn(a, z);
+    const float r = __fmaf_rn(-q0, 6.0f, a);
+    return __fmaf_rn(r, z, q0);
 }
 
 // Offset of scale byte (row r, 16-block b) in the tiled tensor-core layout of

@@ -9,11 +9,11 @@
 //
 // The one rounding.  A product of a bf16 and an FP32 number is exact in FP64, and the
 // sum of two is then rounded to odd in FP32 (FP64's own rounding lies 29 bits below)
-// and to nearest in bf16.  Almost always FP32 is enough: with p = RN(b sin), r = RN(a
-// cos - p) is off by at most 2^-24 (|p| + |r|) and 2^-149 for each of the two roundings,
-// and where r - d and r + d, d = 2^-22 (|p| + |r|) + 2^-126, round to the same bf16
-// number, so does what lies between them.  Otherwise (about one number in 5000) the
-// FP64 form decides.
+// and to nearest in bf16.  Almost always FP32 is enough: its result r, of two or three
+// roundings, is off by less than 2^-23 t (|a| + |b|) + 2^-148, t the larger of |cos| and
+// |sin|, and where r - d and r + d, d = 2^-22 t (|a| + |b|) + 2^-126, round to the same bf16
+// number, so does what lies between them (the sums' own roundings are below 2^-24 t (|a| +
+// |b|)).  Otherwise (about one number in 4000) the FP64 form decides.
 #include "kv_cache.cuh"
 
 #include <algorithm>
@@ -30,7 +30,6 @@ struct AppendArgs {
     int64_t tokens;
     int heads;                   // query heads, 0 without queries
     int per_thread;              // heads that a thread goes over
-    int groups;                  // threads' head groups of a token
     const int32_t* table;
     int64_t ldt;
     int sequences, table_pages;
@@ -39,6 +38,8 @@ struct AppendArgs {
     int64_t angles;
     uint32_t* status;
 };
+
+constexpr float kLeast = 1.17549435082228750797e-38f;  // 2^-126
 
 // bf16 of a c - b s, rounded once.
 __device__ __noinline__ uint32_t turn_exactly(float a, float c, float b, float s)
@@ -50,59 +51,56 @@ __device__ __noinline__ uint32_t turn_exactly(float a, float c, float b, float s
     return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-// Two pairs' a' (or, with the roles exchanged and s negated, b') as packed bf16.
-__device__ __forceinline__ uint32_t turn2(float a0, float c0, float b0, float s0, float a1, float c1, float b1, float s1)
-{
-    const float p0 = __fmul_rn(b0, s0), p1 = __fmul_rn(b1, s1);
-    const float r0 = __fmaf_rn(a0, c0, -p0), r1 = __fmaf_rn(a1, c1, -p1);
-    const float small = 1.17549435082228750797e-38f, part = 2.384185791015625e-7f;  // 2^-126, 2^-22
-    const float d0 = __fmaf_rn(fabsf(p0) + fabsf(r0), part, small), d1 = __fmaf_rn(fabsf(p1) + fabsf(r1), part, small);
-    const uint32_t lo = pack2(r0 - d0, r1 - d1), hi = pack2(r0 + d0, r1 + d1);
-    if (lo == hi) return lo;
-    return turn_exactly(a0, c0, b0, s0) | turn_exactly(a1, c1, b1, s1) << 16;
-}
-
 // Eight consecutive numbers of a cached head, the other half of whose 16-block is the
 // neighbouring lane's: four bytes of codes at q, the scale byte (by the even lane) at sf.
-__device__ __forceinline__ void hold8(uint4 x, float S, uint8_t* q, uint8_t* sf, bool writes)
+// by: S / d for each scale byte.
+__device__ __forceinline__ void hold8(uint4 x, float S, const float* by, uint8_t* q, uint8_t* sf, bool writes)
 {
+    const uint32_t m2 = __vmaxu2(__vimax3_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t byte = e4m3_rne_sat(__fmul_rn(div6_rn(__uint_as_float(m << 16)), S));
+    const float r = by[byte & 127];
     float f[8];
     unpack8(x, f);
-    float m = absmax3(absmax3(absmax3(fabsf(f[0]), f[1], f[2]), f[3], f[4]), f[5], absmax3(fabsf(f[6]), f[7], 0.0f));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t byte = e4m3_rne_sat(__fmul_rn(__fdiv_rn(m, 6.0f), S));
-    const float d = e4m3_value(byte);
-    const float by = d > 0.0f ? __fdiv_rn(S, d) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) mul2(f[i], f[i + 1], f[i], f[i + 1], by, by);
+    for (int i = 0; i < 8; i += 2) mul2(f[i], f[i + 1], f[i], f[i + 1], r, r);
     const uint32_t codes = e2m1x8_rne(f);
     if (!writes) return;
     *reinterpret_cast<uint32_t*>(q) = codes;
     if ((threadIdx.x & 1) == 0) *sf = static_cast<uint8_t>(byte);
 }
 
-// DIM / 16 lanes a head: lane j has elements 8 j.. and ROT / 2 + 8 j.. of the turned
-// part, or the like of the rest, so that it has both numbers of each of its pairs
-// (ROT = -1: pairs of neighbours, any turned part).  A thread goes over several heads
-// of its token with the same sines and cosines.
+// DIM / 16 lanes a head: lane j has elements 8 j.. and rot / 2 + 8 j.. of the turned
+// part, or the like of the rest, so that it has both numbers of each of its pairs (with
+// NEIGHBOURS a pair's numbers are next to one another).  A thread goes over several
+// heads of its token with the same sines and cosines, the next one's numbers on their
+// way; the lanes of a warp have the same heads of neighbouring tokens, so that all of
+// them turn queries or all quantise.
 template <int DIM, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a, const int rot)
+__global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, const int rot)
 {
     constexpr int kLanes = DIM / 16;
+    __shared__ float s_by[2][128];
     wait_for_previous_kernel();
     let_next_kernel_start();
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
+    float S[2], g;
+    global_scales(a.cache.amax[0], S[0], g);
+    global_scales(a.cache.amax[1], S[1], g);
+    {
+        const int which = threadIdx.x >> 7;
+        const float d = e4m3_value(threadIdx.x & 127);
+        s_by[which][threadIdx.x & 127] = d > 0.0f ? __fdiv_rn(S[which], d) : 0.0f;
+    }
+    const int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
-    const int64_t t = item / a.groups;
-    const int group = static_cast<int>(item - t * a.groups);
-    const bool there = t < a.tokens;
     const int turned = rot / 16;  // lanes of the turned part
     const bool turns = lane < turned;
     const int first = turns ? 8 * lane : rot + 8 * (lane - turned);
     const int second = first + (turns ? rot : DIM - rot) / 2;
 
     int64_t at = -1, pos = -1;  // the token's place in a page's row of tokens, as tokens x heads
-    if (there) {
+    if (t < a.tokens) {
         pos = a.position[t];
         const int64_t seq = a.sequence ? a.sequence[t] : t;
         if (pos >= 0 && seq >= 0) {
@@ -110,90 +108,115 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a, const i
             int64_t page = -1;
             if (seq < a.sequences && index < a.table_pages && (!a.cos || pos < a.angles)) page = a.table[seq * a.ldt + index];
             if (page < 0 || page >= a.cache.pages) {
-                if (lane == 0 && group == 0) record_status(a.status, NVFP4_ERR_INDEX);
+                if (lane == 0 && blockIdx.y == 0) record_status(a.status, NVFP4_ERR_INDEX);
             } else {
                 at = (page * a.cache.kv_heads << a.cache.page_shift) + (pos & ((1 << a.cache.page_shift) - 1));
             }
         }
     }
     const bool kept = at >= 0;
-    float c[8], s[8];
-    if (turns && kept) {
-        const int64_t row = pos * (rot / 2);
-        if constexpr (NEIGHBOURS) {
+    const int keys = a.heads, values = a.heads + a.cache.kv_heads, all = values + a.cache.kv_heads;
+    const int h0 = blockIdx.y * a.per_thread, h1 = min(h0 + a.per_thread, all);
+    const auto load = [&](int h, uint4& x, uint4& y) {
+        x = y = make_uint4(0, 0, 0, 0);
+        if (!kept || h >= h1) return;
+        const uint16_t* const from = h < keys     ? a.q + t * a.ldq + h * a.hsq
+                                     : h < values ? a.k + t * a.ldk + (h - keys) * a.hsk
+                                                  : a.v + t * a.ldv + (h - values) * a.hsv;
+        x = *reinterpret_cast<const uint4*>(from + first);
+        y = *reinterpret_cast<const uint4*>(from + second);
+    };
+    uint4 x, y;
+    load(h0, x, y);
+    float c[8], ns[8], k[8];  // cosines, sines negated, 2^-22 of the larger one
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = a.cos[row + first / 2 + i], s[i] = a.sin[row + first / 2 + i];
-                c[4 + i] = a.cos[row + second / 2 + i], s[4 + i] = a.sin[row + second / 2 + i];
-            }
-        } else {
+    for (int i = 0; i < 8; ++i) c[i] = 1.0f, ns[i] = k[i] = 0.0f;
+    if (turns && kept && h0 < values) {
+        // pairs 0..3 and 4..7: at the first and the second place of NEIGHBOURS' pairs, else one after another
+        const float* const pc = a.cos + pos * (rot / 2);
+        const float* const ps = a.sin + pos * (rot / 2);
+        const int p0 = NEIGHBOURS ? first / 2 : first, p1 = NEIGHBOURS ? second / 2 : first + 4;
+        const float4 c0 = *reinterpret_cast<const float4*>(pc + p0), c1 = *reinterpret_cast<const float4*>(pc + p1);
+        const float4 s0 = *reinterpret_cast<const float4*>(ps + p0), s1 = *reinterpret_cast<const float4*>(ps + p1);
+        c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+        ns[0] = -s0.x, ns[1] = -s0.y, ns[2] = -s0.z, ns[3] = -s0.w, ns[4] = -s1.x, ns[5] = -s1.y, ns[6] = -s1.z, ns[7] = -s1.w;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(a.cos + row + first + i);
-                const float4 y = *reinterpret_cast<const float4*>(a.sin + row + first + i);
-                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-            }
-        }
+        for (int i = 0; i < 8; ++i) k[i] = fmaxf(fabsf(c[i]), fabsf(ns[i])) * 2.384185791015625e-7f;  // 2^-22
     }
-    float S[2], g;
-    global_scales(a.cache.amax[0], S[0], g);
-    global_scales(a.cache.amax[1], S[1], g);
-    const int all = a.heads + 2 * a.cache.kv_heads;
+    __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < a.per_thread; ++i) {
-        const int h = group * a.per_thread + i;
-        const bool mine = kept && h < all;
-        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        if (mine) {
-            const uint16_t* from = h < a.heads                       ? a.q + t * a.ldq + h * a.hsq
-                                   : h < a.heads + a.cache.kv_heads ? a.k + t * a.ldk + (h - a.heads) * a.hsk
-                                                                    : a.v + t * a.ldv + (h - a.heads - a.cache.kv_heads) * a.hsv;
-            x = *reinterpret_cast<const uint4*>(from + first);
-            y = *reinterpret_cast<const uint4*>(from + second);
-        }
-        if (mine && turns && h < a.heads + a.cache.kv_heads) {
-            float u[8], w[8];
-            unpack8(x, u);
-            unpack8(y, w);
-            uint32_t p[4], r[4];
+    for (int h = h0; h < h1; ++h) {
+        uint4 xn, yn;
+        load(h + 1, xn, yn);
+        if (turns && kept && h < values) {
+            float u[8], w[8];  // the pairs' numbers
             if constexpr (NEIGHBOURS) {
-                uint32_t e[4], o[4];  // the even and odd elements of pairs 2 j, 2 j + 1
+                float f[8], e[8];
+                unpack8(x, f);
+                unpack8(y, e);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    e[j] = turn2(u[4 * j], c[2 * j], u[4 * j + 1], s[2 * j], u[4 * j + 2], c[2 * j + 1], u[4 * j + 3], s[2 * j + 1]);
-                    o[j] = turn2(u[4 * j + 1], c[2 * j], u[4 * j], -s[2 * j], u[4 * j + 3], c[2 * j + 1], u[4 * j + 2], -s[2 * j + 1]);
-                    e[2 + j] = turn2(w[4 * j], c[4 + 2 * j], w[4 * j + 1], s[4 + 2 * j], w[4 * j + 2], c[5 + 2 * j], w[4 * j + 3], s[5 + 2 * j]);
-                    o[2 + j] = turn2(w[4 * j + 1], c[4 + 2 * j], w[4 * j], -s[4 + 2 * j], w[4 * j + 3], c[5 + 2 * j], w[4 * j + 2], -s[5 + 2 * j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    p[2 * j] = __byte_perm(e[j], o[j], 0x5410), p[2 * j + 1] = __byte_perm(e[j], o[j], 0x7632);
-                    r[2 * j] = __byte_perm(e[2 + j], o[2 + j], 0x5410), r[2 * j + 1] = __byte_perm(e[2 + j], o[2 + j], 0x7632);
-                }
+                for (int j = 0; j < 4; ++j) u[j] = f[2 * j], w[j] = f[2 * j + 1], u[4 + j] = e[2 * j], w[4 + j] = e[2 * j + 1];
             } else {
+                unpack8(x, u);
+                unpack8(y, w);
+            }
+            uint32_t p[8], differ = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[j] = turn2(u[2 * j], c[2 * j], w[2 * j], s[2 * j], u[2 * j + 1], c[2 * j + 1], w[2 * j + 1], s[2 * j + 1]);
-                    r[j] = turn2(w[2 * j], c[2 * j], u[2 * j], -s[2 * j], w[2 * j + 1], c[2 * j + 1], u[2 * j + 1], -s[2 * j + 1]);
+            for (int j = 0; j < 8; j += 2) {
+                float r0, r1, q0, q1, m0, m1, l[4], g[4];
+                mul2(r0, r1, w[j], w[j + 1], ns[j], ns[j + 1]);
+                fma2(r0, r1, u[j], u[j + 1], c[j], c[j + 1]);
+                mul2(q0, q1, w[j], w[j + 1], c[j], c[j + 1]);
+                mul2(m0, m1, u[j], u[j + 1], ns[j], ns[j + 1]);
+                sub2(q0, q1, q0, q1, m0, m1);
+                float d0 = kLeast, d1 = kLeast;
+                fma2(d0, d1, fabsf(u[j]) + fabsf(w[j]), fabsf(u[j + 1]) + fabsf(w[j + 1]), k[j], k[j + 1]);
+                sub2(l[0], l[1], r0, r1, d0, d1);
+                add2(g[0], g[1], r0, r1, d0, d1);
+                sub2(l[2], l[3], q0, q1, d0, d1);
+                add2(g[2], g[3], q0, q1, d0, d1);
+                // words as they are stored: neighbours' pairs one after another, or the pairs' first and then their second numbers
+                if constexpr (NEIGHBOURS) {
+                    p[j] = pack2(l[0], l[2]), p[j + 1] = pack2(l[1], l[3]);
+                    differ |= (p[j] ^ pack2(g[0], g[2])) | (p[j + 1] ^ pack2(g[1], g[3]));
+                } else {
+                    p[j / 2] = pack2(l[0], l[1]), p[4 + j / 2] = pack2(l[2], l[3]);
+                    differ |= (p[j / 2] ^ pack2(g[0], g[1])) | (p[4 + j / 2] ^ pack2(g[2], g[3]));
                 }
             }
-            x = make_uint4(p[0], p[1], p[2], p[3]), y = make_uint4(r[0], r[1], r[2], r[3]);
+            if (differ) {  // the pairs that FP32 left open, looked for again (products may come out fused here or above)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float r = fmaf(u[j], c[j], w[j] * ns[j]), q = w[j] * c[j] - u[j] * ns[j];
+                    const float d = fmaf(fabsf(u[j]) + fabsf(w[j]), k[j], kLeast);
+                    uint32_t both = pack2(r - d, q - d);
+                    if (both != pack2(r + d, q + d))
+                        both = turn_exactly(u[j], c[j], w[j], -ns[j]) | turn_exactly(w[j], c[j], u[j], ns[j]) << 16;
+                    if constexpr (NEIGHBOURS) {
+                        p[j] = both;
+                    } else {
+                        p[j >> 1] = __byte_perm(p[j >> 1], both, j & 1 ? 0x5410 : 0x3254);
+                        p[4 + (j >> 1)] = __byte_perm(p[4 + (j >> 1)], both, j & 1 ? 0x7610 : 0x3276);
+                    }
+                }
+            }
+            x = make_uint4(p[0], p[1], p[2], p[3]), y = make_uint4(p[4], p[5], p[6], p[7]);
         }
-        if (mine && h < a.heads) {
-            uint16_t* const to = a.q_out + t * a.ldo + h * a.hso;
-            *reinterpret_cast<uint4*>(to + first) = x;
-            *reinterpret_cast<uint4*>(to + second) = y;
+        if (h < keys) {
+            if (kept) {
+                uint16_t* const to = a.q_out + t * a.ldo + h * a.hso;
+                *reinterpret_cast<uint4*>(to + first) = x;
+                *reinterpret_cast<uint4*>(to + second) = y;
+            }
+        } else {  // (the lanes of a block meet in hold8: all lanes have the same head)
+            const int which = h >= values;
+            const int64_t token = kept ? (which ? a.cache.half : 0) + at + (static_cast<int64_t>(h - (which ? values : keys)) << a.cache.page_shift) : 0;
+            uint8_t* const q = a.cache.q + token * (DIM / 2);
+            uint8_t* const sf = a.cache.sf + token * (DIM / 16);
+            hold8(x, S[which], s_by[which], q + first / 2, sf + first / 16, kept);
+            hold8(y, S[which], s_by[which], q + second / 2, sf + second / 16, kept);
         }
-        // (the lanes of a block meet in hold8: all lanes come here)
-        const bool holds = mine && h >= a.heads;
-        const bool values = h >= a.heads + a.cache.kv_heads;
-        const int head = holds ? h - a.heads - (values ? a.cache.kv_heads : 0) : 0;
-        const int64_t token = holds ? (values ? a.cache.half : 0) + at + (static_cast<int64_t>(head) << a.cache.page_shift) : 0;
-        uint8_t* const q = a.cache.q + token * (DIM / 2);
-        uint8_t* const sf = a.cache.sf + token * (DIM / 16);
-        hold8(x, S[values], q + first / 2, sf + first / 16, holds);
-        hold8(y, S[values], q + second / 2, sf + second / 16, holds);
+        x = xn, y = yn;
     }
 }
 
@@ -215,7 +238,7 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void*
     if (bad != NVFP4_OK) return bad;
     const int dim = cache->dim, kv = cache->kv_heads;
     if (tokens < 0 || tokens > 0x7fffffffll || sequences < 0 || sequences > 0x7fffffffll || table_pages < 0 ||
-        table_pages > 0x7fffffffll || ldt < table_pages || heads < 0 || heads > 65536 || angles < 0)
+        table_pages > 0x7fffffffll || ldt < table_pages || heads < 0 || heads > 32768 || angles < 0)
         return NVFP4_ERR_SHAPE;
     if ((neighbours != 0 && neighbours != 1) || !cos != !sin || (!q_bf16) != (!q_out) || (heads > 0) != (q_bf16 != nullptr) ||
         (heads > 0 && !cos))
@@ -249,14 +272,18 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void*
     a.sequences = static_cast<int>(sequences), a.table_pages = static_cast<int>(table_pages);
     a.position = position, a.sequence = sequence, a.cos = cos, a.sin = sin, a.angles = angles;
     const int all = heads + 2 * kv, lanes = dim / 16;
-    // several heads a thread once every multiprocessor has its 2048 threads
-    const int64_t rounds = tokens * all * lanes / (static_cast<int64_t>(sms) * 2048);
-    a.per_thread = static_cast<int>(std::min<int64_t>(std::max<int64_t>(rounds, 1), 8));
-    a.groups = (all + a.per_thread - 1) / a.per_thread;
-    const int64_t threads = tokens * a.groups * lanes, grid = (threads + 255) / 256;
-    if (grid > 0x7fffffffll) return NVFP4_ERR_SHAPE;
+    // several heads a thread once every multiprocessor has its threads
+    const int64_t rounds = tokens * all * lanes / (static_cast<int64_t>(sms) * 768);
+    const int per = static_cast<int>(std::min<int64_t>(std::max<int64_t>(rounds, 1), 8));
+    a.per_thread = per;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((tokens * lanes + 255) / 256), static_cast<unsigned>((all + per - 1) / per));
+    cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = a.status ? 0 : 1;
     cudaError_t err = cudaSuccess;
-    const auto go = [&](auto kernel) { err = launch_early(!a.status, kernel, grid, 256, 0, st, a, rot); };
+    const auto go = [&](auto kernel) { err = cudaLaunchKernelEx(&cfg, kernel, a, rot); };
     if (dim == 64) neighbours ? go(append_kernel<64, true>) : go(append_kernel<64, false>);
     else if (dim == 128) neighbours ? go(append_kernel<128, true>) : go(append_kernel<128, false>);
     else neighbours ? go(append_kernel<256, true>) : go(append_kernel<256, false>);

@@ -13,8 +13,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kSlice = 32;                // tokens of a warp's step
-constexpr int kTile = kWarps * kSlice;    // tokens by which work is dealt out
+constexpr int kTile = 128;                // tokens by which work is dealt out
 constexpr float kUp = 14.0f;              // exponentials are 2^14 at their largest: FP16 keeps those down to 2^-28 whole
 constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
 constexpr float kMinusInf = -__builtin_huge_valf();
@@ -32,16 +31,12 @@ struct AttendArgs {
     int rows, blocks, block_rows;  // rows (query, head of the group) of a key head, cut into blocks of so many
     int window;
     float scale;
-    int4* records;             // of each CTA: the item that it begins and others end (item, last CTA, -, whether)
+    int4* records;             // of each CTA: the item that it begins and others end (item, last CTA, sequence, whether),
+                               // and from bit 8 of the last on the status
     float2* part_ml;           // [2 CTAs][block_rows] maximum and sum of a part
     float* part_o;             // [2 CTAs][block_rows][dim]
     uint32_t* status;
 };
-
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
 {
@@ -69,7 +64,7 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two)
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                  "{%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -90,61 +85,71 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// What a sequence's rows see of it: tokens [begin, length), from a 32-token boundary, as tiles.
+// What a sequence's rows see of it: tokens [begin, length), from a tile's boundary on, as tiles.
 struct Span {
     int begin, length, tiles;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int seq)
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
 {
     const int64_t most = static_cast<int64_t>(a.table_pages) << a.cache.page_shift;
     int n = a.lengths[seq];
     if (n < 0 || n > most) {
-        record_status(a.status, NVFP4_ERR_INDEX);
+        *bad = NVFP4_ERR_INDEX;
         n = n < 0 ? 0 : static_cast<int>(most);
     }
     int begin = 0;
-    if (a.window > 0) begin = max(0, n - a.queries + 1 - a.window) & ~(kSlice - 1);
+    if (a.window > 0) begin = max(0, n - a.queries + 1 - a.window) & ~(kTile - 1);
     return {begin, n, max(1, (n - begin + kTile - 1) / kTile)};
 }
 
 template <int DIM, int NT>
 struct Shape {
+    static constexpr int kSlice = NT == 2 || DIM == 256 ? 32 : 64;  // tokens of a warp's step
     static constexpr int kCodes = kSlice * DIM / 2, kScales = kSlice * DIM / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = DIM == 256 ? 2 : 3;
+    static constexpr int kStages = kStage > 5000 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRows = 8 * NT;
     static_assert(kRing >= kRows * DIM * 4, "a warp's sums take its ring's place");
     static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kRing;
-    static constexpr int kCtas = DIM == 128 && NT == 2 ? 3 : DIM == 256 ? 3 : 4;  // of a multiprocessor
+    static constexpr int kCtas = 3;  // of a multiprocessor
 };
 
 template <int DIM, int NT>
 __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_kernel(const AttendArgs a)
 {
     using S = Shape<DIM, NT>;
+    constexpr int kSlice = S::kSlice, kM = kSlice / 16;
     constexpr int kSteps = DIM / 16;       // matrix instructions over the head dimension; 16-blocks of a token
     constexpr int kLaneCodes = DIM / 8;    // bytes of a token's keys that a lane reads
     constexpr int kRows = S::kRows;
-    extern __shared__ __align__(16) uint8_t s_dyn[];
+    extern __shared__ __align__(128) uint8_t s_dyn[];
     __shared__ int s_sum[kWarps];
-    __shared__ int s_seq, s_rel;
+    __shared__ int s_seq, s_rel, s_bad;
     __shared__ float2 s_ml[kWarps][kRows];
+    __shared__ uint64_t s_full[kWarps][S::kStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
     uint8_t* const my = s_dyn + warp * S::kRing;
-    const uint32_t ring = smem_addr(my);
+    uint64_t* const full = s_full[warp];
     const int items = a.cache.kv_heads * a.blocks;  // of a sequence
 
+    if (threadIdx.x == 0) s_bad = 0;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
     wait_for_previous_kernel();
     let_next_kernel_start();
+    __syncthreads();
     // All tiles of all items, sequence by sequence; this CTA's equal run of them, and
     // where it begins: each thread adds up some sequences.
     const int per = (a.sequences + 32 * kWarps - 1) / (32 * kWarps);
     const int s0 = min(a.sequences, static_cast<int>(threadIdx.x) * per), s1 = min(a.sequences, s0 + per);
     int mine = 0;
 #pragma unroll 1
-    for (int s = s0; s < s1; ++s) mine += span_of(a, s).tiles * items;
+    for (int s = s0; s < s1; ++s) mine += span_of(a, s, &s_bad).tiles * items;
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -166,23 +171,37 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
         int s = s0, at = f - (upto - mine);
 #pragma unroll 1
         for (;; ++s) {
-            const int n = span_of(a, s).tiles * items;
+            const int n = span_of(a, s, &s_bad).tiles * items;
             if (at < n) break;
             at -= n;
         }
         s_seq = s, s_rel = at;
     }
-    if (threadIdx.x == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    if (f >= f1) return;
     int seq = s_seq, rel = s_rel;
+    int4 record = make_int4(0, 0, 0, 0);
     float unused, gk, gv;
     global_scales(a.cache.amax[0], unused, gk);
     global_scales(a.cache.amax[1], unused, gv);
+    const int run_shift = min(a.cache.page_shift, kSlice == 64 ? 6 : 5);  // tokens that lie together and are copied at once
+    const int runs = kSlice >> run_shift;                                 // of those in a slice
+    const uint32_t run_bytes = (2 * (DIM / 2) + 2 * (DIM / 16)) << run_shift;
+    // Lane 4 i + j copies, of run i, the keys' codes, the values' codes, the keys' scales or the values' scales.
+    const int my_run = lane >> 2;
+    const bool my_scales = lane & 2, my_values = lane & 1;
+    const uint32_t my_bytes = my_scales ? DIM / 16 : DIM / 2;  // of a token
+    const uint32_t my_place = (my_scales ? 2 * S::kCodes : 0) + (my_values ? (my_scales ? S::kScales : S::kCodes) : 0) +
+                              ((my_run * my_bytes) << run_shift);
+    const uint8_t* const my_half = (my_scales ? a.cache.sf : a.cache.q) + (my_values ? a.cache.half * my_bytes : 0);
+    const uint32_t page_bytes = (a.cache.kv_heads * my_bytes) << a.cache.page_shift;
+    const uint32_t in_page = (1u << a.cache.page_shift) - 1;
+    int put = 0, get = 0;       // stages of the ring
+    uint32_t parity = 0;        // of the stage that is waited for
+    bool late = false;          // a copy did not come
 
 #pragma unroll 1
     while (f < f1) {
-        const Span span = span_of(a, seq);
+        const Span span = span_of(a, seq, &s_bad);
         const int item = rel / span.tiles, first_tile = rel - item * span.tiles;
         const int take = min(span.tiles - first_tile, f1 - f);
         const bool whole = take == span.tiles;
@@ -192,76 +211,57 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
         // this warp's slices
         const int slices = (max(end - begin, 0) + kSlice - 1) / kSlice;
         const int sl0 = slices * warp / kWarps, sl1 = slices * (warp + 1) / kWarps;
-        const int token0 = begin + sl0 * kSlice;
 
-        // Copies of a slice: codes and scales of 32 tokens' keys and values.  Pages of 32
-        // runs of 16 tokens are at hand at a time, one in each lane.
-        int page = -1, pages_from = 0;
-        const auto look_up = [&](int run) {  // this and the 31 runs of 16 tokens behind
-            const int index = (run + lane) >> (a.cache.page_shift - 4);
+        // Copies of a slice: the codes and scales of its tokens' keys and values, a run of a
+        // page each.  The pages of 32 runs are at hand at a time, one in each lane.
+        int page = -1, known = sl0, next = sl0;
+        const auto look_up = [&]() {  // of slice `next` on
+            const int token = begin + next * kSlice + (lane << run_shift);
             page = -1;
-            if ((run + lane) * 16 < end) {
-                page = a.table[seq * a.ldt + index];
+            if (token < end) {
+                page = a.table[seq * a.ldt + (token >> a.cache.page_shift)];
                 if (page < 0 || page >= a.cache.pages) {
-                    record_status(a.status, NVFP4_ERR_INDEX);
+                    s_bad = NVFP4_ERR_INDEX;
                     page = -1;
                 }
             }
-            pages_from = run;
+            known = next;
         };
-        int next = sl0, put = 0;
+        const uint8_t* const my_head = my_half + (static_cast<uint32_t>(head) << a.cache.page_shift) * my_bytes;
         const auto copy_slice = [&]() {
-            if (next < sl1) {
-                const int run = (begin + next * kSlice) / 16;
-                if (run - pages_from >= 32) look_up(run);
-                const uint32_t dst = ring + put * S::kStage;
-                const int in_page = (1 << a.cache.page_shift) - 1;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int p = __shfl_sync(0xffffffffu, page, run + half - pages_from);
-                    const int64_t token = p < 0 ? 0
-                                                : ((static_cast<int64_t>(p) * a.cache.kv_heads + head) << a.cache.page_shift) +
-                                                      ((run + half) * 16 & in_page);
-                    const uint8_t* const q = a.cache.q + token * (DIM / 2);
-                    const uint8_t* const sf = a.cache.sf + token * (DIM / 16);
-                    // 16 tokens of DIM / 32 vectors of 16 codes' bytes each
-#pragma unroll
-                    for (int c = lane; c < DIM / 2; c += 32) {
-                        constexpr int kRow = DIM / 32;
-                        const int tok = c / kRow, col = c % kRow;
-                        // keys: rows in order; values: the even tokens of eight before the odd ones (see below)
-                        const int vtok = (tok & 8) | (tok & 1) << 2 | (tok & 6) >> 1;
-                        int kcol = col, vcol = col;
-                        if (DIM == 128) vcol ^= vtok & 2;
-                        if (DIM == 256) kcol ^= tok & 1, vcol ^= 2 * (vtok & 3);
-                        copy16_async(dst + half * (S::kCodes / 2) + (tok * kRow + kcol) * 16, q + c * 16, p >= 0);
-                        copy16_async(dst + S::kCodes + half * (S::kCodes / 2) + (vtok * kRow + vcol) * 16,
-                                     q + a.cache.half * (DIM / 2) + c * 16, p >= 0);
-                    }
-                    constexpr int kVecs = DIM / 16;  // 16 tokens' scales, in vectors
-                    const int c = lane % kVecs;
-                    if (lane < 2 * kVecs) {
-                        const bool v = lane >= kVecs;
-                        copy16_async(dst + 2 * S::kCodes + (v ? S::kScales : 0) + half * (S::kScales / 2) + c * 16,
-                                     sf + (v ? a.cache.half * (DIM / 16) : 0) + c * 16, p >= 0);
-                    }
-                }
-                ++next;
-            }
-            put = put + 1 == S::kStages ? 0 : put + 1;
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        if (sl0 < sl1) look_up(token0 / 16);
+            if (next >= sl1) return;
+            if ((next - known + 1) * runs > 32) look_up();
+            const int p = __shfl_sync(0xffffffffu, page, (next - known) * runs + my_run);
+            const int token = begin + next * kSlice + (my_run << run_shift);
+            const bool wanted = my_run < runs && token < end, there = wanted && p >= 0;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * (run_bytes >> 2);
+            if (lane == 0) mbar_arrive_expect_tx(&full[put], bytes);
+            __syncwarp();
+            uint8_t* const to = my + put * S::kStage + my_place;
+            if (there) {
+                bulk_copy_g2s(to, my_head + static_cast<uint64_t>(static_cast<uint32_t>(p)) * page_bytes + (token & in_page) * my_bytes,
+                              my_bytes << run_shift, &full[put]);
+            } else if (wanted && my_scales) {  // zeros in a missing page's place
 #pragma unroll 1
-        for (int i = 0; i < S::kStages - 1; ++i) copy_slice();
+                for (int i = 0; i < (DIM / 64) << run_shift; ++i) reinterpret_cast<uint32_t*>(to)[i] = 0;
+                fence_proxy_async_smem();  // (the next copy into this place follows)
+            }
+            ++next;
+            put = put + 1 == S::kStages ? 0 : put + 1;
+        };
+        if (sl0 < sl1 && !late) {
+            look_up();
+#pragma unroll 1
+            for (int i = 0; i < S::kStages; ++i) copy_slice();
+        }
 
         // Queries as FP16, each row at the power of two that brings its largest magnitude
         // to [2^14, 2^15) (as in the few-token products): of step s, lane (r, t) has row r's
-        // elements t DIM / 4 + 4 s + 0..3.
+        // elements t DIM / 4 + 4 s + 0..3.  A negative scale turns their signs, so that the
+        // factors on the products are positive.
         uint32_t qf[NT][kSteps][2];
         float by[NT][2];       // factors on the products of rows 2 t, 2 t + 1: to base-2 logarithms
         int from[NT][2], to[NT][2];  // tokens that those rows see
-        int all_from = 0, all_to = 0x7fffffff;
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
             const int row = 8 * b + r, i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t ex = min(max(top >> 7, 15u), 254u);
-            const float up = __uint_as_float((268u - ex) << 23);
+            const float up = copysignf(__uint_as_float((268u - ex) << 23), a.scale);
 #pragma unroll
             for (int s = 0; s < kSteps / 2; ++s) {
                 float x[8];
@@ -291,25 +291,22 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                     qf[b][2 * s + j / 2][j & 1] = *reinterpret_cast<const uint32_t*>(&two);
                 }
             }
-            // scale g log2(e), then the row's power of two
+            // |scale| g log2(e), then the row's power of two; never zero, so that 0 x infinity does not arise
             const float down = __uint_as_float((ex - 14u) << 23);
-            const float f2 = a.scale * gk * 1.44269502162933349609375f;
+            const float f2 = fabsf(a.scale) * gk * 1.44269502162933349609375f;
 #pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2) {
-                by[b][i2] = f2 * __shfl_sync(0xffffffffu, down, (2 * t + i2) * 4);
-                const int n = 8 * b + 2 * t + i2;
+            for (int j = 0; j < 2; ++j) {
+                by[b][j] = fmaxf(f2 * __shfl_sync(0xffffffffu, down, (2 * t + j) * 4), 1.17549435082228750797e-38f);
+                const int n = 8 * b + 2 * t + j;
                 const int last = span.length - a.queries + (row0 + min(n, rows - 1)) / a.group;
-                to[b][i2] = last + 1;
-                from[b][i2] = a.window > 0 ? max(0, last + 1 - a.window) : 0;
+                to[b][j] = min(last + 1, end);
+                from[b][j] = a.window > 0 ? max(0, last + 1 - a.window) : 0;
             }
         }
-        {   // what every row sees; rows are in the queries' order
-            const int low = span.length - a.queries + row0 / a.group;
-            const int high = span.length - a.queries + (row0 + rows - 1) / a.group;
-            all_to = low + 1;
-            all_from = a.window > 0 ? max(0, high + 1 - a.window) : 0;
-        }
-        float top[NT][2], sum[NT][2], o[NT][kSteps][4];
+        // what every row sees; rows are in the queries' order
+        const int all_to = min(span.length - a.queries + row0 / a.group + 1, end);
+        const int all_from = a.window > 0 ? span.length - a.queries + (row0 + rows - 1) / a.group + 1 - a.window : 0;
+        float top[NT][2], sum[NT][2], o[NT][kSteps][4];  // top: the largest product so far
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
             top[b][0] = top[b][1] = kMinusInf;
@@ -318,39 +315,46 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             for (int i = 0; i < kSteps; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
         }
 
-        int get = 0;
+        // The tokens of a row of eight of a matrix instruction, in an order in which neighbouring
+        // lanes' reads of keys and of values meet other banks: row 2 j, 2 j + 1 has tokens 2 j and 2 j +
+        // 1, or the other way round.
+        const int my_token = r ^ (r >> 1 & 1), even_token = 2 * t ^ (t & 1), odd_token = (2 * t + 1) ^ (t & 1);
 #pragma unroll 1
-        for (int sl = sl0; sl < sl1; ++sl) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-            __syncwarp();  // this slice has come for every lane, and every lane is done with the last one
-            copy_slice();
+        for (int sl = sl0; sl < sl1 && !late; ++sl) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[get], parity))) {
+                // given up: no part of this warp's is worth anything, but nothing may be on its way into
+                // shared memory at the end
+                late = true;
+                s_bad = NVFP4_ERR_TIMEOUT;
+#pragma unroll 1
+                for (int i = 0; i < S::kStages; ++i) mbar_wait(&full[i], i >= get ? parity : parity ^ 1);
+                break;
+            }
+            __syncwarp();  // (zeros that a lane wrote are there for all)
             const uint8_t* const stage = my + get * S::kStage;
-            get = get + 1 == S::kStages ? 0 : get + 1;
             const int place = begin + sl * kSlice;  // of the first token
-            const bool edge = place < all_from || place + kSlice > min(all_to, end);
+            const bool edge = place < all_from || place + kSlice > all_to;
 
-            // x: 32 tokens x rows; lane (r, t): tokens r, r + 8 (+ 16), rows 2 t, 2 t + 1
-            float x[2][NT][4] = {};
+            // products: the slice's tokens x rows; lane (r, t): tokens (my_token) + 8 h + 16 m, rows 2 t, 2 t + 1
+            float x[kM][NT][4] = {};
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < kM; ++m) {
                 uint32_t code[2][kLaneCodes / 4], sc[2][DIM / 64];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int tok = 16 * m + 8 * h + r;
-                    const uint8_t* const row = stage + tok * (DIM / 2);
+                    const int tok = 16 * m + 8 * h + my_token;
+                    const uint8_t* const row = stage + tok * (DIM / 2) + t * kLaneCodes;
+                    const uint8_t* const scales = stage + 2 * S::kCodes + tok * kSteps + t * (DIM / 64);
                     if constexpr (DIM == 64) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(row + t * 8);
+                        const uint2 w = *reinterpret_cast<const uint2*>(row);
                         code[h][0] = w.x, code[h][1] = w.y;
-                        const uint32_t two = e4m3x2_f16(stage[2 * S::kCodes + tok * 4 + t]);
-                        sc[h][0] = __byte_perm(two, 0, 0x1010);
+                        sc[h][0] = __byte_perm(e4m3x2_f16(*scales), 0, 0x1010);
                     } else {
 #pragma unroll
                         for (int v = 0; v < DIM / 128; ++v) {
-                            const int col = DIM == 256 ? (2 * t + v) ^ (r & 1) : t;
-                            const uint4 w = *reinterpret_cast<const uint4*>(row + col * 16);
+                            const uint4 w = reinterpret_cast<const uint4*>(row)[v];
                             code[h][4 * v] = w.x, code[h][4 * v + 1] = w.y, code[h][4 * v + 2] = w.z, code[h][4 * v + 3] = w.w;
-                            const uint32_t two = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(
-                                stage + 2 * S::kCodes + tok * kSteps + t * (DIM / 64) + 2 * v));
+                            const uint32_t two = e4m3x2_f16(reinterpret_cast<const uint16_t*>(scales)[v]);
                             sc[h][2 * v] = __byte_perm(two, 0, 0x1010);
                             sc[h][2 * v + 1] = __byte_perm(two, 0, 0x3232);
                         }
@@ -372,51 +376,48 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                     }
                 }
             }
-            uint32_t p[2][NT][2];  // exponentials, FP16: row r, tokens 2 t, 2 t + 1 (+ 8)
+            uint32_t p[kM][NT][2];  // exponentials, FP16: row r, tokens of rows 2 t, 2 t + 1 (+ 8)
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
+                if (edge) {
+#pragma unroll
+                    for (int m = 0; m < kM; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = place + 16 * m + 8 * (i >> 1) + my_token;
+                            if (at < from[b][i & 1] || at >= to[b][i & 1]) x[m][b][i] = kMinusInf;
+                        }
+                }
                 float high[2] = {kMinusInf, kMinusInf};
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < kM; ++m) {
+                    high[0] = fmaxf(high[0], fmaxf(x[m][b][0], x[m][b][2]));
+                    high[1] = fmaxf(high[1], fmaxf(x[m][b][1], x[m][b][3]));
+                }
+                if (__any_sync(0xffffffffu, high[0] > top[b][0] || high[1] > top[b][1])) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float& v = x[m][b][i];
-                        v *= by[b][i & 1];
-                        if (edge) {
-                            const int at = place + 16 * m + 8 * (i >> 1) + r;
-                            if (at < from[b][i & 1] || at >= min(to[b][i & 1], end)) v = kMinusInf;
-                        }
-                        high[i & 1] = fmaxf(high[i & 1], v);
+                    for (int d = 4; d < 32; d <<= 1) {
+                        high[0] = fmaxf(high[0], __shfl_xor_sync(0xffffffffu, high[0], d));
+                        high[1] = fmaxf(high[1], __shfl_xor_sync(0xffffffffu, high[1], d));
                     }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    high[0] = fmaxf(high[0], __shfl_xor_sync(0xffffffffu, high[0], d));
-                    high[1] = fmaxf(high[1], __shfl_xor_sync(0xffffffffu, high[1], d));
-                }
-                float base[2];
-                bool rises = false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (high[i] > top[b][i]) rises = true;
-                }
-                if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float now = fmaxf(top[b][i], high[i]);
-                        const float less = now == top[b][i] ? 1.0f : exp2_fast(top[b][i] - now);  // (0 from nothing seen)
+                        const float less = now == top[b][i] ? 1.0f : exp2_fast((top[b][i] - now) * by[b][i]);  // (0 from nothing seen)
                         top[b][i] = now;
                         sum[b][i] *= less;
 #pragma unroll
                         for (int s = 0; s < kSteps; ++s) o[b][s][i] *= less, o[b][s][2 + i] *= less;
                     }
                 }
+                float base[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) base[i] = top[b][i] == kMinusInf ? 0.0f : top[b][i] - kUp;
+                for (int i = 0; i < 2; ++i) base[i] = top[b][i] == kMinusInf ? 0.0f : kUp - top[b][i] * by[b][i];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < kM; ++m) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[m][b][i] = exp2_fast(x[m][b][i] - base[i & 1]);
+                        x[m][b][i] = exp2_fast(fmaf(x[m][b][i], by[b][i & 1], base[i & 1]));
                         sum[b][i & 1] += x[m][b][i];
                     }
 #pragma unroll
@@ -426,31 +427,30 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                     }
                 }
             }
-            // o += p v.  Lane (r, t) reads, of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the 16-block (half of
-            // one, two) number r: the pairs of tokens that an operand register holds are put
+            // o += p v.  Lane (r, t) reads, of the tokens of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the 16-block (half
+            // of one, two) number r: the pairs of tokens that an operand register holds are put
             // together from two tokens' codes before these are converted.
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                constexpr int kWords = DIM / 128 > 0 ? DIM / 64 : 1;  // of a token, eight codes each
+            for (int m = 0; m < kM; ++m) {
+                constexpr int kWords = DIM / 64;  // of a token, eight codes each
                 constexpr int kBlocks = DIM == 256 ? 2 : 1;
                 uint32_t code[4][kWords], byte[4][kBlocks];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int tok = 16 * m + 8 * (j >> 1) + 2 * t + (j & 1);
-                    const int slot = 16 * m + 8 * (j >> 1) + 4 * (j & 1) + t;
-                    const uint8_t* const row = stage + S::kCodes + slot * (DIM / 2);
+                    const int tok = 16 * m + 8 * (j >> 1) + ((j & 1) ? odd_token : even_token);
+                    const uint8_t* const row = stage + S::kCodes + tok * (DIM / 2) + r * (DIM / 16);
+                    const uint8_t* const scales = stage + 2 * S::kCodes + S::kScales + tok * kSteps;
                     if constexpr (DIM == 64) {
-                        code[j][0] = *reinterpret_cast<const uint32_t*>(row + r * 4);
-                        byte[j][0] = stage[2 * S::kCodes + S::kScales + tok * 4 + (r >> 1)];
+                        code[j][0] = *reinterpret_cast<const uint32_t*>(row);
+                        byte[j][0] = scales[r >> 1];
                     } else if constexpr (DIM == 128) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ (slot & 2)) * 16 + (r & 1) * 8));
+                        const uint2 w = *reinterpret_cast<const uint2*>(row);
                         code[j][0] = w.x, code[j][1] = w.y;
-                        byte[j][0] = stage[2 * S::kCodes + S::kScales + tok * 8 + r];
+                        byte[j][0] = scales[r];
                     } else {
-                        const uint4 w = *reinterpret_cast<const uint4*>(row + (r ^ 2 * (slot & 3)) * 16);
+                        const uint4 w = *reinterpret_cast<const uint4*>(row);
                         code[j][0] = w.x, code[j][1] = w.y, code[j][2] = w.z, code[j][3] = w.w;
-                        const uint32_t two =
-                            *reinterpret_cast<const uint16_t*>(stage + 2 * S::kCodes + S::kScales + tok * 16 + 2 * r);
+                        const uint32_t two = reinterpret_cast<const uint16_t*>(scales)[r];
                         byte[j][0] = two & 0xFFu, byte[j][1] = two >> 8;
                     }
                 }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                         uint32_t bad = 0;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int at = 8 * (j >> 1) + 2 * t + (j & 1);
+                            const int at = 8 * (j >> 1) + ((j & 1) ? odd_token : even_token);
                             if (place + 16 * m + at >= end) byte[j][k] = 0;
                             if ((byte[j][k] & 0x7Fu) == 0x7Fu) bad |= 1u << at, byte[j][k] = 0;
                         }
@@ -511,10 +511,10 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                             mma_16816(o[b][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], p[m][b][0], p[m][b][1]);
                 }
             }
+            if (++get == S::kStages) get = 0, parity ^= 1;
+            __syncwarp();  // every lane is done with this stage
+            copy_slice();
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-
         // The warps' parts, joined: rows' sums of lane (r, t) are elements r DIM / 8.. of rows
         // 2 t, 2 t + 1.
         float* const s_o = reinterpret_cast<float*>(my);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
                 const int row = 8 * b + 2 * t + i;
-                if (r == 0) s_ml[warp][row] = make_float2(top[b][i], v);
+                if (r == 0) s_ml[warp][row] = make_float2(top[b][i] == kMinusInf ? kMinusInf : top[b][i] * by[b][i], v);
                 if (sl0 < sl1) {
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s)
@@ -535,9 +535,9 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             }
         __syncthreads();
         const int slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
-        if (!whole && first_tile == 0 && threadIdx.x == 0) {
+        if (!whole && first_tile == 0) {
             const int last = f + span.tiles - 1, cut = more * (each + 1);
-            a.records[blockIdx.x] = make_int4(item, last < cut ? last / (each + 1) : more + (last - cut) / each, seq, 1);
+            record = make_int4(item, last < cut ? last / (each + 1) : more + (last - cut) / each, seq, 1);
         }
 #pragma unroll 1
         for (int c = threadIdx.x; c < rows * (DIM / 4); c += 32 * kWarps) {
@@ -570,7 +570,12 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
         }
         f += take, rel += take;
         if (rel == span.tiles * items) ++seq, rel = 0;
+        fence_proxy_async_smem();
         __syncthreads();  // the next part's slices take the sums' place
+    }
+    if (threadIdx.x == 0) {
+        record.w |= s_bad << 8;
+        a.records[blockIdx.x] = record;
     }
 }
 
@@ -585,8 +590,14 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendArgs a)
     let_next_kernel_start();
     const int4 record = a.records[blockIdx.x];
     const int row = blockIdx.y;
+    if (blockIdx.x == 0 && row == 0) {  // the call's status
+        int bad = 0;
+        for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) bad = max(bad, a.records[i].w >> 8);
+        const int worst = __syncthreads_or(bad == NVFP4_ERR_INDEX), slow = __syncthreads_or(bad == NVFP4_ERR_TIMEOUT);
+        if (threadIdx.x == 0) *a.status = slow ? NVFP4_ERR_TIMEOUT : worst ? NVFP4_ERR_INDEX : NVFP4_OK;
+    }
     const int head = record.x / a.blocks, row0 = (record.x - head * a.blocks) * a.block_rows;
-    if (!record.w || row >= min(a.block_rows, a.rows - row0)) return;
+    if (!(record.w & 1) || row >= min(a.block_rows, a.rows - row0)) return;
     const int parts = record.y - static_cast<int>(blockIdx.x) + 1;
     const int lane = threadIdx.x / kVecs, d = threadIdx.x % kVecs;
     const auto place = [&](int part) {
@@ -638,8 +649,7 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
     const int most = dim == 256 || c.rows <= 8 ? 8 : 16;
     c.blocks = (c.rows + most - 1) / most;
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
-    const int wide = dim == 256 ? Shape<256, 1>::kCtas : most == 8 ? Shape<128, 1>::kCtas : dim == 128 ? Shape<128, 2>::kCtas : Shape<64, 2>::kCtas;
-    c.ctas = std::min<int64_t>(static_cast<int64_t>(sms) * wide,
+    c.ctas = std::min<int64_t>(static_cast<int64_t>(sms) * Shape<128, 1>::kCtas,
                                sequences * kv_heads * c.blocks * std::max<int64_t>(1, (capacity + kTile - 1) / kTile + 1));
     return c;
 }
@@ -659,7 +669,7 @@ nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
             return NVFP4_ERR_CUDA;
         raised[dev & 63] = true;
     }
-    if (launch_early(false, attend_kernel<DIM, NT>, cut.ctas, 32 * kWarps, S::kSmem, st, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (launch_early(true, attend_kernel<DIM, NT>, cut.ctas, 32 * kWarps, S::kSmem, st, a) != cudaSuccess) return NVFP4_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -743,7 +753,6 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     at += static_cast<size_t>(2 * cut.ctas) * cut.block_rows * dim * 4;
     a.part_ml = reinterpret_cast<float2*>(at);
     a.status = static_cast<uint32_t*>(workspace) + 2;
-    if (cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dim == 256) return start<256, 1>(a, cut, st);
     const bool one = cut.block_rows <= 8;
     if (dim == 128) return one ? start<128, 1>(a, cut, st) : start<128, 2>(a, cut, st);

@@ -89,14 +89,6 @@ __device__ __forceinline__ float block_sum_turn(float v, float (*s)[32], int& tu
     return t;
 }
 
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1)
-{
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
-        "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(d0), "+f"(d1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 // bf16(a + b), one rounding: the FP32 sum rounded to bf16 is the same number (it
 // is exact unless one addend is below 2^-16 of the other, far from any midpoint).
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
