@@ -10,10 +10,10 @@
 // The one rounding.  A product of a bf16 and an FP32 number is exact in FP64, and the
 // sum of two is then rounded to odd in FP32 (FP64's own rounding lies 29 bits below)
 // and to nearest in bf16.  Almost always FP32 is enough: its result r, of two or three
-// roundings, is off by less than 2^-23 t (|a| + |b|) + 2^-148, t the larger of |cos| and
-// |sin|, and where r - d and r + d, d = 2^-22 t (|a| + |b|) + 2^-126, round to the same bf16
-// number, so does what lies between them (the sums' own roundings are below 2^-24 t (|a| +
-// |b|)).  Otherwise (about one number in 4000) the FP64 form decides.
+// roundings, is off by less than 2^-23 t (|a| + |b|) + 2^-148, t the largest |cos| or |sin|
+// of the thread's pairs, and the sums r - d and r + d by less than 2^-24 (t + 2^-22) (|a| + |b|)
+// more.  Where these, with d = 1.6 * 2^-23 t (|a| + |b|) + 2^-126, round to the same bf16 number,
+// so does what lies between them.  Otherwise (about one number in 2000) the FP64 form decides.
 #include "kv_cache.cuh"
 
 #include <algorithm>
@@ -39,6 +39,7 @@ struct AppendArgs {
     uint32_t* status;
 };
 
+constexpr int kAhead = 4;  // heads whose numbers are on their way
 constexpr float kLeast = 1.17549435082228750797e-38f;  // 2^-126
 
 // bf16 of a c - b s, rounded once.
@@ -74,7 +75,7 @@ __device__ __forceinline__ void hold8(uint4 x, float S, const float* by, uint8_t
 // DIM / 16 lanes a head: lane j has elements 8 j.. and rot / 2 + 8 j.. of the turned
 // part, or the like of the rest, so that it has both numbers of each of its pairs (with
 // NEIGHBOURS a pair's numbers are next to one another).  A thread goes over several
-// heads of its token with the same sines and cosines, the next one's numbers on their
+// heads of its token with the same sines and cosines, the next ones' numbers on their
 // way; the lanes of a warp have the same heads of neighbouring tokens, so that all of
 // them turn queries or all quantise.
 template <int DIM, bool NEIGHBOURS>
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
 {
     constexpr int kLanes = DIM / 16;
     __shared__ float s_by[2][128];
+    __shared__ uint4 s_ahead[kAhead * 512];
     wait_for_previous_kernel();
     let_next_kernel_start();
     float S[2], g;
@@ -117,20 +119,24 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
     const bool kept = at >= 0;
     const int keys = a.heads, values = a.heads + a.cache.kv_heads, all = values + a.cache.kv_heads;
     const int h0 = blockIdx.y * a.per_thread, h1 = min(h0 + a.per_thread, all);
-    const auto load = [&](int h, uint4& x, uint4& y) {
-        x = y = make_uint4(0, 0, 0, 0);
-        if (!kept || h >= h1) return;
-        const uint16_t* const from = h < keys     ? a.q + t * a.ldq + h * a.hsq
-                                     : h < values ? a.k + t * a.ldk + (h - keys) * a.hsk
-                                                  : a.v + t * a.ldv + (h - values) * a.hsv;
-        x = *reinterpret_cast<const uint4*>(from + first);
-        y = *reinterpret_cast<const uint4*>(from + second);
+    // the numbers of the next heads, each thread's for itself
+    const uint32_t mine = smem_addr(s_ahead + threadIdx.x);
+    const auto fetch = [&](int h) {
+        if (kept && h < h1) {
+            const uint16_t* const from = h < keys     ? a.q + t * a.ldq + h * a.hsq
+                                         : h < values ? a.k + t * a.ldk + (h - keys) * a.hsk
+                                                      : a.v + t * a.ldv + (h - values) * a.hsv;
+            const uint32_t to = mine + (h - h0) % kAhead * (512 * 16);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + first) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 256 * 16), "l"(from + second) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint4 x, y;
-    load(h0, x, y);
-    float c[8], ns[8], k[8];  // cosines, sines negated, 2^-22 of the larger one
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.0f, ns[i] = k[i] = 0.0f;
+    for (int i = 0; i < kAhead; ++i) fetch(h0 + i);
+    float c[8], ns[8], k = 0.0f;  // cosines, sines negated, 1.6 * 2^-23 of the largest
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 1.0f, ns[i] = 0.0f;
     if (turns && kept && h0 < values) {
         // pairs 0..3 and 4..7: at the first and the second place of NEIGHBOURS' pairs, else one after another
         const float* const pc = a.cos + pos * (rot / 2);
@@ -141,13 +147,19 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
         c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
         ns[0] = -s0.x, ns[1] = -s0.y, ns[2] = -s0.z, ns[3] = -s0.w, ns[4] = -s1.x, ns[5] = -s1.y, ns[6] = -s1.z, ns[7] = -s1.w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = fmaxf(fabsf(c[i]), fabsf(ns[i])) * 2.384185791015625e-7f;  // 2^-22
+        for (int i = 0; i < 8; ++i) k = fmaxf(k, fmaxf(fabsf(c[i]), fabsf(ns[i])));
+        k *= 1.9073486328125e-7f;
     }
     __syncthreads();
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
-        uint4 xn, yn;
-        load(h + 1, xn, yn);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (kept) {
+            const uint4* const from = s_ahead + (h - h0) % kAhead * 512 + threadIdx.x;
+            x = from[0], y = from[256];
+        }
+        fetch(h + kAhead);
         if (turns && kept && h < values) {
             float u[8], w[8];  // the pairs' numbers
             if constexpr (NEIGHBOURS) {
@@ -170,7 +182,7 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
                 mul2(m0, m1, u[j], u[j + 1], ns[j], ns[j + 1]);
                 sub2(q0, q1, q0, q1, m0, m1);
                 float d0 = kLeast, d1 = kLeast;
-                fma2(d0, d1, fabsf(u[j]) + fabsf(w[j]), fabsf(u[j + 1]) + fabsf(w[j + 1]), k[j], k[j + 1]);
+                fma2(d0, d1, fabsf(u[j]) + fabsf(w[j]), fabsf(u[j + 1]) + fabsf(w[j + 1]), k, k);
                 sub2(l[0], l[1], r0, r1, d0, d1);
                 add2(g[0], g[1], r0, r1, d0, d1);
                 sub2(l[2], l[3], q0, q1, d0, d1);
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float r = fmaf(u[j], c[j], w[j] * ns[j]), q = w[j] * c[j] - u[j] * ns[j];
-                    const float d = fmaf(fabsf(u[j]) + fabsf(w[j]), k[j], kLeast);
+                    const float d = fmaf(fabsf(u[j]) + fabsf(w[j]), k, kLeast);
                     uint32_t both = pack2(r - d, q - d);
                     if (both != pack2(r + d, q + d))
                         both = turn_exactly(u[j], c[j], w[j], -ns[j]) | turn_exactly(w[j], c[j], u[j], ns[j]) << 16;
@@ -216,7 +228,6 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
             hold8(x, S[which], s_by[which], q + first / 2, sf + first / 16, kept);
             hold8(y, S[which], s_by[which], q + second / 2, sf + second / 16, kept);
         }
-        x = xn, y = yn;
     }
 }
 
