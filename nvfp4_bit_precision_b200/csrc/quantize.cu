@@ -1168,7 +1168,7 @@ __device__ __forceinline__ void e2m1x2_to_f32(uint32_t byte, float& lo, float& h
 
 __global__ void __launch_bounds__(256) dequant_kernel(const uint8_t* q, const uint8_t* sf,
                                                       const float* gp, int64_t rows, int64_t cols,
-                                                      int mma_sf, int bf16_out, void* out)
+                                                      int bf16_out, void* out)
 {
     const float g = *gp;
     const int64_t nb = rows * (cols / 16);
@@ -1176,8 +1176,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint8_t* q, const ui
          blk += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = blk / (cols / 16), b = blk - r * (cols / 16);
         const uint2 c = *reinterpret_cast<const uint2*>(q + r * (cols / 2) + b * 8);
-        const int64_t off = mma_sf ? sf_mma_offset(r, b, cols / 16) : r * (cols / 16) + b;
-        const float d = e4m3_value(sf[off]);
+        const float d = e4m3_value(sf[sf_mma_offset(r, b, cols / 16)]);
         float v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -1201,6 +1200,49 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint8_t* q, const ui
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + r * cols + b * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+    }
+}
+
+// The same with row-major scales, where the blocks of all rows lie one after another:
+// eight elements a thread and step, so that a warp's stores are whole lines, four steps'
+// loads in flight.  Keys of 64 x 512 tokens in 8 heads of 128 to bf16 (86 MB) 15 us;
+// with the blocks found by division, 32 bytes a thread, 20 us.
+__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* q, const uint8_t* sf, const float* gp,
+                                                           int64_t eights, int bf16_out, void* out)
+{
+    constexpr int kSteps = 4;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const float g = *gp;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+#pragma unroll 1
+    for (int64_t u0 = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; u0 < eights; u0 += kSteps * stride) {
+        uint32_t codes[kSteps], byte[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int64_t u = u0 + j * stride;
+            codes[j] = u < eights ? reinterpret_cast<const uint32_t*>(q)[u] : 0;
+            byte[j] = u < eights ? sf[u >> 1] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int64_t u = u0 + j * stride;
+            if (u >= eights) break;
+            const float d = e4m3_value(byte[j]);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e2m1x2_to_f32(codes[j] >> (8 * i), v[2 * i], v[2 * i + 1]);
+                v[2 * i] = __fmul_rn(__fmul_rn(v[2 * i], d), g);
+                v[2 * i + 1] = __fmul_rn(__fmul_rn(v[2 * i + 1], d), g);
+            }
+            if (bf16_out) {
+                static_cast<uint4*>(out)[u] = pack8(v);
+            } else {
+                static_cast<float4*>(out)[2 * u] = make_float4(v[0], v[1], v[2], v[3]);
+                static_cast<float4*>(out)[2 * u + 1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
         }
     }
 }
@@ -1625,8 +1667,16 @@ extern "C" nvfp4_status nvfp4_dequantize(const uint8_t* q, const uint8_t* sf, co
     if (!info.ok) return NVFP4_ERR_UNSUPPORTED;
     const int64_t nb = rows * (cols / 16);
     const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((nb + 255) / 256, (int64_t)info.sms * 8));
+    if (sf_layout == NVFP4_SF_ROWMAJOR) {
+        const int64_t eights = 2 * nb, most = static_cast<int64_t>(info.sms) * 8;
+        const int64_t grid = std::min<int64_t>((eights + 255) / 256, most);
+        if (launch_early(true, dequant_rows_kernel, grid, 256, 0, static_cast<cudaStream_t>(stream), q, sf, g, eights,
+                         static_cast<int>(out_dtype == NVFP4_OUT_BF16), out) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    }
     dequant_kernel<<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        q, sf, g, rows, cols, sf_layout == NVFP4_SF_MMA, out_dtype == NVFP4_OUT_BF16, out);
+        q, sf, g, rows, cols, out_dtype == NVFP4_OUT_BF16, out);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
