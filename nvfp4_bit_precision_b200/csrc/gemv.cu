@@ -86,7 +86,7 @@ struct Divisor {
 };
 
 // What becomes of the products.
-enum Epilogue { kProduct, kGated, kSquared };
+enum Epilogue { kProduct, kGated, kSquared, kLateRows };
 
 struct GemvArgs {
     const uint16_t* x;
@@ -210,6 +210,9 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at)
 // of which the halves 64 h + 32 i + 4 u + 0..3 (i < 2) of a 128-row block have tiles 8 h +
 // u; lane (r, t) then has both products of row r, and silu(gate) * up leaves in their
 // place.  kSquared: the squared positive part of the product does.
+//
+// kLateRows: x comes from the kernel before, the rest from before that one; the first
+// weights are asked for while the other kernel ends.
 template <int NT, bool PANELS, int FORM>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs a)
 {
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_acc) + (PANELS ? kPanelTiles * tile_sum_bytes(NT) : 0);
     const int panel_steps = PANELS ? a.panel_steps : steps;
 
-    wait_for_previous_kernel();
+    if (FORM != kLateRows) wait_for_previous_kernel();
     let_next_kernel_start();
     int active = 0;  // groups that have rows
     const bool one = !a.group_offsets;  // one matrix: a CTA has tiles of one segment
@@ -473,6 +476,12 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             int xr = 0, c = warp - kGemvWarps;
             next(xr, c);
             bool primed = false;
+            if constexpr (FORM == kLateRows) {
+#pragma unroll 1
+                for (int s = 0; s < kStages - 1; ++s) copy_step();
+                primed = true;
+                wait_for_previous_kernel();
+            }
 #pragma unroll 1
             do {
                 uint4 v[kAhead];
@@ -787,6 +796,9 @@ nvfp4_status launch_rows(GemvArgs a, int out_dtype, int form, int sms, bool earl
         const bool two = 3 * passes(2) <= 2 * passes(1);
         if (form == kGated)
             return two ? start_gemv<2, false, kGated>(a, Plan(), sms, early, st) : start_gemv<1, false, kGated>(a, Plan(), sms, early, st);
+        if (form == kLateRows)
+            return two ? start_gemv<2, false, kLateRows>(a, Plan(), sms, early, st)
+                       : start_gemv<1, false, kLateRows>(a, Plan(), sms, early, st);
         if (form == kSquared)
             return two ? start_gemv<2, false, kSquared>(a, Plan(), sms, early, st)
                        : start_gemv<1, false, kSquared>(a, Plan(), sms, early, st);
@@ -809,6 +821,71 @@ nvfp4_status launch_gemv(GemvArgs a, int out_dtype, void* workspace, size_t ws_b
     a.status = workspace ? static_cast<uint32_t*>(workspace) + 2 : nullptr;
     if (a.status && cudaMemsetAsync(a.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
     return a.rows == 0 ? NVFP4_OK : launch_rows(a, out_dtype, kProduct, sms, !a.status, st);
+}
+
+constexpr size_t kMlpHead = 256;
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct JoinArgs {
+    const float4* rows;
+    int64_t n_rows, vecs;          // four columns each
+    const int32_t* slot_row;
+    const float* weight;
+    int64_t tokens;
+    int k;
+    const uint2* base;             // NULL = 0
+    uint2* out;
+    const int32_t* row_index;
+    const int32_t* used;           // routed rows
+    uint32_t* status;
+};
+
+// The weighted sums of the tokens' rows on top of base, four columns a thread, as the
+// combine's: FP32 in slot order.  Only the rows come from the kernel before; the slots,
+// the weights and base are read while it ends, and the first CTA looks the indexes
+// over and leaves the call's status.
+__global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
+{
+    constexpr int kSlots = 4;  // whose loads are in flight together
+    let_next_kernel_start();
+    if (blockIdx.x == 0) {
+        bool bad = false;
+        const int64_t used = min(max(static_cast<int64_t>(*a.used), int64_t{0}), a.n_rows);
+        for (int64_t i = threadIdx.x; i < used; i += 256) bad |= a.row_index[i] < 0 || a.row_index[i] >= a.tokens;
+        for (int64_t i = threadIdx.x; i < a.tokens * a.k; i += 256) bad |= a.slot_row[i] >= a.n_rows;
+        const int any = __syncthreads_or(bad);
+        wait_for_previous_kernel();  // (whose call's workspace this is)
+        if (threadIdx.x == 0) *a.status = any ? NVFP4_ERR_INDEX : NVFP4_OK;
+    }
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t u = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; u < a.tokens * a.vecs; u += stride) {
+        const int64_t t = u / a.vecs, c = u - t * a.vecs;
+        uint2 b = make_uint2(0, 0);
+        if (a.base) b = a.base[u];
+        float4 acc = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
+        for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+            int32_t r[kSlots];
+            float w[kSlots];
+            float4 v[kSlots];
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                r[j] = j0 + j < a.k ? a.slot_row[t * a.k + j0 + j] : -1;
+                w[j] = j0 + j < a.k ? a.weight[t * a.k + j0 + j] : 0.0f;
+                if (r[j] >= a.n_rows) r[j] = -1;
+            }
+            wait_for_previous_kernel();
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j)
+                if (r[j] >= 0) v[j] = a.rows[r[j] * a.vecs + c];
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (r[j] < 0) continue;
+                acc.x = fmaf(w[j], v[j].x, acc.x), acc.y = fmaf(w[j], v[j].y, acc.y);
+                acc.z = fmaf(w[j], v[j].z, acc.z), acc.w = fmaf(w[j], v[j].w, acc.w);
+            }
+        }
+        a.out[u] = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
+    }
 }
 
 }  // namespace
@@ -843,11 +920,6 @@ extern "C" nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, 
     return launch_gemv(a, out_dtype, workspace, ws_bytes, stream);
 }
 
-namespace {
-constexpr size_t kMlpHead = 256;
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-}  // namespace
-
 extern "C" size_t nvfp4_expert_mlp_workspace_size(int64_t total_rows, int64_t hidden, int64_t ffn)
 {
     if (total_rows < 1 || hidden < 1 || ffn < 1) return kMlpHead;
@@ -863,40 +935,46 @@ extern "C" nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, in
                                          void* out_bf16, void* workspace, size_t ws_bytes, void* stream)
 {
     if (G < 1 || G > kMaxGemvGroups || !group_offsets || !gate_q != !gate_sf || !gate_q != !gate_g) return NVFP4_ERR_INVALID_ARG;
-    if (hidden % 128 || ffn % 128 || tokens < 0 || k < 1 || k > 64) return NVFP4_ERR_SHAPE;
-    if (total_rows > 0 && !row_index) return NVFP4_ERR_INVALID_ARG;
-    if (!slot_row || !weight || (tokens > 0 && !out_bf16)) return NVFP4_ERR_INVALID_ARG;
-    if (off16(gate_q) || off16(gate_sf) || (reinterpret_cast<uintptr_t>(gate_g) & 3u) || off16(base_bf16) || off16(out_bf16) ||
+    if (!up_q || !up_sf || !up_g || (tokens > 0 && (!slot_row || !weight || !out_bf16)) || (total_rows > 0 && !row_index))
+        return NVFP4_ERR_INVALID_ARG;
+    // (slots are counted in 31 bits)
+    if (hidden <= 0 || hidden % 128 || ffn <= 0 || ffn % 128 || tokens < 0 || total_rows < 0 || k < 1 || k > 64 || tokens > 0x7fffffffll / k)
+        return NVFP4_ERR_SHAPE;
+    if (off16(up_q) || off16(up_sf) || (reinterpret_cast<uintptr_t>(up_g) & 3u) || off16(base_bf16) || off16(out_bf16) ||
         ((reinterpret_cast<uintptr_t>(slot_row) | reinterpret_cast<uintptr_t>(weight)) & 3u))
         return NVFP4_ERR_ALIGN;
-    if (!workspace || off16(workspace) || ws_bytes < nvfp4_expert_mlp_workspace_size(total_rows, hidden, ffn))
-        return NVFP4_ERR_WORKSPACE;
+    if (!workspace || off16(workspace)) return NVFP4_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     GemvArgs up{};
     up.x = static_cast<const uint16_t*>(x_bf16), up.ldx = ldx, up.src_rows = tokens, up.row_index = row_index;
     up.group_offsets = group_offsets, up.groups = G, up.rows = total_rows;
     up.q = up_q, up.sf = up_sf, up.g = up_g, up.n = ffn, up.k = hidden, up.out = ws + kMlpHead, up.ldd = ffn;
     if (gate_q) up.q = gate_q, up.sf = gate_sf, up.g = gate_g, up.q2 = up_q, up.sf2 = up_sf, up.g2 = up_g;
-    if (gate_q && (!up_q || !up_sf || !up_g)) return NVFP4_ERR_INVALID_ARG;
-    if (off16(up_q) || off16(up_sf) || (reinterpret_cast<uintptr_t>(up_g) & 3u)) return NVFP4_ERR_ALIGN;
     if (const nvfp4_status s = check_gemv(up, NVFP4_OUT_BF16)) return s;
     GemvArgs down{};
     down.x = static_cast<const uint16_t*>(up.out), down.ldx = ffn, down.src_rows = total_rows;
     down.group_offsets = group_offsets, down.groups = G, down.rows = total_rows;
     down.q = down_q, down.sf = down_sf, down.g = down_g, down.n = hidden, down.k = ffn, down.ldd = hidden;
-    down.out = ws + kMlpHead + round256(static_cast<size_t>(std::max<int64_t>(total_rows, 0)) * ffn * 2);
+    down.out = ws + kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 2);
     if (const nvfp4_status s = check_gemv(down, NVFP4_OUT_F32)) return s;
+    if (ws_bytes < nvfp4_expert_mlp_workspace_size(total_rows, hidden, ffn)) return NVFP4_ERR_WORKSPACE;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     const int sms = sm100_sms(dev);
     if (!sms) return NVFP4_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    up.status = static_cast<uint32_t*>(workspace) + 2;
-    if (cudaMemsetAsync(up.status, 0, 4, st) != cudaSuccess) return NVFP4_ERR_CUDA;
+    uint32_t* const status = reinterpret_cast<uint32_t*>(ws) + 2;
+    if (tokens == 0) return cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
     if (total_rows > 0) {
-        if (const nvfp4_status s = launch_rows(up, NVFP4_OUT_BF16, gate_q ? kGated : kSquared, sms, false, st)) return s;
-        if (const nvfp4_status s = launch_rows(down, NVFP4_OUT_F32, kProduct, sms, true, st)) return s;
+        if (const nvfp4_status s = launch_rows(up, NVFP4_OUT_BF16, gate_q ? kGated : kSquared, sms, true, st)) return s;
+        if (const nvfp4_status s = launch_rows(down, NVFP4_OUT_F32, kLateRows, sms, true, st)) return s;
     }
-    return nvfp4_combine(down.out, NVFP4_OUT_F32, total_rows, hidden, slot_row, weight, tokens, k, base_bf16, out_bf16, nullptr, 0,
-                         stream);
+    JoinArgs j{};
+    j.rows = static_cast<const float4*>(down.out), j.n_rows = total_rows, j.vecs = hidden / 4;
+    j.slot_row = slot_row, j.weight = weight, j.tokens = tokens, j.k = k;
+    j.base = static_cast<const uint2*>(base_bf16), j.out = static_cast<uint2*>(out_bf16);
+    j.row_index = row_index, j.used = group_offsets + G, j.status = status;
+    const int64_t grid = std::min<int64_t>((tokens * j.vecs + 255) / 256, static_cast<int64_t>(sms) * 8);
+    if (launch_early(total_rows > 0, join_rows_kernel, grid, 256, 0, st, j) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
