@@ -12,9 +12,9 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = 128;                // tokens by which work is dealt out
+constexpr int kWarps = 12;                // of a CTA, one CTA a multiprocessor
 constexpr float kUp = 14.0f;              // exponentials are 2^14 at their largest: FP16 keeps those down to 2^-28 whole
+constexpr int kLeastSlice = 32;
 constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
 constexpr float kMinusInf = -__builtin_huge_valf();
 
@@ -31,10 +31,11 @@ struct AttendArgs {
     int rows, blocks, block_rows;  // rows (query, head of the group) of a key head, cut into blocks of so many
     int window;
     float scale;
-    int4* records;             // of each CTA: the item that it begins and others end (item, last CTA, sequence, whether),
-                               // and from bit 8 of the last on the status
-    float2* part_ml;           // [2 CTAs][block_rows] maximum and sum of a part
-    float* part_o;             // [2 CTAs][block_rows][dim]
+    int by_item;               // records are counted by items, else by workers
+    int4* records;             // of the items that a worker begins: item, its first and last worker, sequence (first < 0: one worker's)
+    int* bad;                  // of each CTA: what is to be reported
+    float2* part_ml;           // [2 workers][block_rows] maximum and sum of a part
+    float* part_o;             // [2 workers][block_rows][dim]
     uint32_t* status;
 };
 
@@ -85,10 +86,11 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// What a sequence's rows see of it: tokens [begin, length), from a tile's boundary on, as tiles.
+// What a sequence's rows see of it: tokens [begin, length), from a slice's boundary on, as slices.
 struct Span {
-    int begin, length, tiles;
+    int begin, length, slices;
 };
+template <int SLICE>
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
 {
     const int64_t most = static_cast<int64_t>(a.table_pages) << a.cache.page_shift;
@@ -98,8 +100,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
         n = n < 0 ? 0 : static_cast<int>(most);
     }
     int begin = 0;
-    if (a.window > 0) begin = max(0, n - a.queries + 1 - a.window) & ~(kTile - 1);
-    return {begin, n, max(1, (n - begin + kTile - 1) / kTile)};
+    if (a.window > 0) begin = max(0, n - a.queries + 1 - a.window) & ~(SLICE - 1);
+    return {begin, n, max(1, (n - begin + SLICE - 1) / SLICE)};
 }
 
 template <int DIM, int NT>
@@ -107,26 +109,26 @@ struct Shape {
     static constexpr int kSlice = NT == 2 || DIM == 256 ? 32 : 64;  // tokens of a warp's step
     static constexpr int kCodes = kSlice * DIM / 2, kScales = kSlice * DIM / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = kStage > 5000 ? 2 : 3;
+    static constexpr int kStages = kStage > 5000 ? 2 : kStage > 2500 ? 3 : 4;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kRows = 8 * NT;
-    static_assert(kRing >= kRows * DIM * 4, "a warp's sums take its ring's place");
     static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kRing;
-    static constexpr int kCtas = 3;  // of a multiprocessor
 };
 
+// Each warp is a worker of its own: it takes an equal run of all slices of all (sequence,
+// key head, block of rows) items, keeps its own maximum, sums and copies on their way, and
+// leaves an item's result, or its part of one that other workers share.
 template <int DIM, int NT>
-__global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_kernel(const AttendArgs a)
+__global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs a)
 {
     using S = Shape<DIM, NT>;
     constexpr int kSlice = S::kSlice, kM = kSlice / 16;
     constexpr int kSteps = DIM / 16;       // matrix instructions over the head dimension; 16-blocks of a token
     constexpr int kLaneCodes = DIM / 8;    // bytes of a token's keys that a lane reads
-    constexpr int kRows = S::kRows;
+    constexpr int kThreads = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t s_dyn[];
     __shared__ int s_sum[kWarps];
-    __shared__ int s_seq, s_rel, s_bad;
-    __shared__ float2 s_ml[kWarps][kRows];
+    __shared__ int s_upto[kThreads];
+    __shared__ int s_bad;
     __shared__ uint64_t s_full[kWarps][S::kStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
@@ -143,117 +145,130 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
     wait_for_previous_kernel();
     let_next_kernel_start();
     __syncthreads();
-    // All tiles of all items, sequence by sequence; this CTA's equal run of them, and
-    // where it begins: each thread adds up some sequences.
-    const int per = (a.sequences + 32 * kWarps - 1) / (32 * kWarps);
-    const int s0 = min(a.sequences, static_cast<int>(threadIdx.x) * per), s1 = min(a.sequences, s0 + per);
-    int mine = 0;
-#pragma unroll 1
-    for (int s = s0; s < s1; ++s) mine += span_of(a, s, &s_bad).tiles * items;
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-    }
-    if (lane == 31) s_sum[warp] = upto;
-    __syncthreads();
+    // All slices of all items, sequence by sequence: each thread adds up some sequences.
+    const int per = (a.sequences + kThreads - 1) / kThreads;
     int all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) upto += s_sum[w];
-        all += s_sum[w];
-    }
-    const int ctas = gridDim.x, each = all / ctas, more = all - each * ctas;
-    int f = static_cast<int>(blockIdx.x) * each + min(static_cast<int>(blockIdx.x), more);
-    const int f1 = f + each + (static_cast<int>(blockIdx.x) < more ? 1 : 0);
-    if (f >= upto - mine && f < upto) {
-        int s = s0, at = f - (upto - mine);
+    {
+        const int s0 = min(a.sequences, static_cast<int>(threadIdx.x) * per), s1 = min(a.sequences, s0 + per);
+        int upto = 0;
 #pragma unroll 1
-        for (;; ++s) {
-            const int n = span_of(a, s, &s_bad).tiles * items;
-            if (at < n) break;
-            at -= n;
+        for (int s = s0; s < s1; ++s) upto += span_of<kSlice>(a, s, &s_bad).slices * items;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
         }
-        s_seq = s, s_rel = at;
+        if (lane == 31) s_sum[warp] = upto;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += s_sum[w];
+            all += s_sum[w];
+        }
+        s_upto[threadIdx.x] = upto;
     }
     __syncthreads();
-    int seq = s_seq, rel = s_rel;
-    int4 record = make_int4(0, 0, 0, 0);
+    // This worker's run; neighbours are on different multiprocessors.  A slice takes a worker about
+    // as long as 16 more parts take the join of an item, so that runs grow as the root of an item's slices
+    // where there are few of these.
+    int least = 1;
+    while (16 * least * least < all / (a.sequences * items)) ++least;
+    const int workers = min(static_cast<int>(gridDim.x) * kWarps, (all + least - 1) / least);
+    const int worker = warp * gridDim.x + blockIdx.x;
+    const int each = all / workers, more = all - each * workers;
+    int left = worker < workers ? each + (worker < more ? 1 : 0) : 0;
+    if (left == 0 && lane == 0 && !a.by_item) a.records[worker] = make_int4(0, -1, 0, 0);
+    int seq = 0, rel = 0;  // where it begins: the sequence, the slice in it
+    if (left > 0) {
+        const int f = worker * each + min(worker, more);
+        int before = 0;  // threads whose sequences lie before
+#pragma unroll
+        for (int i = 0; i < kThreads; i += 32) before += __popc(__ballot_sync(0xffffffffu, s_upto[i + lane] <= f));
+        seq = before * per, rel = f - (before ? s_upto[before - 1] : 0);
+#pragma unroll 1
+        for (;; ++seq) {
+            const int n = span_of<kSlice>(a, seq, &s_bad).slices * items;
+            if (rel < n) break;
+            rel -= n;
+        }
+    }
+
+    // Copies, ahead of the work and across the items: the codes and scales of a slice's tokens'
+    // keys and values, a run of a page each.  Lane 4 i + j copies, of run i, the keys' codes, the
+    // values' codes, the keys' scales or the values' scales.  The pages of 32 runs are at hand at a
+    // time, one in each lane.
+    const int run_shift = min(a.cache.page_shift, kSlice == 64 ? 6 : 5);
+    const int runs = kSlice >> run_shift;  // of a slice
+    const int my_run = lane >> 2;
+    const bool my_scales = lane & 2;
+    const uint32_t my_bytes = my_scales ? DIM / 16 : DIM / 2;  // of a token
+    uint8_t* const my_place = my + (my_scales ? 2 * S::kCodes : 0) + (lane & 1 ? (my_scales ? S::kScales : S::kCodes) : 0) +
+                              ((my_run * my_bytes) << run_shift);
+    const uint8_t* const my_half = (my_scales ? a.cache.sf : a.cache.q) + (lane & 1 ? a.cache.half * my_bytes : 0);
+    int put = 0;                                      // stage of the ring
+    int c_left = left, c_seq = seq, c_rel = rel;      // slices to copy; where the next item's begin
+    int c_part = 0, c_token = 0, c_end = 0, c_head = 0, c_of = 0;  // of the item at hand: slices left, next token, end, head, sequence
+    int page = -1, known = 0;                         // pages at hand, and how many of them are used
+    const auto copy_slice = [&]() {
+        if (c_left == 0) return;
+        --c_left;
+        if (c_part == 0) {
+            const Span span = span_of<kSlice>(a, c_seq, &s_bad);
+            const int item = c_rel / span.slices, first = c_rel - item * span.slices;
+            c_part = min(span.slices - first, c_left + 1);
+            c_head = item / a.blocks, c_of = c_seq;
+            c_token = span.begin + first * kSlice, c_end = min(span.length, c_token + c_part * kSlice);
+            c_rel += c_part;
+            if (c_rel == span.slices * items) ++c_seq, c_rel = 0;
+            known = 32;
+        }
+        --c_part;
+        if (known + runs > 32) {
+            const int token = c_token + (lane << run_shift);
+            page = -1;
+            if (token < c_end) {
+                page = a.table[c_of * a.ldt + (token >> a.cache.page_shift)];
+                if (page < 0 || page >= a.cache.pages) s_bad = NVFP4_ERR_INDEX, page = -1;
+            }
+            known = 0;
+        }
+        const int p = __shfl_sync(0xffffffffu, page, known + my_run);
+        known += runs;
+        const int token = c_token + (my_run << run_shift);
+        c_token += kSlice;
+        const bool wanted = my_run < runs && token < c_end, there = wanted && p >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * ((DIM / 2 + DIM / 16) / 2 << run_shift);
+        if (lane == 0) mbar_arrive_expect_tx(&full[put], bytes);
+        __syncwarp();
+        uint8_t* const to = my_place + put * S::kStage;
+        if (there) {
+            const uint32_t in_page = token & ((1 << a.cache.page_shift) - 1);
+            const uint64_t at = ((static_cast<uint64_t>(p) * a.cache.kv_heads + c_head) << a.cache.page_shift) + in_page;
+            bulk_copy_g2s(to, my_half + at * my_bytes, my_bytes << run_shift, &full[put]);
+        } else if (wanted && my_scales) {  // zeros in a missing page's place
+#pragma unroll 1
+            for (int i = 0; i < (DIM / 64) << run_shift; ++i) reinterpret_cast<uint32_t*>(to)[i] = 0;
+            fence_proxy_async_smem();  // (the next copy into this place follows)
+        }
+        put = put + 1 == S::kStages ? 0 : put + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) copy_slice();
+
+    bool late = false;          // a copy did not come
+    int get = 0;                // stage that is worked on
+    uint32_t parity = 0;        // of its barrier
     float unused, gk, gv;
     global_scales(a.cache.amax[0], unused, gk);
     global_scales(a.cache.amax[1], unused, gv);
-    const int run_shift = min(a.cache.page_shift, kSlice == 64 ? 6 : 5);  // tokens that lie together and are copied at once
-    const int runs = kSlice >> run_shift;                                 // of those in a slice
-    const uint32_t run_bytes = (2 * (DIM / 2) + 2 * (DIM / 16)) << run_shift;
-    // Lane 4 i + j copies, of run i, the keys' codes, the values' codes, the keys' scales or the values' scales.
-    const int my_run = lane >> 2;
-    const bool my_scales = lane & 2, my_values = lane & 1;
-    const uint32_t my_bytes = my_scales ? DIM / 16 : DIM / 2;  // of a token
-    const uint32_t my_place = (my_scales ? 2 * S::kCodes : 0) + (my_values ? (my_scales ? S::kScales : S::kCodes) : 0) +
-                              ((my_run * my_bytes) << run_shift);
-    const uint8_t* const my_half = (my_scales ? a.cache.sf : a.cache.q) + (my_values ? a.cache.half * my_bytes : 0);
-    const uint32_t page_bytes = (a.cache.kv_heads * my_bytes) << a.cache.page_shift;
-    const uint32_t in_page = (1u << a.cache.page_shift) - 1;
-    int put = 0, get = 0;       // stages of the ring
-    uint32_t parity = 0;        // of the stage that is waited for
-    bool late = false;          // a copy did not come
-
 #pragma unroll 1
-    while (f < f1) {
-        const Span span = span_of(a, seq, &s_bad);
-        const int item = rel / span.tiles, first_tile = rel - item * span.tiles;
-        const int take = min(span.tiles - first_tile, f1 - f);
-        const bool whole = take == span.tiles;
+    while (left > 0 && !late) {
+        const Span span = span_of<kSlice>(a, seq, &s_bad);
+        const int item = rel / span.slices, first = rel - item * span.slices;
+        const int take = min(span.slices - first, left);
         const int head = item / a.blocks, row0 = (item - head * a.blocks) * a.block_rows;
         const int rows = min(a.block_rows, a.rows - row0);
-        const int begin = span.begin + first_tile * kTile, end = min(span.length, begin + take * kTile);
-        // this warp's slices
-        const int slices = (max(end - begin, 0) + kSlice - 1) / kSlice;
-        const int sl0 = slices * warp / kWarps, sl1 = slices * (warp + 1) / kWarps;
-
-        // Copies of a slice: the codes and scales of its tokens' keys and values, a run of a
-        // page each.  The pages of 32 runs are at hand at a time, one in each lane.
-        int page = -1, known = sl0, next = sl0;
-        const auto look_up = [&]() {  // of slice `next` on
-            const int token = begin + next * kSlice + (lane << run_shift);
-            page = -1;
-            if (token < end) {
-                page = a.table[seq * a.ldt + (token >> a.cache.page_shift)];
-                if (page < 0 || page >= a.cache.pages) {
-                    s_bad = NVFP4_ERR_INDEX;
-                    page = -1;
-                }
-            }
-            known = next;
-        };
-        const uint8_t* const my_head = my_half + (static_cast<uint32_t>(head) << a.cache.page_shift) * my_bytes;
-        const auto copy_slice = [&]() {
-            if (next >= sl1) return;
-            if ((next - known + 1) * runs > 32) look_up();
-            const int p = __shfl_sync(0xffffffffu, page, (next - known) * runs + my_run);
-            const int token = begin + next * kSlice + (my_run << run_shift);
-            const bool wanted = my_run < runs && token < end, there = wanted && p >= 0;
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * (run_bytes >> 2);
-            if (lane == 0) mbar_arrive_expect_tx(&full[put], bytes);
-            __syncwarp();
-            uint8_t* const to = my + put * S::kStage + my_place;
-            if (there) {
-                bulk_copy_g2s(to, my_head + static_cast<uint64_t>(static_cast<uint32_t>(p)) * page_bytes + (token & in_page) * my_bytes,
-                              my_bytes << run_shift, &full[put]);
-            } else if (wanted && my_scales) {  // zeros in a missing page's place
-#pragma unroll 1
-                for (int i = 0; i < (DIM / 64) << run_shift; ++i) reinterpret_cast<uint32_t*>(to)[i] = 0;
-                fence_proxy_async_smem();  // (the next copy into this place follows)
-            }
-            ++next;
-            put = put + 1 == S::kStages ? 0 : put + 1;
-        };
-        if (sl0 < sl1 && !late) {
-            look_up();
-#pragma unroll 1
-            for (int i = 0; i < S::kStages; ++i) copy_slice();
-        }
+        const int begin = span.begin + first * kSlice, end = min(span.length, begin + take * kSlice);
 
         // Queries as FP16, each row at the power of two that brings its largest magnitude
         // to [2^14, 2^15) (as in the few-token products): of step s, lane (r, t) has row r's
@@ -261,7 +276,6 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
         // factors on the products are positive.
         uint32_t qf[NT][kSteps][2];
         float by[NT][2];       // factors on the products of rows 2 t, 2 t + 1: to base-2 logarithms
-        int from[NT][2], to[NT][2];  // tokens that those rows see
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
             const int row = 8 * b + r, i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
@@ -295,17 +309,14 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             const float down = __uint_as_float((ex - 14u) << 23);
             const float f2 = fabsf(a.scale) * gk * 1.44269502162933349609375f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2; ++j)
                 by[b][j] = fmaxf(f2 * __shfl_sync(0xffffffffu, down, (2 * t + j) * 4), 1.17549435082228750797e-38f);
-                const int n = 8 * b + 2 * t + j;
-                const int last = span.length - a.queries + (row0 + min(n, rows - 1)) / a.group;
-                to[b][j] = min(last + 1, end);
-                from[b][j] = a.window > 0 ? max(0, last + 1 - a.window) : 0;
-            }
         }
-        // what every row sees; rows are in the queries' order
-        const int all_to = min(span.length - a.queries + row0 / a.group + 1, end);
-        const int all_from = a.window > 0 ? span.length - a.queries + (row0 + rows - 1) / a.group + 1 - a.window : 0;
+        // the tokens that row 8 b + 2 t + j sees, [last + 1 - window, last] of the part's; what every row sees
+        // (rows are in the queries' order)
+        const auto last_of = [&](int n) { return span.length - a.queries + (row0 + min(n, rows - 1)) / a.group; };
+        const int all_to = min(last_of(0) + 1, end);
+        const int all_from = a.window > 0 ? last_of(rows) + 1 - a.window : 0;
         float top[NT][2], sum[NT][2], o[NT][kSteps][4];  // top: the largest product so far
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
@@ -320,19 +331,18 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
         // 1, or the other way round.
         const int my_token = r ^ (r >> 1 & 1), even_token = 2 * t ^ (t & 1), odd_token = (2 * t + 1) ^ (t & 1);
 #pragma unroll 1
-        for (int sl = sl0; sl < sl1 && !late; ++sl) {
+        for (int place = begin, k = take; k > 0; --k, place += kSlice) {  // place: of the slice's first token
             if (!__all_sync(0xffffffffu, mbar_wait(&full[get], parity))) {
-                // given up: no part of this warp's is worth anything, but nothing may be on its way into
-                // shared memory at the end
-                late = true;
+                // given up: what this worker leaves is worth nothing, but nothing may be on its way into shared
+                // memory at the end
                 s_bad = NVFP4_ERR_TIMEOUT;
 #pragma unroll 1
                 for (int i = 0; i < S::kStages; ++i) mbar_wait(&full[i], i >= get ? parity : parity ^ 1);
+                late = true;
                 break;
             }
             __syncwarp();  // (zeros that a lane wrote are there for all)
             const uint8_t* const stage = my + get * S::kStage;
-            const int place = begin + sl * kSlice;  // of the first token
             const bool edge = place < all_from || place + kSlice > all_to;
 
             // products: the slice's tokens x rows; lane (r, t): tokens (my_token) + 8 h + 16 m, rows 2 t, 2 t + 1
@@ -381,12 +391,16 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             for (int b = 0; b < NT; ++b) {
                 if (edge) {
 #pragma unroll
-                    for (int m = 0; m < kM; ++m)
+                    for (int j = 0; j < 2; ++j) {
+                        const int last = last_of(8 * b + 2 * t + j), from = a.window > 0 ? last + 1 - a.window : 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = place + 16 * m + 8 * (i >> 1) + my_token;
-                            if (at < from[b][i & 1] || at >= to[b][i & 1]) x[m][b][i] = kMinusInf;
-                        }
+                        for (int m = 0; m < kM; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = place + 16 * m + 8 * h + my_token;
+                                if (at < from || at > last || at >= end) x[m][b][2 * h + j] = kMinusInf;
+                            }
+                    }
                 }
                 float high[2] = {kMinusInf, kMinusInf};
 #pragma unroll
@@ -458,13 +472,13 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
                     // Tokens that no row sees count as zeros.  A scale that is NaN must not reach, as 0 x NaN,
                     // rows that do not see its token: it goes to those that do here.
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) {
+                    for (int k2 = 0; k2 < kBlocks; ++k2) {
                         uint32_t bad = 0;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int at = 8 * (j >> 1) + ((j & 1) ? odd_token : even_token);
-                            if (place + 16 * m + at >= end) byte[j][k] = 0;
-                            if ((byte[j][k] & 0x7Fu) == 0x7Fu) bad |= 1u << at, byte[j][k] = 0;
+                            if (place + 16 * m + at >= end) byte[j][k2] = 0;
+                            if ((byte[j][k2] & 0x7Fu) == 0x7Fu) bad |= 1u << at, byte[j][k2] = 0;
                         }
                         bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
                         bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
@@ -472,16 +486,20 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
 #pragma unroll
-                                for (int i = 0; i < 2; ++i)
+                                for (int i = 0; i < 2; ++i) {
+                                    const int last = last_of(8 * b + 2 * t + i), from = a.window > 0 ? last + 1 - a.window : 0;
+                                    bool sees = false;
 #pragma unroll 1
                                     for (int at = 0; at < 16; ++at) {
                                         const int token = place + 16 * m + at;
-                                        if ((bad >> at & 1) && token >= from[b][i] && token < to[b][i]) {
-#pragma unroll
-                                            for (int s = k * (kSteps / kBlocks); s < (k + 1) * (kSteps / kBlocks); ++s)
-                                                o[b][s][i] = o[b][s][2 + i] = __int_as_float(0x7fffffff);
-                                        }
+                                        sees |= (bad >> at & 1) && token >= from && token <= last;
                                     }
+                                    if (sees) {
+#pragma unroll
+                                        for (int s = k2 * (kSteps / kBlocks); s < (k2 + 1) * (kSteps / kBlocks); ++s)
+                                            o[b][s][i] = o[b][s][2 + i] = __int_as_float(0x7fffffff);
+                                    }
+                                }
                         }
                     }
                 }
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) sc[h][k] = e4m3x2_f16(byte[2 * h][k] | byte[2 * h + 1][k] << 8);
+                    for (int k2 = 0; k2 < kBlocks; ++k2) sc[h][k2] = e4m3x2_f16(byte[2 * h][k2] | byte[2 * h + 1][k2] << 8);
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
                     uint32_t even[2][4], odd[2][4];  // elements 2 i and 2 i + 1 of eight
@@ -515,132 +533,126 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<DIM, NT>::kCtas) attend_ker
             __syncwarp();  // every lane is done with this stage
             copy_slice();
         }
-        // The warps' parts, joined: rows' sums of lane (r, t) are elements r DIM / 8.. of rows
-        // 2 t, 2 t + 1.
-        float* const s_o = reinterpret_cast<float*>(my);
+
+        if (late) break;
+        // The result, or a part: lane (r, t) has elements r DIM / 8.. of rows 2 t, 2 t + 1.
+        const bool whole = take == span.slices;
+        const int slot = 2 * worker + (first == 0 ? 1 : 0);
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float v = sum[b][i];
+                float l = sum[b][i];
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+                const float high = top[b][i] == kMinusInf ? kMinusInf : top[b][i] * by[b][i];
                 const int row = 8 * b + 2 * t + i;
-                if (r == 0) s_ml[warp][row] = make_float2(top[b][i] == kMinusInf ? kMinusInf : top[b][i] * by[b][i], v);
-                if (sl0 < sl1) {
+                if (row >= rows) continue;
+                if (whole) {
+                    const float n = l == 0.0f ? 0.0f : gv / l;
+                    const int query = (row0 + row) / a.group, h = (row0 + row) - query * a.group;
+                    const int64_t at = (static_cast<int64_t>(seq) * a.queries + query) * a.heads + head * a.group + h;
+                    uint2* const to = reinterpret_cast<uint2*>(a.out + at * DIM + r * (DIM / 8));
 #pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-                        *reinterpret_cast<float2*>(s_o + row * DIM + r * (DIM / 8) + 2 * s) = make_float2(o[b][s][i], o[b][s][2 + i]);
+                    for (int s = 0; s < kSteps; s += 2)
+                        to[s / 2] = make_uint2(pack2(o[b][s][i] * n, o[b][s][2 + i] * n), pack2(o[b][s + 1][i] * n, o[b][s + 1][2 + i] * n));
+                    if (a.lse && r == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+                } else {
+                    const int64_t at = static_cast<int64_t>(slot) * a.block_rows + row;
+                    float4* const to = reinterpret_cast<float4*>(a.part_o + at * DIM + r * (DIM / 8));
+#pragma unroll
+                    for (int s = 0; s < kSteps; s += 2)
+                        to[s / 2] = make_float4(o[b][s][i], o[b][s][2 + i], o[b][s + 1][i], o[b][s + 1][2 + i]);
+                    if (r == 0) a.part_ml[at] = make_float2(high, l);
                 }
             }
-        __syncthreads();
-        const int slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
-        if (!whole && first_tile == 0) {
-            const int last = f + span.tiles - 1, cut = more * (each + 1);
-            record = make_int4(item, last < cut ? last / (each + 1) : more + (last - cut) / each, seq, 1);
+        left -= take;
+        // the worker that begins an item says who else has a part of it
+        if (lane == 0 && first == 0 && (a.by_item || left == 0)) {
+            const int end_at = worker * each + min(worker, more) + (each + (worker < more ? 1 : 0)) - left - take + span.slices - 1;
+            const int cut = more * (each + 1);
+            const int last = end_at < cut ? end_at / (each + 1) : more + (end_at - cut) / each;
+            a.records[a.by_item ? seq * items + item : worker] = make_int4(item, whole ? -1 : worker, last, seq);
+        } else if (lane == 0 && left == 0 && !a.by_item) {
+            a.records[worker] = make_int4(0, -1, 0, 0);
         }
-#pragma unroll 1
-        for (int c = threadIdx.x; c < rows * (DIM / 4); c += 32 * kWarps) {
-            const int row = c / (DIM / 4), d = 4 * (c % (DIM / 4));
-            float high = kMinusInf;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) high = fmaxf(high, s_ml[w][row].x);
-            const float base = high == kMinusInf ? 0.0f : high;
-            float l = 0.0f;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (slices * w / kWarps == slices * (w + 1) / kWarps) continue;  // that warp had nothing to do
-                const float2 ml = s_ml[w][row];
-                const float part = exp2_fast(ml.x - base);
-                const float4 u = *reinterpret_cast<const float4*>(s_dyn + w * S::kRing + (row * DIM + d) * 4);
-                l += ml.y * part;
-                v.x += u.x * part, v.y += u.y * part, v.z += u.z * part, v.w += u.w * part;
-            }
-            if (whole) {
-                const float n = l == 0.0f ? 0.0f : gv / l;
-                const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
-                const int64_t at = (static_cast<int64_t>(seq) * a.queries + i) * a.heads + head * a.group + h;
-                *reinterpret_cast<uint2*>(a.out + at * DIM + d) = make_uint2(pack2(v.x * n, v.y * n), pack2(v.z * n, v.w * n));
-                if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
-            } else {
-                *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * a.block_rows + row) * DIM + d) = v;
-                if (d == 0) a.part_ml[static_cast<int64_t>(slot) * a.block_rows + row] = make_float2(high, l);
-            }
-        }
-        f += take, rel += take;
-        if (rel == span.tiles * items) ++seq, rel = 0;
-        fence_proxy_async_smem();
-        __syncthreads();  // the next part's slices take the sums' place
+        rel += take;
+        if (rel == span.slices * items) ++seq, rel = 0;
     }
-    if (threadIdx.x == 0) {
-        record.w |= s_bad << 8;
-        a.records[blockIdx.x] = record;
-    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.bad[blockIdx.x] = s_bad;
 }
 
-// The parts of the item that CTA `blockIdx.x` of the attention began and later ones ended.
+// The parts of an item that several workers share, a row of it each CTA.
 template <int DIM>
-__global__ void __launch_bounds__(256) join_kernel(const AttendArgs a)
+__global__ void __launch_bounds__(256) join_kernel(const AttendArgs a, int ctas, int workers)
 {
     constexpr int kVecs = DIM / 4, kLanes = 256 / kVecs;
     __shared__ float4 s_v[kLanes][kVecs];
-    __shared__ float s_l[kLanes];
+    __shared__ float2 s_ml[kLanes];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int4 record = a.records[blockIdx.x];
     const int row = blockIdx.y;
     if (blockIdx.x == 0 && row == 0) {  // the call's status
-        int bad = 0;
-        for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) bad = max(bad, a.records[i].w >> 8);
-        const int worst = __syncthreads_or(bad == NVFP4_ERR_INDEX), slow = __syncthreads_or(bad == NVFP4_ERR_TIMEOUT);
-        if (threadIdx.x == 0) *a.status = slow ? NVFP4_ERR_TIMEOUT : worst ? NVFP4_ERR_INDEX : NVFP4_OK;
+        const int bad = static_cast<int>(threadIdx.x) < ctas ? a.bad[threadIdx.x] : NVFP4_OK;
+        const int index = __syncthreads_or(bad == NVFP4_ERR_INDEX), late = __syncthreads_or(bad == NVFP4_ERR_TIMEOUT);
+        if (threadIdx.x == 0) *a.status = late ? NVFP4_ERR_TIMEOUT : index ? NVFP4_ERR_INDEX : NVFP4_OK;
     }
     const int head = record.x / a.blocks, row0 = (record.x - head * a.blocks) * a.block_rows;
-    if (!(record.w & 1) || row >= min(a.block_rows, a.rows - row0)) return;
-    const int parts = record.y - static_cast<int>(blockIdx.x) + 1;
+    const int first = record.y, parts = record.z - first + 1;
+    if (first < 0 || row >= min(a.block_rows, a.rows - row0)) return;
+    // (a worker that gave up leaves no record: whatever lies there names nothing outside)
+    if (parts < 2 || record.z >= workers || record.x < 0 || head >= a.cache.kv_heads || record.w < 0 || record.w >= a.sequences) return;
     const int lane = threadIdx.x / kVecs, d = threadIdx.x % kVecs;
     const auto place = [&](int part) {
-        const int slot = part == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + part);
+        const int slot = part == 0 ? 2 * first + 1 : 2 * (first + part);
         return static_cast<int64_t>(slot) * a.block_rows + row;
     };
-    float high = kMinusInf;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) high = fmaxf(high, a.part_ml[place(i)].x);
-    const float base = high == kMinusInf ? 0.0f : high;
-    float l = 0.0f;
+    constexpr int kParts = 4;  // whose loads are in flight together
+    float high = kMinusInf, l = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = lane; i < parts; i += kLanes) {
-        const float2 ml = a.part_ml[place(i)];
-        const float4 u = *reinterpret_cast<const float4*>(a.part_o + place(i) * DIM + 4 * d);
-        const float part = exp2_fast(ml.x - base);
-        l += ml.y * part;
-        v.x += u.x * part, v.y += u.y * part, v.z += u.z * part, v.w += u.w * part;
+    const auto add = [&](float2 ml, float4 u) {
+        const float now = fmaxf(high, ml.x), base = now == kMinusInf ? 0.0f : now;
+        const float mine = exp2_fast(high - base), part = exp2_fast(ml.x - base);
+        high = now;
+        l = l * mine + ml.y * part;
+        v.x = v.x * mine + u.x * part, v.y = v.y * mine + u.y * part;
+        v.z = v.z * mine + u.z * part, v.w = v.w * mine + u.w * part;
+    };
+#pragma unroll 1
+    for (int i0 = lane; i0 < parts; i0 += kParts * kLanes) {
+        float2 ml[kParts];
+        float4 u[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int part = min(i0 + i * kLanes, parts - 1);
+            ml[i] = a.part_ml[place(part)];
+            u[i] = *reinterpret_cast<const float4*>(a.part_o + place(part) * DIM + 4 * d);
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            if (i0 + i * kLanes < parts) add(ml[i], u[i]);
     }
     s_v[lane][d] = v;
-    if (d == 0) s_l[lane] = l;
+    if (d == 0) s_ml[lane] = make_float2(high, l);
     __syncthreads();
     if (lane > 0) return;
 #pragma unroll
-    for (int i = 1; i < kLanes; ++i) {
-        const float4 u = s_v[i][d];
-        l += s_l[i];
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-    }
+    for (int i = 1; i < kLanes; ++i) add(s_ml[i], s_v[i][d]);
     float unused, gv;
     global_scales(a.cache.amax[1], unused, gv);
     const float n = l == 0.0f ? 0.0f : gv / l;
     const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
-    const int64_t at = (static_cast<int64_t>(record.z) * a.queries + i) * a.heads + head * a.group + h;
+    const int64_t at = (static_cast<int64_t>(record.w) * a.queries + i) * a.heads + head * a.group + h;
     *reinterpret_cast<uint2*>(a.out + at * DIM + 4 * d) = make_uint2(pack2(v.x * n, v.y * n), pack2(v.z * n, v.w * n));
     if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
 }
 
-// Rows of a block and the CTAs of the attention.  (sms: at most as many multiprocessors)
+// Rows of a block, the CTAs of the attention and its records.
 struct Cut {
     int rows, blocks, block_rows;
-    int64_t ctas;
+    int64_t ctas, workers, records;
 };
 Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int64_t capacity, int sms)
 {
@@ -649,8 +661,10 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
     const int most = dim == 256 || c.rows <= 8 ? 8 : 16;
     c.blocks = (c.rows + most - 1) / most;
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
-    c.ctas = std::min<int64_t>(static_cast<int64_t>(sms) * Shape<128, 1>::kCtas,
-                               sequences * kv_heads * c.blocks * std::max<int64_t>(1, (capacity + kTile - 1) / kTile + 1));
+    const int64_t items = sequences * kv_heads * c.blocks;
+    c.ctas = std::min<int64_t>(sms, items * (capacity / kLeastSlice + 2));  // (no more than there can be slices)
+    c.workers = c.ctas * kWarps;
+    c.records = std::min(items, c.workers);
     return c;
 }
 
@@ -674,15 +688,16 @@ nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.ctas), static_cast<unsigned>(cut.block_rows)), cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.records), static_cast<unsigned>(cut.block_rows)), cfg.blockDim = dim3(256);
     cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a, static_cast<int>(cut.ctas), static_cast<int>(cut.workers)) != cudaSuccess) return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-size_t workspace_bytes(int64_t ctas, int block_rows, int dim)
+size_t workspace_bytes(const Cut& c, int dim)
 {
-    return kHeadBytes + static_cast<size_t>(ctas) * (sizeof(int4) + 2 * static_cast<size_t>(block_rows) * (sizeof(float2) + 4 * dim)) + 16;
+    const size_t parts = 2 * static_cast<size_t>(c.workers) * c.block_rows;
+    return kHeadBytes + kMostSms * 4 + static_cast<size_t>(c.records) * sizeof(int4) + parts * (sizeof(float2) + 4 * static_cast<size_t>(dim)) + 16;
 }
 
 }  // namespace
@@ -697,7 +712,7 @@ extern "C" size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queri
         (dim != 64 && dim != 128 && dim != 256) || queries > (1 << 20) || heads > 65536)
         return kHeadBytes;
     const Cut c = cut_of(std::min<int64_t>(sequences, 1 << 20), queries, heads, kv_heads, dim, std::min<int64_t>(capacity, 1ll << 31), kMostSms);
-    return workspace_bytes(c.ctas, c.block_rows, dim);
+    return workspace_bytes(c, dim);
 }
 
 extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh, int64_t sequences,
@@ -726,7 +741,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     if (static_cast<int64_t>(queries) * (heads / kv) > (1 << 24)) return NVFP4_ERR_SHAPE;
     if (sequences > 0) {
         const Cut c = cut_of(sequences, queries, heads, kv, dim, capacity, 1);
-        if ((capacity / kTile + 2) > 0x7fffffffll / (sequences * kv) / c.blocks) return NVFP4_ERR_SHAPE;
+        if ((capacity / kLeastSlice + 2) > 0x7fffffffll / (sequences * kv) / c.blocks) return NVFP4_ERR_SHAPE;
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
@@ -737,7 +752,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
         return cudaMemsetAsync(static_cast<uint8_t*>(workspace) + 8, 0, 4, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
     }
     const Cut cut = cut_of(sequences, queries, heads, kv, dim, capacity, std::min(sms, kMostSms));
-    if (ws_bytes < workspace_bytes(cut.ctas, cut.block_rows, dim)) return NVFP4_ERR_WORKSPACE;
+    if (ws_bytes < workspace_bytes(cut, dim)) return NVFP4_ERR_WORKSPACE;
     a.q = static_cast<const uint16_t*>(q_bf16), a.ldb = ldb, a.ldi = ldi, a.ldh = ldh;
     a.out = static_cast<uint16_t*>(out_bf16), a.lse = lse;
     a.table = table, a.ldt = ldt, a.lengths = lengths;
@@ -746,11 +761,14 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     a.rows = cut.rows, a.blocks = cut.blocks, a.block_rows = cut.block_rows;
     a.window = static_cast<int>(std::min<int64_t>(window, 0x7fffffff));
     a.scale = scale;
+    a.by_item = cut.records < cut.workers;
     uint8_t* at = static_cast<uint8_t*>(workspace) + kHeadBytes;
+    a.bad = reinterpret_cast<int*>(at);
+    at += kMostSms * 4;
     a.records = reinterpret_cast<int4*>(at);
-    at += cut.ctas * sizeof(int4);
+    at += cut.records * sizeof(int4);
     a.part_o = reinterpret_cast<float*>(at);
-    at += static_cast<size_t>(2 * cut.ctas) * cut.block_rows * dim * 4;
+    at += static_cast<size_t>(2 * cut.workers) * cut.block_rows * dim * 4;
     a.part_ml = reinterpret_cast<float2*>(at);
     a.status = static_cast<uint32_t*>(workspace) + 2;
     if (dim == 256) return start<256, 1>(a, cut, st);
