@@ -12,7 +12,6 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kWarps = 12;                // of a CTA, one CTA a multiprocessor
 constexpr float kUp = 14.0f;              // exponentials are 2^14 at their largest: FP16 keeps those down to 2^-28 whole
 constexpr int kLeastSlice = 32;
 constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
@@ -38,6 +37,16 @@ struct AttendArgs {
     float* part_o;             // [2 workers][block_rows][dim]
     uint32_t* status;
 };
+
+// Asynchronous copies to shared memory; zeros where there is nothing to read.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
 {
@@ -104,24 +113,36 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
     return {begin, n, max(1, (n - begin + SLICE - 1) / SLICE)};
 }
 
-template <int DIM, int NT>
+// Warps of a CTA, one CTA a multiprocessor: as many as the registers of `tiles` of eight rows leave room for.
+constexpr int warps_of(int dim, int tiles) { return dim * tiles > 128 ? 8 : 12; }
+template <int DIM, int NT, int SLICE>  // SLICE: tokens of a warp's step
 struct Shape {
-    static constexpr int kSlice = NT == 2 || DIM == 256 ? 32 : 64;  // tokens of a warp's step
+    static constexpr int kSlice = SLICE;
+    static constexpr int kWarps = warps_of(DIM, NT);
     static constexpr int kCodes = kSlice * DIM / 2, kScales = kSlice * DIM / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = kStage > 5000 ? 2 : kStage > 2500 ? 3 : 4;
+    static constexpr int kStages = kStage * kWarps * 3 > 224000 ? 2 : kStage > 2500 ? 3 : 4;
     static constexpr int kRing = kStages * kStage;
     static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kRing;
+    // Where the 16-byte vector `col` of token `tok`'s codes lies: the tokens of a slice in order, and the
+    // vectors of eight of them so that the reads of keys (by neighbouring tokens) and of values (by tokens 0, 3, 4, 7
+    // and 1, 2, 5, 6, a 16-block each lane) meet every bank once.
+    static __device__ __forceinline__ int vector_of(int tok, int col)
+    {
+        if (DIM == 64) return (tok ^ (tok >> 2 & 1)) * 2 + col;
+        if (DIM == 128) return tok * 4 + (col ^ (tok >> 1 & 2));
+        return tok * 8 + (col ^ (tok & 7));
+    }
 };
 
 // Each warp is a worker of its own: it takes an equal run of all slices of all (sequence,
 // key head, block of rows) items, keeps its own maximum, sums and copies on their way, and
 // leaves an item's result, or its part of one that other workers share.
-template <int DIM, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs a)
+template <int DIM, int NT, int SLICE>
+__global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_kernel(const AttendArgs a)
 {
-    using S = Shape<DIM, NT>;
-    constexpr int kSlice = S::kSlice, kM = kSlice / 16;
+    using S = Shape<DIM, NT, SLICE>;
+    constexpr int kWarps = S::kWarps, kSlice = SLICE, kM = kSlice / 16;
     constexpr int kSteps = DIM / 16;       // matrix instructions over the head dimension; 16-blocks of a token
     constexpr int kLaneCodes = DIM / 8;    // bytes of a token's keys that a lane reads
     constexpr int kThreads = 32 * kWarps;
@@ -129,19 +150,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
     __shared__ int s_sum[kWarps];
     __shared__ int s_upto[kThreads];
     __shared__ int s_bad;
-    __shared__ uint64_t s_full[kWarps][S::kStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
     uint8_t* const my = s_dyn + warp * S::kRing;
-    uint64_t* const full = s_full[warp];
+    const uint32_t ring = smem_addr(my);
     const int items = a.cache.kv_heads * a.blocks;  // of a sequence
 
     if (threadIdx.x == 0) s_bad = 0;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1);
-        fence_barrier_init();
-    }
     wait_for_previous_kernel();
     let_next_kernel_start();
     __syncthreads();
@@ -194,75 +209,102 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
     }
 
     // Copies, ahead of the work and across the items: the codes and scales of a slice's tokens'
-    // keys and values, a run of a page each.  Lane 4 i + j copies, of run i, the keys' codes, the
-    // values' codes, the keys' scales or the values' scales.  The pages of 32 runs are at hand at a
-    // time, one in each lane.
+    // keys and values.  The pages of 32 runs of tokens that lie together are at hand at a time, one in
+    // each lane; where a slice is one run, its pointers are taken once.
+    constexpr int kCopies = S::kCodes / 512;           // of a slice's keys or values, 32 vectors each
+    constexpr int kCopyTokens = 1024 / DIM;            // of one copy
     const int run_shift = min(a.cache.page_shift, kSlice == 64 ? 6 : 5);
     const int runs = kSlice >> run_shift;  // of a slice
-    const int my_run = lane >> 2;
-    const bool my_scales = lane & 2;
-    const uint32_t my_bytes = my_scales ? DIM / 16 : DIM / 2;  // of a token
-    uint8_t* const my_place = my + (my_scales ? 2 * S::kCodes : 0) + (lane & 1 ? (my_scales ? S::kScales : S::kCodes) : 0) +
-                              ((my_run * my_bytes) << run_shift);
-    const uint8_t* const my_half = (my_scales ? a.cache.sf : a.cache.q) + (lane & 1 ? a.cache.half * my_bytes : 0);
+    const int in_page = (1 << a.cache.page_shift) - 1;
+    const int64_t half_codes = a.cache.half * (DIM / 2), half_scales = a.cache.half * (DIM / 16);
+    const auto place_of = [&](int i) {  // of this lane's vector of copy i: the place repeats every eight tokens
+        return (S::vector_of((i * kCopyTokens + lane / (DIM / 32)) & 7, lane % (DIM / 32)) - (i * kCopyTokens & 7) * (DIM / 32)) * 16 +
+               (DIM == 64 ? (lane / 2 & 8) * 32 : 0);
+    };
+    const uint32_t even_place = ring + place_of(0), odd_place = DIM == 256 ? ring + place_of(1) : even_place;
     int put = 0;                                      // stage of the ring
     int c_left = left, c_seq = seq, c_rel = rel;      // slices to copy; where the next item's begin
     int c_part = 0, c_token = 0, c_end = 0, c_head = 0, c_of = 0;  // of the item at hand: slices left, next token, end, head, sequence
     int page = -1, known = 0;                         // pages at hand, and how many of them are used
+    const auto at_page = [&](int p, int token) {
+        return ((static_cast<int64_t>(p) * a.cache.kv_heads + c_head) << a.cache.page_shift) + (token & in_page);
+    };
     const auto copy_slice = [&]() {
-        if (c_left == 0) return;
-        --c_left;
-        if (c_part == 0) {
-            const Span span = span_of<kSlice>(a, c_seq, &s_bad);
-            const int item = c_rel / span.slices, first = c_rel - item * span.slices;
-            c_part = min(span.slices - first, c_left + 1);
-            c_head = item / a.blocks, c_of = c_seq;
-            c_token = span.begin + first * kSlice, c_end = min(span.length, c_token + c_part * kSlice);
-            c_rel += c_part;
-            if (c_rel == span.slices * items) ++c_seq, c_rel = 0;
-            known = 32;
-        }
-        --c_part;
-        if (known + runs > 32) {
-            const int token = c_token + (lane << run_shift);
-            page = -1;
-            if (token < c_end) {
-                page = a.table[c_of * a.ldt + (token >> a.cache.page_shift)];
-                if (page < 0 || page >= a.cache.pages) s_bad = NVFP4_ERR_INDEX, page = -1;
+        if (c_left > 0) {
+            --c_left;
+            if (c_part == 0) {
+                const Span span = span_of<kSlice>(a, c_seq, &s_bad);
+                const int item = c_rel / span.slices, first = c_rel - item * span.slices;
+                c_part = min(span.slices - first, c_left + 1);
+                c_head = item / a.blocks, c_of = c_seq;
+                c_token = span.begin + first * kSlice, c_end = min(span.length, c_token + c_part * kSlice);
+                c_rel += c_part;
+                if (c_rel == span.slices * items) ++c_seq, c_rel = 0;
+                known = 32;
             }
-            known = 0;
-        }
-        const int p = __shfl_sync(0xffffffffu, page, known + my_run);
-        known += runs;
-        const int token = c_token + (my_run << run_shift);
-        c_token += kSlice;
-        const bool wanted = my_run < runs && token < c_end, there = wanted && p >= 0;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * ((DIM / 2 + DIM / 16) / 2 << run_shift);
-        if (lane == 0) mbar_arrive_expect_tx(&full[put], bytes);
-        __syncwarp();
-        uint8_t* const to = my_place + put * S::kStage;
-        if (there) {
-            const uint32_t in_page = token & ((1 << a.cache.page_shift) - 1);
-            const uint64_t at = ((static_cast<uint64_t>(p) * a.cache.kv_heads + c_head) << a.cache.page_shift) + in_page;
-            bulk_copy_g2s(to, my_half + at * my_bytes, my_bytes << run_shift, &full[put]);
-        } else if (wanted && my_scales) {  // zeros in a missing page's place
+            --c_part;
+            if (known + runs > 32) {
+                const int token = c_token + (lane << run_shift);
+                page = -1;
+                if (token < c_end) {
+                    page = a.table[c_of * a.ldt + (token >> a.cache.page_shift)];
+                    if (page < 0 || page >= a.cache.pages) s_bad = NVFP4_ERR_INDEX, page = -1;
+                }
+                known = 0;
+            }
+            const uint32_t stage = put * S::kStage;
+            const int p0 = __shfl_sync(0xffffffffu, page, known);
+            if (runs == 1 && p0 >= 0) {
+                const int64_t at = at_page(p0, c_token);
+                const uint8_t* const q = a.cache.q + at * (DIM / 2) + lane * 16;
+                const uint8_t* const sf = a.cache.sf + at * (DIM / 16) + lane * 16;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const uint32_t to = (i & 1 ? odd_place : even_place) + stage + i * 512;
+                    copy16_async(to, q + i * 512);
+                    copy16_async(to + S::kCodes, q + half_codes + i * 512);
+                }
+#pragma unroll
+                for (int i = 0; i < S::kScales; i += 512) {
+                    if (lane * 16 + i < S::kScales) {
+                        copy16_async(ring + stage + 2 * S::kCodes + lane * 16 + i, sf + i);
+                        copy16_async(ring + stage + 2 * S::kCodes + S::kScales + lane * 16 + i, sf + half_scales + i);
+                    }
+                }
+            } else {  // several runs, or zeros in a missing page's place
 #pragma unroll 1
-            for (int i = 0; i < (DIM / 64) << run_shift; ++i) reinterpret_cast<uint32_t*>(to)[i] = 0;
-            fence_proxy_async_smem();  // (the next copy into this place follows)
+                for (int i = 0; i < kCopies; ++i) {
+                    const int run = i * kCopyTokens >> run_shift, p = __shfl_sync(0xffffffffu, page, known + run);
+                    const uint8_t* const q = a.cache.q + (p < 0 ? 0 : at_page(p, c_token + i * kCopyTokens) * (DIM / 2) + lane * 16);
+                    const uint32_t to = (i & 1 ? odd_place : even_place) + stage + i * 512;
+                    copy16_async(to, q, p >= 0);
+                    copy16_async(to + S::kCodes, p < 0 ? q : q + half_codes, p >= 0);
+                }
+#pragma unroll
+                for (int i = 0; i < S::kScales; i += 512) {
+                    const int token = (lane * 16 + i) / (DIM / 16), p = __shfl_sync(0xffffffffu, page, known + (token >> run_shift));
+                    if (lane * 16 + i < S::kScales) {
+                        const uint8_t* const sf = a.cache.sf + (p < 0 ? 0 : at_page(p, c_token + token) * (DIM / 16));
+                        copy16_async(ring + stage + 2 * S::kCodes + lane * 16 + i, sf, p >= 0);
+                        copy16_async(ring + stage + 2 * S::kCodes + S::kScales + lane * 16 + i, p < 0 ? sf : sf + half_scales, p >= 0);
+                    }
+                }
+            }
+            known += runs;
+            c_token += kSlice;
+            put = put + 1 == S::kStages ? 0 : put + 1;
         }
-        put = put + 1 == S::kStages ? 0 : put + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
     for (int i = 0; i < S::kStages; ++i) copy_slice();
 
-    bool late = false;          // a copy did not come
     int get = 0;                // stage that is worked on
-    uint32_t parity = 0;        // of its barrier
     float unused, gk, gv;
     global_scales(a.cache.amax[0], unused, gk);
     global_scales(a.cache.amax[1], unused, gv);
 #pragma unroll 1
-    while (left > 0 && !late) {
+    while (left > 0) {
         const Span span = span_of<kSlice>(a, seq, &s_bad);
         const int item = rel / span.slices, first = rel - item * span.slices;
         const int take = min(span.slices - first, left);
@@ -332,16 +374,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
         const int my_token = r ^ (r >> 1 & 1), even_token = 2 * t ^ (t & 1), odd_token = (2 * t + 1) ^ (t & 1);
 #pragma unroll 1
         for (int place = begin, k = take; k > 0; --k, place += kSlice) {  // place: of the slice's first token
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[get], parity))) {
-                // given up: what this worker leaves is worth nothing, but nothing may be on its way into shared
-                // memory at the end
-                s_bad = NVFP4_ERR_TIMEOUT;
-#pragma unroll 1
-                for (int i = 0; i < S::kStages; ++i) mbar_wait(&full[i], i >= get ? parity : parity ^ 1);
-                late = true;
-                break;
-            }
-            __syncwarp();  // (zeros that a lane wrote are there for all)
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
+            __syncwarp();  // this slice has come for every lane
             const uint8_t* const stage = my + get * S::kStage;
             const bool edge = place < all_from || place + kSlice > all_to;
 
@@ -353,16 +387,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = 16 * m + 8 * h + my_token;
-                    const uint8_t* const row = stage + tok * (DIM / 2) + t * kLaneCodes;
+                    const uint8_t* const codes = stage + (16 * m + 8 * h) * (DIM / 2);
                     const uint8_t* const scales = stage + 2 * S::kCodes + tok * kSteps + t * (DIM / 64);
                     if constexpr (DIM == 64) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(row);
+                        const uint2 w = *reinterpret_cast<const uint2*>(codes + S::vector_of(my_token, t >> 1) * 16 + (t & 1) * 8);
                         code[h][0] = w.x, code[h][1] = w.y;
                         sc[h][0] = __byte_perm(e4m3x2_f16(*scales), 0, 0x1010);
                     } else {
 #pragma unroll
                         for (int v = 0; v < DIM / 128; ++v) {
-                            const uint4 w = reinterpret_cast<const uint4*>(row)[v];
+                            const uint4 w = reinterpret_cast<const uint4*>(codes)[S::vector_of(my_token, t * (DIM / 128) + v)];
                             code[h][4 * v] = w.x, code[h][4 * v + 1] = w.y, code[h][4 * v + 2] = w.z, code[h][4 * v + 3] = w.w;
                             const uint32_t two = e4m3x2_f16(reinterpret_cast<const uint16_t*>(scales)[v]);
                             sc[h][2 * v] = __byte_perm(two, 0, 0x1010);
@@ -451,18 +485,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
                 uint32_t code[4][kWords], byte[4][kBlocks];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int tok = 16 * m + 8 * (j >> 1) + ((j & 1) ? odd_token : even_token);
-                    const uint8_t* const row = stage + S::kCodes + tok * (DIM / 2) + r * (DIM / 16);
+                    const int of_eight = (j & 1) ? odd_token : even_token, tok = 16 * m + 8 * (j >> 1) + of_eight;
+                    const uint8_t* const codes = stage + S::kCodes + (16 * m + 8 * (j >> 1)) * (DIM / 2);
                     const uint8_t* const scales = stage + 2 * S::kCodes + S::kScales + tok * kSteps;
                     if constexpr (DIM == 64) {
-                        code[j][0] = *reinterpret_cast<const uint32_t*>(row);
+                        code[j][0] = *reinterpret_cast<const uint32_t*>(codes + S::vector_of(of_eight, r >> 2) * 16 + (r & 3) * 4);
                         byte[j][0] = scales[r >> 1];
                     } else if constexpr (DIM == 128) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(row);
+                        const uint2 w = *reinterpret_cast<const uint2*>(codes + S::vector_of(of_eight, r >> 1) * 16 + (r & 1) * 8);
                         code[j][0] = w.x, code[j][1] = w.y;
                         byte[j][0] = scales[r];
                     } else {
-                        const uint4 w = *reinterpret_cast<const uint4*>(row);
+                        const uint4 w = reinterpret_cast<const uint4*>(codes)[S::vector_of(of_eight, r)];
                         code[j][0] = w.x, code[j][1] = w.y, code[j][2] = w.z, code[j][3] = w.w;
                         const uint32_t two = reinterpret_cast<const uint16_t*>(scales)[r];
                         byte[j][0] = two & 0xFFu, byte[j][1] = two >> 8;
@@ -529,12 +563,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
                             mma_16816(o[b][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], p[m][b][0], p[m][b][1]);
                 }
             }
-            if (++get == S::kStages) get = 0, parity ^= 1;
+            get = get + 1 == S::kStages ? 0 : get + 1;
             __syncwarp();  // every lane is done with this stage
             copy_slice();
         }
 
-        if (late) break;
         // The result, or a part: lane (r, t) has elements r DIM / 8.. of rows 2 t, 2 t + 1.
         const bool whole = take == span.slices;
         const int slot = 2 * worker + (first == 0 ? 1 : 0);
@@ -583,114 +616,152 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const AttendArgs
     if (threadIdx.x == 0) a.bad[blockIdx.x] = s_bad;
 }
 
-// The parts of an item that several workers share, a row of it each CTA.
+// The parts of the items that several workers share: a warp (half of one, the same twice)
+// takes a row, or with few rows a share of its parts.  A CTA has one row where gridDim.y
+// counts rows, else all of an item's.
+constexpr int kJoinWarps = 8;
 template <int DIM>
-__global__ void __launch_bounds__(256) join_kernel(const AttendArgs a, int ctas, int workers)
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttendArgs a, int ctas)
 {
-    constexpr int kVecs = DIM / 4, kLanes = 256 / kVecs;
-    __shared__ float4 s_v[kLanes][kVecs];
-    __shared__ float2 s_ml[kLanes];
+    constexpr int kVecs = DIM / 4;                          // of a row
+    constexpr int kEach = kVecs > 32 ? kVecs / 32 : 1;      // of a lane
+    constexpr int kRowLanes = kVecs < 32 ? kVecs : 32;
+    constexpr int kUnits = 32 * kJoinWarps / kRowLanes;     // rows, or shares of them, at a time
+    constexpr int kParts = kEach == 1 ? 8 : 4;              // whose loads are in flight together
+    __shared__ float4 s_v[kUnits][kVecs];
+    __shared__ float2 s_ml[kUnits];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int4 record = a.records[blockIdx.x];
-    const int row = blockIdx.y;
-    if (blockIdx.x == 0 && row == 0) {  // the call's status
+    if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's status
         const int bad = static_cast<int>(threadIdx.x) < ctas ? a.bad[threadIdx.x] : NVFP4_OK;
-        const int index = __syncthreads_or(bad == NVFP4_ERR_INDEX), late = __syncthreads_or(bad == NVFP4_ERR_TIMEOUT);
-        if (threadIdx.x == 0) *a.status = late ? NVFP4_ERR_TIMEOUT : index ? NVFP4_ERR_INDEX : NVFP4_OK;
+        const int index = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.status = index ? NVFP4_ERR_INDEX : NVFP4_OK;
     }
     const int head = record.x / a.blocks, row0 = (record.x - head * a.blocks) * a.block_rows;
     const int first = record.y, parts = record.z - first + 1;
-    if (first < 0 || row >= min(a.block_rows, a.rows - row0)) return;
-    // (a worker that gave up leaves no record: whatever lies there names nothing outside)
-    if (parts < 2 || record.z >= workers || record.x < 0 || head >= a.cache.kv_heads || record.w < 0 || record.w >= a.sequences) return;
-    const int lane = threadIdx.x / kVecs, d = threadIdx.x % kVecs;
-    const auto place = [&](int part) {
-        const int slot = part == 0 ? 2 * first + 1 : 2 * (first + part);
-        return static_cast<int64_t>(slot) * a.block_rows + row;
-    };
-    constexpr int kParts = 4;  // whose loads are in flight together
-    float high = kMinusInf, l = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const auto add = [&](float2 ml, float4 u) {
-        const float now = fmaxf(high, ml.x), base = now == kMinusInf ? 0.0f : now;
-        const float mine = exp2_fast(high - base), part = exp2_fast(ml.x - base);
-        high = now;
-        l = l * mine + ml.y * part;
-        v.x = v.x * mine + u.x * part, v.y = v.y * mine + u.y * part;
-        v.z = v.z * mine + u.z * part, v.w = v.w * mine + u.w * part;
-    };
-#pragma unroll 1
-    for (int i0 = lane; i0 < parts; i0 += kParts * kLanes) {
-        float2 ml[kParts];
-        float4 u[kParts];
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            const int part = min(i0 + i * kLanes, parts - 1);
-            ml[i] = a.part_ml[place(part)];
-            u[i] = *reinterpret_cast<const float4*>(a.part_o + place(part) * DIM + 4 * d);
-        }
-#pragma unroll
-        for (int i = 0; i < kParts; ++i)
-            if (i0 + i * kLanes < parts) add(ml[i], u[i]);
-    }
-    s_v[lane][d] = v;
-    if (d == 0) s_ml[lane] = make_float2(high, l);
-    __syncthreads();
-    if (lane > 0) return;
-#pragma unroll
-    for (int i = 1; i < kLanes; ++i) add(s_ml[i], s_v[i][d]);
+    if (first < 0) return;
+    const int from = gridDim.y > 1 ? blockIdx.y : 0;
+    const int rows = min(gridDim.y > 1 ? from + 1 : a.block_rows, a.rows - row0) - from;
+    if (rows <= 0) return;
+    int shares = 1;  // of a row's parts
+    while (2 * shares * rows <= kUnits) shares *= 2;
+    const int unit = threadIdx.x / kRowLanes, d = threadIdx.x % kRowLanes;
     float unused, gv;
     global_scales(a.cache.amax[1], unused, gv);
-    const float n = l == 0.0f ? 0.0f : gv / l;
-    const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
-    const int64_t at = (static_cast<int64_t>(record.w) * a.queries + i) * a.heads + head * a.group + h;
-    *reinterpret_cast<uint2*>(a.out + at * DIM + 4 * d) = make_uint2(pack2(v.x * n, v.y * n), pack2(v.z * n, v.w * n));
-    if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+#pragma unroll 1
+    for (int u0 = 0; u0 < rows * shares; u0 += kUnits) {
+        const int u = u0 + unit, share = u % shares, row = from + u / shares;
+        float high = kMinusInf, l = 0.0f;
+        float4 v[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const auto add = [&](float2 ml, const float4 (&w)[kEach]) {
+            const float now = fmaxf(high, ml.x), base = now == kMinusInf ? 0.0f : now;
+            const float mine = exp2_fast(high - base), part = exp2_fast(ml.x - base);
+            high = now;
+            l = l * mine + ml.y * part;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                v[e].x = v[e].x * mine + w[e].x * part, v[e].y = v[e].y * mine + w[e].y * part;
+                v[e].z = v[e].z * mine + w[e].z * part, v[e].w = v[e].w * mine + w[e].w * part;
+            }
+        };
+        if (u < rows * shares) {
+#pragma unroll 1
+            for (int i0 = share; i0 < parts; i0 += kParts * shares) {
+                float2 ml[kParts];
+                float4 w[kParts][kEach];
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) {
+                    const int part = min(i0 + i * shares, parts - 1);
+                    const int64_t at = static_cast<int64_t>(part == 0 ? 2 * first + 1 : 2 * (first + part)) * a.block_rows + row;
+                    ml[i] = a.part_ml[at];
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) w[i][e] = reinterpret_cast<const float4*>(a.part_o + at * DIM)[d + 32 * e];
+                }
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    if (i0 + i * shares < parts) add(ml[i], w[i]);
+            }
+        }
+        if (shares > 1) {  // (then one turn takes all)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) s_v[unit][d + 32 * e] = v[e];
+            if (d == 0) s_ml[unit] = make_float2(high, l);
+            __syncthreads();
+            if (share > 0) continue;
+#pragma unroll 1
+            for (int i = 1; i < shares; ++i) {
+                float4 w[kEach];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) w[e] = s_v[unit + i][d + 32 * e];
+                add(s_ml[unit + i], w);
+            }
+        }
+        if (u >= rows * shares) continue;
+        const float n = l == 0.0f ? 0.0f : gv / l;
+        const int i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
+        const int64_t at = (static_cast<int64_t>(record.w) * a.queries + i) * a.heads + head * a.group + h;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            reinterpret_cast<uint2*>(a.out + at * DIM)[d + 32 * e] =
+                make_uint2(pack2(v[e].x * n, v[e].y * n), pack2(v[e].z * n, v[e].w * n));
+        if (a.lse && d == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+    }
 }
 
 // Rows of a block, the CTAs of the attention and its records.
 struct Cut {
     int rows, blocks, block_rows;
+    int tiles;     // of eight rows that a block has
+    int slice;     // tokens of a step
     int64_t ctas, workers, records;
 };
 Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int64_t capacity, int sms)
 {
     Cut c;
     c.rows = queries * (heads / kv_heads);
-    const int most = dim == 256 || c.rows <= 8 ? 8 : 16;
+    const int most = dim == 256 ? 8 : 16;
     c.blocks = (c.rows + most - 1) / most;
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
+    c.tiles = (c.block_rows + 7) / 8;
     const int64_t items = sequences * kv_heads * c.blocks;
+    c.slice = c.tiles > 1 || dim == 256 || items * (capacity / 64 + 1) <= 8000 ? 32 : 64;
     c.ctas = std::min<int64_t>(sms, items * (capacity / kLeastSlice + 2));  // (no more than there can be slices)
-    c.workers = c.ctas * kWarps;
+    c.workers = c.ctas * warps_of(dim, c.tiles);
     c.records = std::min(items, c.workers);
     return c;
 }
 
 constexpr int kMostSms = 192;  // of the workspace's size, which is known without a device
 
-template <int DIM, int NT>
+template <int DIM, int NT, int SLICE>
 nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
 {
-    using S = Shape<DIM, NT>;
+    using S = Shape<DIM, NT, SLICE>;
     static bool raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!raised[dev & 63]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(attend_kernel<DIM, NT>),
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(attend_kernel<DIM, NT, SLICE>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem)) != cudaSuccess)
             return NVFP4_ERR_CUDA;
         raised[dev & 63] = true;
     }
-    if (launch_early(true, attend_kernel<DIM, NT>, cut.ctas, 32 * kWarps, S::kSmem, st, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (launch_early(true, attend_kernel<DIM, NT, SLICE>, cut.ctas, 32 * S::kWarps, S::kSmem, st, a) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.records), static_cast<unsigned>(cut.block_rows)), cfg.blockDim = dim3(256);
+    // a CTA for each row while that fills no more than the multiprocessors
+    const bool apart = cut.records * cut.block_rows <= 4 * cut.ctas;
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.records), apart ? static_cast<unsigned>(cut.block_rows) : 1);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a, static_cast<int>(cut.ctas), static_cast<int>(cut.workers)) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a, static_cast<int>(cut.ctas)) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
@@ -771,8 +842,11 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     at += static_cast<size_t>(2 * cut.workers) * cut.block_rows * dim * 4;
     a.part_ml = reinterpret_cast<float2*>(at);
     a.status = static_cast<uint32_t*>(workspace) + 2;
-    if (dim == 256) return start<256, 1>(a, cut, st);
-    const bool one = cut.block_rows <= 8;
-    if (dim == 128) return one ? start<128, 1>(a, cut, st) : start<128, 2>(a, cut, st);
-    return one ? start<64, 1>(a, cut, st) : start<64, 2>(a, cut, st);
+    if (dim == 256) return start<256, 1, 32>(a, cut, st);
+    if (dim == 128) {
+        if (cut.tiles == 2) return start<128, 2, 32>(a, cut, st);
+        return cut.slice == 32 ? start<128, 1, 32>(a, cut, st) : start<128, 1, 64>(a, cut, st);
+    }
+    if (cut.tiles == 2) return start<64, 2, 32>(a, cut, st);
+    return cut.slice == 32 ? start<64, 1, 32>(a, cut, st) : start<64, 1, 64>(a, cut, st);
 }
