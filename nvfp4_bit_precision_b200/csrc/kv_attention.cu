@@ -71,6 +71,14 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two)
     return d;
 }
 
+// Each half of a register in both halves of another (which the products take as they read it).
+__device__ __forceinline__ void both_halves(uint32_t two, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 %0, {l, l};\n\tmov.b32 %1, {h, h};\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(two));
+}
+
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
 {
@@ -392,15 +400,14 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                     if constexpr (DIM == 64) {
                         const uint2 w = *reinterpret_cast<const uint2*>(codes + S::vector_of(my_token, t >> 1) * 16 + (t & 1) * 8);
                         code[h][0] = w.x, code[h][1] = w.y;
-                        sc[h][0] = __byte_perm(e4m3x2_f16(*scales), 0, 0x1010);
+                        uint32_t unused_half;
+                        both_halves(e4m3x2_f16(*scales), sc[h][0], unused_half);
                     } else {
 #pragma unroll
                         for (int v = 0; v < DIM / 128; ++v) {
                             const uint4 w = reinterpret_cast<const uint4*>(codes)[S::vector_of(my_token, t * (DIM / 128) + v)];
                             code[h][4 * v] = w.x, code[h][4 * v + 1] = w.y, code[h][4 * v + 2] = w.z, code[h][4 * v + 3] = w.w;
-                            const uint32_t two = e4m3x2_f16(reinterpret_cast<const uint16_t*>(scales)[v]);
-                            sc[h][2 * v] = __byte_perm(two, 0, 0x1010);
-                            sc[h][2 * v + 1] = __byte_perm(two, 0, 0x3232);
+                            both_halves(e4m3x2_f16(reinterpret_cast<const uint16_t*>(scales)[v]), sc[h][2 * v], sc[h][2 * v + 1]);
                         }
                     }
                 }
