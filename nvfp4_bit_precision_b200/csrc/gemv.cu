@@ -88,6 +88,14 @@ struct Divisor {
 // What becomes of the products.
 enum Epilogue { kProduct, kGated, kSquared, kLateRows };
 
+// What kLateRows reads before it waits: past the first-level cache, which may hold it as it was
+// before the kernels that are done by then.
+template <int FORM, typename T>
+__device__ __forceinline__ T before(const T* p)
+{
+    return FORM == kLateRows ? __ldcg(p) : *p;
+}
+
 struct GemvArgs {
     const uint16_t* x;
     int64_t ldx;
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         static_assert(kMaxGemvGroups <= 32 * kGemvWarps, "a thread for each group");
         const int rows = static_cast<int>(a.rows), e = threadIdx.x;
         int lo = 0, hi = 0;
-        if (e < a.groups) lo = a.group_offsets[e], hi = a.group_offsets[e + 1];
+        if (e < a.groups) lo = before<FORM>(a.group_offsets + e), hi = before<FORM>(a.group_offsets + e + 1);
         const int first = min(max(lo, 0), rows), count = min(hi, rows) - first;
         const unsigned has = __ballot_sync(0xffffffffu, count > 0);
         int upto = count > 0 ? a.by_seg_rows(count - 1) + 1 : 0;
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         const int x_rows = s_seg_x[segs];
         float g = 0.0f;  // of the x row that is this thread's index
         if (static_cast<int>(threadIdx.x) < x_rows) {
-            g = a.g[s_x_row[threadIdx.x].w];
+            g = before<FORM>(a.g + s_x_row[threadIdx.x].w);
             if constexpr (FORM == kGated)  // (the up matrix's takes the matrix's place)
                 s_x_row[threadIdx.x].w = __float_as_int(a.g2[s_x_row[threadIdx.x].w]);
         }
@@ -842,17 +850,20 @@ struct JoinArgs {
 
 // The weighted sums of the tokens' rows on top of base, four columns a thread, as the
 // combine's: FP32 in slot order.  Only the rows come from the kernel before; the slots,
-// the weights and base are read while it ends, and the first CTA looks the indexes
-// over and leaves the call's status.
+// the weights and base are read while it ends (past the first-level cache), and the first
+// CTA looks the indexes over and leaves the call's status.
 __global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
 {
     constexpr int kSlots = 4;  // whose loads are in flight together
     let_next_kernel_start();
     if (blockIdx.x == 0) {
         bool bad = false;
-        const int64_t used = min(max(static_cast<int64_t>(*a.used), int64_t{0}), a.n_rows);
-        for (int64_t i = threadIdx.x; i < used; i += 256) bad |= a.row_index[i] < 0 || a.row_index[i] >= a.tokens;
-        for (int64_t i = threadIdx.x; i < a.tokens * a.k; i += 256) bad |= a.slot_row[i] >= a.n_rows;
+        const int64_t used = min(max(static_cast<int64_t>(__ldcg(a.used)), int64_t{0}), a.n_rows);
+        for (int64_t i = threadIdx.x; i < used; i += 256) {
+            const int32_t r = __ldcg(a.row_index + i);
+            bad |= r < 0 || r >= a.tokens;
+        }
+        for (int64_t i = threadIdx.x; i < a.tokens * a.k; i += 256) bad |= __ldcg(a.slot_row + i) >= a.n_rows;
         const int any = __syncthreads_or(bad);
         wait_for_previous_kernel();  // (whose call's workspace this is)
         if (threadIdx.x == 0) *a.status = any ? NVFP4_ERR_INDEX : NVFP4_OK;
@@ -861,7 +872,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
     for (int64_t u = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; u < a.tokens * a.vecs; u += stride) {
         const int64_t t = u / a.vecs, c = u - t * a.vecs;
         uint2 b = make_uint2(0, 0);
-        if (a.base) b = a.base[u];
+        if (a.base) b = __ldcg(a.base + u);
         float4 acc = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
         for (int j0 = 0; j0 < a.k; j0 += kSlots) {
             int32_t r[kSlots];
@@ -869,8 +880,8 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
             float4 v[kSlots];
 #pragma unroll
             for (int j = 0; j < kSlots; ++j) {
-                r[j] = j0 + j < a.k ? a.slot_row[t * a.k + j0 + j] : -1;
-                w[j] = j0 + j < a.k ? a.weight[t * a.k + j0 + j] : 0.0f;
+                r[j] = j0 + j < a.k ? __ldcg(a.slot_row + t * a.k + j0 + j) : -1;
+                w[j] = j0 + j < a.k ? __ldcg(a.weight + t * a.k + j0 + j) : 0.0f;
                 if (r[j] >= a.n_rows) r[j] = -1;
             }
             wait_for_previous_kernel();

@@ -810,8 +810,8 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     if (sequences > 0 && (!q_bf16 || !out_bf16 || !lengths || (table_pages > 0 && !table))) return NVFP4_ERR_INVALID_ARG;
     if (ldb < 0 || ldi < 0 || (heads > 1 && ldh < dim)) return NVFP4_ERR_SHAPE;
     const int64_t capacity = table_pages * cache->page_size;
-    // (places in a sequence and the tiles of all are 31-bit numbers)
-    if (capacity > 0x7fffff00ll) return NVFP4_ERR_SHAPE;
+    // (places in a sequence are 31-bit numbers, and so are they less the queries and a window)
+    if (capacity > 0x7f000000ll) return NVFP4_ERR_SHAPE;
     if (off16(q_bf16) || off16(out_bf16) || ldb % 8 || ldi % 8 || ldh % 8 ||
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(lse)) & 3u))
         return NVFP4_ERR_ALIGN;
@@ -837,7 +837,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     a.sequences = static_cast<int>(sequences), a.table_pages = static_cast<int>(table_pages);
     a.queries = queries, a.heads = heads, a.group = heads / kv;
     a.rows = cut.rows, a.blocks = cut.blocks, a.block_rows = cut.block_rows;
-    a.window = static_cast<int>(std::min<int64_t>(window, 0x7fffffff));
+    a.window = window >= capacity ? 0 : static_cast<int>(window);
     a.scale = scale;
     a.by_item = cut.records < cut.workers;
     uint8_t* at = static_cast<uint8_t*>(workspace) + kHeadBytes;

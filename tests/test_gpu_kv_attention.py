@@ -134,6 +134,20 @@ def test_negative_scale_and_growing_scores(nv):
         check(nv, cache, q, sf, qb, np.arange(n // page)[None], [n], page, scale=scale)
 
 
+def test_windows(nv):
+    """A window as long as the table or longer is none; one of a token leaves each query its own."""
+    import torch
+    rng = np.random.default_rng(16)
+    cache, q, sf = filled(nv, rng, 12, 1, 16, 64)
+    table, lengths = rng.permutation(12).reshape(2, 6), [96, 33]
+    qb = bits(rng, (2, 3, 2, 64))
+    whole = check(nv, cache, q, sf, qb, table, lengths, 16)
+    for window in (96, 97, 2 ** 31 - 1, 2 ** 31, 2 ** 62):
+        assert torch.equal(nv.kv_attention(to_dev(qb), cache, i32(table), i32(lengths), window=window), whole)
+    for window in (1, 2, 16, 95):
+        check(nv, cache, q, sf, qb, table, lengths, 16, window)
+
+
 def test_strides(nv):
     """Queries as a piece of a projection's output, a table as a piece of a larger one."""
     import torch
