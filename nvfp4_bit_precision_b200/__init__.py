@@ -1155,38 +1155,50 @@ def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None,
     dev = _one_device("kv_append", k, v, cache.q, cache.sf, cache.amax, table, position, sequence, cos, sin, q, q_out,
                       workspace)
     view = _cache_view("kv_append", cache)
-    tokens, dim = k.shape[0], view.dim
-    ldk, hsk = _heads_of("kv_append: k", k, tokens, view.kv_heads, dim)
-    ldv, hsv = _heads_of("kv_append: v", v, tokens, view.kv_heads, dim)
+    kv, dim = view.kv_heads, view.dim
+    tokens = k.shape[0]
+    ldk, hsk = _heads_of("kv_append: k", k, tokens, kv, dim)
+    ldv, hsv = _heads_of("kv_append: v", v, tokens, kv, dim)
     sequences, pages, ldt = _table_of("kv_append", table)
-    _flat("kv_append: position", position, torch.int32, tokens)
+    i32 = torch.int32
+    if position.dtype is not i32 or position.shape != (tokens,) or not position.is_contiguous():
+        raise ValueError(f"kv_append: position int32 {(tokens,)} expected, got {position.dtype} {tuple(position.shape)}")
     sp = cp = np = qp = op = wp = None
     if sequence is not None:
-        _flat("kv_append: sequence", sequence, torch.int32, tokens)
+        if sequence.dtype is not i32 or sequence.shape != (tokens,) or not sequence.is_contiguous():
+            raise ValueError(f"kv_append: sequence int32 {(tokens,)} expected, got {sequence.dtype} {tuple(sequence.shape)}")
         sp = sequence.data_ptr()
     angles = rot = heads = ldq = hsq = ldo = hso = nb = 0
     if cos is not None or sin is not None:
-        _need(cos is not None and sin is not None and cos.dim() == 2, "kv_append: cos and sin [angles, rot/2] go together")
-        angles, rot = cos.shape[0], 2 * cos.shape[1]
-        _flat("kv_append: cos", cos, torch.float32, angles, rot // 2)
-        _flat("kv_append: sin", sin, torch.float32, angles, rot // 2)
+        if cos is None or sin is None or len(cos.shape) != 2:
+            raise ValueError("kv_append: cos and sin [angles, rot/2] go together")
+        shape = cos.shape
+        f32 = torch.float32
+        if (sin.shape != shape or cos.dtype is not f32 or sin.dtype is not f32 or not cos.is_contiguous()
+                or not sin.is_contiguous()):
+            raise ValueError(f"kv_append: cos and sin contiguous float32 of one shape expected, got {cos.dtype} "
+                             f"{tuple(shape)} and {sin.dtype} {tuple(sin.shape)}")
+        angles, rot = shape[0], 2 * shape[1]
         cp, np = cos.data_ptr(), sin.data_ptr()
     if q is not None:
-        _need(cp is not None, "kv_append: q is turned by cos and sin, which are missing")
+        if cp is None:
+            raise ValueError("kv_append: q is turned by cos and sin, which are missing")
         heads = q.shape[1] if q.dim() == 3 else 0
         ldq, hsq = _heads_of("kv_append: q", q, tokens, heads, dim)
         if q_out is None:
-            q_out = torch.empty_strided((tokens, heads, dim), (heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
-        ldo, hso = _heads_of("kv_append: q_out", q_out, tokens, heads, dim)
+            ldo, hso = heads * dim, dim
+            q_out = torch.empty_strided((tokens, heads, dim), (ldo, dim, 1), dtype=torch.bfloat16, device=dev)
+        else:
+            ldo, hso = _heads_of("kv_append: q_out", q_out, tokens, heads, dim)
         qp, op = q.data_ptr(), q_out.data_ptr()
-    else:
-        _need(q_out is None, "kv_append: q_out without q")
+    elif q_out is not None:
+        raise ValueError("kv_append: q_out without q")
     if workspace is not None:
         wp, nb = workspace.data_ptr(), workspace.numel()
     _check(_lib.nvfp4_kv_append(ctypes.byref(view), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, tokens,
                                 table.data_ptr(), ldt, sequences, pages, position.data_ptr(), sp, cp, np, angles, rot,
-                                1 if interleaved else 0, qp, ldq, hsq, heads, op, ldo, hso, wp, nb, _raw_stream(dev)),
-           "nvfp4_kv_append")
+                                1 if interleaved else 0, qp, ldq, hsq, heads, op, ldo, hso, wp, nb,
+                                torch._C._cuda_getCurrentRawStream(dev.index)), "nvfp4_kv_append")
     return q_out
 
 

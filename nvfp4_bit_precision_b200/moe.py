@@ -174,7 +174,6 @@ def expert_gemv(x: torch.Tensor, routing: Routing, up: ExpertWeights, down: Expe
     return combine(rows, routing.slot_row, routing.weight, base)
 
 
-@torch.no_grad()
 def expert_mlp(x: torch.Tensor, routing: Routing, up: ExpertWeights, down: ExpertWeights,
                gate: ExpertWeights | None = None, base: torch.Tensor | None = None) -> torch.Tensor:
     """``expert_gemv`` with the activation inside the products: silu(gate) * up, or max(up, 0)^2 without a gate.  The
