@@ -12,7 +12,10 @@
 namespace nvfp4 {
 namespace {
 
-constexpr float kUp = 14.0f;              // exponentials are 2^14 at their largest: FP16 keeps those down to 2^-28 whole
+// Exponentials are taken from a running maximum that is raised only where a product passes it by
+// kSlack in the exponent: they are 2^9 at that maximum and at most 2^15, within FP16, whose
+// eleven bits they have down to 2^-23 of it.
+constexpr float kUp = 9.0f, kSlack = 6.0f;
 constexpr int kLeastSlice = 32;
 constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
 constexpr float kMinusInf = -__builtin_huge_valf();
@@ -367,11 +370,12 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
         const auto last_of = [&](int n) { return span.length - a.queries + (row0 + min(n, rows - 1)) / a.group; };
         const int all_to = min(last_of(0) + 1, end);
         const int all_from = a.window > 0 ? last_of(rows) + 1 - a.window : 0;
-        float top[NT][2], sum[NT][2], o[NT][kSteps][4];  // top: the largest product so far
+        // top: the running maximum of the products, base: what it adds to an exponent, limit: the product that raises it
+        float top[NT][2], base[NT][2], limit[NT][2], sum[NT][2], o[NT][kSteps][4];
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
-            top[b][0] = top[b][1] = kMinusInf;
-            sum[b][0] = sum[b][1] = 0.0f;
+            top[b][0] = top[b][1] = limit[b][0] = limit[b][1] = kMinusInf;
+            base[b][0] = base[b][1] = sum[b][0] = sum[b][1] = 0.0f;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
         }
@@ -428,9 +432,9 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                 }
             }
             uint32_t p[kM][NT][2];  // exponentials, FP16: row r, tokens of rows 2 t, 2 t + 1 (+ 8)
+            if (edge) {
 #pragma unroll
-            for (int b = 0; b < NT; ++b) {
-                if (edge) {
+                for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int last = last_of(8 * b + 2 * t + j), from = a.window > 0 ? last + 1 - a.window : 0;
@@ -442,37 +446,41 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                                 if (at < from || at > last || at >= end) x[m][b][2 * h + j] = kMinusInf;
                             }
                     }
-                }
-                float high[2] = {kMinusInf, kMinusInf};
+            }
+            float high[NT][2];
+            bool rises = false;
 #pragma unroll
-                for (int m = 0; m < kM; ++m) {
-                    high[0] = fmaxf(high[0], fmaxf(x[m][b][0], x[m][b][2]));
-                    high[1] = fmaxf(high[1], fmaxf(x[m][b][1], x[m][b][3]));
-                }
-                if (__any_sync(0xffffffffu, high[0] > top[b][0] || high[1] > top[b][1])) {
+            for (int b = 0; b < NT; ++b)
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        high[0] = fmaxf(high[0], __shfl_xor_sync(0xffffffffu, high[0], d));
-                        high[1] = fmaxf(high[1], __shfl_xor_sync(0xffffffffu, high[1], d));
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    high[b][i] = fmaxf(x[0][b][i], x[0][b][2 + i]);
+#pragma unroll
+                    for (int m = 1; m < kM; ++m) high[b][i] = fmaxf(high[b][i], fmaxf(x[m][b][i], x[m][b][2 + i]));
+                    rises |= high[b][i] > limit[b][i];
+                }
+            if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float now = fmaxf(top[b][i], high[i]);
+                        float now = fmaxf(top[b][i], high[b][i]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
                         const float less = now == top[b][i] ? 1.0f : exp2_fast((top[b][i] - now) * by[b][i]);  // (0 from nothing seen)
                         top[b][i] = now;
+                        if (now > kMinusInf) base[b][i] = kUp - now * by[b][i], limit[b][i] = now + __fdividef(kSlack, by[b][i]);
                         sum[b][i] *= less;
 #pragma unroll
                         for (int s = 0; s < kSteps; ++s) o[b][s][i] *= less, o[b][s][2 + i] *= less;
                     }
-                }
-                float base[2];
+            }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) base[i] = top[b][i] == kMinusInf ? 0.0f : kUp - top[b][i] * by[b][i];
+            for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int m = 0; m < kM; ++m) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[m][b][i] = exp2_fast(fmaf(x[m][b][i], by[b][i & 1], base[i & 1]));
+                        x[m][b][i] = exp2_fast(fmaf(x[m][b][i], by[b][i & 1], base[b][i & 1]));
                         sum[b][i & 1] += x[m][b][i];
                     }
 #pragma unroll
@@ -481,7 +489,6 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                         p[m][b][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&two));
                     }
                 }
-            }
             // o += p v.  Lane (r, t) reads, of the tokens of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the 16-block (half
             // of one, two) number r: the pairs of tokens that an operand register holds are put
             // together from two tokens' codes before these are converted.

@@ -105,7 +105,8 @@ def attend(q, k, v, length, scale, window=0):
             e = ((17 * (dim // 16) + 8) * 2.0 ** -23 * mags).max() + 2.0 ** -20 * (1 + np.abs(x).max())
             n = end - begin
             lbound[i, h] = e + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + abs(lse[i, h]))
-            # An exponential in FP16: half a step, 2^-11 of it, or 2^-39 of the largest where it is small; both sums.
+            # An exponential in FP16: half a step, 2^-11 of it, or, where it is below FP16's normal numbers, 2^-25; they are
+            # taken times 2^9 or more at the largest, so that this is 2^-34 of it; both sums.
             obound[i, h] = (p @ np.abs(V)) * (2.0 ** -11 + 2 * e + (17 * (n // 16 + 8) + n + 64) * 2.0 ** -23) + \
-                2.0 ** -39 * np.abs(V).sum(0)
+                2.0 ** -34 * np.abs(V).sum(0)
     return out, lse, obound, lbound
