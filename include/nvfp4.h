@@ -693,7 +693,7 @@ const char* nvfp4_status_string(nvfp4_status s);
 /* Library version: major * 10000 + minor * 100 + patch (200: adds mx_sf_layout
  * to nvfp4_quant_params, the sf_layout argument of mxfp4_quantize, mxfp8_gemm,
  * mxfp4_gemm and mxfp8_sf_mma_bytes; 300: adds the norm, routing, combine and
- * gemv calls). */
+ * gemv calls; 400: adds the paged cache, attention over it and nvfp4_expert_mlp). */
 int nvfp4_version(void);
 
 #ifdef __cplusplus

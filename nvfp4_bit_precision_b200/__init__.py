@@ -3,7 +3,8 @@ block-scaled GEMM.
 
 The C functions keep their names (``nvfp4_quantize``, ``nvfp4_dequantize``,
 ``mxfp8_quantize``, ``mxfp4_quantize``, ``nvfp4_gemm``, ``nvfp4_grouped_gemm``, ``nvfp4_rmsnorm``,
-``nvfp4_route``, ``nvfp4_combine``, ``nvfp4_gemv``, ``nvfp4_grouped_gemv`` and the backward calls); this
+``nvfp4_route``, ``nvfp4_combine``, ``nvfp4_gemv``, ``nvfp4_grouped_gemv``, ``nvfp4_expert_mlp``,
+``nvfp4_kv_append``, ``nvfp4_kv_attention`` and the backward calls); this
 module only marshals arguments: torch tensors become device pointers and the current torch
 stream becomes the ``cudaStream_t``.  Every arithmetic step runs in the CUDA
 kernels of ``libnvfp4.so``.  There is no fallback: importing this package
@@ -11,8 +12,8 @@ raises if the library is missing, and every call raises ``NVFP4Error`` on a
 non-zero status.
 
 The convenience wrappers (``quantize``, ``dequantize``, ``mxfp8``, ``mxfp4``, ``gemm``,
-``grouped_gemm``, ``rmsnorm``, ``route``, ``combine``, ``gemv``, ``grouped_gemv``) allocate their outputs
-with torch and call the C functions.
+``grouped_gemm``, ``rmsnorm``, ``route``, ``combine``, ``gemv``, ``grouped_gemv``, ``expert_mlp``, ``kv_append``,
+``kv_attention``) allocate their outputs with torch and call the C functions.
 """
 from __future__ import annotations
 

@@ -14,6 +14,13 @@
 // of the thread's pairs, and the sums r - d and r + d by less than 2^-24 (t + 2^-22) (|a| + |b|)
 // more.  Where these, with d = 1.6 * 2^-23 t (|a| + |b|) + 2^-126, round to the same bf16 number,
 // so does what lies between them.  Otherwise (about one number in 2000) the FP64 form decides.
+//
+// What bounds it: HBM where there is much to do.  16384 tokens with 32 query and 8 key heads
+// of 128 (354 MB) about 60 us, 5.9 TB/s; without the rotation the same.  One token 3 us, a
+// launch and three loads that wait for one another.  Steps on the way (with the cache read
+// back, 26 us): every lane quantising, what it turned and what it did not, 150 us; packed
+// arithmetic, S / d from a table, queries apart from keys and values 120; the next four
+// heads' numbers on their way through shared memory 102.
 #include "kv_cache.cuh"
 
 #include <algorithm>

@@ -5,6 +5,29 @@
 // over the cached tokens j that a query sees.  One pass over the cache with the running
 // maximum and sum of the softmax; work is split over the length, and the parts of a
 // head are joined by a second kernel.
+//
+// The rows of a key head, its queries times the heads of its group, share each read of a
+// key and a value.  Arithmetic, on the warp-level tensor core instructions:
+//  - a code pair becomes two FP16 values in one conversion, and one packed multiply by the
+//    block scale gives e2m1 * e4m3: exact in FP16;
+//  - queries are FP16 at a power of two per row, exact down to 2^-32 of the row's largest;
+//  - products are keys times queries (16 tokens x 8 rows), so that eight rows fill an
+//    instruction; the exponentials change places by an 8x8 transpose in registers;
+//  - two tokens' codes are interleaved by nibbles before their conversion, which gives the
+//    operand's pairs of tokens without touching the converted values;
+//  - products and sums are FP32; an exponential goes into the second product as FP16.
+//
+// What bounds it.  64 sequences of 5120 tokens on average, 40 heads over 8 key heads of 128
+// (383 MB): 79 us on the device, 4.9 TB/s; four of 81920 on average (434 MB) 84 us.  The
+// copies alone take 63 and 66 us (the copy rate), the join 5; decoding and products
+// overlap with the copies all but 12 us: 1100 instructions a warp and 64 tokens, at 58% of
+// the issue slots with the ALU pipe (conversions) 49% busy, and as many again would not fit.
+// Steps on the way, for the 64 sequences: four-warp CTAs with one softmax each and 16-byte
+// copies 106 us; steps of 64 tokens instead of 32, three CTAs a multiprocessor 95; a worker
+// a warp, copies ahead across items 85; joins a warp a row instead of a CTA a row 82.5;
+// codes copied to places free of bank conflicts (bulk copies, whose lanes take turns,
+// before) 80; the maximum raised only where it must be 78.5.  Products held apart by two
+// sums each, values decoded ahead of the softmax, 8 or 16 warps: none faster.
 #include "kv_cache.cuh"
 
 #include <algorithm>
@@ -124,7 +147,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
     return {begin, n, max(1, (n - begin + SLICE - 1) / SLICE)};
 }
 
-// Warps of a CTA, one CTA a multiprocessor: as many as the registers of `tiles` of eight rows leave room for.
+// Warps of a CTA, one CTA a multiprocessor: 168 registers a thread with 12, 255 with 8.  (Heads of 256 41.5
+// us with 8 and 50.4 with 12, where registers spill; 16 rows of 128 52 and 60; 8 rows of 128 94 and 80.)
 constexpr int warps_of(int dim, int tiles) { return dim * tiles > 128 ? 8 : 12; }
 template <int DIM, int NT, int SLICE>  // SLICE: tokens of a warp's step
 struct Shape {
@@ -741,6 +765,8 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
     c.tiles = (c.block_rows + 7) / 8;
     const int64_t items = sequences * kv_heads * c.blocks;
+    // Steps of 64 tokens save a tenth of the instructions, those of 32 share out short work better: one
+    // sequence of 32768 tokens 22.2 us with 32 and 25.2 with 64; 64 sequences of 5120 95 and 82.5.
     c.slice = c.tiles > 1 || dim == 256 || items * (capacity / 64 + 1) <= 8000 ? 32 : 64;
     c.ctas = std::min<int64_t>(sms, items * (capacity / kLeastSlice + 2));  // (no more than there can be slices)
     c.workers = c.ctas * warps_of(dim, c.tiles);

@@ -1206,7 +1206,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint8_t* q, const ui
 
 // The same with row-major scales, where the blocks of all rows lie one after another:
 // eight elements a thread and step, so that a warp's stores are whole lines, four steps'
-// loads in flight.  Keys of 64 x 512 tokens in 8 heads of 128 to bf16 (86 MB) 15 us;
+// loads in flight.  Keys of 64 x 512 tokens in 8 heads of 128 to bf16 (86 MB) 17 us;
 // with the blocks found by division, 32 bytes a thread, 20 us.
 __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* q, const uint8_t* sf, const float* gp,
                                                            int64_t eights, int bf16_out, void* out)
@@ -1708,4 +1708,4 @@ extern "C" const char* nvfp4_status_string(nvfp4_status s)
     return "unknown status";
 }
 
-extern "C" int nvfp4_version(void) { return 300; }
+extern "C" int nvfp4_version(void) { return 400; }

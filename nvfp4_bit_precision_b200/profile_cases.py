@@ -14,6 +14,9 @@
     python -m nvfp4_bit_precision_b200.profile_cases route TOKENS EXPERTS [--warm W]
     python -m nvfp4_bit_precision_b200.profile_cases weighted-combine TOKENS HIDDEN [--warm W]
     python -m nvfp4_bit_precision_b200.profile_cases gemv ROWS N K [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases kv-append TOKENS HEADS [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases kv-attention SEQUENCES LENGTH HEADS [--warm W]
+    python -m nvfp4_bit_precision_b200.profile_cases expert-mlp TOKENS HIDDEN FFN [--warm W]
 
 Each runs W untimed launches of the case, then one more, on synthetic operands
 (codes and in-range scale bytes drawn on the device; bf16 inputs ~N(0, 1e-3)),
@@ -229,11 +232,71 @@ def _gemv(nv, torch, rows, N, K, warm):
         nv.gemv(x, w)
 
 
+def _random_cache(nv, torch, pages, kv_heads, page, dim):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    u8 = dict(dtype=torch.uint8, device="cuda", generator=g)
+    c = nv.kv_cache(pages, kv_heads, page, dim, 8.0, 8.0)
+    c.q.copy_(torch.randint(0, 256, tuple(c.q.shape), **u8))
+    c.sf.copy_(torch.randint(0x30, 0x40, tuple(c.sf.shape), **u8))
+    return c
+
+
+def _kv_append(nv, torch, tokens, heads, warm):
+    """Tokens of one sequence each 2048 long, 8 key heads of 128, keys and queries turned."""
+    page, dim, kv, each = 64, 128, 8, min(tokens, 2048)
+    n = -(-tokens // each)
+    table = torch.randperm(n * -(-each // page), device="cuda").to(torch.int32).reshape(n, -1)
+    cache = _random_cache(nv, torch, table.numel(), kv, page, dim)
+    qkv = _bf16(torch, (tokens, heads + 2 * kv, dim), 1.0, 0)
+    at = torch.arange(tokens, device="cuda")
+    angle = (at[:each, None].double() * 10000.0 ** (-torch.arange(0, dim, 2, device="cuda").double() / dim))
+    for _ in range(warm + 1):
+        nv.kv_append(cache, qkv[:, heads:heads + kv], qkv[:, heads + kv:], table, (at % each).to(torch.int32),
+                     (at // each).to(torch.int32), cos=angle.cos().float(), sin=angle.sin().float(), q=qkv[:, :heads])
+
+
+def _kv_attention(nv, torch, sequences, length, heads, warm):
+    """One query token of each sequence over its whole cache, 8 key heads of 128."""
+    page, dim, kv = 64, 128, 8
+    table = torch.randperm(sequences * -(-length // page), device="cuda").to(torch.int32).reshape(sequences, -1)
+    cache = _random_cache(nv, torch, table.numel(), kv, page, dim)
+    q = _bf16(torch, (sequences, 1, heads, dim), 1.0, 0)
+    lengths = torch.full((sequences,), length, dtype=torch.int32, device="cuda")
+    size = nv.nvfp4_kv_attention_workspace_size(sequences, 1, heads, kv, dim, table.shape[1] * page)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for _ in range(warm + 1):
+        nv.kv_attention(q, cache, table, lengths, workspace=ws)
+    return ws
+
+
+def _expert_mlp(nv, torch, tokens, hidden, ffn, warm):
+    """A few tokens through four of 64 gated experts."""
+    from .moe import ExpertWeights
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    u8 = dict(dtype=torch.uint8, device="cuda", generator=g)
+
+    def weights(n, k):
+        return ExpertWeights(torch.randint(0, 256, (64, n, k // 2), **u8),
+                             torch.randint(0x30, 0x40, (64 * nv.nvfp4_sf_mma_bytes(n, k),), **u8),
+                             torch.full((64,), 0.01 / k ** 0.5, device="cuda"), n)
+
+    up, gate, down = weights(ffn, hidden), weights(ffn, hidden), weights(hidden, ffn)
+    x = _bf16(torch, (tokens, hidden), 1.0, 0)
+    r = nv.route(_bf16(torch, (tokens, 64), 1.5, 1).float(), 4)
+    ws = torch.zeros(nv.nvfp4_expert_mlp_workspace_size(4 * tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+    for _ in range(warm + 1):
+        nv.expert_mlp(x, r, up, down, gate, x, workspace=ws)
+    return ws
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["gemm", "mxfp8-gemm", "grouped-gemm", "quant-grad", "quant-act",
                                          "quant-weight", "mxfp4", "dispatch", "combine", "norm",
-                                         "norm-backward", "route", "weighted-combine", "gemv"])
+                                         "norm-backward", "route", "weighted-combine", "gemv", "kv-append",
+                                         "kv-attention", "expert-mlp"])
     ap.add_argument("dims", type=int, nargs="+")
     ap.add_argument("--warm", type=int, default=3)
     args = ap.parse_args(argv)
@@ -258,6 +321,12 @@ def main(argv=None) -> int:
         ws = _combine(nv, torch, *args.dims[:2], args.warm)
     elif args.case == "gemv":
         ws = _gemv(nv, torch, *args.dims[:3], args.warm)
+    elif args.case == "kv-append":
+        ws = _kv_append(nv, torch, *args.dims[:2], args.warm)
+    elif args.case == "kv-attention":
+        ws = _kv_attention(nv, torch, *args.dims[:3], args.warm)
+    elif args.case == "expert-mlp":
+        ws = _expert_mlp(nv, torch, *args.dims[:3], args.warm)
     elif args.case in ("norm", "norm-backward", "route", "weighted-combine"):
         case = {"norm": _norm, "norm-backward": _norm_backward, "route": _route,
                 "weighted-combine": _weighted_combine}[args.case]
