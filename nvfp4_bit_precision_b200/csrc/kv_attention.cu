@@ -218,11 +218,12 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
         s_upto[threadIdx.x] = upto;
     }
     __syncthreads();
-    // This worker's run; neighbours are on different multiprocessors.  A slice takes a worker about
-    // as long as 16 more parts take the join of an item, so that runs grow as the root of an item's slices
-    // where there are few of these.
+    // This worker's run; neighbours are on different multiprocessors.  Where items are long and few, the
+    // join of their parts costs as much as their slices: runs are at least the root of a sixteenth of an
+    // item's slices (one head over 131072 tokens 26.6 us, with runs of two slices 54; eight heads over
+    // 32768 21.3 and 24.2; two over 4096 10.4, with a slice 11, with three 11.8).
     int least = 1;
-    while (16 * least * least < all / (a.sequences * items)) ++least;
+    while (16 * (least + 1) * (least + 1) <= all / (a.sequences * items)) ++least;
     const int workers = min(static_cast<int>(gridDim.x) * kWarps, (all + least - 1) / least);
     const int worker = warp * gridDim.x + blockIdx.x;
     const int each = all / workers, more = all - each * workers;
