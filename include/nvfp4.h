@@ -671,9 +671,8 @@ size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int hea
  * the exponentials go into the product with v as FP16, 2^-12 off at most.
  * The table is read up to a sequence's length.  A page outside the cache counts as
  * zeros, a length outside 0..table_pages * page_size as the nearer end; both are
- * reported in the workspace's status word (NVFP4_ERR_INDEX).  Meant for up to about
- * 16 rows (queries * heads / kv_heads; 8 where dim is 256): the cache is read again
- * for every so many.  Results do not depend on timing; they may depend on the other
+ * reported in the workspace's status word (NVFP4_ERR_INDEX).  Meant for few rows
+ * (queries * heads / kv_heads): the cache is decoded again for every eight.  Results do not depend on timing; they may depend on the other
  * sequences of a call, by the places where a long one is cut.
  */
 nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh,

@@ -147,13 +147,17 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int seq, int* bad)
     return {begin, n, max(1, (n - begin + SLICE - 1) / SLICE)};
 }
 
+// Rows that work on a slice together: one matrix instruction's.  (Sixteen, with eight warps for their
+// registers: 16 heads a key head over 32 sequences of 5120 47 us against 49.5, but 12 rows over four
+// short ones 15.8 against 15.4, and 20 rows of five drafts 25.9 against 23.5.)
+constexpr int kRows = 8;
 // Warps of a CTA, one CTA a multiprocessor: 168 registers a thread with 12, 255 with 8.  (Heads of 256 41.5
-// us with 8 and 50.4 with 12, where registers spill; 16 rows of 128 52 and 60; 8 rows of 128 94 and 80.)
-constexpr int warps_of(int dim, int tiles) { return dim * tiles > 128 ? 8 : 12; }
-template <int DIM, int NT, int SLICE>  // SLICE: tokens of a warp's step
+// us with 8 and 50.4 with 12, where registers spill; heads of 128 94 and 80.)
+constexpr int warps_of(int dim) { return dim == 256 ? 8 : 12; }
+template <int DIM, int SLICE>  // SLICE: tokens of a warp's step
 struct Shape {
     static constexpr int kSlice = SLICE;
-    static constexpr int kWarps = warps_of(DIM, NT);
+    static constexpr int kWarps = warps_of(DIM);
     static constexpr int kCodes = kSlice * DIM / 2, kScales = kSlice * DIM / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
     static constexpr int kStages = kStage * kWarps * 3 > 224000 ? 2 : kStage > 2500 ? 3 : 4;
@@ -173,10 +177,10 @@ struct Shape {
 // Each warp is a worker of its own: it takes an equal run of all slices of all (sequence,
 // key head, block of rows) items, keeps its own maximum, sums and copies on their way, and
 // leaves an item's result, or its part of one that other workers share.
-template <int DIM, int NT, int SLICE>
-__global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_kernel(const AttendArgs a)
+template <int DIM, int SLICE>
+__global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kernel(const AttendArgs a)
 {
-    using S = Shape<DIM, NT, SLICE>;
+    using S = Shape<DIM, SLICE>;
     constexpr int kWarps = S::kWarps, kSlice = SLICE, kM = kSlice / 16;
     constexpr int kSteps = DIM / 16;       // matrix instructions over the head dimension; 16-blocks of a token
     constexpr int kLaneCodes = DIM / 8;    // bytes of a token's keys that a lane reads
@@ -352,17 +356,16 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
         // to [2^14, 2^15) (as in the few-token products): of step s, lane (r, t) has row r's
         // elements t DIM / 4 + 4 s + 0..3.  A negative scale turns their signs, so that the
         // factors on the products are positive.
-        uint32_t qf[NT][kSteps][2];
-        float by[NT][2];       // factors on the products of rows 2 t, 2 t + 1: to base-2 logarithms
-#pragma unroll
-        for (int b = 0; b < NT; ++b) {
-            const int row = 8 * b + r, i = (row0 + row) / a.group, h = (row0 + row) - i * a.group;
+        uint32_t qf[kSteps][2];
+        float by[2];       // factors on the products of rows 2 t, 2 t + 1: to base-2 logarithms
+        {
+            const int i = (row0 + r) / a.group, h = (row0 + r) - i * a.group;
             uint4 v[kSteps / 2];
             uint32_t top = 0;
 #pragma unroll
             for (int s = 0; s < kSteps / 2; ++s) {
                 v[s] = make_uint4(0, 0, 0, 0);
-                if (row < rows)
+                if (r < rows)
                     v[s] = *reinterpret_cast<const uint4*>(a.q + seq * a.ldb + i * a.ldi + (head * a.group + h) * a.ldh +
                                                            t * (DIM / 4) + 8 * s);
                 const uint32_t m = __vmaxu2(
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const __half2 two = __floats2half2_rn(x[2 * j] * up, x[2 * j + 1] * up);
-                    qf[b][2 * s + j / 2][j & 1] = *reinterpret_cast<const uint32_t*>(&two);
+                    qf[2 * s + j / 2][j & 1] = *reinterpret_cast<const uint32_t*>(&two);
                 }
             }
             // |scale| g log2(e), then the row's power of two; never zero, so that 0 x infinity does not arise
@@ -388,22 +391,19 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
             const float f2 = fabsf(a.scale) * gk * 1.44269502162933349609375f;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                by[b][j] = fmaxf(f2 * __shfl_sync(0xffffffffu, down, (2 * t + j) * 4), 1.17549435082228750797e-38f);
+                by[j] = fmaxf(f2 * __shfl_sync(0xffffffffu, down, (2 * t + j) * 4), 1.17549435082228750797e-38f);
         }
-        // the tokens that row 8 b + 2 t + j sees, [last + 1 - window, last] of the part's; what every row sees
+        // the tokens that row 2 t + j sees, [last + 1 - window, last] of the part's; what every row sees
         // (rows are in the queries' order)
         const auto last_of = [&](int n) { return span.length - a.queries + (row0 + min(n, rows - 1)) / a.group; };
         const int all_to = min(last_of(0) + 1, end);
         const int all_from = a.window > 0 ? last_of(rows) + 1 - a.window : 0;
         // top: the running maximum of the products, base: what it adds to an exponent, limit: the product that raises it
-        float top[NT][2], base[NT][2], limit[NT][2], sum[NT][2], o[NT][kSteps][4];
+        float top[2], base[2], limit[2], sum[2], o[kSteps][4];
+        top[0] = top[1] = limit[0] = limit[1] = kMinusInf;
+        base[0] = base[1] = sum[0] = sum[1] = 0.0f;
 #pragma unroll
-        for (int b = 0; b < NT; ++b) {
-            top[b][0] = top[b][1] = limit[b][0] = limit[b][1] = kMinusInf;
-            base[b][0] = base[b][1] = sum[b][0] = sum[b][1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
-        }
+        for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
         // The tokens of a row of eight of a matrix instruction, in an order in which neighbouring
         // lanes' reads of keys and of values meet other banks: row 2 j, 2 j + 1 has tokens 2 j and 2 j +
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
             const bool edge = place < all_from || place + kSlice > all_to;
 
             // products: the slice's tokens x rows; lane (r, t): tokens (my_token) + 8 h + 16 m, rows 2 t, 2 t + 1
-            float x[kM][NT][4] = {};
+            float x[kM][4] = {};
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
                 uint32_t code[2][kLaneCodes / 4], sc[2][DIM / 64];
@@ -449,71 +449,60 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[h][i] = mul_f16x2(v[h][i], sc[h][w / 2]);
                     }
-#pragma unroll
-                    for (int b = 0; b < NT; ++b) {
-                        mma_16816(x[m][b], v[0][0], v[1][0], v[0][1], v[1][1], qf[b][2 * w][0], qf[b][2 * w][1]);
-                        mma_16816(x[m][b], v[0][2], v[1][2], v[0][3], v[1][3], qf[b][2 * w + 1][0], qf[b][2 * w + 1][1]);
-                    }
+                    mma_16816(x[m], v[0][0], v[1][0], v[0][1], v[1][1], qf[2 * w][0], qf[2 * w][1]);
+                    mma_16816(x[m], v[0][2], v[1][2], v[0][3], v[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
                 }
             }
-            uint32_t p[kM][NT][2];  // exponentials, FP16: row r, tokens of rows 2 t, 2 t + 1 (+ 8)
+            uint32_t p[kM][2];  // exponentials, FP16: row r, tokens of rows 2 t, 2 t + 1 (+ 8)
             if (edge) {
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
+                for (int j = 0; j < 2; ++j) {
+                    const int last = last_of(2 * t + j), from = a.window > 0 ? last + 1 - a.window : 0;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int last = last_of(8 * b + 2 * t + j), from = a.window > 0 ? last + 1 - a.window : 0;
+                    for (int m = 0; m < kM; ++m)
 #pragma unroll
-                        for (int m = 0; m < kM; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int at = place + 16 * m + 8 * h + my_token;
-                                if (at < from || at > last || at >= end) x[m][b][2 * h + j] = kMinusInf;
-                            }
-                    }
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = place + 16 * m + 8 * h + my_token;
+                            if (at < from || at > last || at >= end) x[m][2 * h + j] = kMinusInf;
+                        }
+                }
             }
-            float high[NT][2];
+            float high[2];
             bool rises = false;
 #pragma unroll
-            for (int b = 0; b < NT; ++b)
+            for (int i = 0; i < 2; ++i) {
+                high[i] = fmaxf(x[0][i], x[0][2 + i]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    high[b][i] = fmaxf(x[0][b][i], x[0][b][2 + i]);
-#pragma unroll
-                    for (int m = 1; m < kM; ++m) high[b][i] = fmaxf(high[b][i], fmaxf(x[m][b][i], x[m][b][2 + i]));
-                    rises |= high[b][i] > limit[b][i];
-                }
+                for (int m = 1; m < kM; ++m) high[i] = fmaxf(high[i], fmaxf(x[m][i], x[m][2 + i]));
+                rises |= high[i] > limit[i];
+            }
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
+                for (int i = 0; i < 2; ++i) {
+                    float now = fmaxf(top[i], high[i]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float now = fmaxf(top[b][i], high[b][i]);
+                    for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+                    const float less = now == top[i] ? 1.0f : exp2_fast((top[i] - now) * by[i]);  // (0 from nothing seen)
+                    top[i] = now;
+                    if (now > kMinusInf) base[i] = kUp - now * by[i], limit[i] = now + __fdividef(kSlack, by[i]);
+                    sum[i] *= less;
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-                        const float less = now == top[b][i] ? 1.0f : exp2_fast((top[b][i] - now) * by[b][i]);  // (0 from nothing seen)
-                        top[b][i] = now;
-                        if (now > kMinusInf) base[b][i] = kUp - now * by[b][i], limit[b][i] = now + __fdividef(kSlack, by[b][i]);
-                        sum[b][i] *= less;
-#pragma unroll
-                        for (int s = 0; s < kSteps; ++s) o[b][s][i] *= less, o[b][s][2 + i] *= less;
-                    }
+                    for (int s = 0; s < kSteps; ++s) o[s][i] *= less, o[s][2 + i] *= less;
+                }
             }
 #pragma unroll
-            for (int b = 0; b < NT; ++b)
+            for (int m = 0; m < kM; ++m) {
 #pragma unroll
-                for (int m = 0; m < kM; ++m) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[m][b][i] = exp2_fast(fmaf(x[m][b][i], by[b][i & 1], base[b][i & 1]));
-                        sum[b][i & 1] += x[m][b][i];
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const __half2 two = __floats2half2_rn(x[m][b][2 * h], x[m][b][2 * h + 1]);
-                        p[m][b][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&two));
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    x[m][i] = exp2_fast(fmaf(x[m][i], by[i & 1], base[i & 1]));
+                    sum[i & 1] += x[m][i];
                 }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __half2 two = __floats2half2_rn(x[m][2 * h], x[m][2 * h + 1]);
+                    p[m][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&two));
+                }
+            }
             // o += p v.  Lane (r, t) reads, of the tokens of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the 16-block (half
             // of one, two) number r: the pairs of tokens that an operand register holds are put
             // together from two tokens' codes before these are converted.
@@ -557,22 +546,20 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                         bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
                         if (bad) {
 #pragma unroll
-                            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const int last = last_of(8 * b + 2 * t + i), from = a.window > 0 ? last + 1 - a.window : 0;
-                                    bool sees = false;
+                            for (int i = 0; i < 2; ++i) {
+                                const int last = last_of(2 * t + i), from = a.window > 0 ? last + 1 - a.window : 0;
+                                bool sees = false;
 #pragma unroll 1
-                                    for (int at = 0; at < 16; ++at) {
-                                        const int token = place + 16 * m + at;
-                                        sees |= (bad >> at & 1) && token >= from && token <= last;
-                                    }
-                                    if (sees) {
-#pragma unroll
-                                        for (int s = k2 * (kSteps / kBlocks); s < (k2 + 1) * (kSteps / kBlocks); ++s)
-                                            o[b][s][i] = o[b][s][2 + i] = __int_as_float(0x7fffffff);
-                                    }
+                                for (int at = 0; at < 16; ++at) {
+                                    const int token = place + 16 * m + at;
+                                    sees |= (bad >> at & 1) && token >= from && token <= last;
                                 }
+                                if (sees) {
+#pragma unroll
+                                    for (int s = k2 * (kSteps / kBlocks); s < (k2 + 1) * (kSteps / kBlocks); ++s)
+                                        o[s][i] = o[s][2 + i] = __int_as_float(0x7fffffff);
+                                }
+                            }
                         }
                     }
                 }
@@ -596,10 +583,8 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
                         }
                     }
 #pragma unroll
-                    for (int b = 0; b < NT; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_16816(o[b][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], p[m][b][0], p[m][b][1]);
+                    for (int i = 0; i < 4; ++i)
+                        mma_16816(o[4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], p[m][0], p[m][1]);
                 }
             }
             get = get + 1 == S::kStages ? 0 : get + 1;
@@ -611,33 +596,31 @@ __global__ void __launch_bounds__(32 * Shape<DIM, NT, SLICE>::kWarps, 1) attend_
         const bool whole = take == span.slices;
         const int slot = 2 * worker + (first == 0 ? 1 : 0);
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
+        for (int i = 0; i < 2; ++i) {
+            float l = sum[i];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float l = sum[b][i];
+            for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+            const float high = top[i] == kMinusInf ? kMinusInf : top[i] * by[i];
+            const int row = 2 * t + i;
+            if (row >= rows) continue;
+            if (whole) {
+                const float n = l == 0.0f ? 0.0f : gv / l;
+                const int query = (row0 + row) / a.group, h = (row0 + row) - query * a.group;
+                const int64_t at = (static_cast<int64_t>(seq) * a.queries + query) * a.heads + head * a.group + h;
+                uint2* const to = reinterpret_cast<uint2*>(a.out + at * DIM + r * (DIM / 8));
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-                const float high = top[b][i] == kMinusInf ? kMinusInf : top[b][i] * by[b][i];
-                const int row = 8 * b + 2 * t + i;
-                if (row >= rows) continue;
-                if (whole) {
-                    const float n = l == 0.0f ? 0.0f : gv / l;
-                    const int query = (row0 + row) / a.group, h = (row0 + row) - query * a.group;
-                    const int64_t at = (static_cast<int64_t>(seq) * a.queries + query) * a.heads + head * a.group + h;
-                    uint2* const to = reinterpret_cast<uint2*>(a.out + at * DIM + r * (DIM / 8));
+                for (int s = 0; s < kSteps; s += 2)
+                    to[s / 2] = make_uint2(pack2(o[s][i] * n, o[s][2 + i] * n), pack2(o[s + 1][i] * n, o[s + 1][2 + i] * n));
+                if (a.lse && r == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
+            } else {
+                const int64_t at = static_cast<int64_t>(slot) * a.block_rows + row;
+                float4* const to = reinterpret_cast<float4*>(a.part_o + at * DIM + r * (DIM / 8));
 #pragma unroll
-                    for (int s = 0; s < kSteps; s += 2)
-                        to[s / 2] = make_uint2(pack2(o[b][s][i] * n, o[b][s][2 + i] * n), pack2(o[b][s + 1][i] * n, o[b][s + 1][2 + i] * n));
-                    if (a.lse && r == 0) a.lse[at] = 0.693147182464599609375f * (high + (log2f(l) - kUp));
-                } else {
-                    const int64_t at = static_cast<int64_t>(slot) * a.block_rows + row;
-                    float4* const to = reinterpret_cast<float4*>(a.part_o + at * DIM + r * (DIM / 8));
-#pragma unroll
-                    for (int s = 0; s < kSteps; s += 2)
-                        to[s / 2] = make_float4(o[b][s][i], o[b][s][2 + i], o[b][s + 1][i], o[b][s + 1][2 + i]);
-                    if (r == 0) a.part_ml[at] = make_float2(high, l);
-                }
+                for (int s = 0; s < kSteps; s += 2)
+                    to[s / 2] = make_float4(o[s][i], o[s][2 + i], o[s + 1][i], o[s + 1][2 + i]);
+                if (r == 0) a.part_ml[at] = make_float2(high, l);
             }
+        }
         left -= take;
         // the worker that begins an item says who else has a part of it
         if (lane == 0 && first == 0 && (a.by_item || left == 0)) {
@@ -753,7 +736,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttendArgs 
 // Rows of a block, the CTAs of the attention and its records.
 struct Cut {
     int rows, blocks, block_rows;
-    int tiles;     // of eight rows that a block has
     int slice;     // tokens of a step
     int64_t ctas, workers, records;
 };
@@ -761,36 +743,34 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
 {
     Cut c;
     c.rows = queries * (heads / kv_heads);
-    const int most = dim == 256 ? 8 : 16;
-    c.blocks = (c.rows + most - 1) / most;
+    c.blocks = (c.rows + kRows - 1) / kRows;
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
-    c.tiles = (c.block_rows + 7) / 8;
     const int64_t items = sequences * kv_heads * c.blocks;
     // Steps of 64 tokens save a tenth of the instructions, those of 32 share out short work better: one
     // sequence of 32768 tokens 22.2 us with 32 and 25.2 with 64; 64 sequences of 5120 95 and 82.5.
-    c.slice = c.tiles > 1 || dim == 256 || items * (capacity / 64 + 1) <= 8000 ? 32 : 64;
+    c.slice = dim == 256 || items * (capacity / 64 + 1) <= 8000 ? 32 : 64;
     c.ctas = std::min<int64_t>(sms, items * (capacity / kLeastSlice + 2));  // (no more than there can be slices)
-    c.workers = c.ctas * warps_of(dim, c.tiles);
+    c.workers = c.ctas * warps_of(dim);
     c.records = std::min(items, c.workers);
     return c;
 }
 
 constexpr int kMostSms = 192;  // of the workspace's size, which is known without a device
 
-template <int DIM, int NT, int SLICE>
+template <int DIM, int SLICE>
 nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
 {
-    using S = Shape<DIM, NT, SLICE>;
+    using S = Shape<DIM, SLICE>;
     static bool raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!raised[dev & 63]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(attend_kernel<DIM, NT, SLICE>),
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(attend_kernel<DIM, SLICE>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem)) != cudaSuccess)
             return NVFP4_ERR_CUDA;
         raised[dev & 63] = true;
     }
-    if (launch_early(true, attend_kernel<DIM, NT, SLICE>, cut.ctas, 32 * S::kWarps, S::kSmem, st, a) != cudaSuccess)
+    if (launch_early(true, attend_kernel<DIM, SLICE>, cut.ctas, 32 * S::kWarps, S::kSmem, st, a) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -883,11 +863,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
     at += static_cast<size_t>(2 * cut.workers) * cut.block_rows * dim * 4;
     a.part_ml = reinterpret_cast<float2*>(at);
     a.status = static_cast<uint32_t*>(workspace) + 2;
-    if (dim == 256) return start<256, 1, 32>(a, cut, st);
-    if (dim == 128) {
-        if (cut.tiles == 2) return start<128, 2, 32>(a, cut, st);
-        return cut.slice == 32 ? start<128, 1, 32>(a, cut, st) : start<128, 1, 64>(a, cut, st);
-    }
-    if (cut.tiles == 2) return start<64, 2, 32>(a, cut, st);
-    return cut.slice == 32 ? start<64, 1, 32>(a, cut, st) : start<64, 1, 64>(a, cut, st);
+    if (dim == 256) return start<256, 32>(a, cut, st);
+    if (dim == 128) return cut.slice == 32 ? start<128, 32>(a, cut, st) : start<128, 64>(a, cut, st);
+    return cut.slice == 32 ? start<64, 32>(a, cut, st) : start<64, 64>(a, cut, st);
 }
