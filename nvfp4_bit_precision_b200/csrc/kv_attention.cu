@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttendArgs 
     constexpr int kEach = kVecs > 32 ? kVecs / 32 : 1;      // of a lane
     constexpr int kRowLanes = kVecs < 32 ? kVecs : 32;
     constexpr int kUnits = 32 * kJoinWarps / kRowLanes;     // rows, or shares of them, at a time
-    constexpr int kParts = kEach == 1 ? 8 : 4;              // whose loads are in flight together
+    constexpr int kParts = 8;                               // whose loads are in flight together
     __shared__ float4 s_v[kUnits][kVecs];
     __shared__ float2 s_ml[kUnits];
     wait_for_previous_kernel();
