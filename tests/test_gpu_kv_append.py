@@ -179,6 +179,53 @@ def test_tokens_without_a_place(nv):
         np.testing.assert_array_equal(host(cache.sf), host(other.sf))
 
 
+def test_two_tokens_at_one_place(nv):
+    """Each block of eight codes and each scale byte there is one of theirs; the places beside it are as they were."""
+    rng = np.random.default_rng(6)
+    dim, page, kv = 128, 16, 2
+    cache = random_cache(nv, rng, 2, kv, page, dim)
+    cq, csf = host(cache.q).copy(), host(cache.sf).copy()
+    k, v = bits(rng, (2, kv, dim)), bits(rng, (2, kv, dim))
+    nv.kv_append(cache, to_dev(k), to_dev(v), i32([[1]]), i32([5, 5]), i32([0, 0]))
+    gq, gsf = host(cache.q), host(cache.sf)
+    for which, b in ((0, k), (1, v)):
+        codes, scales = K.quantise(W.bf16_bits_to_f32(b), host(cache.amax)[which])
+        got, gots = gq[which, 1, :, 5].reshape(kv, -1, 4), gsf[which, 1, :, 5]
+        codes = codes.reshape(2, kv, -1, 4)
+        assert np.all((got == codes[0]).all(-1) | (got == codes[1]).all(-1))
+        assert np.all((gots == scales[0]) | (gots == scales[1]))
+    gq[:, 1, :, 5], gsf[:, 1, :, 5] = cq[:, 1, :, 5], csf[:, 1, :, 5]
+    np.testing.assert_array_equal(gq, cq)
+    np.testing.assert_array_equal(gsf, csf)
+
+
+def test_streams_and_graphs(nv):
+    """On another stream, captured and replayed with other tokens at other places."""
+    import torch
+    rng = np.random.default_rng(7)
+    dim, page, kv, heads, n = 64, 16, 2, 4, 3
+    cos, sin = (dev(a) for a in K.tables(dim, 64))
+    a, b = (nv.kv_cache(12, kv, page, dim, 4.0, 4.0) for _ in range(2))
+    table = i32(rng.permutation(12).reshape(n, 4))
+    qkv, place = to_dev(bits(rng, (n, heads + 2 * kv, dim))), i32([0, 3, 40])
+    call = lambda c, **kw: nv.kv_append(c, qkv[:, heads:heads + kv], qkv[:, heads + kv:], table, place, cos=cos, sin=sin,  # noqa: E731
+                                        q=qkv[:, :heads], **kw)
+    want = call(a)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(b, stream=stream)
+    stream.synchronize()
+    assert torch.equal(got, want) and torch.equal(a.q, b.q) and torch.equal(a.sf, b.sf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(b)
+    for i in range(5):
+        qkv.copy_(to_dev(bits(rng, tuple(qkv.shape))))
+        place += 1
+        graph.replay()
+        assert torch.equal(out, call(a)) and torch.equal(a.q, b.q) and torch.equal(a.sf, b.sf)
+
+
 def test_nothing_to_append(nv):
     import torch
     cache = nv.kv_cache(1, 2, 16, 64)

@@ -96,6 +96,23 @@ def test_cut_lengths(nv, n, lengths):
     check(nv, cache, q, sf, bits(rng, (n, 1, 6, dim), 2.0), table, lengths, page)
 
 
+@pytest.mark.parametrize("heads,new", [(3, 1), (9, 1), (9, 3)])
+def test_more_items_than_workers(nv, heads, new):
+    """Short sequences by the hundred, a few long ones among them, the first and the last too."""
+    rng = np.random.default_rng(heads + new)
+    n, dim, kv, page = 700, 64, 3, 16
+    lengths = rng.integers(0, 60, n)
+    lengths[[0, 137, 138, 500, 699]] = [700, 1024, 3, 1000, 650]
+    pages = int(sum(-(-lengths // page))) + 1
+    cache, q, sf = filled(nv, rng, pages, kv, page, dim)
+    table, at = np.full((n, 64), -1), 0
+    order = rng.permutation(pages)
+    for i, m in enumerate(-(-lengths // page)):
+        table[i, :m] = order[at:at + m]
+        at += m
+    check(nv, cache, q, sf, bits(rng, (n, new, heads, dim)), table, [int(x) for x in lengths], page)
+
+
 @pytest.mark.parametrize("n", [129, 300])
 def test_more_sequences_than_threads(nv, n):
     rng = np.random.default_rng(n)
