@@ -653,7 +653,8 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k_bf16, in
                              void* q_out, int64_t ldo, int64_t hso, void* workspace, size_t ws_bytes,
                              void* stream);
 
-/* Workspace bytes of nvfp4_kv_attention; capacity = table_pages * page_size. */
+/* Workspace bytes of nvfp4_kv_attention; capacity = table_pages * page_size (those of the
+ * status word alone for sizes that the call refuses). */
 size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int heads, int kv_heads,
                                          int dim, int64_t capacity);
 

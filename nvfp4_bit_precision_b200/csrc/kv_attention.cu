@@ -756,6 +756,15 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
     return c;
 }
 
+constexpr int64_t kMostRows = 1 << 24;  // of a key head
+
+// Slices of all items are counted in 31 bits on the device.
+bool counts_fit(int64_t sequences, int queries, int heads, int kv_heads, int64_t capacity)
+{
+    const int64_t rows = static_cast<int64_t>(queries) * (heads / kv_heads);
+    return rows <= kMostRows && capacity / kLeastSlice + 2 <= 0x7fffffffll / (sequences * kv_heads) / ((rows + kRows - 1) / kRows);
+}
+
 constexpr int kMostSms = 192;  // of the workspace's size, which is known without a device
 
 template <int DIM, int SLICE>
@@ -802,10 +811,10 @@ extern "C" size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queri
                                                     int64_t capacity)
 {
     if (sequences < 1 || queries < 1 || kv_heads < 1 || heads < kv_heads || capacity < 0 ||
-        (dim != 64 && dim != 128 && dim != 256) || queries > (1 << 20) || heads > 65536)
-        return kHeadBytes;
-    const Cut c = cut_of(std::min<int64_t>(sequences, 1 << 20), queries, heads, kv_heads, dim, std::min<int64_t>(capacity, 1ll << 31), kMostSms);
-    return workspace_bytes(c, dim);
+        (dim != 64 && dim != 128 && dim != 256) || sequences > (1 << 20) || queries > (1 << 20) || heads > 65536 ||
+        !counts_fit(sequences, queries, heads, kv_heads, capacity))
+        return kHeadBytes;  // (nothing to do, or sizes that the call refuses)
+    return workspace_bytes(cut_of(sequences, queries, heads, kv_heads, dim, capacity, kMostSms), dim);
 }
 
 extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh, int64_t sequences,
@@ -831,11 +840,8 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int6
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(lse)) & 3u))
         return NVFP4_ERR_ALIGN;
     if (!workspace || off16(workspace) || ws_bytes < kHeadBytes) return NVFP4_ERR_WORKSPACE;
-    if (static_cast<int64_t>(queries) * (heads / kv) > (1 << 24)) return NVFP4_ERR_SHAPE;
-    if (sequences > 0) {
-        const Cut c = cut_of(sequences, queries, heads, kv, dim, capacity, 1);
-        if ((capacity / kLeastSlice + 2) > 0x7fffffffll / (sequences * kv) / c.blocks) return NVFP4_ERR_SHAPE;
-    }
+    if (static_cast<int64_t>(queries) * (heads / kv) > kMostRows) return NVFP4_ERR_SHAPE;
+    if (sequences > 0 && !counts_fit(sequences, queries, heads, kv, capacity)) return NVFP4_ERR_SHAPE;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     const int sms = sm100_sms(dev);

@@ -2,6 +2,8 @@
 status before any device work, and the wrappers raise before they call them.  Stand-in addresses: on machines without
 a GPU only, where nothing could be launched on them."""
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -97,6 +99,16 @@ def test_attention_workspace(nv):
     assert size(0, 1, 8, 8, 128, 100) == size(1, 0, 8, 8, 128, 100) == size(1, 1, 4, 8, 128, 100) == size(1, 1, 8, 8, 96, 100) == 256
     assert 256 < size(1, 1, 8, 8, 128, 0) <= size(1, 1, 8, 8, 128, 100) <= size(1, 1, 32, 8, 128, 10000) <= size(64, 1, 32, 8, 128, 10000) < 1 << 26
     assert size(1 << 20, 1 << 10, 64, 1, 256, 1 << 31) < 1 << 26
+
+
+@pytest.mark.parametrize("sizes", [(1, 65536, 65536, 1, 128, 100), (4, 1 << 20, 65536, 1, 64, 4096), (1, 65536, 32768, 1, 64, 100),
+                                   (64, 1 << 20, 65536, 3, 64, 100), (1 << 20, 1 << 20, 65536, 65536, 64, 1 << 31), (1, 1, 8, 8, 128, 1 << 62),
+                                   ((1 << 20) + 1, 1, 8, 8, 128, 100)])
+def test_attention_workspace_of_sizes_that_are_refused(sizes):
+    """Products of sizes past 31 and 64 bits: the status word's bytes, in a process of its own, which must not end."""
+    call = f"import nvfp4_bit_precision_b200 as nv; print(nv.nvfp4_kv_attention_workspace_size{sizes})"
+    done = subprocess.run([sys.executable, "-c", call], capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0 and done.stdout.strip() == "256", (done.returncode, done.stdout)
 
 
 def mlp(nv, **kw):
