@@ -373,7 +373,11 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         // (with PANELS `one` holds; without the test here the loop over the steps came out a
         // sixth slower: 32 rows x 5120 x 20480 87 us against 75)
         const int segs = s_run[2], f1 = s_run[1], tile0 = PANELS && one ? f0 : s_run[3];
-        if (f0 >= f1) return;
+        if (f0 >= f1) {
+            // (no rows for this CTA: the kernel behind takes this one's end for that of the one before)
+            if constexpr (FORM == kLateRows) wait_for_previous_kernel();
+            return;
+        }
         const int fe = min(min(f1, f0 - tile0 + segs * tiles), PANELS ? f0 + kPanelTiles : f1);
 
 #pragma unroll 1

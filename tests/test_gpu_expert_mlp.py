@@ -224,3 +224,39 @@ def test_same_results_again(nv):
     for _ in range(3):
         graph.replay()
     assert torch.equal(out, nv.expert_mlp(x, r, up, down, gate))
+
+
+def test_routings_that_change_behind_an_empty_one(nv):
+    """The routing's tensors are written anew as soon as a call that had no rows is behind: neither call sees the
+    other's, eager or captured (a call ends only when all its kernels have)."""
+    import torch
+    rng = np.random.default_rng(6)
+    hidden, ffn, G, tokens = 256, 128, 4, 6
+    up, _ = matrices(rng, G, ffn, hidden)
+    down, _ = matrices(rng, G, hidden, ffn)
+    gate, _ = matrices(rng, G, ffn, hidden)
+    x, base = to_dev(bits(rng, (tokens, hidden))), to_dev(bits(rng, (tokens, hidden)))
+    r = routing(nv, np.stack([rng.permutation(G)[:2] for _ in range(tokens)]), rng.random((tokens, 2)).astype(np.float32), G)
+    none = [torch.full_like(r.expert, -1), r.weight, torch.zeros_like(r.group_offsets), torch.full_like(r.row_index, -1),
+            torch.full_like(r.slot_row, -1)]
+    full = [r.expert, r.weight, r.group_offsets, r.row_index, r.slot_row]
+    want = nv.expert_mlp(x, r, up, down, gate, base)
+    now = [t.clone() for t in none]
+    live = nv.Routing(*now, None)
+    ws = torch.zeros(nv.nvfp4_expert_mlp_workspace_size(2 * tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+
+    def turn():
+        a = nv.expert_mlp(x, live, up, down, gate, base, workspace=ws)
+        torch._foreach_copy_(now, full)
+        b = nv.expert_mlp(x, live, up, down, gate, base, workspace=ws)
+        torch._foreach_copy_(now, none)
+        return a, b
+
+    outs = [turn() for _ in range(100)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs.append(turn())
+    graph.replay()
+    for a, b in outs:
+        assert torch.equal(a, base) and torch.equal(b, want)
+    assert nv.nvfp4_workspace_status(ws) == 0
