@@ -857,7 +857,7 @@ struct JoinArgs {
     const uint2* base;             // NULL = 0
     uint2* out;
     const int32_t* row_index;
-    const int32_t* used;           // routed rows
+    const int32_t* used;           // routed rows: group_offsets[G]
     uint32_t* status;
 };
 
@@ -869,14 +869,15 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
 {
     constexpr int kSlots = 4;  // whose loads are in flight together
     let_next_kernel_start();
+    // rows that the products have written (what lies behind them in the workspace is of no call)
+    const int64_t used = min(max(static_cast<int64_t>(__ldcg(a.used)), int64_t{0}), a.n_rows);
     if (blockIdx.x == 0) {
         bool bad = false;
-        const int64_t used = min(max(static_cast<int64_t>(__ldcg(a.used)), int64_t{0}), a.n_rows);
         for (int64_t i = threadIdx.x; i < used; i += 256) {
             const int32_t r = __ldcg(a.row_index + i);
             bad |= r < 0 || r >= a.tokens;
         }
-        for (int64_t i = threadIdx.x; i < a.tokens * a.k; i += 256) bad |= __ldcg(a.slot_row + i) >= a.n_rows;
+        for (int64_t i = threadIdx.x; i < a.tokens * a.k; i += 256) bad |= __ldcg(a.slot_row + i) >= used;
         const int any = __syncthreads_or(bad);
         wait_for_previous_kernel();  // (whose call's workspace this is)
         if (threadIdx.x == 0) *a.status = any ? NVFP4_ERR_INDEX : NVFP4_OK;
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinArgs a)
             for (int j = 0; j < kSlots; ++j) {
                 r[j] = j0 + j < a.k ? __ldcg(a.slot_row + t * a.k + j0 + j) : -1;
                 w[j] = j0 + j < a.k ? __ldcg(a.weight + t * a.k + j0 + j) : 0.0f;
-                if (r[j] >= a.n_rows) r[j] = -1;
+                if (r[j] >= used) r[j] = -1;
             }
             wait_for_previous_kernel();
 #pragma unroll

@@ -260,3 +260,31 @@ def test_routings_that_change_behind_an_empty_one(nv):
     for a, b in outs:
         assert torch.equal(a, base) and torch.equal(b, want)
     assert nv.nvfp4_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_slots_behind_the_routed_rows(nv, gated):
+    """A slot that names a row behind group_offsets[G], which no product writes, is left out and reported, whatever
+    the workspace held there."""
+    import torch
+    rng = np.random.default_rng(7)
+    hidden, ffn, G, tokens = 256, 128, 3, 9
+    up, _ = matrices(rng, G, ffn, hidden)
+    down, _ = matrices(rng, G, hidden, ffn)
+    gate = matrices(rng, G, ffn, hidden)[0] if gated else None
+    x, base = to_dev(bits(rng, (tokens, hidden))), to_dev(bits(rng, (tokens, hidden)))
+    ids = np.stack([rng.permutation(G)[:2] for _ in range(tokens)])
+    ids[4], ids[7, 1] = -1, -1                                  # three slots without an expert: 15 routed rows of 18
+    r = routing(nv, ids, rng.random((tokens, 2)).astype(np.float32), G)
+    size = nv.nvfp4_expert_mlp_workspace_size(2 * tokens, hidden, ffn)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = nv.expert_mlp(x, r, up, down, gate, base, workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 0 and int(r.group_offsets[-1]) == 15
+    for row in (15, 17):
+        slots = r.slot_row.clone()
+        slots[4, 0] = slots[7, 1] = row
+        for left in (0x00, 0x3F, 0xFF):
+            ws.fill_(left)
+            got = nv.expert_mlp(x, nv.Routing(r.expert, r.weight, r.group_offsets, r.row_index, slots, None), up, down, gate, base, workspace=ws)
+            assert nv.nvfp4_workspace_status(ws) == 8
+            assert torch.equal(got, want)
