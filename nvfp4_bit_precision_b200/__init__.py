@@ -736,6 +736,13 @@ def _bytes(name: str, t, least: int) -> None:
         raise ValueError(f"{name}: at least {least} contiguous bytes expected, got {t.dtype} {tuple(t.shape)}")
 
 
+def _scratch(name: str, workspace):
+    """Address and bytes of a caller's workspace (an expanded one has fewer than its elements say)."""
+    if not workspace.is_contiguous():
+        raise ValueError(f"{name}: contiguous workspace expected, got strides {workspace.stride()}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _on(stream):
     if isinstance(stream, int):  # (ExternalStream(0) would be a new stream, not the default one)
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
@@ -811,7 +818,8 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, work
         if workspace is None:
             workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_size(rows, cols), dtype=torch.uint8,
                                     device=dev)
-        dwp, wp, nb = dw.data_ptr(), workspace.data_ptr(), workspace.numel()
+        dwp = dw.data_ptr()
+        wp, nb = _scratch("rmsnorm_backward", workspace)
     _check(_lib.nvfp4_rmsnorm_backward(dy.data_ptr(), ldy, h.data_ptr(), ldh,
                                        dh.data_ptr() if dh is not None else None, lddh, weight.data_ptr(), wdt,
                                        rstd.data_ptr(), rows, cols, dx.data_ptr(), cols, dwp, wp, nb,
@@ -858,7 +866,7 @@ def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: 
         if n > 256:
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     if workspace is not None:
-        wp, n = workspace.data_ptr(), workspace.numel()
+        wp, n = _scratch("route", workspace)
     _check(_lib.nvfp4_route(logits.data_ptr(), dt, ld, bias.data_ptr() if bias is not None else None, tokens,
                             experts, ctypes.byref(p), r.expert.data_ptr(), r.weight.data_ptr(),
                             r.group_offsets.data_ptr(), r.row_index.data_ptr(), r.slot_row.data_ptr(), wp, n,
@@ -908,7 +916,7 @@ def combine(rows, slot_row, weight, base=None, *, workspace=None, stream=None):
         bp = base.data_ptr()
     nb = 0
     if workspace is not None:
-        wp, nb = workspace.data_ptr(), workspace.numel()
+        wp, nb = _scratch("combine", workspace)
     out = _matrix(dev, torch.bfloat16, tokens, cols)
     _check(_lib.nvfp4_combine(rows.data_ptr(), dt, n, cols, slot_row.data_ptr(), weight.data_ptr(), tokens, k,
                               bp, out.data_ptr(), wp, nb, _raw_stream(dev)), "nvfp4_combine")
@@ -936,7 +944,7 @@ def combine_backward(dout, rows, slot_row, weight, group_offsets=None, *, worksp
     dweight = _matrix(dev, torch.float32, tokens, k)
     wp, nb = None, 0
     if workspace is not None:
-        wp, nb = workspace.data_ptr(), workspace.numel()
+        wp, nb = _scratch("combine_backward", workspace)
     _check(_lib.nvfp4_combine_backward(dout.data_ptr(), rows.data_ptr(), dt, n, cols, slot_row.data_ptr(),
                                        weight.data_ptr(), tokens, k, used, drows.data_ptr(), dweight.data_ptr(),
                                        wp, nb, _raw_stream(dev)), "nvfp4_combine_backward")
@@ -995,7 +1003,7 @@ def grouped_gemv(group_offsets, x, qb, sfb, gb, N: int, row_index=None, out_dtyp
         _flat("grouped_gemv: row_index", row_index, torch.int32, rows)
         ip = row_index.data_ptr()
     if workspace is not None:
-        wp, nb = workspace.data_ptr(), workspace.numel()
+        wp, nb = _scratch("grouped_gemv", workspace)
     out, ldd = _gemv_out("grouped_gemv", out_dtype, rows, N, out, dev)
     _check(_lib.nvfp4_grouped_gemv(G, group_offsets.data_ptr(), rows, x.data_ptr(), ldx, src, ip,
                                    qb.data_ptr(), sfb.data_ptr(), gb.data_ptr(), N, K, out_dtype,
@@ -1042,12 +1050,12 @@ def expert_mlp(x, routing: Routing, up, down, gate=None, base=None, *, workspace
         bp = base.data_ptr()
     if workspace is None:
         workspace = torch.empty(nvfp4_expert_mlp_workspace_size(rows, hidden, ffn), dtype=torch.uint8, device=dev)
+    wp, nb = _scratch("expert_mlp", workspace)
     out = _matrix(dev, torch.bfloat16, tokens, hidden)
     _check(_lib.nvfp4_expert_mlp(G, offsets.data_ptr(), rows, x.data_ptr(), ldx, tokens, row_index.data_ptr(), gp, gsp,
                                  ggp, uq.data_ptr(), us.data_ptr(), ug.data_ptr(), dq.data_ptr(), ds.data_ptr(),
                                  dg.data_ptr(), hidden, ffn, slot_row.data_ptr(), weight.data_ptr(), k, bp,
-                                 out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
-           "nvfp4_expert_mlp")
+                                 out.data_ptr(), wp, nb, _raw_stream(dev)), "nvfp4_expert_mlp")
     return out
 
 
@@ -1195,7 +1203,7 @@ def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None,
     elif q_out is not None:
         raise ValueError("kv_append: q_out without q")
     if workspace is not None:
-        wp, nb = workspace.data_ptr(), workspace.numel()
+        wp, nb = _scratch("kv_append", workspace)
     _check(_lib.nvfp4_kv_append(ctypes.byref(view), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, tokens,
                                 table.data_ptr(), ldt, sequences, pages, position.data_ptr(), sp, cp, np, angles, rot,
                                 1 if interleaved else 0, qp, ldq, hsq, heads, op, ldo, hso, wp, nb,
@@ -1231,14 +1239,14 @@ def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = 
     if workspace is None:
         workspace = torch.empty(_attention_bytes(n, new, heads, view.kv_heads, dim, pages * view.page_size),
                                 dtype=torch.uint8, device=dev)
+    wp, nb = _scratch("kv_attention", workspace)
     out = torch.empty_strided(shape, (new * heads * dim, heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
     sums = torch.empty((n, new, heads), dtype=torch.float32, device=dev) if lse else None
     # (strides over a single sequence, token or head are never used, and torch leaves them arbitrary)
     _check(_lib.nvfp4_kv_attention(q.data_ptr(), ldb if n > 1 else 0, ldi if new > 1 else 0, ldh if heads > 1 else dim, n,
                                    new, heads, ctypes.byref(view), table.data_ptr(), ldt, pages, lengths.data_ptr(),
                                    dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                                   sums.data_ptr() if lse else None, workspace.data_ptr(), workspace.numel(),
-                                   _raw_stream(dev)), "nvfp4_kv_attention")
+                                   sums.data_ptr() if lse else None, wp, nb, _raw_stream(dev)), "nvfp4_kv_attention")
     return (out, sums) if lse else out
 
 

@@ -155,3 +155,32 @@ def test_wrappers_refuse(nv):
     w = nv.NVFP4Tensor(place, place, place, 1, 1, 0)
     with pytest.raises(ValueError, match="CUDA"):
         nv.expert_mlp(x[:, 0], r, w, w)
+
+
+def test_wrappers_refuse_workspaces_that_are_not_contiguous(nv, monkeypatch):
+    """A byte expanded to the size asked for: its elements are counted, but there is one."""
+    monkeypatch.setattr(nv, "_one_device", lambda name, *t: t[0].device)
+    monkeypatch.setattr(nv, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    c = nv.kv_cache(2, 2, 16, 64, device="cpu")
+    kv, table, place = z(3, 2, 64), z(3, 2, dtype=i32), z(3, dtype=i32)
+    w = nv.NVFP4Tensor(z(2, 128, 64, dtype=u8), z(2 * 128 * 8, dtype=u8), z(2, dtype=f32), 128, 128, nv.NVFP4_SF_MMA)
+    w.n = 128
+    x, off, slots, weight = z(3, 128), z(3, dtype=i32), z(3, 1, dtype=i32), z(3, 1, dtype=f32)
+    r = nv.Routing(slots, weight, off, place, slots, None)
+    calls = [lambda ws: nv.kv_append(c, kv, kv, table, place, workspace=ws),
+             lambda ws: nv.kv_attention(kv[:, None], c, table, place, workspace=ws),
+             lambda ws: nv.expert_mlp(x, r, w, w, workspace=ws),
+             lambda ws: nv.grouped_gemv(off, x, w.q, w.sf, w.g, 128, workspace=ws),
+             lambda ws: nv.combine(x, slots, weight, workspace=ws),
+             lambda ws: nv.combine_backward(x, x, slots, weight, off, workspace=ws),
+             lambda ws: nv.route(z(3, 2, dtype=f32), 1, workspace=ws),
+             lambda ws: nv.rmsnorm_backward(x, x, z(128), z(3, dtype=f32), workspace=ws)]
+    for call in calls:
+        for ws in (z(1, dtype=u8).expand(1 << 24), z(1 << 12, dtype=u8)[::2]):
+            with pytest.raises(ValueError, match="contiguous workspace"):
+                call(ws)
+        with pytest.raises(nv.NVFP4Error, match="no sm_100|unsupported|CUDA"):  # (every check passed: no device)
+            call(z(1 << 24, dtype=u8))
