@@ -258,9 +258,9 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void*
     if (tokens < 0 || tokens > 0x7fffffffll || sequences < 0 || sequences > 0x7fffffffll || table_pages < 0 ||
         table_pages > 0x7fffffffll || ldt < table_pages || heads < 0 || heads > 32768 || angles < 0)
         return NVFP4_ERR_SHAPE;
-    if ((neighbours != 0 && neighbours != 1) || !cos != !sin || (!q_bf16) != (!q_out) || (heads > 0) != (q_bf16 != nullptr) ||
-        (heads > 0 && !cos))
-        return NVFP4_ERR_INVALID_ARG;
+    if ((neighbours != 0 && neighbours != 1) || !cos != !sin || (heads > 0 && !cos)) return NVFP4_ERR_INVALID_ARG;
+    // (tensors without a token may have no address)
+    if (tokens > 0 && ((!q_bf16) != (!q_out) || (heads > 0) != (q_bf16 != nullptr))) return NVFP4_ERR_INVALID_ARG;
     if (cos ? rot < 32 || rot > dim || rot % 32 : rot != 0) return NVFP4_ERR_SHAPE;
     if (tokens > 0 && (!k_bf16 || !v_bf16 || !table || !position || sequences < 1 || table_pages < 1))
         return NVFP4_ERR_INVALID_ARG;

@@ -67,6 +67,13 @@ def test_append_accepts(nv):
         assert append(nv, **change) in PAST
 
 
+def test_append_accepts_no_tokens(nv):
+    """Tensors without a token have no address, those of the queries among them."""
+    none = dict(tokens=0, k=None, v=None, position=None, q=None, qo=None)
+    for change in (none, dict(none, heads=0), dict(none, heads=0, cos=None, sin=None, rot=0), dict(none, sequence=None, sequences=0, table=None)):
+        assert append(nv, **change) in PAST
+
+
 def attend(nv, **kw):
     c = view(nv, kw)
     a = dict(q=FAKE, ldb=1024, ldi=512, ldh=128, sequences=3, queries=2, heads=4)

@@ -234,6 +234,18 @@ def test_nothing_to_append(nv):
     assert not cache.q.any()
 
 
+def test_no_tokens_with_queries(nv):
+    """An empty batch is one like any other: queries without a token come back as they are."""
+    import torch
+    cache = nv.kv_cache(1, 2, 16, 64)
+    cos, sin = (dev(a) for a in K.tables(64, 4))
+    k, q = (torch.empty((0, n, 64), dtype=torch.bfloat16, device="cuda") for n in (2, 8))
+    for out in (None, q):
+        got = nv.kv_append(cache, k, k, i32([[0]]), i32([]), i32([]), cos=cos, sin=sin, q=q, q_out=out)
+        assert got.shape == (0, 8, 64)
+    assert not cache.q.any()
+
+
 def test_offsets_past_32_bits(nv):
     """A cache of 5 GiB of keys' codes: its last page, and the values' behind it."""
     import torch
