@@ -636,7 +636,7 @@ typedef struct {
  * pairs (x[i], x[i + rot / 2]), or with neighbours = 1 (x[2 i], x[2 i + 1]), exact
  * up to one rounding to bf16; the keys are then quantised as nvfp4_quantize does it.
  * q [tokens][heads][dim] is turned likewise into q_out (which may be q, at the same
- * strides); heads = 0 and NULL without queries.  Without cos, rot = 0.
+ * strides), whose heads do not overlap; heads = 0 and NULL without queries.  Without cos, rot = 0.
  * A token with a negative position or sequence is left out, its row of q_out as it
  * was.  One whose sequence, place or page does not exist, or whose position is not
  * below angles, is left out and reported in the optional workspace's status word
