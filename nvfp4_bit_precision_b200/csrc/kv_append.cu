@@ -269,13 +269,13 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void*
     if (!strides_ok(ldk, hsk, kv) || !strides_ok(ldv, hsv, kv) ||
         (q_bf16 && (!strides_ok(ldq, hsq, heads) || (tokens > 1 && ldo < dim) || (heads > 1 && hso < dim))))
         return NVFP4_ERR_SHAPE;
-    // the heads that are written lie apart: a token's within its stride, or the tokens of a head within the heads'
-    if (q_bf16 && tokens > 1 && heads > 1 && (ldo - dim) / (heads - 1) < hso && (hso - dim) / (tokens - 1) < ldo)
-        return NVFP4_ERR_SHAPE;
     if (off16(k_bf16) || off16(v_bf16) || off16(q_bf16) || off16(q_out) || off16(cos) || off16(sin) || ldk % 8 || hsk % 8 ||
         ldv % 8 || hsv % 8 || (q_bf16 && (ldq % 8 || hsq % 8 || ldo % 8 || hso % 8)) ||
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(position) | reinterpret_cast<uintptr_t>(sequence)) & 3u))
         return NVFP4_ERR_ALIGN;
+    // the heads that are written lie apart: a token's within its stride, or the tokens of a head within the heads'
+    if (q_bf16 && tokens > 1 && heads > 1 && (ldo - dim) / (heads - 1) < hso && (hso - dim) / (tokens - 1) < ldo)
+        return NVFP4_ERR_SHAPE;
     if (workspace && (ws_bytes < 16 || off16(workspace))) return NVFP4_ERR_WORKSPACE;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;

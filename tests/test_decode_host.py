@@ -64,7 +64,7 @@ def test_append_argument_errors(nv, change, status):
 def test_append_refuses_heads_that_overlap(nv):
     """Turned queries are written: each head has its own place, token by token or head by head."""
     for ldo, hso, status in ((128, 128, SHAPE), (256, 128, SHAPE), (504, 128, SHAPE), (128, 256, SHAPE), (128, 376, SHAPE), (512, 128, PAST),
-                             (128, 384, PAST), (1024, 136, PAST), (1 << 40, 1 << 20, PAST), (1 << 62, 1 << 62, SHAPE)):
+                             (128, 384, PAST), (1024, 136, PAST), (512, 136, SHAPE), (1 << 40, 1 << 20, PAST), (1 << 62, 1 << 62, SHAPE)):
         assert append(nv, ldo=ldo, hso=hso) in (status if status is PAST else (status,)), (ldo, hso)
     assert append(nv, ldo=0, hso=128, tokens=1) in PAST and append(nv, ldo=128, hso=0, heads=1) in PAST
 
