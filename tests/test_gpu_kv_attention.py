@@ -287,3 +287,160 @@ def test_same_results_again(nv):
     lengths.fill_(700)
     graph.replay()
     assert torch.equal(out, nv.kv_attention(qd, cache, table, lengths))
+
+
+# ------------------------------------------------------------------------------------------ wide tables
+def kernels_of(call):
+    """The (mangled) names of the kernels that a call launches, from its captured graph."""
+    import os
+    import tempfile
+    import warnings
+    import torch
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    graph.enable_debug_mode()
+    with torch.cuda.graph(graph):
+        call()
+    with tempfile.TemporaryDirectory() as d, warnings.catch_warnings():
+        warnings.simplefilter("ignore")  # (torch announces the dump as one)
+        graph.debug_dump(os.path.join(d, "graph.dot"))
+        with open(os.path.join(d, "graph.dot")) as f:
+            return f.read()
+
+
+def widened(table, lengths, page, tokens):
+    """The table as wide as `tokens` tokens, with no page behind a sequence's last."""
+    wide = np.full((len(lengths), tokens // page), -1, dtype=np.int64)
+    for s, n in enumerate(lengths):
+        m = -(-int(n) // page)
+        wide[s, :m] = table[s, :m]
+    return wide
+
+
+WIDE = 1 << 20  # tokens of a table that a serving program allocates for its longest context
+
+
+@pytest.mark.parametrize("dim,step", [(64, 64), (128, 64), (256, 32)])
+def test_steps_go_by_the_tables_width(nv, dim, step):
+    """Narrow tables take steps of 32 tokens, wide ones of 64 for heads of up to 128: the tests below run what they say."""
+    import torch
+    cache = nv.kv_cache(4, 2, 16, dim)
+    q = torch.zeros((3, 1, 4, dim), dtype=torch.bfloat16, device="cuda")
+    names = []
+    for table in (np.zeros((3, 4)), np.zeros((3, WIDE // 16))):
+        args = (q, cache, i32(table), i32([5, 0, 64]))
+        nv.kv_attention(*args)
+        names.append(kernels_of(lambda: nv.kv_attention(*args)))  # noqa: B023
+    for text, want in zip(names, (32, step)):
+        assert f"attend_kernelILi{dim}ELi{want}E" in text, text[:2000]
+
+
+@pytest.mark.parametrize("dim,kv,group", [(128, 2, 4), (128, 1, 17), (128, 3, 1), (64, 3, 2), (64, 1, 9), (256, 2, 3)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 1024])
+@pytest.mark.parametrize("new,window", [(1, 0), (3, 0), (1, 50), (4, 33), (6, 64)])
+def test_ragged_in_a_wide_table(nv, dim, kv, group, page, new, window):
+    rng = np.random.default_rng(dim + 7 * kv + group + page + new + window)
+    lengths = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 300, 517]
+    most = -(-517 // page)
+    pages = len(lengths) * most + 2
+    cache, q, sf = filled(nv, rng, pages, kv, page, dim)
+    table = rng.permutation(pages)[:len(lengths) * most].reshape(len(lengths), most)
+    check(nv, cache, q, sf, bits(rng, (len(lengths), new, kv * group, dim), 1.5), table, lengths, page, window,
+          td=i32(widened(table, lengths, page, WIDE)))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,lengths", [(1, [9000]), (3, [20000, 1, 700]), (200, None)])
+def test_cut_lengths_in_a_wide_table(nv, dim, n, lengths):
+    rng = np.random.default_rng(n + dim)
+    kv, page = 2, 64
+    lengths = lengths or list(rng.integers(0, 400, n))
+    most = -(-max(lengths) // page)
+    cache, q, sf = filled(nv, rng, n * most, kv, page, dim)
+    table = rng.permutation(n * most).reshape(n, most)
+    check(nv, cache, q, sf, bits(rng, (n, 1, 6, dim), 2.0), table, [int(x) for x in lengths], page,
+          td=i32(widened(table, lengths, page, 1 << 18 if n > 3 else WIDE * 8)))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_masked_tokens_do_not_matter_in_a_wide_table(nv, dim, page):
+    """NaN scales behind the end of a sequence, in pages of others, before the window and among the later of the query
+    tokens, in steps of 64 tokens."""
+    import torch
+    rng = np.random.default_rng(dim + page)
+    kv, new, n = 2, 3, 200
+    most = -(-n // page)
+    cache, q, sf = filled(nv, rng, 2 * most, kv, page, dim)
+    own = rng.permutation(2 * most)[:most]
+    others = np.setdiff1d(np.arange(2 * most), own)
+    table = i32(widened(own[None], [n], page, WIDE * 8))
+    qd = to_dev(bits(rng, (1, new, 2 * kv, dim)))
+
+    def spoil(c, which, token, head=slice(None), block=slice(None), byte=0x7F):
+        c.sf[which, int(own[token // page]), head, token % page, block] = byte
+
+    for window in (0, 70):
+        want, wl = nv.kv_attention(qd, cache, table, i32([n]), window=window, lse=True)
+        bad = nv.KVCache(cache.q.clone(), cache.sf.clone(), cache.amax, cache.g)
+        for w in (0, 1):
+            bad.sf[w, others] = 0xFF
+            for token in range(n, most * page):
+                spoil(bad, w, token)
+            for token in range(n - 2 - window if window else 0):
+                spoil(bad, w, token)
+        got, gl = nv.kv_attention(qd, bad, table, i32([n]), window=window, lse=True)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        # the last token, seen by the last query alone: one block of its value
+        spoil(bad, 1, n - 1, 0, 1)
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.equal(got[:, :2], want[:, :2]) and torch.equal(got[:, 2, 2:], want[:, 2, 2:])
+        nan = torch.isnan(got[0, 2, :2].float())
+        assert nan[:, 16:32].all() and not nan[:, :16].any() and not nan[:, 32:].any()
+        # its key in the other head: the whole row
+        spoil(bad, 1, n - 1, 0, 1, 1)
+        spoil(bad, 0, n - 1, 1, 0)
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.equal(got[:, :2], want[:, :2]) and torch.isnan(got[0, 2, 2:].float()).all()
+        # a value that all see
+        spoil(bad, 0, n - 1, 1, 0, 1)
+        spoil(bad, 1, n - 10, 0, 0)
+        got = nv.kv_attention(qd, bad, table, i32([n]), window=window)
+        assert torch.isnan(got[0, :, :2, :16].float()).all() and not torch.isnan(got[0, :, 2:].float()).any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_bad_pages_in_a_wide_table(nv, dim, page):
+    """A page outside the cache counts as zeros, wherever it lies in a step of 64 tokens, and is reported."""
+    import torch
+    rng = np.random.default_rng(dim + page)
+    n = 400
+    most = -(-n // page)
+    cache, q, sf = filled(nv, rng, most, 1, page, dim)
+    zero = nv.KVCache(torch.cat([cache.q, torch.zeros_like(cache.q[:, :1])], 1), torch.cat([cache.sf, torch.zeros_like(cache.sf[:, :1])], 1),
+                      cache.amax, cache.g)
+    qd = to_dev(bits(rng, (1, 1, 4, dim)))
+    own = rng.permutation(most)
+    ws = torch.zeros(nv.nvfp4_kv_attention_workspace_size(1, 1, 4, 1, dim, WIDE * 8), dtype=torch.uint8, device="cuda")
+    for at in ([0], [most - 1], [most // 2], list(range(0, most, 2)), list(range(most))):
+        entry = lambda x: i32(widened(np.where(np.isin(np.arange(most), at), x, own)[None], [n], page, WIDE * 8))  # noqa: B023, E731
+        want = nv.kv_attention(qd, zero, entry(most), i32([n]), workspace=ws)
+        assert nv.nvfp4_workspace_status(ws) == 0
+        for bad in (-1, most, 2 ** 31 - 1):
+            got = nv.kv_attention(qd, cache, entry(bad), i32([n]), workspace=ws)
+            assert nv.nvfp4_workspace_status(ws) == 8
+            assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------------------------------ many queries
+@pytest.mark.parametrize("dim,kv,group,page", [(64, 1, 2, 16), (128, 2, 1, 64), (256, 1, 3, 32)])
+@pytest.mark.parametrize("new,window", [(33, 0), (128, 0), (128, 40), (1000, 0), (1000, 77)])
+def test_a_prompts_queries(nv, dim, kv, group, page, new, window):
+    """More queries than a block has rows: of a sequence that is longer, as long, and (its first queries see nothing)
+    shorter."""
+    rng = np.random.default_rng(dim + new + window)
+    lengths = [new + 77, new, new // 2 + 1, 0]
+    most = -(-lengths[0] // page)
+    cache, q, sf = filled(nv, rng, 4 * most, kv, page, dim)
+    table = rng.permutation(4 * most).reshape(4, most)
+    check(nv, cache, q, sf, bits(rng, (4, new, kv * group, dim), 1.5), table, lengths, page, window)
