@@ -264,3 +264,96 @@ def test_offsets_past_32_bits(nv):
     q = to_dev(bits(rng, (1, 2, 16, dim)))
     a, b = (nv.kv_attention(q, c, i32([[p]]), i32([page - 3])) for c, p in ((cache, pages - 1), (small, 0)))
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dim,page,kv,heads,rot,neighbours,tokens", [
+    (64, 16, 4, 16, 32, True, 3003), (64, 64, 3, 7, 64, False, 20000), (128, 64, 5, 0, 0, False, 9000), (128, 128, 2, 3, 64, True, 6000),
+    (256, 32, 2, 6, 256, True, 2600), (256, 32, 2, 5, 32, False, 5000)])
+def test_many_tokens(nv, dim, page, kv, heads, rot, neighbours, tokens):
+    """Several heads a thread, most of them not a divisor of all heads: ragged prompts, their tokens in any order and some
+    left out, the queries turned in place in a piece of the projection's output."""
+    import torch
+    rng = np.random.default_rng(dim + kv + heads + tokens)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert tokens * (heads + 2 * kv) * (dim // 16) >= 2 * 768 * sms  # (a thread for each head would be more than are at once)
+    n = 7
+    counts = rng.multinomial(tokens, np.full(n, 1 / n))
+    starts = rng.integers(0, 40, n)
+    sequence = np.repeat(np.arange(n), counts)
+    position = np.concatenate([np.arange(s, s + c) for s, c in zip(starts, counts)])
+    order = rng.permutation(tokens)
+    sequence, position = sequence[order], position[order]
+    position[5::97], sequence[9::101] = -1, -2
+    most = -(-int((starts + counts).max()) // page)
+    table = rng.permutation(n * most + 1)[:n * most].reshape(n, most)
+    cache = random_cache(nv, rng, n * most + 1, kv, page, dim)
+    cq, csf = host(cache.q).copy(), host(cache.sf).copy()
+    qkv = bits(rng, (tokens, heads + 2 * kv, dim), 2.0)
+    d = to_dev(qkv)
+    q, k, v = d[:, :heads], d[:, heads:heads + kv], d[:, heads + kv:]
+    cos, sin = K.tables(rot, most * page) if rot else (None, None)
+    ws = cache.q.new_zeros(256)
+    got = nv.kv_append(cache, k, v, i32(table), i32(position), i32(sequence), cos=dev(cos) if rot else None, sin=dev(sin) if rot else None,
+                       interleaved=neighbours, q=q if heads else None, q_out=q if heads else None, workspace=ws)
+    assert nv.nvfp4_workspace_status(ws) == 0
+    there = (position >= 0) & (sequence >= 0)
+    at = np.maximum(position, 0)
+    want = qkv.copy()
+    if rot:
+        want[there] = K.turn(qkv[there], cos, sin, at[there], rot, neighbours)
+    p, s = position[there], sequence[there]
+    pages, slots = table[s, p // page], p % page
+    for which, b in ((0, want[there, heads:heads + kv]), (1, qkv[there, heads + kv:])):
+        codes, scales = K.quantise(W.bf16_bits_to_f32(b), host(cache.amax)[which])
+        cq[which][pages, :, slots], csf[which][pages, :, slots] = codes, scales
+    np.testing.assert_array_equal(host(cache.q), cq)
+    np.testing.assert_array_equal(host(cache.sf), csf)
+    if heads:
+        assert got is q
+        np.testing.assert_array_equal(host(d)[:, :heads], want[:, :heads])
+    np.testing.assert_array_equal(host(d)[:, heads:], qkv[:, heads:])
+
+
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_non_finite_numbers_stay_in_their_blocks(nv, neighbours):
+    """What is not finite spoils the blocks of its own pair and no other byte, and no other pair of the queries."""
+    rng = np.random.default_rng(8)
+    dim, page, kv, heads, n = 64, 16, 2, 3, 6
+    cos, sin = (dev(a) for a in K.tables(dim, 16))
+    good = bits(rng, (n, heads + 2 * kv, dim))
+    one, two = (18, 19) if neighbours else (18, 18 + dim // 2)  # a pair's places
+    for bad in (0x7F80, 0xFF80, 0x7FC0):
+        qkv = good.copy()
+        for h in (1, heads + 1, heads + kv):                    # of token 2: a query, a key, a value
+            qkv[2, h, 18] = bad
+        held, turned = [], []
+        for x in (good, qkv):
+            c = nv.kv_cache(1, kv, page, dim, 4.0, 4.0)
+            d = to_dev(x)
+            turned.append(host(nv.kv_append(c, d[:, heads:heads + kv], d[:, heads + kv:], i32([[0]]), i32(np.arange(n)), i32(np.zeros(n)),
+                                            cos=cos, sin=sin, interleaved=neighbours, q=d[:, :heads])))
+            held.append((host(c.q)[:, 0].reshape(2, kv, page, dim // 16, 8), host(c.sf)[:, 0].copy()))
+        same = np.ones((2, kv, page, dim // 16), bool)
+        same[0, 1, 2, [one // 16, two // 16]] = same[1, 0, 2, 18 // 16] = False
+        np.testing.assert_array_equal(held[1][0][same], held[0][0][same])
+        np.testing.assert_array_equal(held[1][1][same], held[0][1][same])
+        same = np.ones((n, heads, dim), bool)
+        same[2, 1, [one, two]] = False
+        np.testing.assert_array_equal(turned[1][same], turned[0][same])
+        assert not np.isfinite(W.bf16_bits_to_f32(turned[1][~same])).any()
+
+
+@pytest.mark.parametrize("rows,cols", [(30011, 112), (5, 16), (1001, 2416)])
+def test_read_back(nv, rows, cols):
+    """Row-major NVFP4 bytes of any kind in both output types; the largest with several steps a thread and a last one that
+    is not full."""
+    import torch
+    rng = np.random.default_rng(rows)
+    q = rng.integers(0, 256, (rows, cols // 2), dtype=np.uint8)
+    sf = rng.integers(0, 256, (rows, cols // 16), dtype=np.uint8)
+    sf[(sf & 127) == 127] = 5
+    g = np.float32(0.0123)
+    t = nv.NVFP4Tensor(dev(q), dev(sf), torch.tensor([g], device="cuda"), rows, cols, nv.NVFP4_SF_ROWMAJOR)
+    want = K.decode(q, sf, 1.0).astype(np.float32) * g  # (the first product has six bits, the second is rounded once)
+    np.testing.assert_array_equal(host(nv.dequantize(t)), want)
+    np.testing.assert_array_equal(host(nv.dequantize(t, nv.NVFP4_OUT_BF16)), W.f32_to_bf16_bits(want))
