@@ -288,3 +288,47 @@ def test_slots_behind_the_routed_rows(nv, gated):
             got = nv.expert_mlp(x, nv.Routing(r.expert, r.weight, r.group_offsets, r.row_index, slots, None), up, down, gate, base, workspace=ws)
             assert nv.nvfp4_workspace_status(ws) == 8
             assert torch.equal(got, want)
+
+
+def reference_by_expert(x, ids, weight, up, down, gate, base):
+    """``reference``, all rows of an expert at once (its bounds are those of each row)."""
+    out = base.copy()
+    err, mags = np.zeros_like(out), np.abs(out)
+    for e in range(len(up)):
+        t, j = np.nonzero(ids == e)
+        if not t.size:
+            continue
+        u, du = products(x[t], up[e])
+        if gate is not None:
+            z, dz = products(x[t], gate[e])
+            s = z / (1 + np.exp(-z))
+            h, dh = s * u, np.abs(s) * du + 1.1 * dz * (np.abs(u) + du) + 2.0 ** -20 * np.abs(s * u)
+        else:
+            p = np.maximum(u, 0)
+            h, dh = p * p, 2 * p * du + du * du + 2.0 ** -23 * p * p
+        dh = dh + 2.0 ** -8 * (np.abs(h) + dh)
+        y, dy = products(h, down[e])
+        dy = dy + dh @ np.abs(down[e]).T * (1 + 2.0 ** -12)
+        w = weight[t, j][:, None].astype(np.float64)
+        np.add.at(out, t, w * y)
+        np.add.at(err, t, np.abs(w) * dy)
+        np.add.at(mags, t, np.abs(w * y))
+    return out, err + (ids.shape[1] + 2) * 2.0 ** -24 * mags + 2.0 ** -8 * np.abs(out) + 2.0 ** -7 * err
+
+
+@pytest.mark.parametrize("tokens,top_k,G,hidden,ffn", [(96, 2, 12, 640, 4096), (40, 1, 6, 1024, 6272), (16, 8, 128, 256, 128), (5, 8, 256, 128, 256),
+                                                       (200, 2, 256, 128, 128)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_wide_experts_and_many(nv, tokens, top_k, G, hidden, ffn, gated):
+    """Down products of which a CTA's segments do not fit at once (rows of h of 8 and 12 KB); as many experts as are
+    taken, most of them without a row."""
+    from nvfp4_bit_precision_b200 import moe
+    rng = np.random.default_rng(tokens + G + hidden + ffn)
+    up, upw = matrices(rng, G, ffn, hidden)
+    down, downw = matrices(rng, G, hidden, ffn)
+    gate, gatew = matrices(rng, G, ffn, hidden) if gated else (None, None)
+    ids = np.stack([rng.permutation(G)[:top_k] for _ in range(tokens)])
+    weight = rng.random((tokens, top_k)).astype(np.float32) - np.float32(0.2)
+    x, base = bits(rng, (tokens, hidden)), bits(rng, (tokens, hidden))
+    got = moe.expert_mlp(to_dev(x), routing(nv, ids, weight, G), up, down, gate, to_dev(base))
+    compare(got, *reference_by_expert(val(x), ids, weight, upw, downw, gatew, val(base)))
