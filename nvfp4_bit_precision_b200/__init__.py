@@ -528,8 +528,8 @@ def quantize(x, *, rowwise: bool = True, colwise: bool = False, rounding: int = 
         p.mx_q_col, p.mx_sf_col = mq.data_ptr(), me.data_ptr()
         out["mx_col"] = (mq, me)
     ws = workspace if workspace is not None else _workspace(dev)
-    nvfp4_quantize(x, n_rows, cols, ld, p, q_row, sf_row, g_row, q_col, sf_col, g_col, ws,
-                   ws.numel(), stream)
+    nvfp4_quantize(x, n_rows, cols, ld, p, q_row, sf_row, g_row, q_col, sf_col, g_col,
+                   *_scratch("quantize", ws), stream)
     out["workspace"] = ws
     return out
 
@@ -583,7 +583,7 @@ def mx4_gemm(qa, sfa, qb, sfb, out_dtype: int = NVFP4_OUT_BF16, out=None, amax_o
     dt = torch.bfloat16 if out_dtype == NVFP4_OUT_BF16 else torch.float32
     D = out if out is not None else torch.empty((M, N), dtype=dt, device=qa.device)
     ws = workspace if workspace is not None else _workspace(qa.device)
-    mxfp4_gemm(qa, sfa, qb, sfb, M, N, K, out_dtype, D, D.stride(0), amax_out, ws, ws.numel(),
+    mxfp4_gemm(qa, sfa, qb, sfb, M, N, K, out_dtype, D, D.stride(0), amax_out, *_scratch("mx4_gemm", ws),
                stream)
     return D
 
@@ -609,7 +609,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype: int = NVFP4_OUT_BF16, out=No
         out = torch.empty((M, N), dtype=dt, device=a.q.device)
     ws = workspace if workspace is not None else _workspace(a.q.device)
     nvfp4_gemm(a.q, a.sf, a.g, b.q, b.sf, b.g, M, N, K, out_dtype, out, out.stride(0), amax_out,
-               ws, ws.numel(), stream)
+               *_scratch("gemm", ws), stream)
     return out
 
 
@@ -623,7 +623,7 @@ def mx_gemm(qa, sfa, qb, sfb, out_dtype: int = NVFP4_OUT_BF16, out=None, amax_ou
     dt = torch.bfloat16 if out_dtype == NVFP4_OUT_BF16 else torch.float32
     D = out if out is not None else torch.empty((M, N), dtype=dt, device=qa.device)
     ws = workspace if workspace is not None else _workspace(qa.device)
-    mxfp8_gemm(qa, sfa, qb, sfb, M, N, K, out_dtype, D, D.stride(0), amax_out, ws, ws.numel(),
+    mxfp8_gemm(qa, sfa, qb, sfb, M, N, K, out_dtype, D, D.stride(0), amax_out, *_scratch("mx_gemm", ws),
                stream)
     return D
 
@@ -638,7 +638,7 @@ def grouped_gemm(group_offsets, a: NVFP4Tensor, qb, sfb, gb, N: int, out_dtype: 
         out = torch.empty((a.rows, N), dtype=dt, device=a.q.device)
     ws = workspace if workspace is not None else _workspace(a.q.device)
     nvfp4_grouped_gemm(G, group_offsets, a.rows, a.q, a.sf, a.g, qb, sfb, gb, N, a.k, out_dtype,
-                       out, amax_out, ws, ws.numel(), stream)
+                       out, amax_out, *_scratch("grouped_gemm", ws), stream)
     return out
 
 
@@ -655,8 +655,8 @@ def gather_rows(t: NVFP4Tensor, row_index, group_offsets=None, workspace=None, s
     n = nvfp4_sf_mma_grouped_bytes(rows, G, t.k) if G else nvfp4_sf_mma_bytes(rows, t.k)
     sf = torch.zeros(n, **u8)
     ws = workspace if workspace is not None else _workspace(t.q.device)
-    nvfp4_gather_rows(t.q, t.sf, t.rows, t.k, row_index, rows, group_offsets, G, q, sf, ws,
-                      ws.numel(), stream)
+    nvfp4_gather_rows(t.q, t.sf, t.rows, t.k, row_index, rows, group_offsets, G, q, sf,
+                      *_scratch("gather_rows", ws), stream)
     return NVFP4Tensor(q, sf, t.g, rows, t.k, NVFP4_SF_MMA)
 
 

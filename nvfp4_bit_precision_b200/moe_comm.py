@@ -90,7 +90,7 @@ def combine_mxfp8(expert_rows, rows_from, plan: ExpertParallelPlan, weight, grou
     expert output), FP32 accumulation in slot order."""
     import torch
     from . import mxfp8_combine as _combine
-    from . import mxfp8_quantize, NVFP4_ROWWISE
+    from . import mxfp8_quantize, NVFP4_ROWWISE, _scratch
     R, H = expert_rows.shape
     dev = expert_rows.device
     u8 = dict(dtype=torch.uint8, device=dev)
@@ -107,8 +107,8 @@ def combine_mxfp8(expert_rows, rows_from, plan: ExpertParallelPlan, weight, grou
     slot_row = torch.from_numpy(plan.slot_row).to(dev)
     w = torch.as_tensor(weight, dtype=torch.float32).to(dev).contiguous()
     ws = workspace if workspace is not None else torch.zeros(256, **u8)
-    _combine(q_back, e8_back, q_back.shape[0], H, slot_row, w, plan.tokens, plan.k, out, ws,
-             ws.numel())
+    _combine(q_back, e8_back, q_back.shape[0], H, slot_row, w, plan.tokens, plan.k, out,
+             *_scratch("combine_mxfp8", ws))
     return out
 
 

@@ -193,6 +193,13 @@ def test_wrappers_refuse_workspaces_that_are_not_contiguous(nv, monkeypatch):
              lambda ws: nv.combine_backward(x, x, slots, weight, off, workspace=ws),
              lambda ws: nv.route(z(3, 2, dtype=f32), 1, workspace=ws),
              lambda ws: nv.rmsnorm_backward(x, x, z(128), z(3, dtype=f32), workspace=ws)]
+    a = nv.NVFP4Tensor(z(128, 64, dtype=u8), z(128 * 8, dtype=u8), z(1, dtype=f32), 128, 128, nv.NVFP4_SF_MMA)
+    codes, e8 = z(128, 128, dtype=u8), z(128 * 4, dtype=u8)
+    calls += [lambda ws: nv.gemm(a, a, workspace=ws, stream=0),
+              lambda ws: nv.grouped_gemm(z(2, dtype=i32), a, a.q[None], a.sf, a.g, 128, workspace=ws, stream=0),
+              lambda ws: nv.mx_gemm(codes, e8, codes, e8, workspace=ws, stream=0),
+              lambda ws: nv.mx4_gemm(codes, e8, codes, e8, workspace=ws, stream=0),
+              lambda ws: nv.gather_rows(a, z(5, dtype=i32), workspace=ws, stream=0)]
     for call in calls:
         for ws in (z(1, dtype=u8).expand(1 << 24), z(1 << 12, dtype=u8)[::2]):
             with pytest.raises(ValueError, match="contiguous workspace"):

@@ -337,3 +337,12 @@ def test_quantize_column_slice_of_wider_tensor(nv, orc, c0):
         np.testing.assert_array_equal(host(out["mx_col"][0]), mq)
         np.testing.assert_array_equal(host(out["mx_col"][1]), me)
         assert nv.nvfp4_workspace_status(out["workspace"]) == 0
+
+
+def test_workspace_that_is_not_contiguous_is_refused(nv):
+    """A byte expanded to the size asked for has no room for the status word; nothing is launched."""
+    import torch
+    x = torch.zeros((16, 32), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(256)
+    with pytest.raises(ValueError, match="contiguous workspace"):
+        nv.quantize(x, workspace=ws)
