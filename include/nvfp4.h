@@ -669,12 +669,15 @@ size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int hea
  * tokens included; out contiguous bf16; lse (NULL: not wanted) FP32 [sequences]
  * [queries][heads]: log sum_n exp(scale <q, k_n>).  A query that sees no token (as
  * in a sequence of length 0) has out 0 and lse -inf.  Softmax and sums are FP32;
- * the exponentials go into the product with v as FP16, 2^-12 off at most.
+ * each exponential goes into the product with v (not into its own sum) rounded to
+ * FP16, off by at most 2^-11 of itself and 2^-34 of its row's largest.
  * The table is read up to a sequence's length.  A page outside the cache counts as
  * zeros, a length outside 0..table_pages * page_size as the nearer end; both are
  * reported in the workspace's status word (NVFP4_ERR_INDEX).  Meant for few rows
- * (queries * heads / kv_heads): the cache is decoded again for every eight.  Results do not depend on timing; they may depend on the other
- * sequences of a call, by the places where a long one is cut.
+ * (queries * heads / kv_heads): the cache is decoded again for every eight.
+ * Results do not depend on timing.  Their last bits may depend on the other
+ * sequences of a call and on the table's width: by these go the places where a long
+ * sequence is cut and the tokens (32 or 64) that a running maximum is taken of.
  */
 nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ldb, int64_t ldi, int64_t ldh,
                                 int64_t sequences, int queries, int heads,

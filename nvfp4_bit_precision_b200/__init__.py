@@ -1015,7 +1015,8 @@ def expert_mlp(x, routing: Routing, up, down, gate=None, base=None, *, workspace
     """The experts of a MoE layer for a few tokens x [tokens, hidden] bf16: each routed row through its expert's gate
     and up matrices, silu(gate) * up (without a gate max(up, 0)^2), its down matrix, and the weighted sum per token
     on top of base.  up, down and gate: ``moe.ExpertWeights`` (or the like: q, sf, g, n).  ``workspace``:
-    nvfp4_expert_mlp_workspace_size bytes, which then hold the status word too."""
+    nvfp4_expert_mlp_workspace_size bytes, which then hold the status word too.  For inference: no gradients; meant for
+    up to about eight rows an expert (with more, ``grouped_gemm`` of quantised rows is faster)."""
     if stream is not None:
         with _on(stream):
             return expert_mlp(x, routing, up, down, gate, base, workspace=workspace)
@@ -1075,7 +1076,9 @@ def _experts_matrix(name: str, q, sf, g, G: int, n: int, k: int) -> None:
 class KVCache:
     """A paged cache of keys and values in NVFP4, blocks along the head dimension: codes uint8 [2, pages, kv_heads,
     page_size, dim/2] and E4M3 bytes uint8 [2, pages, kv_heads, page_size, dim/16], the keys first; amax f32 [2], the
-    largest magnitudes that keys and values are expected to have (larger ones saturate), and g = amax / 2688."""
+    largest magnitudes that keys and values are expected to have (larger ones saturate), and g = amax / 2688.  The two
+    belong together (append and attention read amax, ``dequantize`` g) and stay as they are while the cache holds anything:
+    what is in it was quantised with them."""
     q: object
     sf: object
     amax: object
@@ -1156,7 +1159,7 @@ def kv_append(cache: KVCache, k, v, table, position, sequence=None, *, cos=None,
     position, pairs (i, i + rot/2) or with ``interleaved`` (2i, 2i + 1), and q's (bf16 [tokens, heads, dim]) into
     ``q_out`` (a new tensor; q itself may be given), which is returned.  Tokens with a negative position or sequence are
     left out (their rows of q_out too); tokens without a place in the cache are left out and reported in the optional
-    ``workspace`` (256 bytes)."""
+    ``workspace`` (256 bytes).  For inference: no gradients."""
     if stream is not None:
         with _on(stream):
             return kv_append(cache, k, v, table, position, sequence, cos=cos, sin=sin, interleaved=interleaved, q=q,
@@ -1218,7 +1221,8 @@ def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = 
     included), of them the ``window`` last ones (0: all).  Query heads share the kv heads in order; scale is 1 /
     sqrt(dim) without one.  Returns bf16 [sequences, queries, heads, dim]; with ``lse`` also the logarithm of each
     row's sum of exponentials, f32 [sequences, queries, heads].  Rows that see nothing are 0, their lse -inf.
-    ``workspace``: nvfp4_kv_attention_workspace_size bytes, which then hold the status word too."""
+    ``workspace``: nvfp4_kv_attention_workspace_size bytes, which then hold the status word too.  For inference: no
+    gradients; meant for few rows (the cache is decoded again for every eight of queries * heads / kv_heads)."""
     if stream is not None:
         with _on(stream):
             return kv_attention(q, cache, table, lengths, scale=scale, window=window, lse=lse, workspace=workspace)
