@@ -584,11 +584,13 @@ size_t nvfp4_expert_mlp_workspace_size(int64_t total_rows, int64_t hidden, int64
  * x [tokens, ldx] bf16; gate (all three pointers NULL: none) and up [G, ffn, hidden / 2],
  * down [G, hidden, ffn / 2] with consecutive NVFP4_SF_MMA blocks and g [G]; base, out
  * [tokens, hidden] bf16 (base NULL = 0; out may be base).  The products and what
- * becomes of them are FP32; h is rounded to bf16, the x of the last product.
+ * becomes of them are FP32; h enters the last product as FP16 at a power of two a
+ * row, off by at most 2^-11 of itself and 2^-38 of its row's largest.
  * Slots with a negative row are left out; a row_index outside x gives a row of
  * zeros, a slot_row at or behind group_offsets[G] or total_rows is left out, and
- * both are reported in the workspace's status word.  hidden and ffn multiples of 128 and at most 45056,
- * 1 <= G <= 256, 1 <= k <= 64; otherwise as nvfp4_grouped_gemv and nvfp4_combine.
+ * both are reported in the workspace's status word.  hidden and ffn multiples of 128
+ * and at most 45056, 1 <= G <= 256, 1 <= k <= 64; otherwise as nvfp4_grouped_gemv
+ * and nvfp4_combine.
  */
 nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, int64_t total_rows,
                               const void* x_bf16, int64_t ldx, int64_t tokens,

@@ -32,8 +32,9 @@
 // into L2 was slower (one row: 16.9 to 19.4 us): x waits behind them.
 //
 // A few tokens' experts in three launches: the gate's and up products with the activation
-// as their epilogue, h in bf16 (the x of the last product, whose tests and tolerances are
-// those of any bf16 x), the down products, the weighted sums.  One token's four experts of
+// as their epilogue, h in FP32 (rounded once, where the down products bring it into shared
+// memory as FP16: 2^-11 of itself; h in bf16, whose loads are half, gave three of those bits
+// away and saved 1%), the down products, the weighted sums.  One token's four experts of
 // three 4096 x 1536 matrices (42 MB) 21 us on the device, eight tokens' (179 MB) 51, 32
 // tokens' without gates (262 MB) 79; with the down matrices asked for only after the first
 // products' end, the combine's own launch and a status word cleared by a memset 26.7, 59.5
@@ -179,6 +180,25 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // numbers: they, too, then fit into FP16, and a sum is infinite or NaN by those alone.
 __device__ __forceinline__ uint32_t x_exponent(uint32_t top) { return min(max(top >> 7, 15u), 254u); }
 
+// Eight numbers times a power of two as FP16.
+__device__ __forceinline__ uint4 to_f16x8(const float (&f)[8], float up)
+{
+    __half2 h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        mul2(lo, hi, f[2 * j], f[2 * j + 1], up, up);
+        h[j] = __floats2half2_rn(lo, hi);
+    }
+    return *reinterpret_cast<const uint4*>(h);
+}
+
+__device__ __forceinline__ void unpack2_f16(uint32_t two, float& lo, float& hi)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+    lo = f.x, hi = f.y;
+}
+
 // Asynchronous copies to shared memory; zeros where there is nothing to read.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
 {
@@ -228,8 +248,8 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at)
 // u; lane (r, t) then has both products of row r, and silu(gate) * up leaves in their
 // place.  kSquared: the squared positive part of the product does.
 //
-// kLateRows: x comes from the kernel before, the rest from before that one; the first
-// weights are asked for while the other kernel ends.
+// kLateRows: x comes from the kernel before, in FP32, the rest from before that one; the
+// first weights are asked for while the other kernel ends.
 template <int NT, bool PANELS, int FORM>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs a)
 {
@@ -257,6 +277,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
     float* const s_sums = reinterpret_cast<float*>(s_dyn + kGemvWarps * kStages * kStageBytes);  // [2][warps][kRed]
     float* const my_head = s_sums + warp * kRed;                        // sums of a tile that an earlier warp began
     float* const my_sums = s_sums + (kGemvWarps + warp) * kRed;         // sums of a tile that this one began
+    // kLateRows: the exponents of the x rows' steps, until there are sums
+    uint32_t* const s_step = reinterpret_cast<uint32_t*>(s_sums + kGemvWarps * kRed);
+    static_assert(max_x_pairs(NT, false) <= kGemvWarps * kRed, "as many (row, step) pairs as shared memory holds");
     float* const s_acc = s_sums + 2 * kGemvWarps * kRed;  // with panels: [kPanelTiles][8 NT][16]
     uint8_t* const s_x = reinterpret_cast<uint8_t*>(s_acc) + (PANELS ? kPanelTiles * tile_sum_bytes(NT) : 0);
     const int panel_steps = PANELS ? a.panel_steps : steps;
@@ -492,17 +515,51 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             c += kGemvWarps;
             while (c >= psteps) c -= psteps, ++xr;
         };
+        if constexpr (FORM == kLateRows) {
+            // a warp has the columns of a step together, but not a row: the step becomes FP16 at its own power of
+            // two, whose place the row's takes below
+            constexpr int kAhead = 4;
+#pragma unroll 1
+            for (int s = 0; s < kStages - 1; ++s) copy_step();
+            wait_for_previous_kernel();
+            int xr = 0, c = warp - kGemvWarps;
+            next(xr, c);
+#pragma unroll 1
+            do {
+                uint4 v[kAhead][2];
+                int at[kAhead], of[kAhead], pair[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int4 row = s_x_row[min(xr, x_rows - 1)];
+                    const int k = c * kStep + 64 * t + 8 * r;
+                    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+                    if (xr < x_rows && row.x >= 0 && k < a.k) {
+                        const uint4* const from = reinterpret_cast<const uint4*>(a.x + 2 * (row.x * a.ldx + k));
+                        v[i][0] = from[0], v[i][1] = from[1];
+                    }
+                    at[i] = row.y + (c * 8 + r) * row.z + t * 16;
+                    of[i] = xr, pair[i] = xr * steps + c;
+                    next(xr, c);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (of[i] >= x_rows) break;
+                    const uint32_t u[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+                    uint32_t m = 0;
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m = max(m, u[j] & 0x7FFFFFFFu), f[j] = __uint_as_float(u[j]);
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, m) >> 16, ex = x_exponent(top);
+                    *reinterpret_cast<uint4*>(s_x + at[i]) = to_f16x8(f, __uint_as_float((268u - ex) << 23));
+                    if (lane == 0) s_step[pair[i]] = ex, atomicMax(&s_top[of[i]], top);
+                }
+            } while (xr < x_rows);
+        } else
         {
             constexpr int kAhead = 4 * NT;  // loads in flight together
             int xr = 0, c = warp - kGemvWarps;
             next(xr, c);
             bool primed = false;
-            if constexpr (FORM == kLateRows) {
-#pragma unroll 1
-                for (int s = 0; s < kStages - 1; ++s) copy_step();
-                primed = true;
-                wait_for_previous_kernel();
-            }
 #pragma unroll 1
             do {
                 uint4 v[kAhead];
@@ -544,16 +601,17 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
             while (xr < x_rows) {
                 const int4 row = s_x_row[xr];
                 uint4* const at = reinterpret_cast<uint4*>(s_x + t * 16 + row.y + (c * 8 + r) * row.z);
-                const float up = __uint_as_float((268u - x_exponent(s_top[xr])) << 23);
                 float f[8];
-                unpack8(*at, f);
-                __half2 h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mul2(f[2 * j], f[2 * j + 1], f[2 * j], f[2 * j + 1], up, up);
-                    h[j] = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+                if constexpr (FORM == kLateRows) {  // (exact, but for what falls below FP16's normal numbers)
+                    const uint32_t less = min(x_exponent(s_top[xr]) - s_step[xr * steps + c], 100u);
+                    const uint4 u = *at;
+                    unpack2_f16(u.x, f[0], f[1]), unpack2_f16(u.y, f[2], f[3]), unpack2_f16(u.z, f[4], f[5]), unpack2_f16(u.w, f[6], f[7]);
+                    *at = to_f16x8(f, __uint_as_float((127u - less) << 23));
+                } else {
+                    const float up = __uint_as_float((268u - x_exponent(s_top[xr])) << 23);
+                    unpack8(*at, f);
+                    *at = to_f16x8(f, up);
                 }
-                *at = *reinterpret_cast<const uint4*>(h);
                 next(xr, c);
             }
         }
@@ -619,7 +677,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         const auto store_gated = [&](int tok, int m, float gate, float up, float2 by, float by2) {
             const float z = gate * by.x * by.y, v = z / (1.0f + __expf(-z)) * (up * by2 * by.y);
             const int64_t n = static_cast<int64_t>(tile >> 3) * 64 + 4 * (tile & 7) + 32 * (m >> 2) + (m & 3);
-            static_cast<__nv_bfloat16*>(a.out)[(row0 + tok) * a.ldd + n] = __float2bfloat16_rn(v);
+            static_cast<float*>(a.out)[(row0 + tok) * a.ldd + n] = v;
         };
         if (j0 < j1) enter();
 #pragma unroll 1
@@ -948,7 +1006,7 @@ extern "C" nvfp4_status nvfp4_grouped_gemv(int G, const int32_t* group_offsets, 
 extern "C" size_t nvfp4_expert_mlp_workspace_size(int64_t total_rows, int64_t hidden, int64_t ffn)
 {
     if (total_rows < 1 || hidden < 1 || ffn < 1) return kMlpHead;
-    return kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 2) + static_cast<size_t>(total_rows) * hidden * 4;
+    return kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 4) + static_cast<size_t>(total_rows) * hidden * 4;
 }
 
 extern "C" nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, int64_t total_rows, const void* x_bf16,
@@ -975,12 +1033,12 @@ extern "C" nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, in
     up.group_offsets = group_offsets, up.groups = G, up.rows = total_rows;
     up.q = up_q, up.sf = up_sf, up.g = up_g, up.n = ffn, up.k = hidden, up.out = ws + kMlpHead, up.ldd = ffn;
     if (gate_q) up.q = gate_q, up.sf = gate_sf, up.g = gate_g, up.q2 = up_q, up.sf2 = up_sf, up.g2 = up_g;
-    if (const nvfp4_status s = check_gemv(up, NVFP4_OUT_BF16)) return s;
+    if (const nvfp4_status s = check_gemv(up, NVFP4_OUT_F32)) return s;
     GemvArgs down{};
     down.x = static_cast<const uint16_t*>(up.out), down.ldx = ffn, down.src_rows = total_rows;
     down.group_offsets = group_offsets, down.groups = G, down.rows = total_rows;
     down.q = down_q, down.sf = down_sf, down.g = down_g, down.n = hidden, down.k = ffn, down.ldd = hidden;
-    down.out = ws + kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 2);
+    down.out = ws + kMlpHead + round256(static_cast<size_t>(total_rows) * ffn * 4);
     if (const nvfp4_status s = check_gemv(down, NVFP4_OUT_F32)) return s;
     if (ws_bytes < nvfp4_expert_mlp_workspace_size(total_rows, hidden, ffn)) return NVFP4_ERR_WORKSPACE;
     int dev = 0;
@@ -991,7 +1049,7 @@ extern "C" nvfp4_status nvfp4_expert_mlp(int G, const int32_t* group_offsets, in
     uint32_t* const status = reinterpret_cast<uint32_t*>(ws) + 2;
     if (tokens == 0) return cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
     if (total_rows > 0) {
-        if (const nvfp4_status s = launch_rows(up, NVFP4_OUT_BF16, gate_q ? kGated : kSquared, sms, true, st)) return s;
+        if (const nvfp4_status s = launch_rows(up, NVFP4_OUT_F32, gate_q ? kGated : kSquared, sms, true, st)) return s;
         if (const nvfp4_status s = launch_rows(down, NVFP4_OUT_F32, kLateRows, sms, true, st)) return s;
     }
     JoinArgs j{};

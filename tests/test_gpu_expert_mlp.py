@@ -332,3 +332,36 @@ def test_wide_experts_and_many(nv, tokens, top_k, G, hidden, ffn, gated):
     x, base = bits(rng, (tokens, hidden)), bits(rng, (tokens, hidden))
     got = moe.expert_mlp(to_dev(x), routing(nv, ids, weight, G), up, down, gate, to_dev(base))
     compare(got, *reference_by_expert(val(x), ids, weight, upw, downw, gatew, val(base)))
+
+
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("gated", [True, False])
+def test_what_h_is_rounded_to(nv, gated, tokens):
+    """h enters the last product in FP16 at a power of two a row: 2^-11 of itself, 2^-38 of the row's largest.  Down
+    matrices that hand h through, a base that takes most of it away again."""
+    import torch
+    from nvfp4_bit_precision_b200 import moe
+    rng = np.random.default_rng(8)
+    hidden = ffn = 384
+    up, upw = matrices(rng, 1, ffn, hidden)
+    gate, gatew = matrices(rng, 1, ffn, hidden, 4.0) if gated else (None, None)
+    q = np.zeros((1, hidden, ffn // 2), np.uint8)
+    at = np.arange(hidden)
+    q[0, at, at // 2] = np.where(at % 2, 0x20, 0x02)                                     # 1.0
+    down = moe.ExpertWeights(dev(q), torch.full((hidden * ffn // 16,), 0x38, dtype=torch.uint8, device="cuda"), torch.ones(1, device="cuda"), hidden)
+    x = val(bits(rng, (tokens, hidden))) * np.exp2(rng.integers(-12, 12, (tokens, 1)))
+    xb = W.f32_to_bf16_bits(x.astype(np.float32))
+    u, du = products(val(xb), upw[0])
+    if gated:
+        z, dz = products(val(xb), gatew[0])
+        s = z / (1 + np.exp(-z))
+        h, dh = s * u, np.abs(s) * du + 1.1 * dz * (np.abs(u) + du) + 2.0 ** -20 * np.abs(s * u)
+    else:
+        p = np.maximum(u, 0)
+        h, dh = p * p, 2 * p * du + du * du + 2.0 ** -23 * p * p
+    base = W.f32_to_bf16_bits(-h.astype(np.float32))
+    got = moe.expert_mlp(to_dev(xb), routing(nv, np.zeros((tokens, 1), int), np.ones((tokens, 1), np.float32), 1), up, down, gate, to_dev(base))
+    ref = val(base) + h
+    dh = dh + 2.0 ** -11 * (np.abs(h) + dh) + 2.0 ** -38 * np.abs(h).max(1, keepdims=True)
+    # (the last product's sum of one number and zeros, its factors and the weighted sum: 8 roundings to FP32)
+    compare(got, ref, dh * (1 + 2.0 ** -7) + 2.0 ** -20 * np.abs(h) + 2.0 ** -8 * np.abs(ref))
