@@ -816,10 +816,12 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, *, dweight: bool = True, work
     if dweight:
         dw = torch.empty_like(weight)
         if workspace is None:
-            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_size(rows, cols), dtype=torch.uint8,
-                                    device=dev)
+            nb = nvfp4_rmsnorm_backward_workspace_size(rows, cols)
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
+        else:
+            wp, nb = _scratch("rmsnorm_backward", workspace)
         dwp = dw.data_ptr()
-        wp, nb = _scratch("rmsnorm_backward", workspace)
     _check(_lib.nvfp4_rmsnorm_backward(dy.data_ptr(), ldy, h.data_ptr(), ldh,
                                        dh.data_ptr() if dh is not None else None, lddh, weight.data_ptr(), wdt,
                                        rstd.data_ptr(), rows, cols, dx.data_ptr(), cols, dwp, wp, nb,
@@ -860,13 +862,14 @@ def route(logits, top_k: int, *, score: int = NVFP4_SOFTMAX, bias=None, groups: 
     r = Routing(_matrix(dev, i32, tokens, top_k), _matrix(dev, torch.float32, tokens, top_k),
                 torch.empty(experts + 1, dtype=i32, device=dev),
                 torch.empty(tokens * top_k, dtype=i32, device=dev), _matrix(dev, i32, tokens, top_k), p)
-    wp, n = None, 0
-    if workspace is None:
+    wp = None
+    if workspace is not None:
+        wp, n = _scratch("route", workspace)
+    else:
         n = nvfp4_route_workspace_size(tokens, experts)
         if n > 256:
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    if workspace is not None:
-        wp, n = _scratch("route", workspace)
+            wp = workspace.data_ptr()
     _check(_lib.nvfp4_route(logits.data_ptr(), dt, ld, bias.data_ptr() if bias is not None else None, tokens,
                             experts, ctypes.byref(p), r.expert.data_ptr(), r.weight.data_ptr(),
                             r.group_offsets.data_ptr(), r.row_index.data_ptr(), r.slot_row.data_ptr(), wp, n,
@@ -1050,8 +1053,11 @@ def expert_mlp(x, routing: Routing, up, down, gate=None, base=None, *, workspace
         _flat("expert_mlp: base", base, torch.bfloat16, tokens, hidden)
         bp = base.data_ptr()
     if workspace is None:
-        workspace = torch.empty(nvfp4_expert_mlp_workspace_size(rows, hidden, ffn), dtype=torch.uint8, device=dev)
-    wp, nb = _scratch("expert_mlp", workspace)
+        nb = nvfp4_expert_mlp_workspace_size(rows, hidden, ffn)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nb = _scratch("expert_mlp", workspace)
     out = _matrix(dev, torch.bfloat16, tokens, hidden)
     _check(_lib.nvfp4_expert_mlp(G, offsets.data_ptr(), rows, x.data_ptr(), ldx, tokens, row_index.data_ptr(), gp, gsp,
                                  ggp, uq.data_ptr(), us.data_ptr(), ug.data_ptr(), dq.data_ptr(), ds.data_ptr(),
@@ -1241,9 +1247,11 @@ def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = 
         raise ValueError(f"kv_attention: a table of {sequences} sequences for {n}")
     _flat("kv_attention: lengths", lengths, torch.int32, n)
     if workspace is None:
-        workspace = torch.empty(_attention_bytes(n, new, heads, view.kv_heads, dim, pages * view.page_size),
-                                dtype=torch.uint8, device=dev)
-    wp, nb = _scratch("kv_attention", workspace)
+        nb = _attention_bytes(n, new, heads, view.kv_heads, dim, pages * view.page_size)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nb = _scratch("kv_attention", workspace)
     out = torch.empty_strided(shape, (new * heads * dim, heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
     sums = torch.empty((n, new, heads), dtype=torch.float32, device=dev) if lse else None
     # (strides over a single sequence, token or head are never used, and torch leaves them arbitrary)
