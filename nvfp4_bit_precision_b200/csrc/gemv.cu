@@ -35,11 +35,13 @@
 // as their epilogue, h in FP32 (rounded once, where the down products bring it into shared
 // memory as FP16: 2^-11 of itself; h in bf16, whose loads are half, gave three of those bits
 // away and saved 1%), the down products, the weighted sums.  One token's four experts of
-// three 4096 x 1536 matrices (42 MB) 21 us on the device, eight tokens' (179 MB) 51, 32
-// tokens' without gates (262 MB) 79; with the down matrices asked for only after the first
-// products' end, the combine's own launch and a status word cleared by a memset 26.7, 59.5
-// and 89.  The three starts are 14 us of the 21, 20 of the 51 and 24 of the 79; copies
-// without any decoding take 18, 45 and 67.
+// three 4096 x 1536 matrices (42 MB) 21.6 us on the device, eight tokens' (179 MB) 54.7, 32
+// tokens' without gates (262 MB) 84.2, medians of draws of experts.  On one draw, with the
+// down matrices asked for only after the first products' end, the combine's own launch and a
+// status word cleared by a memset 26.7, 59.5 and 89, without them 21, 51 and 79; copies
+// without any decoding 18, 45 and 67.  The launches alone (no rows) take 4.8 to 5.7 us; with
+// the loads that wait for one another (offsets, indexes, x, first weights, h), through
+// matrices of 128 x 128, 11.5 us for one token and 14.5 for more.
 #include "common.cuh"
 #include "gemv_plan.h"
 

@@ -15,12 +15,16 @@
 // more.  Where these, with d = 1.6 * 2^-23 t (|a| + |b|) + 2^-126, round to the same bf16 number,
 // so does what lies between them.  Otherwise (about one number in 2000) the FP64 form decides.
 //
-// What bounds it: HBM where there is much to do.  16384 tokens with 32 query and 8 key heads
-// of 128 (354 MB) about 60 us, 5.9 TB/s; without the rotation the same.  One token 3 us, a
-// launch and three loads that wait for one another.  Steps on the way (with the cache read
-// back, 26 us): every lane quantising, what it turned and what it did not, 150 us; packed
-// arithmetic, S / d from a table, queries apart from keys and values 120; the next four
-// heads' numbers on their way through shared memory 102.
+// What bounds it: instructions and HBM alike where there is much to do.  16384 tokens with 32
+// query and 8 key heads of 128 (354 MB, 54 us at the copy rate) 79.4 us on the device, 4.5
+// TB/s: 290 instructions a warp and head, of which turning is 40%, fill two thirds of the
+// issue slots.  Keys and values alone, not turned (86 MB), 23.6 us.  64 tokens with 40 query
+// heads 3.7 us, one token 3, a launch and three loads that wait for one another.  The 80
+// registers that leave room for three CTAs spill 24 or 32 bytes, 2% of the instructions.
+// Steps on the way (with the cache read back, 16 us): every lane quantising, what it turned
+// and what it did not, 150 us; packed arithmetic, S / d from a table, queries apart from keys
+// and values 120; the next four heads' numbers on their way through shared memory 102; with
+// nvfp4_dequantize's later steps 95.5.
 #include "kv_cache.cuh"
 
 #include <algorithm>

@@ -39,6 +39,8 @@ namespace {
 // Exponentials are taken from a running maximum that is raised only where a product passes it by
 // kSlack in the exponent: they are 2^9 at that maximum and at most 2^15, within FP16, whose
 // eleven bits they have down to 2^-23 of it.
+// (The sum takes them before that rounding, and so does the log-sum: of many equal products the
+// result is off by the rounding that they share, 2^-11 at most, and the log-sum by none.)
 constexpr float kUp = 9.0f, kSlack = 6.0f;
 constexpr int kLeastSlice = 32;
 constexpr size_t kHeadBytes = 256;        // of the workspace, the status word among them
@@ -748,7 +750,9 @@ Cut cut_of(int64_t sequences, int queries, int heads, int kv_heads, int dim, int
     c.block_rows = (c.rows + c.blocks - 1) / c.blocks;
     const int64_t items = sequences * kv_heads * c.blocks;
     // Steps of 64 tokens save a tenth of the instructions, those of 32 share out short work better: one
-    // sequence of 32768 tokens 22.2 us with 32 and 25.2 with 64; 64 sequences of 5120 95 and 82.5.
+    // sequence of 32768 tokens 22.1 us with 32 and 23.9 with 64; 64 sequences of 5120 95 and 82.5.  The
+    // host knows the table's width and not the lengths, so short sequences in a wide table take 64 (one of
+    // 1000 tokens 9.3 us, in a table for 131072 10.1; eight of 300 10.2 and 10.5).
     c.slice = dim == 256 || items * (capacity / 64 + 1) <= 8000 ? 32 : 64;
     c.ctas = std::min<int64_t>(sms, items * (capacity / kLeastSlice + 2));  // (no more than there can be slices)
     c.workers = c.ctas * warps_of(dim);
