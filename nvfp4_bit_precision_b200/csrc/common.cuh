@@ -582,6 +582,43 @@ __device__ __forceinline__ float div6_rn(float a)
     return __fmaf_rn(r, z, q0);
 }
 
+// Asynchronous copies to shared memory; zeros where there is nothing to read.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Eight E2M1 codes as FP16, pairs in order.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// c += a b for 16 x 16 and 16 x 8 FP16 operands, sums in FP32.
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Offset of scale byte (row r, 16-block b) in the tiled tensor-core layout of
 // an operand whose rows hold k16 = K/16 blocks: 128x4 atoms of 512 bytes,
 // atoms ordered with the K group fastest.
@@ -622,14 +659,14 @@ __device__ __forceinline__ void let_next_kernel_start()
 
 // (`early` false: an ordinary launch, as after a memset, which is no kernel.)
 template <typename... Params, typename... Args>
-inline cudaError_t launch_early(bool early, void (*kernel)(Params...), int64_t grid, int block, size_t smem,
+inline cudaError_t launch_early(bool early, void (*kernel)(Params...), dim3 grid, int block, size_t smem,
                                 cudaStream_t stream, Args... args)
 {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid)), cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.gridDim = grid, cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem, cfg.stream = stream;
     cfg.attrs = &attr, cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);

@@ -138,22 +138,6 @@ struct GemvArgs {
     uint32_t* status;
 };
 
-__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
-        : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // The E4M3 scales of four 16-blocks, each in both halves of a register.
 __device__ __forceinline__ void four_scales(uint32_t word, uint32_t (&s)[4])
 {
@@ -166,15 +150,6 @@ __device__ __forceinline__ void four_scales(uint32_t word, uint32_t (&s)[4])
     s[1] = __byte_perm(lo, 0, 0x3232);
     s[2] = __byte_perm(hi, 0, 0x1010);
     s[3] = __byte_perm(hi, 0, 0x3232);
-}
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                 "{%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The exponent field by which a row of x is scaled, from its largest magnitude (bf16
@@ -201,18 +176,10 @@ __device__ __forceinline__ void unpack2_f16(uint32_t two, float& lo, float& hi)
     lo = f.x, hi = f.y;
 }
 
-// Asynchronous copies to shared memory; zeros where there is nothing to read.
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
+// Eight bytes to shared memory (copy16_async for what is less than it takes).
 __device__ __forceinline__ void copy8_async(uint32_t dst, const void* src, bool there)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 load_shared(uint32_t at)
 {

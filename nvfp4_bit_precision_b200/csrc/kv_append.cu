@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendArgs a, cons
                                          : h < values ? a.k + t * a.ldk + (h - keys) * a.hsk
                                                       : a.v + t * a.ldv + (h - values) * a.hsv;
             const uint32_t to = mine + (h - h0) % kAhead * (512 * 16);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + first) : "memory");
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 256 * 16), "l"(from + second) : "memory");
+            copy16_async(to, from + first);
+            copy16_async(to + 256 * 16, from + second);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -301,14 +301,9 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const void*
     const int64_t rounds = tokens * all * lanes / (static_cast<int64_t>(sms) * 768);
     const int per = static_cast<int>(std::min<int64_t>(std::max<int64_t>(rounds, 1), 8));
     a.per_thread = per;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((tokens * lanes + 255) / 256), static_cast<unsigned>((all + per - 1) / per));
-    cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = a.status ? 0 : 1;
+    const dim3 grid(static_cast<unsigned>((tokens * lanes + 255) / 256), static_cast<unsigned>((all + per - 1) / per));
     cudaError_t err = cudaSuccess;
-    const auto go = [&](auto kernel) { err = cudaLaunchKernelEx(&cfg, kernel, a, rot); };
+    const auto go = [&](auto kernel) { err = launch_early(!a.status, kernel, grid, 256, 0, st, a, rot); };
     if (dim == 64) neighbours ? go(append_kernel<64, true>) : go(append_kernel<64, false>);
     else if (dim == 128) neighbours ? go(append_kernel<128, true>) : go(append_kernel<128, false>);
     else neighbours ? go(append_kernel<256, true>) : go(append_kernel<256, false>);

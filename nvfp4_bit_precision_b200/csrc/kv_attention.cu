@@ -67,32 +67,6 @@ struct AttendArgs {
     uint32_t* status;
 };
 
-// Asynchronous copies to shared memory; zeros where there is nothing to read.
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&p)[4])
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
-        : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two)
 {
     uint32_t d;
@@ -106,15 +80,6 @@ __device__ __forceinline__ void both_halves(uint32_t two, uint32_t& lo, uint32_t
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 %0, {l, l};\n\tmov.b32 %1, {h, h};\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(two));
-}
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                 "{%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // An 8x8 matrix of 16-bit numbers, a row in four lanes, transposed.
@@ -786,16 +751,10 @@ nvfp4_status start(const AttendArgs& a, const Cut& cut, cudaStream_t st)
     }
     if (launch_early(true, attend_kernel<DIM, SLICE>, cut.ctas, 32 * S::kWarps, S::kSmem, st, a) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     // a CTA for each row while that fills no more than the multiprocessors
     const bool apart = cut.records * cut.block_rows <= 4 * cut.ctas;
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.records), apart ? static_cast<unsigned>(cut.block_rows) : 1);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<DIM>, a, static_cast<int>(cut.ctas)) != cudaSuccess)
+    const dim3 grid(static_cast<unsigned>(cut.records), apart ? static_cast<unsigned>(cut.block_rows) : 1);
+    if (launch_early(true, join_kernel<DIM>, grid, 32 * kJoinWarps, 0, st, a, static_cast<int>(cut.ctas)) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
