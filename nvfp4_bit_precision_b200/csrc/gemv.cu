@@ -34,7 +34,7 @@
 // A few tokens' experts in three launches: the gate's and up products with the activation
 // as their epilogue, h in FP32 (rounded once, where the down products bring it into shared
 // memory as FP16: 2^-11 of itself; h in bf16, whose loads are half, gave three of those bits
-// away and saved 1%), the down products, the weighted sums.  One token's four experts of
+// away and saved up to 1%), the down products, the weighted sums.  One token's four experts of
 // three 4096 x 1536 matrices (42 MB) 21.6 us on the device, eight tokens' (179 MB) 54.7, 32
 // tokens' without gates (262 MB) 84.2, medians of draws of experts.  On one draw, with the
 // down matrices asked for only after the first products' end, the combine's own launch and a
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
         if constexpr (FORM == kLateRows) {
             // a warp has the columns of a step together, but not a row: the step becomes FP16 at its own power of
             // two, whose place the row's takes below
-            constexpr int kAhead = 4;
+            constexpr int kAhead = 2;  // (four: one token's experts 22.6 us instead of 22.1, 8 tokens' 67.8 and 67.3; one: slower too)
 #pragma unroll 1
             for (int s = 0; s < kStages - 1; ++s) copy_step();
             wait_for_previous_kernel();
