@@ -673,7 +673,8 @@ size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int hea
  * in a sequence of length 0) has out 0 and lse -inf.  Softmax and sums are FP32;
  * each exponential goes into the product with v (not into its own sum) rounded to
  * FP16, off by at most 2^-11 of itself and 2^-34 of its row's largest.
- * The table is read up to a sequence's length.  A page outside the cache counts as
+ * The table is read up to a sequence's length; with a window the pages before the
+ * first query's may be gone (any entry).  Another page outside the cache counts as
  * zeros, a length outside 0..table_pages * page_size as the nearer end; both are
  * reported in the workspace's status word (NVFP4_ERR_INDEX).  Meant for few rows
  * (queries * heads / kv_heads): the cache is decoded again for every eight.

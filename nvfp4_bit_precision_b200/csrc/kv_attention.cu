@@ -230,6 +230,12 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
                (DIM == 64 ? (lane / 2 & 8) * 32 : 0);
     };
     const uint32_t even_place = ring + place_of(0), odd_place = DIM == 256 ? ring + place_of(1) : even_place;
+    // The first token that a sequence's queries see: the pages before it, of which a slice may hold some, may be gone.
+    const auto first_seen = [&](int s) {
+        if (a.window == 0) return 0;
+        const int64_t most = static_cast<int64_t>(a.table_pages) << a.cache.page_shift;
+        return static_cast<int>(min(static_cast<int64_t>(a.lengths[s]), most)) - a.queries + 1 - a.window;
+    };
     int put = 0;                                      // stage of the ring
     int c_left = left, c_seq = seq, c_rel = rel;      // slices to copy; where the next item's begin
     int c_part = 0, c_token = 0, c_end = 0, c_head = 0, c_of = 0;  // of the item at hand: slices left, next token, end, head, sequence
@@ -256,7 +262,10 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
                 page = -1;
                 if (token < c_end) {
                     page = a.table[c_of * a.ldt + (token >> a.cache.page_shift)];
-                    if (page < 0 || page >= a.cache.pages) s_bad = NVFP4_ERR_INDEX, page = -1;
+                    if (page < 0 || page >= a.cache.pages) {
+                        if (token + (1 << run_shift) > first_seen(c_of)) s_bad = NVFP4_ERR_INDEX;
+                        page = -1;
+                    }
                 }
                 known = 0;
             }

@@ -444,3 +444,32 @@ def test_a_prompts_queries(nv, dim, kv, group, page, new, window):
     cache, q, sf = filled(nv, rng, 4 * most, kv, page, dim)
     table = rng.permutation(4 * most).reshape(4, most)
     check(nv, cache, q, sf, bits(rng, (4, new, kv * group, dim), 1.5), table, lengths, page, window)
+
+
+@pytest.mark.parametrize("dim,wide", [(64, False), (64, True), (128, False), (128, True), (256, False)])
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_pages_before_the_window_are_not_read(nv, dim, wide, page):
+    """A program that gives back the pages which no query's window reaches any more has no page there: that is no
+    error, and what the queries see is as it was.  A missing page that one query sees is reported."""
+    import torch
+    rng = np.random.default_rng(dim + page + wide)
+    tokens = WIDE * 8 if wide else 512
+    lengths = [500, 333, 77, 16, 0]
+    most = -(-max(lengths) // page)
+    cache, q, sf = filled(nv, rng, len(lengths) * most, 2, page, dim)
+    table = rng.permutation(len(lengths) * most).reshape(len(lengths), most)
+    full = widened(table, lengths, page, tokens)
+    size = nv.nvfp4_kv_attention_workspace_size(len(lengths), 3, 4, 2, dim, tokens)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for new, window in ((1, 1), (1, 17), (3, 33), (2, 100), (3, 64)):
+        qd = to_dev(bits(rng, (len(lengths), new, 4, dim)))
+        want, wl = nv.kv_attention(qd, cache, i32(full), i32(lengths), window=window, lse=True)
+        left = full.copy()
+        for s, n in enumerate(lengths):
+            left[s, :max(0, n - new + 1 - window) // page] = -1
+        got, gl = nv.kv_attention(qd, cache, i32(left), i32(lengths), window=window, lse=True, workspace=ws)
+        assert nv.nvfp4_workspace_status(ws) == 0, (new, window)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        left[0, max(0, lengths[0] - new + 1 - window) // page] = -1
+        nv.kv_attention(qd, cache, i32(left), i32(lengths), window=window, workspace=ws)
+        assert nv.nvfp4_workspace_status(ws) == 8, (new, window)
