@@ -375,10 +375,12 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
         const auto last_of = [&](int n) { return span.length - a.queries + (row0 + min(n, rows - 1)) / a.group; };
         const int all_to = min(last_of(0) + 1, end);
         const int all_from = a.window > 0 ? last_of(rows) + 1 - a.window : 0;
-        // top: the running maximum of the products, base: what it adds to an exponent, limit: the product that raises it
-        float top[2], base[2], limit[2], sum[2], o[kSteps][4];
+        // top: the running maximum of the products, from_top: the same, 0 before there is one, limit: the product that
+        // raises it.  (A product less the maximum is exact next to it, whatever its size; as one fused a x - a top, the
+        // second rounded, products past 2^26 in the exponent left FP16: 0.5% faster.)
+        float top[2], from_top[2], limit[2], sum[2], o[kSteps][4];
         top[0] = top[1] = limit[0] = limit[1] = kMinusInf;
-        base[0] = base[1] = sum[0] = sum[1] = 0.0f;
+        from_top[0] = from_top[1] = sum[0] = sum[1] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
                     for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
                     const float less = now == top[i] ? 1.0f : exp2_fast((top[i] - now) * by[i]);  // (0 from nothing seen)
                     top[i] = now;
-                    if (now > kMinusInf) base[i] = kUp - now * by[i], limit[i] = now + __fdividef(kSlack, by[i]);
+                    if (now > kMinusInf) from_top[i] = now, limit[i] = now + __fdividef(kSlack, by[i]);
                     sum[i] *= less;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s) o[s][i] *= less, o[s][2 + i] *= less;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
             for (int m = 0; m < kM; ++m) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[m][i] = exp2_fast(fmaf(x[m][i], by[i & 1], base[i & 1]));
+                    x[m][i] = exp2_fast(fmaf(x[m][i] - from_top[i & 1], by[i & 1], kUp));
                     sum[i & 1] += x[m][i];
                 }
 #pragma unroll

@@ -473,3 +473,39 @@ def test_pages_before_the_window_are_not_read(nv, dim, wide, page):
         left[0, max(0, lengths[0] - new + 1 - window) // page] = -1
         nv.kv_attention(qd, cache, i32(left), i32(lengths), window=window, workspace=ws)
         assert nv.nvfp4_workspace_status(ws) == 8, (new, window)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 27, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("dim,wide", [(64, False), (64, True), (128, False), (128, True), (256, False)])
+def test_scores_of_any_size(nv, dim, wide, size):
+    """Products that lie far above or below zero and far apart: the token of the largest has it all, in a whole sequence,
+    among parts that are joined, behind a maximum that rises at every token and one that falls."""
+    rng = np.random.default_rng(dim + wide)
+    page, n = 16, 2400
+    pages = n // page
+    cache, q, sf = filled(nv, rng, pages, 1, page, dim, (2688.0, 4.0))
+    # keys of one element, 1 to 6 times a block scale of 2^-2 to 2^3: rising, the last 16-block of tokens the largest twice over
+    k = np.zeros((n, dim), np.float32)
+    k[:, 0] = np.exp2(np.linspace(-2, 1, n)).astype(np.float32)
+    k[n // 2, 0] = 12.0
+    for order in (np.arange(n), np.arange(n)[::-1], rng.permutation(n)):
+        kq, ksf = K.quantise(k[order].reshape(pages, 1, page, dim), 2688.0)
+        q[0], sf[0] = kq, ksf
+        cache.q[0].copy_(dev(q[0]))
+        cache.sf[0].copy_(dev(sf[0]))
+        keys = K.decode(kq, ksf, host(cache.g)[0])[:, 0].reshape(n, dim)[:, 0]
+        v = K.decode(q[1], sf[1], host(cache.g)[1])[:, 0].reshape(n, dim)
+        qb = np.zeros((1, 1, 2, dim), np.uint16)
+        qb[..., 0] = W.f32_to_bf16_bits(np.array([[[size, -size]]], np.float32))
+        table = np.arange(pages)[None]
+        td = i32(widened(table, [n], page, WIDE * 8)) if wide else i32(table)
+        out, lse = nv.kv_attention(to_dev(qb), cache, td, i32([n]), scale=64.0, lse=True)
+        got, sums = val(host(out))[0, 0], host(lse)[0, 0].astype(np.float64)
+        x = 64.0 * size * keys
+        for row, score in ((0, x), (1, -x)):
+            top = score.max()
+            p = np.where(score == top, 1.0, 0.0)                    # (the next is 64 size 2^-6 below)
+            assert (top - np.unique(score)[-2]) >= 2.0 ** 7
+            ref = p @ v / p.sum()
+            assert np.all(np.abs(got[row] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * (p @ np.abs(v)) / p.sum())
+            assert abs(sums[row] - top - np.log(p.sum())) <= 2.0 ** -20 * (1 + abs(top))
