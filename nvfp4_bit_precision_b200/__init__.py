@@ -1224,11 +1224,12 @@ def kv_attention(q, cache: KVCache, table, lengths, *, scale: Optional[float] = 
                  workspace=None, stream=None):
     """Attention of the last tokens of each sequence, q bf16 [sequences, queries, heads, dim], over the cache: query i
     sees the cached tokens up to its own place lengths[s] - queries + i (lengths int32 [sequences], the queries' tokens
-    included), of them the ``window`` last ones (0: all; pages before the first query's may be gone).  Query heads share the kv heads in order; scale is 1 /
-    sqrt(dim) without one.  Returns bf16 [sequences, queries, heads, dim]; with ``lse`` also the logarithm of each
-    row's sum of exponentials, f32 [sequences, queries, heads].  Rows that see nothing are 0, their lse -inf.
-    ``workspace``: nvfp4_kv_attention_workspace_size bytes, which then hold the status word too.  For inference: no
-    gradients; meant for few rows (the cache is decoded again for every eight of queries * heads / kv_heads)."""
+    included), of them the ``window`` last ones (0: all; pages before the first query's may be gone).  Query heads share
+    the kv heads in order; scale is 1 / sqrt(dim) without one.  Returns bf16 [sequences, queries, heads, dim]; with
+    ``lse`` also the logarithm of each row's sum of exponentials, f32 [sequences, queries, heads].  Rows that see nothing
+    are 0, their lse -inf.  ``workspace``: nvfp4_kv_attention_workspace_size bytes, which then hold the status word too.
+    For inference: no gradients; meant for few rows (the cache is decoded again for every eight of queries * heads /
+    kv_heads)."""
     if stream is not None:
         with _on(stream):
             return kv_attention(q, cache, table, lengths, scale=scale, window=window, lse=lse, workspace=workspace)
