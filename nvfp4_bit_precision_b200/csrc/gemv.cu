@@ -35,8 +35,8 @@
 // as their epilogue, h in FP32 (rounded once, where the down products bring it into shared
 // memory as FP16: 2^-11 of itself; h in bf16, whose loads are half, gave three of those bits
 // away and saved up to 1%), the down products, the weighted sums.  One token's four experts of
-// three 4096 x 1536 matrices (42 MB) 21.6 us on the device, eight tokens' (179 MB) 54.7, 32
-// tokens' without gates (262 MB) 84.2, medians of draws of experts.  On one draw, with the
+// three 4096 x 1536 matrices (42 MB) 21.6 us on the device, eight tokens' (179 MB) 53.9, 32
+// tokens' without gates (262 MB) 83.4, medians of draws of experts.  On one draw, with the
 // down matrices asked for only after the first products' end, the combine's own launch and a
 // status word cleared by a memset 26.7, 59.5 and 89, without them 21, 51 and 79; copies
 // without any decoding 18, 45 and 67.  The launches alone (no rows) take 4.8 to 5.7 us; with

@@ -18,16 +18,17 @@
 //  - products and sums are FP32; an exponential goes into the second product as FP16.
 //
 // What bounds it.  64 sequences of 5120 tokens on average, 40 heads over 8 key heads of 128
-// (383 MB): 78.5 us on the device, 4.9 TB/s; four long ones 83.6 us at 428 MB, 87.5 at 450.
-// The copies alone take 63 and 66.5 us (the copy rate), the join 6; decoding and products
-// overlap with the copies all but 9 to 11 us: 1040 instructions a warp and 64 tokens at 58%
-// of the issue slots, the ALU pipe (conversions) 49% busy.  One sequence of 1000 tokens 9.5
-// to 10 us, 3.8 of them the join.
+// (383 MB): 79.3 us on the device, 4.8 TB/s; four long ones 88.7 us at 450 MB.  The copies
+// alone take 63 us (at 428 MB 66.5: the copy rate), the join 6; decoding and products overlap
+// with the copies all but about 10 us: 1060 instructions a warp and 64 tokens at 58% of the
+// issue slots, the ALU pipe (conversions) 48% busy.  With pages of 16, looked up and copied
+// run by run, 101 us.  One sequence of 1000 tokens 9.3 to 10 us, 3.8 of them the join.
 // Steps on the way, for the 64 sequences: four-warp CTAs with one softmax each and 16-byte
 // copies 106 us; steps of 64 tokens instead of 32, three CTAs a multiprocessor 95; a worker
 // a warp, copies ahead across items 85; joins a warp a row instead of a CTA a row 82.5;
 // codes copied to places free of bank conflicts (bulk copies, whose lanes take turns,
-// before) 80; the maximum raised only where it must be 78.5.  Products held apart by two
+// before) 80; the maximum raised only where it must be 78.5; scores of any size and pages
+// gone before a window, which the forms up to there did not take, 79.3.  Products held apart by two
 // sums each, values decoded ahead of the softmax, 8, 14 or 16 warps: none faster.
 #include "kv_cache.cuh"
 
