@@ -636,9 +636,10 @@ typedef struct {
  * With cos and sin (FP32 [angles][rot / 2], rows by position) the first rot
  * elements of a head are turned: (a, b) -> (a cos - b sin, b cos + a sin) for the
  * pairs (x[i], x[i + rot / 2]), or with neighbours = 1 (x[2 i], x[2 i + 1]), exact
- * up to one rounding to bf16; the keys are then quantised as nvfp4_quantize does it.
- * q [tokens][heads][dim] is turned likewise into q_out (which may be q, at the same
- * strides), whose heads do not overlap; heads = 0 and NULL without queries.  Without cos, rot = 0.
+ * up to one rounding to bf16 (where each product is finite in FP32); the keys are
+ * then quantised as nvfp4_quantize does it.  q [tokens][heads][dim] is turned likewise
+ * into q_out (which may be q, at the same strides), whose heads do not overlap;
+ * heads = 0 and NULL without queries.  Without cos, rot = 0.
  * A token with a negative position or sequence is left out, its row of q_out as it
  * was.  One whose sequence, place or page does not exist, or whose position is not
  * below angles, is left out and reported in the optional workspace's status word
