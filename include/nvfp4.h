@@ -663,7 +663,8 @@ size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int queries, int hea
 
 /*
  * nvfp4_kv_attention -- attention of a few query tokens per sequence over a cache,
- * the queries in bf16 (not quantised), the cached keys and values as they stand:
+ * the queries in bf16 (not quantised; a head's elements below 2^-31 of its largest
+ * are taken to 2^-39 of that), the cached keys and values as they stand:
  *   out[s][i][h] = sum_n p_n v_n,  p = softmax(scale <q[s][i][h], k_n>)
  * over the tokens n that query i sees: those up to its own place lengths[s] -
  * queries + i, of the window (0: all) last ones.  Query heads h belong to key head h
