@@ -523,8 +523,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_kernel(const GemvArgs
                     if (lane == 0) s_step[pair[i]] = ex, atomicMax(&s_top[of[i]], top);
                 }
             } while (xr < x_rows);
-        } else
-        {
+        } else {
             constexpr int kAhead = 4 * NT;  // loads in flight together
             int xr = 0, c = warp - kGemvWarps;
             next(xr, c);

@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(32 * Shape<DIM, SLICE>::kWarps, 1) attend_kern
         const int all_to = min(last_of(0) + 1, end);
         const int all_from = a.window > 0 ? last_of(rows) + 1 - a.window : 0;
         // top: the running maximum of the products, from_top: the same, 0 before there is one, limit: the product that
-        // raises it.  (A product less the maximum is exact next to it, whatever its size; as one fused a x - a top, the
-        // second rounded, products past 2^26 in the exponent left FP16: 0.5% faster.)
+        // raises it.  (Next to the maximum a product less it is exact, whatever their size.  Fused, as by x - (by top) with
+        // the second rounded, was 0.5% faster, but off by a 2^-24 of the score: past 2^26 that left FP16.)
         float top[2], from_top[2], limit[2], sum[2], o[kSteps][4];
         top[0] = top[1] = limit[0] = limit[1] = kMinusInf;
         from_top[0] = from_top[1] = sum[0] = sum[1] = 0.0f;
